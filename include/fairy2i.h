@@ -351,6 +351,110 @@ int fairy2i_gemm_noalloc(const uint8_t* packed, const float* scales, int64_t n, 
                          const void* x, int x_dtype, float* x_scale, int64_t N,
                          void* y, int y_dtype, hipStream_t stream);
 
+/* ---- beside the packed layers: low-rank adapters, the vocabulary loss, gradient clipping ----
+ * Serving one frozen packed layer for many tenants, and tuning on top of it (the card's "Method"
+ * keeps full-precision weights for training; here the packed layer stays fixed and small matrices
+ * beside it learn).  Plain real-valued operators in the x~ / y~ layout above. */
+
+/* Low-rank adapters of many requests at once: for every row i of segment s, with a = seg_adapter[s],
+ *     y_i = base_i + alpha_a B_a (A_a x_i)
+ * base is usually the projection's own output (fairy2i_gemv, fairy2i_gemm), and y may be base.
+ *   x            [N][2m], x_dtype FAIRY2I_F32 or FAIRY2I_BF16; 1 <= N <= 2^20.
+ *   A, B         [L][r][2m] and [L][2n][r], x's dtype; 1 <= L <= 4096, 1 <= r <= 128.  A smaller
+ *                rank than the pool's is a zero-padded one.
+ *   alpha        fp32 [L].
+ *   seg_start    int32 [S+1] on the device, nondecreasing: segment s is rows seg_start[s] ..
+ *                seg_start[s+1]-1 (possibly none), limited to rows 0..N-1.  A decode batch is one
+ *                segment per request; neighbouring rows of one adapter may share a segment.
+ *                1 <= S <= 2^20.
+ *   seg_adapter  int32 [S] on the device; the same adapter may serve several segments.
+ *   base, y      [N][2n], y_dtype FAIRY2I_F32 or FAIRY2I_BF16; y is base or does not overlap it.
+ *                Rows in no segment, and rows of a segment whose adapter is outside [0, L) (-1, say),
+ *                are not written.
+ * fp32 sums; y is rounded once.  Rows do not affect each other: a NaN or infinity in one request's
+ * row or adapter stays in the rows of that row's adapter.  (An infinite entry of B gives NaN or
+ * infinity in its outputs, as 0 * infinity may occur.)
+ *   workspace    fairy2i_lora_workspace_bytes(...) bytes, 16-byte aligned; calls that share one must
+ *                not overlap.
+ * A, B, x, base and y 16-byte aligned; m as everywhere (m % 64 == 0), m, n <= 2^20. */
+size_t fairy2i_lora_workspace_bytes(int count, int64_t N, int64_t m, int r, int64_t S);
+int fairy2i_lora(const void* x, int x_dtype, int64_t N, int64_t m, const void* A, const void* B, const float* alpha,
+                 int64_t L, int r, int64_t n, const int32_t* seg_start, const int32_t* seg_adapter, int64_t S,
+                 const void* base, void* y, int y_dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* One projection of a grouped call: its adapters, its base and its output, with n complex rows. */
+typedef struct {
+  const void* A;
+  const void* B;
+  const float* alpha;
+  const void* base;
+  void* y;
+  int64_t n;
+} fairy2i_lora_item;
+
+/* fairy2i_lora for `count` projections that read the same x (q, k and v; gate and up) and share N,
+ * m, L, r, the segments and the dtypes, eight to a launch.  items is a HOST array, read during the
+ * call only.  workspace: fairy2i_lora_workspace_bytes with the same count. */
+int fairy2i_lora_grouped(const fairy2i_lora_item* items, int count, const void* x, int x_dtype, int64_t N, int64_t m,
+                         int64_t L, int r, const int32_t* seg_start, const int32_t* seg_adapter, int64_t S, int y_dtype,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Gradient of fairy2i_lora: with dy the gradient of y,
+ *     dh_i = alpha_a B_a^T dy_i      dx_i = dx_base_i + A_a^T dh_i
+ *     dA_a = sum_i dh_i x_i^T        dB_a = sum_i alpha_a dy_i (A_a x_i)^T     (rows i of adapter a)
+ *   dy           [N][2n], x's dtype.
+ *   dx_base, dx  [N][2m], dx_dtype FAIRY2I_F32 or FAIRY2I_BF16: dx_base is the gradient through
+ *                the shared projection and dx may be dx_base; both NULL: dx is not computed.  Rows
+ *                without an adapter are not written.
+ *   dA, dB       out, fp32 [L][r][2m] and [L][2n][r]; zero for an adapter that no row uses.  An
+ *                adapter of several segments gets the sum over all of them.
+ * The sums over rows run in a fixed order, so results do not depend on scheduling.  Other arguments
+ * as fairy2i_lora; x here is the x of the forward call. */
+size_t fairy2i_lora_backward_workspace_bytes(int64_t N, int64_t m, int64_t n, int64_t L, int r, int64_t S, int x_dtype);
+int fairy2i_lora_backward(const void* dy, const void* x, int x_dtype, int64_t N, int64_t m, const void* A, const void* B,
+                          const float* alpha, int64_t L, int r, int64_t n, const int32_t* seg_start,
+                          const int32_t* seg_adapter, int64_t S, const void* dx_base, void* dx, int dx_dtype, float* dA,
+                          float* dB, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Softmax cross entropy of a vocabulary projection, without storing the logits l_iv = <h_i, W_v>
+ * (per-token loss, as the card's perplexity tables average it):
+ *     lse_i = log sum_v exp l_iv      loss_i = lse_i - l_{i, target_i}
+ *   h       [N][K], W [V][K], x_dtype FAIRY2I_F32 or FAIRY2I_BF16 (both); K % 64 == 0,
+ *           64 <= K <= 65536; 1 <= N <= 2^20, 1 <= V <= 2^24, N V <= 2^36.
+ *   target  int64 [N]; a target outside [0, V) (-100, say) marks a token that does not count: its
+ *           loss is 0.
+ *   loss, lse  out, fp32 [N].
+ * Sums are fp32 with a running maximum.  workspace: fairy2i_vocab_loss_workspace_bytes(...) bytes,
+ * 16-byte aligned; calls that share one must not overlap. */
+size_t fairy2i_vocab_loss_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype);
+int fairy2i_vocab_loss(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K, const int64_t* target,
+                       float* loss, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Its gradient: with g_i the gradient of loss_i (1/count for a mean) and lse from the forward call,
+ *     p_iv = g_i (exp(l_iv - lse_i) - [v = target_i])   (0 for tokens that do not count)
+ *     dh_i = sum_v p_iv W_v        dW_v = sum_i p_iv h_i
+ * in pieces of the vocabulary, whose logits are computed again; p is held in x_dtype between the two
+ * products, sums are fp32 and each output is rounded once.
+ *   dh [N][K], dW [V][K], x_dtype; either may be NULL (not computed: a frozen W needs no dW). */
+size_t fairy2i_vocab_loss_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype);
+int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K,
+                                const int64_t* target, const float* lse, const float* g, void* dh, void* dW,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Global gradient norm over many tensors, and clipping:
+ *     norm = sqrt(sum of g^2 over all tensors)     c = min(1, max_norm / (norm + 1e-6))     out = c g
+ *   grads, out, numel, dtypes  HOST arrays of count device pointers, sizes and dtypes (FAIRY2I_F32 or
+ *           FAIRY2I_BF16 per tensor), read during the call only; tensors need their element's
+ *           alignment only (16 bytes run faster).  out NULL: in place; out[k] is grads[k] or does not
+ *           overlap any gradient.  A tensor of 0 elements is skipped (its pointers may be NULL).
+ *   max_norm  >= 0; INFINITY computes the norm alone and leaves in-place gradients as they are.
+ *   norm    out, fp32 [1].  Not finite if a gradient is not finite: c is then 0 or NaN.
+ * Squares and sums are fp64 in a fixed order; c is applied in fp32 and each output rounded once.
+ *   workspace  fairy2i_clip_grads_workspace_bytes(count, numel) bytes, 16-byte aligned. */
+size_t fairy2i_clip_grads_workspace_bytes(int count, const int64_t* numel);
+int fairy2i_clip_grads(int count, const void* const* grads, void* const* out, const int64_t* numel, const int* dtypes,
+                       float max_norm, float* norm, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 const char* fairy2i_status_string(int status);
 const char* fairy2i_last_error(void);   /* thread-local detail of the last non-OK return */
 int fairy2i_abi_version(void);

@@ -1,0 +1,237 @@
+"""Vocabulary cross entropy (fairy2i_vocab_loss) and its gradient against the formulas in 64 bits.
+
+Tolerances from the arithmetic, with u the inputs' unit roundoff (finfo.eps / 2):
+  logit   d_iv = (K + 8) 2^-24 sum_k |h_ik W_vk|                  (fp32 sums of exact or once-rounded products)
+  lse     max_v d_iv + 2^-18 + 2^-22 |lse|                        (exponentials and their sum: 64 roundings)
+  loss    lse's + d_it + 2^-23 (|lse| + |loss|)
+  p       |p| (u + d_iv + lse's + 2^-20) + 2^-23 |g| at the target (one rounding to the inputs' dtype)
+  dh, dW  the p's errors through the product, (V + 16) or (N + 16) 2^-24 of the absolute terms for the
+          fp32 sums, and u of the result."""
+import math
+
+import pytest
+import torch
+
+from gpu_util import announce, device
+
+import widely_linear_gemv_amd as f2
+
+pytestmark = pytest.mark.gpu
+E24 = 2.0 ** -24
+
+
+def make(N, V, K, dt, seed, dev, ignored=0.2, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    h = torch.randn(N, K, generator=g).to(dt)
+    W = (torch.randn(V, K, generator=g) * spread * K ** -0.5).to(dt)
+    t = torch.randint(0, V, (N,), generator=g)
+    skip = torch.rand(N, generator=g) < ignored
+    t[skip] = torch.tensor([-100, V, -1, 1 << 40])[torch.arange(int(skip.sum())) % 4]
+    gr = torch.rand(N, generator=g) / N
+    c = {"h": h, "W": W, "t": t, "g": gr}
+    return c, {k: v.to(dev) for k, v in c.items()}
+
+
+def reference(c):
+    h, W, t = c["h"].double(), c["W"].double(), c["t"]
+    N, K = h.shape
+    V = W.shape[0]
+    z = h @ W.t()
+    d = (K + 8) * E24 * (h.abs() @ W.abs().t())
+    lse = torch.logsumexp(z, 1)
+    dl = d.max(1).values + 2.0 ** -18 + 2.0 ** -22 * lse.abs()
+    ok = (t >= 0) & (t < V)
+    at = t.clamp(0, V - 1)
+    row = torch.arange(N)
+    loss = torch.where(ok, lse - z[row, at], torch.zeros(N, dtype=torch.float64))
+    dloss = torch.where(ok, dl + d[row, at] + 2.0 ** -23 * (lse.abs() + loss.abs()), torch.zeros(N, dtype=torch.float64))
+    return z, d, lse, dl, loss, dloss, ok, at
+
+
+def grad_reference(c):
+    z, d, lse, dl, _, _, ok, at = reference(c)
+    h, W = c["h"].double(), c["W"].double()
+    N, V = z.shape
+    u = torch.finfo(c["h"].dtype).eps / 2
+    row = torch.arange(N)
+    g = torch.where(ok, c["g"].double(), torch.zeros(N, dtype=torch.float64))
+    soft = (z - lse[:, None]).exp()
+    p = soft.clone()
+    p[row, at] -= 1.0
+    p = p * g[:, None]
+    ep = g[:, None] * soft * (d + dl[:, None] + 2.0 ** -20) + u * p.abs()
+    ep[row, at] += 2.0 ** -23 * g
+    dh, dW = p @ W, p.t() @ h
+    bh = ep @ W.abs() + (V + 16) * E24 * (p.abs() @ W.abs()) + u * dh.abs()
+    bW = ep.t() @ h.abs() + (N + 16) * E24 * (p.abs().t() @ h.abs()) + u * dW.abs()
+    return dh, bh, dW, bW
+
+
+def close(got, want, bound, label):
+    got = got.double().cpu()
+    assert torch.isfinite(got).all(), label
+    over = ((got - want).abs() - bound).max().item()
+    assert over <= 0, (label, over)
+
+
+SIZES = [(1, 1, 64), (1, 5000, 128), (3, 17, 64), (16, 257, 192), (33, 1000, 256), (65, 129, 64), (130, 8193, 128),
+         (128, 128, 1088), (257, 33, 320), (300, 16500, 64)]
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "N%d-V%d-K%d" % s)
+def test_loss_and_gradient(size, dt):
+    dev = device()
+    c, d = make(*size, dt, 5, dev)
+    N, V, K = size
+    announce("vocab loss", size, dt)
+    loss, lse = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"])
+    _, _, wl, bl, wo, bo, ok, _ = reference(c)
+    close(lse, wl, bl, "lse")
+    close(loss, wo, bo, "loss")
+    assert not loss.cpu()[~ok].any()
+    announce("vocab gradient", size, dt)
+    nan = lambda t: torch.full_like(t, float("nan"))
+    dh, dW = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"], dh=nan(d["h"]), dW=nan(d["W"]))
+    wh, bh, wW, bW = grad_reference(c)
+    close(dh, wh, bh, "dh")
+    close(dW, wW, bW, "dW")
+    assert not dh.cpu()[~ok].any()
+    only_h = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"], want_dW=False)
+    only_W = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"], want_dh=False)
+    assert only_h[1] is None and only_W[0] is None
+    assert torch.equal(only_h[0], dh) and torch.equal(only_W[1], dW)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_wide_logits(dt):
+    """Logits hundreds apart: the running maximum keeps every exponential in range."""
+    dev = device()
+    c, d = make(40, 700, 64, dt, 6, dev, spread=150.0)
+    announce("vocab wide logits", dt)
+    loss, lse = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"])
+    _, _, wl, bl, wo, bo, _, _ = reference(c)
+    close(lse, wl, bl, "lse")
+    close(loss, wo, bo, "loss")
+
+
+def test_no_token_counts():
+    dev = device()
+    c, d = make(9, 100, 64, torch.bfloat16, 7, dev)
+    d["t"].fill_(-100)
+    announce("vocab no token counts")
+    loss, lse = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"])
+    dh, dW = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"])
+    assert not loss.any() and not dh.any() and not dW.any() and torch.isfinite(lse).all()
+
+
+def test_bad_rows_stay_apart():
+    """A NaN row and an infinite one: their own loss and dh only; NaN in a row that does not count
+    reaches no gradient."""
+    dev = device()
+    c, d = make(20, 300, 64, torch.bfloat16, 8, dev, ignored=0.0)
+    d["t"][4] = -100
+    loss, lse = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"])
+    dh, dW = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"])
+    bad = d["h"].clone()
+    bad[4] = float("nan")
+    announce("vocab NaN in an ignored row")
+    loss2, lse2 = f2.fairy2i_vocab_loss(bad, d["W"], d["t"])
+    keep = [i for i in range(20) if i != 4]
+    assert loss2[4] == 0 and torch.isnan(lse2[4]) and torch.equal(lse2[keep], lse[keep]) and torch.equal(loss2[keep], loss[keep])
+    dh2, _ = f2.fairy2i_vocab_loss_backward(bad, d["W"], d["t"], lse2, d["g"], want_dW=False)
+    assert torch.equal(dh2, dh)
+    bad[2] = float("inf")
+    announce("vocab infinite row")
+    loss3, lse3 = f2.fairy2i_vocab_loss(bad, d["W"], d["t"])
+    keep = [i for i in range(20) if i not in (2, 4)]
+    assert not torch.isfinite(lse3[2]) and torch.equal(lse3[keep], lse[keep]) and torch.equal(loss3[keep], loss[keep])
+
+
+def test_gradient_against_differences():
+    """Along random directions of h and W: central differences of the loss.  The loss is smooth with
+    third derivatives under 2 |v|^3-like terms of the logits' change; with t = 2^-7 and unit-size
+    logit directions the truncation is under t^2 of the gradient's own scale."""
+    dev = device()
+    N, V, K = 12, 90, 64
+    c, d = make(N, V, K, torch.float32, 9, dev, ignored=0.0)
+    loss, lse = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"])
+    dh, dW = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"])
+    gsum = d["g"].double().sum().item()
+    for name, grad in (("h", dh), ("W", dW)):
+        v = torch.randn(d[name].shape, generator=torch.Generator().manual_seed(3)).to(dev)
+        v = v / (K ** 0.5 if name == "W" else 1.0)
+        t, vals = 2.0 ** -7, []
+        for sign in (1, -1):
+            e = dict(d)
+            e[name] = d[name] + sign * t * v
+            announce("vocab difference", name, sign)
+            vals.append((f2.fairy2i_vocab_loss(e["h"], e["W"], e["t"])[0].double() * d["g"].double()).sum().item())
+        want = (vals[0] - vals[1]) / (2 * t)
+        got = (grad.double() * v.double()).sum().item()
+        # a logit moves by q = <direction>, at most `move`; |third derivative of lse| <= 4 move^3
+        move = ((v @ d["W"].t()) if name == "h" else (d["h"] @ v.t())).abs().max().item()
+        bound = gsum * (t * t * 4 * move ** 3 / 6 + 2 * 2.0 ** -17 / (2 * t))
+        assert abs(got - want) <= bound, (name, got, want, bound)
+
+
+def test_streams_graphs_and_shared_workspace():
+    dev = device()
+    N, V, K = 70, 3000, 128
+    c, d = make(N, V, K, torch.bfloat16, 10, dev)
+    loss, lse = (t.clone() for t in f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"]))
+    dh, dW = (t.clone() for t in f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    announce("vocab on a side stream")
+    l2, s2 = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"], stream=side)
+    g2 = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], s2, d["g"], stream=side)
+    side.synchronize()
+    assert torch.equal(l2, loss) and torch.equal(g2[0], dh) and torch.equal(g2[1], dW)
+    bf = f2.BF16
+    ws = torch.empty(max(f2.fairy2i_vocab_loss_workspace_bytes(N, V, K, bf),
+                         f2.fairy2i_vocab_loss_backward_workspace_bytes(N, V, K, bf)), dtype=torch.uint8, device=dev)
+    announce("vocab graphs")
+    graphs = []
+    for _ in range(2):                                  # two graphs over one workspace, replayed in turn
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+            a = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"], workspace=ws)
+            b = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], a[1], d["g"], workspace=ws)
+        graphs.append((g, a, b))
+    for k in range(4):
+        for g, a, b in graphs:
+            ws.fill_(255)
+            a[0].zero_()
+            b[0].fill_(3.0)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(a[0], loss) and torch.equal(a[1], lse) and torch.equal(b[0], dh) and torch.equal(b[1], dW), k
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_vocabulary_offsets_past_32_bits(dt):
+    """A vocabulary whose last rows lie past 2^32 bytes: tokens whose targets sit there, few hidden
+    columns elsewhere zero, so that the whole answer is known in closed form."""
+    dev = device()
+    K = 1024
+    V = (1 << 21) + 77 if dt == torch.bfloat16 else (1 << 20) + 77     # 2^32 bytes and more
+    N = 3
+    announce("vocab offsets", dt, V)
+    W = torch.zeros((V, K), dtype=dt, device=dev)
+    h = torch.zeros((N, K), dtype=dt, device=dev)
+    h[:, 0] = 1.0
+    W[V - 1, 0] = 12.0
+    W[5, 0] = 3.0
+    t = torch.tensor([V - 1, 5, V - 2], device=dev)
+    loss, lse = f2.fairy2i_vocab_loss(h, W, t)
+    want = math.log(math.exp(12.0) + math.exp(3.0) + (V - 2))
+    for i, l in enumerate((12.0, 3.0, 0.0)):
+        assert abs(lse[i].item() - want) <= 2.0 ** -17 * want and abs(loss[i].item() - (want - l)) <= 2.0 ** -17 * want
+    dh, _ = f2.fairy2i_vocab_loss_backward(h, W, t, lse, torch.ones(N, device=dev), want_dW=False)
+    mean = (12 * math.exp(12.0) + 3 * math.exp(3.0)) / math.exp(want)
+    u = torch.finfo(dt).eps / 2
+    for i, l in enumerate((12.0, 3.0, 0.0)):
+        # two or three non-zero terms of size <= 12, each rounded once, and the result
+        assert abs(dh[i, 0].item() - (mean - l)) <= 2 * u * 12 + u * abs(mean - l) + 2.0 ** -14
+        assert not dh[i, 1:].any()

@@ -9,7 +9,9 @@ every call raises -- there is no fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -69,6 +71,30 @@ SIGNATURES["fairy2i_gemv_grouped"] = (_INT, [ctypes.POINTER(GemvItem), _INT, _I6
                                               _INT, _INT, _P])
 SIGNATURES["fairy2i_gemv_strided"] = (_INT, [_P, _I64, _P, _I64, _I64, _I64, _INT, _P, _INT, _I64, _P, _I64,
                                               _INT, _I64, _INT, _P])
+
+
+
+class LoraItem(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("alpha", ctypes.c_void_p),
+                ("base", ctypes.c_void_p), ("y", ctypes.c_void_p), ("n", ctypes.c_int64)]
+
+
+_F32 = ctypes.c_float
+SIGNATURES["fairy2i_lora_workspace_bytes"] = (_SZ, [_INT, _I64, _I64, _INT, _I64])
+SIGNATURES["fairy2i_lora"] = (_INT, [_P, _INT, _I64, _I64, _P, _P, _P, _I64, _INT, _I64, _P, _P, _I64, _P, _P, _INT,
+                                     _P, _SZ, _P])
+SIGNATURES["fairy2i_lora_grouped"] = (_INT, [ctypes.POINTER(LoraItem), _INT, _P, _INT, _I64, _I64, _I64, _INT, _P, _P,
+                                             _I64, _INT, _P, _SZ, _P])
+SIGNATURES["fairy2i_lora_backward_workspace_bytes"] = (_SZ, [_I64, _I64, _I64, _I64, _INT, _I64, _INT])
+SIGNATURES["fairy2i_lora_backward"] = (_INT, [_P, _P, _INT, _I64, _I64, _P, _P, _P, _I64, _INT, _I64, _P, _P, _I64, _P,
+                                              _P, _INT, _P, _P, _P, _SZ, _P])
+SIGNATURES["fairy2i_vocab_loss_workspace_bytes"] = (_SZ, [_I64, _I64, _I64, _INT])
+SIGNATURES["fairy2i_vocab_loss"] = (_INT, [_P, _P, _INT, _I64, _I64, _I64, _P, _P, _P, _P, _SZ, _P])
+SIGNATURES["fairy2i_vocab_loss_backward_workspace_bytes"] = (_SZ, [_I64, _I64, _I64, _INT])
+SIGNATURES["fairy2i_vocab_loss_backward"] = (_INT, [_P, _P, _INT, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P])
+SIGNATURES["fairy2i_clip_grads_workspace_bytes"] = (_SZ, [_INT, ctypes.POINTER(_I64)])
+SIGNATURES["fairy2i_clip_grads"] = (_INT, [_INT, ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.POINTER(_I64),
+                                           ctypes.POINTER(_INT), _F32, _P, _P, _SZ, _P])
 
 _lib = None
 
@@ -613,3 +639,286 @@ def fairy2i_gemm_noalloc(packed: torch.Tensor, scales: torch.Tensor, x: torch.Te
                                       _ptr(x_scale), N, _ptr(y), _DTYPE[y.dtype], _stream(stream)))
     return y
 
+
+
+# ---- beside the packed layers: low-rank adapters, the vocabulary loss, gradient clipping ----
+# These calls take stream= too (_on_stream adds it): they run, and allocate what the caller gives no
+# tensor for, on that stream of the operands' device.
+
+def _scope(t, stream):
+    """Context of a call on t's device and the given stream, or the device's current one.  What the
+    call allocates then belongs to the stream that uses it."""
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        return contextlib.nullcontext()                 # the argument checks refuse it
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"stream: on {stream.device}, the operands are on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return contextlib.nullcontext()
+
+
+def _on_stream(fn):
+    """Runs fn(first, ...) in the _scope of its first tensor and its stream argument."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kwargs):
+        if not isinstance(first, torch.Tensor) and first is not None:
+            first = list(first)
+        with _scope(first[0] if isinstance(first, list) and first else first, stream):
+            return fn(first, *args, **kwargs)
+    return call
+
+
+def _workspace(workspace, nbytes, dev):
+    """The call's workspace: allocated when None, checked otherwise."""
+    if workspace is None:
+        return torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+    _tensor(workspace, "workspace")
+    _min_bytes(workspace, "workspace", nbytes)
+    _on_gpu(workspace, "workspace")
+    return workspace
+
+
+def _check_plain(t, name, dtypes, shape):
+    _tensor(t, name)
+    _dtype(t, name, *dtypes)
+    _shape(t, name, shape)
+    _on_gpu(t, name)
+
+
+def _overlap(a, b):
+    """Whether two contiguous tensors share memory without being the same range."""
+    a0, b0 = a.data_ptr(), b.data_ptr()
+    a1, b1 = a0 + a.numel() * a.element_size(), b0 + b.numel() * b.element_size()
+    return a0 < b1 and b0 < a1 and (a0, a1) != (b0, b1)
+
+
+def _check_segments(seg_start, seg_adapter):
+    _tensor(seg_adapter, "seg_adapter")
+    _dtype(seg_adapter, "seg_adapter", torch.int32)
+    if seg_adapter.dim() != 1 or seg_adapter.shape[0] < 1:
+        raise ValueError(f"seg_adapter: shape {tuple(seg_adapter.shape)}, need [S] with S >= 1")
+    S = seg_adapter.shape[0]
+    _on_gpu(seg_adapter, "seg_adapter")
+    _check_plain(seg_start, "seg_start", (torch.int32,), (S + 1,))
+    return S
+
+
+def _check_adapters(x, A, B, alpha, name=""):
+    """A [L][r][2m], B [L][2n][r] of x's dtype and alpha [L]; returns (L, r, 2n)."""
+    _tensor(A, name + "A")
+    _tensor(B, name + "B")
+    _dtype(A, name + "A", x.dtype)
+    _dtype(B, name + "B", x.dtype)
+    if A.dim() != 3 or A.shape[2] != x.shape[1]:
+        raise ValueError(f"{name}A: shape {tuple(A.shape)}, need [L][r][{x.shape[1]}]")
+    L, r = A.shape[0], A.shape[1]
+    if B.dim() != 3 or B.shape[0] != L or B.shape[2] != r or B.shape[1] % 2:
+        raise ValueError(f"{name}B: shape {tuple(B.shape)}, need [{L}][2n][{r}]")
+    _on_gpu(A, name + "A")
+    _on_gpu(B, name + "B")
+    _check_plain(alpha, name + "alpha", (torch.float32,), (L,))
+    return L, r, B.shape[1]
+
+
+def fairy2i_lora_workspace_bytes(count: int, N: int, m: int, r: int, S: int) -> int:
+    return int(lib().fairy2i_lora_workspace_bytes(count, N, m, r, S))
+
+
+@_on_stream
+def fairy2i_lora_grouped(x: torch.Tensor, items, seg_start: torch.Tensor, seg_adapter: torch.Tensor, *, workspace=None):
+    """Low-rank adapters beside projections that read the same x [N][2m].  items: sequence of
+    (A [L][r][2m], B [L][2n][r], alpha [L], base [N][2n], y [N][2n] or None for base itself); L, r and
+    the dtypes are shared.  Segment s is rows seg_start[s] .. seg_start[s+1]-1 and uses adapter
+    seg_adapter[s] (int32 on the GPU); y = base + alpha B A x on its rows, other rows of y are not
+    written.  Returns the list of y."""
+    items = list(items)
+    if not items:
+        raise ValueError("fairy2i_lora_grouped: no items")
+    _check_x(x)
+    N, two_m = x.shape
+    S = _check_segments(seg_start, seg_adapter)
+    arr = (LoraItem * len(items))()
+    named = [(x, "x"), (seg_start, "seg_start"), (seg_adapter, "seg_adapter")]
+    ys = []
+    for k, (A, B, alpha, base, y) in enumerate(items):
+        name = f"items[{k}]." if len(items) > 1 else ""
+        Lk, rk, two_n = _check_adapters(x, A, B, alpha, name)
+        if k == 0:
+            L, r = Lk, rk
+        elif (Lk, rk) != (L, r):
+            raise ValueError(f"{name}A: {Lk} adapters of rank {rk}, items[0] has {L} of rank {r}")
+        y = base if y is None else y
+        _check_y(base, (N, two_n), x.device, name + "base")
+        _check_plain(y, name + "y", (base.dtype,), (N, two_n))
+        if base.dtype != items[0][3].dtype:
+            raise ValueError(f"{name}base: dtype {base.dtype}, items[0] has {items[0][3].dtype}")
+        if _overlap(y, base):
+            raise ValueError(f"{name}y: overlaps base without being base")
+        arr[k] = LoraItem(A.data_ptr(), B.data_ptr(), alpha.data_ptr(), base.data_ptr(), y.data_ptr(), two_n // 2)
+        named += [(A, name + "A"), (B, name + "B"), (alpha, name + "alpha"), (base, name + "base"), (y, name + "y")]
+        ys.append(y)
+    workspace = _workspace(workspace, fairy2i_lora_workspace_bytes(len(items), N, two_m // 2, r, S), x.device)
+    _gpu(*named, (workspace, "workspace"))
+    _check(lib().fairy2i_lora_grouped(arr, len(items), _ptr(x), _DTYPE[x.dtype], N, two_m // 2, L, r, _ptr(seg_start),
+                                      _ptr(seg_adapter), S, _DTYPE[ys[0].dtype], _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), _stream()))
+    return ys
+
+
+def fairy2i_lora(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, alpha: torch.Tensor, seg_start: torch.Tensor,
+                 seg_adapter: torch.Tensor, base: torch.Tensor, *, y=None, workspace=None, stream=None) -> torch.Tensor:
+    """fairy2i_lora_grouped for one projection; y None writes base in place.  Returns y."""
+    return fairy2i_lora_grouped(x, [(A, B, alpha, base, y)], seg_start, seg_adapter, workspace=workspace,
+                                stream=stream)[0]
+
+
+def fairy2i_lora_backward_workspace_bytes(N: int, m: int, n: int, L: int, r: int, S: int, x_dtype: int) -> int:
+    return int(lib().fairy2i_lora_backward_workspace_bytes(N, m, n, L, r, S, x_dtype))
+
+
+@_on_stream
+def fairy2i_lora_backward(dy: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, alpha: torch.Tensor,
+                          seg_start: torch.Tensor, seg_adapter: torch.Tensor, *, dx_base=None, dx=None, dA=None, dB=None,
+                          workspace=None):
+    """Gradient of fairy2i_lora.  dy [N][2n] (x's dtype); dx_base [N][2m] is the gradient through the
+    shared projection: dx = dx_base + A^T dh on rows with an adapter (dx None: in place; dx_base None:
+    no dx).  Returns (dx or None, dA fp32 [L][r][2m], dB fp32 [L][2n][r])."""
+    _check_x(x)
+    N, two_m = x.shape
+    S = _check_segments(seg_start, seg_adapter)
+    L, r, two_n = _check_adapters(x, A, B, alpha)
+    _check_plain(dy, "dy", (x.dtype,), (N, two_n))
+    if dx_base is None and dx is not None:
+        raise ValueError("dx: needs dx_base")
+    if dx_base is not None:
+        dx = dx_base if dx is None else dx
+        _check_y(dx_base, (N, two_m), x.device, "dx_base")
+        _check_plain(dx, "dx", (dx_base.dtype,), (N, two_m))
+        if _overlap(dx, dx_base):
+            raise ValueError("dx: overlaps dx_base without being dx_base")
+    if dA is None:
+        dA = torch.empty((L, r, two_m), dtype=torch.float32, device=x.device)
+    if dB is None:
+        dB = torch.empty((L, two_n, r), dtype=torch.float32, device=x.device)
+    _check_plain(dA, "dA", (torch.float32,), (L, r, two_m))
+    _check_plain(dB, "dB", (torch.float32,), (L, two_n, r))
+    nbytes = fairy2i_lora_backward_workspace_bytes(N, two_m // 2, two_n // 2, L, r, S, _DTYPE[x.dtype])
+    workspace = _workspace(workspace, nbytes, x.device)
+    _gpu((x, "x"), (dy, "dy"), (A, "A"), (B, "B"), (alpha, "alpha"), (seg_start, "seg_start"),
+         (seg_adapter, "seg_adapter"), (dx_base, "dx_base"), (dx, "dx"), (dA, "dA"), (dB, "dB"), (workspace, "workspace"))
+    _check(lib().fairy2i_lora_backward(_ptr(dy), _ptr(x), _DTYPE[x.dtype], N, two_m // 2, _ptr(A), _ptr(B), _ptr(alpha),
+                                       L, r, two_n // 2, _ptr(seg_start), _ptr(seg_adapter), S, _ptr(dx_base), _ptr(dx),
+                                       F32 if dx is None else _DTYPE[dx.dtype], _ptr(dA), _ptr(dB), _ptr(workspace),
+                                       workspace.numel() * workspace.element_size(), _stream()))
+    return dx, dA, dB
+
+
+def _check_head(h, W, target):
+    """h [N][K], W [V][K] of one dtype and target int64 [N]; returns (N, V, K)."""
+    _tensor(h, "h")
+    _tensor(W, "W")
+    _dtype(h, "h", torch.float32, torch.bfloat16)
+    _dtype(W, "W", h.dtype)
+    if h.dim() != 2:
+        raise ValueError(f"h: shape {tuple(h.shape)}, need [N][K]")
+    if W.dim() != 2 or W.shape[1] != h.shape[1]:
+        raise ValueError(f"W: shape {tuple(W.shape)}, need [V][{h.shape[1]}]")
+    _on_gpu(h, "h")
+    _on_gpu(W, "W")
+    _check_plain(target, "target", (torch.int64,), (h.shape[0],))
+    return h.shape[0], W.shape[0], h.shape[1]
+
+
+def fairy2i_vocab_loss_workspace_bytes(N: int, V: int, K: int, x_dtype: int) -> int:
+    return int(lib().fairy2i_vocab_loss_workspace_bytes(N, V, K, x_dtype))
+
+
+@_on_stream
+def fairy2i_vocab_loss(h: torch.Tensor, W: torch.Tensor, target: torch.Tensor, *, loss=None, lse=None, workspace=None):
+    """Per-token cross entropy of the vocabulary projection l = h W^T, h [N][K], W [V][K], without
+    storing l: (loss, lse) fp32 [N].  Tokens whose target (int64) is outside [0, V) get loss 0."""
+    N, V, K = _check_head(h, W, target)
+    loss = torch.empty((N,), dtype=torch.float32, device=h.device) if loss is None else loss
+    lse = torch.empty((N,), dtype=torch.float32, device=h.device) if lse is None else lse
+    _check_plain(loss, "loss", (torch.float32,), (N,))
+    _check_plain(lse, "lse", (torch.float32,), (N,))
+    workspace = _workspace(workspace, fairy2i_vocab_loss_workspace_bytes(N, V, K, _DTYPE[h.dtype]), h.device)
+    _gpu((h, "h"), (W, "W"), (target, "target"), (loss, "loss"), (lse, "lse"), (workspace, "workspace"))
+    _check(lib().fairy2i_vocab_loss(_ptr(h), _ptr(W), _DTYPE[h.dtype], N, V, K, _ptr(target), _ptr(loss), _ptr(lse),
+                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream()))
+    return loss, lse
+
+
+def fairy2i_vocab_loss_backward_workspace_bytes(N: int, V: int, K: int, x_dtype: int) -> int:
+    return int(lib().fairy2i_vocab_loss_backward_workspace_bytes(N, V, K, x_dtype))
+
+
+@_on_stream
+def fairy2i_vocab_loss_backward(h: torch.Tensor, W: torch.Tensor, target: torch.Tensor, lse: torch.Tensor,
+                                g: torch.Tensor, *, want_dh: bool = True, want_dW: bool = True, dh=None, dW=None,
+                                workspace=None):
+    """Gradient of fairy2i_vocab_loss: lse from the forward call, g fp32 [N] the gradient of each
+    token's loss.  Returns (dh [N][K] or None, dW [V][K] or None), h's dtype; want_dh / want_dW False
+    skip one of them (a frozen W needs no dW)."""
+    N, V, K = _check_head(h, W, target)
+    _check_plain(lse, "lse", (torch.float32,), (N,))
+    _check_plain(g, "g", (torch.float32,), (N,))
+    if not want_dh and not want_dW:
+        raise ValueError("fairy2i_vocab_loss_backward: nothing to compute")
+    if (dh is not None and not want_dh) or (dW is not None and not want_dW):
+        raise ValueError("an output was given for a gradient that is not wanted")
+    if want_dh:
+        dh = torch.empty_like(h) if dh is None else dh
+        _check_plain(dh, "dh", (h.dtype,), (N, K))
+    if want_dW:
+        dW = torch.empty_like(W) if dW is None else dW
+        _check_plain(dW, "dW", (h.dtype,), (V, K))
+    workspace = _workspace(workspace, fairy2i_vocab_loss_backward_workspace_bytes(N, V, K, _DTYPE[h.dtype]), h.device)
+    _gpu((h, "h"), (W, "W"), (target, "target"), (lse, "lse"), (g, "g"), (dh, "dh"), (dW, "dW"), (workspace, "workspace"))
+    _check(lib().fairy2i_vocab_loss_backward(_ptr(h), _ptr(W), _DTYPE[h.dtype], N, V, K, _ptr(target), _ptr(lse),
+                                             _ptr(g), _ptr(dh), _ptr(dW), _ptr(workspace),
+                                             workspace.numel() * workspace.element_size(), _stream()))
+    return dh, dW
+
+
+def fairy2i_clip_grads_workspace_bytes(numels) -> int:
+    numels = list(numels)
+    return int(lib().fairy2i_clip_grads_workspace_bytes(len(numels), (_I64 * len(numels))(*numels)))
+
+
+@_on_stream
+def fairy2i_clip_grads(grads, max_norm: float, *, out=None, norm=None, workspace=None) -> torch.Tensor:
+    """Global norm of a list of gradients (fp32 or bf16 each, on one GPU) and clipping to max_norm:
+    each gradient times min(1, max_norm / (norm + 1e-6)), in place or into the list `out`.  Returns
+    the norm, fp32 [1]."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("fairy2i_clip_grads: no gradients")
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError(f"out: {len(outs)} outputs for {len(grads)} gradients")
+    for k, (g, o) in enumerate(zip(grads, outs)):
+        _tensor(g, f"grads[{k}]")
+        _dtype(g, f"grads[{k}]", torch.float32, torch.bfloat16)
+        _on_gpu(g, f"grads[{k}]")
+        if o is not g:
+            _check_plain(o, f"out[{k}]", (g.dtype,), g.shape)
+            if _overlap(o, g):
+                raise ValueError(f"out[{k}]: overlaps its gradient without being it")
+    dev = grads[0].device
+    norm = torch.empty((1,), dtype=torch.float32, device=dev) if norm is None else norm
+    _check_plain(norm, "norm", (torch.float32,), (1,))
+    if not max_norm >= 0:
+        raise ValueError(f"max_norm: {max_norm}, need at least 0")
+    n = len(grads)
+    numel = (_I64 * n)(*[g.numel() for g in grads])
+    workspace = _workspace(workspace, int(lib().fairy2i_clip_grads_workspace_bytes(n, numel)), dev)
+    _gpu(*[(g, f"grads[{k}]") for k, g in enumerate(grads)], *[(o, f"out[{k}]") for k, o in enumerate(outs)],
+         (norm, "norm"), (workspace, "workspace"))
+    _check(lib().fairy2i_clip_grads(n, (_P * n)(*[g.data_ptr() for g in grads]),
+                                    None if out is None else (_P * n)(*[o.data_ptr() for o in outs]), numel,
+                                    (_INT * n)(*[_DTYPE[g.dtype] for g in grads]), max_norm, _ptr(norm),
+                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream()))
+    return norm

@@ -53,6 +53,9 @@ SOURCES = {
     "gemv_f8x.hip": [],
     "prefill.hip": ["-ffp-contract=off"],
     "dequant.hip": ["-ffp-contract=off"],
+    "lora.hip": [],
+    "vocab_loss.hip": [],
+    "clip.hip": [],
     "api.cpp": ["-x", "hip"],
 }
 

@@ -625,3 +625,247 @@ int fairy2i_gemm(const uint8_t* packed, const float* scales, int64_t n, int64_t 
 }
 
 }  // extern "C"
+
+// ---- low-rank adapters, vocabulary loss, gradient clipping ----
+
+namespace {
+
+// Launch geometry bounds of the adapter kernels: 256 outputs (32 transposed rows) per workgroup in a
+// grid dimension of at most 65535.
+constexpr int64_t kMaxLoraSide = int64_t(1) << 20;
+constexpr int64_t kMaxAdapters = 4096;
+constexpr int64_t kMaxSegments = int64_t(1) << 20;
+
+int check_float_dtype(int dtype, const char* name) {
+  if (dtype != FAIRY2I_F32 && dtype != FAIRY2I_BF16)
+    return fail(FAIRY2I_ERR_DTYPE, "%s %d: need F32 or BF16", name, dtype);
+  return FAIRY2I_OK;
+}
+
+int check_workspace(const void* workspace, size_t have, size_t need) {
+  if (need > 0 && (!workspace || have < need))
+    return fail(FAIRY2I_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace ? have : size_t(0), need);
+  if (workspace && !aligned(workspace, 16)) return fail(FAIRY2I_ERR_ALIGN, "workspace needs 16-byte alignment");
+  return FAIRY2I_OK;
+}
+
+int check_lora_n(int64_t n) {
+  if (n < 1 || n > kMaxLoraSide) return fail(FAIRY2I_ERR_SHAPE, "n = %lld out of range", (long long)n);
+  return FAIRY2I_OK;
+}
+
+bool lora_sizes_ok(int64_t N, int64_t m, int64_t r, int64_t S) {
+  return N >= 1 && N <= kMaxTokens && m >= 64 && m <= kMaxLoraSide && m % 64 == 0 && r >= 1 && r <= f2i::kMaxLoraRank &&
+         S >= 1 && S <= kMaxSegments;
+}
+
+int check_lora_sizes(int64_t N, int64_t m, int64_t L, int r, int64_t S) {
+  if (N < 1 || N > kMaxTokens) return fail(FAIRY2I_ERR_SHAPE, "N = %lld out of range", (long long)N);
+  if (m < 64 || m > kMaxLoraSide || m % 64 != 0)
+    return fail(FAIRY2I_ERR_SHAPE, "m = %lld: need 64 <= m <= %lld and m %% 64 == 0", (long long)m, (long long)kMaxLoraSide);
+  if (L < 1 || L > kMaxAdapters) return fail(FAIRY2I_ERR_SHAPE, "L = %lld: need 1 <= L <= %lld adapters", (long long)L, (long long)kMaxAdapters);
+  if (r < 1 || r > f2i::kMaxLoraRank) return fail(FAIRY2I_ERR_SHAPE, "r = %d: need 1 <= r <= %d", r, f2i::kMaxLoraRank);
+  if (S < 1 || S > kMaxSegments) return fail(FAIRY2I_ERR_SHAPE, "S = %lld: need 1 <= S <= %lld segments", (long long)S, (long long)kMaxSegments);
+  return FAIRY2I_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fairy2i_lora_workspace_bytes(int count, int64_t N, int64_t m, int r, int64_t S) {
+  if (count < 1 || !lora_sizes_ok(N, m, r, S)) return 0;
+  return f2i::lora_workspace_bytes(count, N, m, r, S);
+}
+
+int fairy2i_lora_grouped(const fairy2i_lora_item* items, int count, const void* x, int x_dtype, int64_t N, int64_t m,
+                         int64_t L, int r, const int32_t* seg_start, const int32_t* seg_adapter, int64_t S, int y_dtype,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!items || !x || !seg_start || !seg_adapter)
+    return fail(FAIRY2I_ERR_NULL, "items, x, seg_start and seg_adapter are required");
+  if (count < 1) return fail(FAIRY2I_ERR_SHAPE, "count = %d: need at least one item", count);
+  for (int k = 0; k < count; ++k)
+    if (!items[k].A || !items[k].B || !items[k].alpha || !items[k].base || !items[k].y)
+      return fail(FAIRY2I_ERR_NULL, "item %d: A, B, alpha, base and y are required", k);
+  if (int s = check_float_dtype(x_dtype, "x_dtype")) return s;
+  if (int s = check_float_dtype(y_dtype, "y_dtype")) return s;
+  if (int s = check_lora_sizes(N, m, L, r, S)) return s;
+  for (int k = 0; k < count; ++k)
+    if (int s = check_lora_n(items[k].n)) return s;
+  if (!aligned(x, 16) || !aligned(seg_start, 4) || !aligned(seg_adapter, 4))
+    return fail(FAIRY2I_ERR_ALIGN, "x needs 16-byte alignment, seg_start and seg_adapter 4");
+  for (int k = 0; k < count; ++k)
+    if (!aligned(items[k].A, 16) || !aligned(items[k].B, 16) || !aligned(items[k].base, 16) || !aligned(items[k].y, 16) ||
+        !aligned(items[k].alpha, 4))
+      return fail(FAIRY2I_ERR_ALIGN, "item %d: A, B, base and y need 16-byte alignment, alpha 4", k);
+  if (int s = check_workspace(workspace, workspace_bytes, f2i::lora_workspace_bytes(count, N, m, r, S))) return s;
+  const f2i::LoraArgs args{x, x_dtype == FAIRY2I_BF16, y_dtype == FAIRY2I_BF16, (int)N, (int)S, (int)L, r, m,
+                           seg_start, seg_adapter, workspace};
+  for (int k0 = 0; k0 < count; k0 += f2i::kMaxLoraItems) {
+    f2i::LoraItem grp[f2i::kMaxLoraItems];
+    const int num = std::min(count - k0, f2i::kMaxLoraItems);
+    for (int k = 0; k < num; ++k) {
+      const fairy2i_lora_item& it = items[k0 + k];
+      grp[k] = f2i::LoraItem{it.A, it.B, it.alpha, it.base, it.y, it.n};
+    }
+    const hipError_t e = f2i::launch_lora(args, grp, num, stream);
+    if (e != hipSuccess) return hip_status(e, "lora launch");
+  }
+  return ok();
+}
+
+int fairy2i_lora(const void* x, int x_dtype, int64_t N, int64_t m, const void* A, const void* B, const float* alpha,
+                 int64_t L, int r, int64_t n, const int32_t* seg_start, const int32_t* seg_adapter, int64_t S,
+                 const void* base, void* y, int y_dtype, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const fairy2i_lora_item it{A, B, alpha, base, y, n};
+  return fairy2i_lora_grouped(&it, 1, x, x_dtype, N, m, L, r, seg_start, seg_adapter, S, y_dtype, workspace,
+                              workspace_bytes, stream);
+}
+
+size_t fairy2i_lora_backward_workspace_bytes(int64_t N, int64_t m, int64_t n, int64_t L, int r, int64_t S, int x_dtype) {
+  if (!lora_sizes_ok(N, m, r, S) || n < 1 || n > kMaxLoraSide || L < 1 || L > kMaxAdapters) return 0;
+  return f2i::lora_backward_workspace_bytes(N, m, n, r, (int)L, S, x_dtype == FAIRY2I_BF16);
+}
+
+int fairy2i_lora_backward(const void* dy, const void* x, int x_dtype, int64_t N, int64_t m, const void* A, const void* B,
+                          const float* alpha, int64_t L, int r, int64_t n, const int32_t* seg_start,
+                          const int32_t* seg_adapter, int64_t S, const void* dx_base, void* dx, int dx_dtype, float* dA,
+                          float* dB, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!dy || !x || !A || !B || !alpha || !seg_start || !seg_adapter || !dA || !dB)
+    return fail(FAIRY2I_ERR_NULL, "dy, x, A, B, alpha, seg_start, seg_adapter, dA and dB are required");
+  if (!dx != !dx_base) return fail(FAIRY2I_ERR_NULL, "dx and dx_base go together");
+  if (int s = check_float_dtype(x_dtype, "x_dtype")) return s;
+  if (dx)
+    if (int s = check_float_dtype(dx_dtype, "dx_dtype")) return s;
+  if (int s = check_lora_sizes(N, m, L, r, S)) return s;
+  if (int s = check_lora_n(n)) return s;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(dx, 16) ||
+      !aligned(dx_base, 16) || !aligned(dA, 16) || !aligned(dB, 16) || !aligned(alpha, 4) || !aligned(seg_start, 4) ||
+      !aligned(seg_adapter, 4))
+    return fail(FAIRY2I_ERR_ALIGN, "dy, x, A, B, dx_base, dx, dA and dB need 16-byte alignment, alpha and the segments 4");
+  if (int s = check_workspace(workspace, workspace_bytes,
+                              f2i::lora_backward_workspace_bytes(N, m, n, r, (int)L, S, x_dtype == FAIRY2I_BF16)))
+    return s;
+  const f2i::LoraBackwardArgs args{dy, x, A, B, alpha, dx_base, dx, dA, dB, x_dtype == FAIRY2I_BF16,
+                                   dx_dtype == FAIRY2I_BF16, (int)N, (int)S, (int)L, r, m, n, seg_start, seg_adapter,
+                                   workspace};
+  return hip_status(f2i::launch_lora_backward(args, stream), "lora backward launch");
+}
+
+// N V bounds the tiles of one launch (2^32 work-items at the smallest tile).
+static bool vocab_sizes_ok(int64_t N, int64_t V, int64_t K) {
+  return N >= 1 && N <= kMaxTokens && V >= 1 && V <= (int64_t(1) << 24) && N * V <= (int64_t(1) << 36) && K >= 64 &&
+         K <= 65536 && K % 64 == 0;
+}
+
+static int check_vocab_sizes(int64_t N, int64_t V, int64_t K) {
+  if (vocab_sizes_ok(N, V, K)) return FAIRY2I_OK;
+  return fail(FAIRY2I_ERR_SHAPE, "N = %lld, V = %lld, K = %lld: need 1 <= N <= 2^20, 1 <= V <= 2^24, N V <= 2^36, "
+              "64 <= K <= 65536 and K %% 64 == 0", (long long)N, (long long)V, (long long)K);
+}
+
+size_t fairy2i_vocab_loss_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype) {
+  return vocab_sizes_ok(N, V, K) ? f2i::vocab_loss_workspace_bytes(N, V, K, x_dtype == FAIRY2I_BF16) : 0;
+}
+
+int fairy2i_vocab_loss(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K, const int64_t* target,
+                       float* loss, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!h || !W || !target || !loss || !lse) return fail(FAIRY2I_ERR_NULL, "h, W, target, loss and lse are required");
+  if (int s = check_float_dtype(x_dtype, "x_dtype")) return s;
+  if (int s = check_vocab_sizes(N, V, K)) return s;
+  if (!aligned(h, 16) || !aligned(W, 16) || !aligned(target, 8) || !aligned(loss, 4) || !aligned(lse, 4))
+    return fail(FAIRY2I_ERR_ALIGN, "h and W need 16-byte alignment, target 8, loss and lse 4");
+  if (int s = check_workspace(workspace, workspace_bytes, fairy2i_vocab_loss_workspace_bytes(N, V, K, x_dtype))) return s;
+  f2i::VocabArgs a{};
+  a.h = h; a.W = W; a.target = target; a.N = N; a.V = V; a.K = K; a.bf16 = x_dtype == FAIRY2I_BF16;
+  a.loss = loss; a.lse_out = lse; a.ws = workspace;
+  return hip_status(f2i::launch_vocab_loss(a, stream), "vocabulary loss launch");
+}
+
+size_t fairy2i_vocab_loss_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype) {
+  return vocab_sizes_ok(N, V, K) ? f2i::vocab_loss_backward_workspace_bytes(N, V, K, x_dtype == FAIRY2I_BF16) : 0;
+}
+
+int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K,
+                                const int64_t* target, const float* lse, const float* g, void* dh, void* dW,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!h || !W || !target || !lse || !g) return fail(FAIRY2I_ERR_NULL, "h, W, target, lse and g are required");
+  if (!dh && !dW) return fail(FAIRY2I_ERR_NULL, "one of dh and dW is required");
+  if (int s = check_float_dtype(x_dtype, "x_dtype")) return s;
+  if (int s = check_vocab_sizes(N, V, K)) return s;
+  if (!aligned(h, 16) || !aligned(W, 16) || !aligned(dh, 16) || !aligned(dW, 16) || !aligned(target, 8) ||
+      !aligned(lse, 4) || !aligned(g, 4))
+    return fail(FAIRY2I_ERR_ALIGN, "h, W, dh and dW need 16-byte alignment, target 8, lse and g 4");
+  if (int s = check_workspace(workspace, workspace_bytes, fairy2i_vocab_loss_backward_workspace_bytes(N, V, K, x_dtype)))
+    return s;
+  f2i::VocabArgs a{};
+  a.h = h; a.W = W; a.target = target; a.N = N; a.V = V; a.K = K; a.bf16 = x_dtype == FAIRY2I_BF16;
+  a.lse = lse; a.g = g; a.dh = dh; a.dW = dW; a.ws = workspace;
+  return hip_status(f2i::launch_vocab_loss_backward(a, stream), "vocabulary loss backward launch");
+}
+
+static int64_t clip_total_pieces(int count, const int64_t* numel) {
+  int64_t pieces = 0;
+  for (int k = 0; k < count; ++k)
+    if (numel[k] > 0) pieces += f2i::clip_pieces(numel[k]);
+  return pieces;
+}
+
+size_t fairy2i_clip_grads_workspace_bytes(int count, const int64_t* numel) {
+  if (count < 0 || (count > 0 && !numel)) return 0;
+  return 16 + (size_t)clip_total_pieces(count, numel) * sizeof(double);
+}
+
+int fairy2i_clip_grads(int count, const void* const* grads, void* const* out, const int64_t* numel, const int* dtypes,
+                       float max_norm, float* norm, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (count < 0) return fail(FAIRY2I_ERR_SHAPE, "count = %d", count);
+  if (!norm || (count > 0 && (!grads || !numel || !dtypes)))
+    return fail(FAIRY2I_ERR_NULL, "norm and the grads, numel and dtypes arrays are required");
+  if (!(max_norm >= 0.f)) return fail(FAIRY2I_ERR_SHAPE, "max_norm = %g: need max_norm >= 0", (double)max_norm);
+  for (int k = 0; k < count; ++k) {
+    if (numel[k] < 0 || numel[k] > (int64_t(1) << 36))
+      return fail(FAIRY2I_ERR_SHAPE, "tensor %d: %lld elements out of range", k, (long long)numel[k]);
+    if (int s = check_float_dtype(dtypes[k], "dtype")) return s;
+    if (numel[k] == 0) continue;
+    if (!grads[k] || (out && !out[k])) return fail(FAIRY2I_ERR_NULL, "tensor %d: gradient and output are required", k);
+    const size_t a = dtypes[k] == FAIRY2I_BF16 ? 2 : 4;
+    if (!aligned(grads[k], a) || (out && !aligned(out[k], a)))
+      return fail(FAIRY2I_ERR_ALIGN, "tensor %d: gradients and outputs need their element's alignment", k);
+  }
+  if (!aligned(norm, 4)) return fail(FAIRY2I_ERR_ALIGN, "norm needs 4-byte alignment");
+  if (int s = check_workspace(workspace, workspace_bytes, fairy2i_clip_grads_workspace_bytes(count, numel))) return s;
+  float* coef = static_cast<float*>(workspace);
+  double* part = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + 16);
+  int64_t pieces = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t at = 0;
+    for (int k = 0; k < count;) {
+      f2i::ClipGroup grp;
+      grp.count = 0;
+      grp.piece0 = at;
+      int64_t blocks = 0;
+      for (; k < count && grp.count < f2i::kMaxClipItems; ++k) {
+        if (numel[k] == 0) continue;
+        const int64_t p = f2i::clip_pieces(numel[k]);
+        if (grp.count > 0 && blocks + p >= (int64_t(1) << 24)) break;       // 2^32 work-items a launch
+        void* o = out ? out[k] : const_cast<void*>(grads[k]);
+        grp.items[grp.count++] = f2i::ClipItem{grads[k], o, numel[k], (int)blocks, dtypes[k] == FAIRY2I_BF16,
+                                               aligned(grads[k], 16) && aligned(o, 16)};
+        blocks += p;
+      }
+      if (grp.count == 0) continue;
+      const hipError_t e = pass == 0 ? f2i::launch_clip_square(grp, (int)blocks, part, stream)
+                                     : f2i::launch_clip_scale(grp, (int)blocks, coef, stream);
+      if (e != hipSuccess) return hip_status(e, "gradient clipping launch");
+      at += blocks;
+    }
+    if (pass == 0) {
+      pieces = at;
+      const hipError_t e = f2i::launch_clip_norm(part, pieces, max_norm, norm, coef, stream);
+      if (e != hipSuccess) return hip_status(e, "gradient norm launch");
+    }
+  }
+  return ok();
+}
+
+}  // extern "C"

@@ -216,4 +216,117 @@ hipError_t launch_act_quant(const void* x, int x_bf16, int N, int two_m, int8_t*
 hipError_t launch_gemm(const uint8_t* packed, const float* scales, int n, int m, int T,
                        const int8_t* q, const float* delta, int N, void* y, int y_mode,
                        hipStream_t s);
+
+// ---- low-rank adapters (lora.hip) ----
+constexpr int kMaxLoraItems = 8;      // projections per launch; the tables travel in the kernel arguments
+constexpr int kMaxLoraRank = 128;
+struct LoraItem {
+  const void* A;        // [L][r][2m]
+  const void* B;        // [L][2n][r]
+  const float* alpha;   // [L]
+  const void* base;     // [N][2n]
+  void* y;              // [N][2n], may be base
+  int64_t n;
+};
+struct LoraArgs {
+  const void* x;        // [N][2m]
+  int x_bf16, y_bf16, N, S, L, r;
+  int64_t m;
+  const int32_t* seg_start;
+  const int32_t* seg_adapter;
+  void* ws;
+};
+struct LoraBackwardArgs {
+  const void* dy;       // [N][2n], x's dtype
+  const void* x;        // [N][2m]
+  const void* A;
+  const void* B;
+  const float* alpha;
+  const void* dx_base;  // [N][2m] or null with dx
+  void* dx;             // [N][2m] or null
+  float* dA;            // [L][r][2m]
+  float* dB;            // [L][2n][r]
+  int x_bf16, dx_bf16, N, S, L, r;
+  int64_t m, n;
+  const int32_t* seg_start;
+  const int32_t* seg_adapter;
+  void* ws;
+};
+// The kernels' own tables.
+struct LoraReduceItem {
+  const void* x;        // [N][K]
+  const void* W;        // [L][r][ldw]
+  float* part;          // [chunk][N][rp]
+  float* joined;        // [N][rp] (k_reduce_join)
+  int64_t K, ldw;
+  int chunk;
+};
+struct LoraReduceGroup {
+  LoraReduceItem items[kMaxLoraItems];
+};
+struct LoraExpandItem {
+  const float* part;    // [nchunk][N][rp]
+  const void* W;        // [L][M][r]
+  const float* alpha;   // null: the partial sums are scaled already
+  const void* base;
+  void* y;
+  int64_t M;
+  int nchunk;
+};
+struct LoraExpandGroup {
+  LoraExpandItem items[kMaxLoraItems];
+};
+struct LoraOuterItem {
+  const void* x;        // [N][C]
+  const float* factor;  // [N][rp]
+  float* out;           // [split][L][r][C] (rank_major) or [split][L][C][r]
+  int64_t C;
+  int rank_major;
+};
+struct LoraOuterGroup {
+  LoraOuterItem items[2];
+};
+size_t lora_workspace_bytes(int count, int64_t N, int64_t m, int r, int64_t S);
+hipError_t launch_lora(const LoraArgs& p, const LoraItem* items, int count, hipStream_t s);
+size_t lora_backward_workspace_bytes(int64_t N, int64_t m, int64_t n, int r, int L, int64_t S, int x_bf16);
+hipError_t launch_lora_backward(const LoraBackwardArgs& p, hipStream_t s);
+
+// ---- vocabulary cross entropy (vocab_loss.hip) ----
+struct VocabArgs {
+  const void* h;          // [N][K]
+  const void* W;          // [V][K]
+  const int64_t* target;  // [N]
+  int64_t N, V, K;
+  int bf16;
+  float* loss;            // [N] (forward)
+  float* lse_out;         // [N] (forward)
+  const float* lse;       // [N] (backward)
+  const float* g;         // [N] (backward)
+  void* dh;               // [N][K] or null
+  void* dW;               // [V][K] or null
+  void* ws;
+};
+size_t vocab_loss_workspace_bytes(int64_t N, int64_t V, int64_t K, int bf16);
+size_t vocab_loss_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int bf16);
+hipError_t launch_vocab_loss(const VocabArgs& a, hipStream_t s);
+hipError_t launch_vocab_loss_backward(const VocabArgs& a, hipStream_t s);
+
+// ---- gradient clipping (clip.hip) ----
+constexpr int kMaxClipItems = 100;    // tensors per launch; the table travels in the kernel arguments
+struct ClipItem {
+  const void* g;
+  void* out;
+  int64_t numel;
+  int first_piece;        // of the launch
+  uint8_t bf16, vec;      // vec: g and out 16-byte aligned
+};
+struct ClipGroup {
+  int count;
+  int64_t piece0;         // the launch's first piece among all pieces
+  ClipItem items[kMaxClipItems];
+};
+int64_t clip_pieces(int64_t numel);
+hipError_t launch_clip_square(const ClipGroup& grp, int pieces, double* part, hipStream_t s);
+hipError_t launch_clip_norm(const double* part, int64_t pieces, float max_norm, float* norm, float* coef, hipStream_t s);
+hipError_t launch_clip_scale(const ClipGroup& grp, int pieces, const float* coef, hipStream_t s);
 }  // namespace f2i
