@@ -30,21 +30,28 @@ namespace {
 
 enum { kLoss = 0, kGrad = 1, kHidden = 2, kWeight = 3 };
 
+// acc += a b on the matrix cores, one 16-byte operand per lane.  The accumulator is tied to its own
+// accumulation registers: left to itself the compiler moves the 256 of a 128 x 128 wave tile about,
+// which cost a third of the time.  (Consecutive calls use different accumulators, and settle()
+// separates the last one from whatever reads them.)
 template <typename T>
-__device__ __forceinline__ v4f mma(v4u a, v4u b, v4f c) {
+__device__ __forceinline__ void mma(v4f& acc, const v4u& a, const v4u& b) {
   if constexpr (sizeof(T) == 2) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[e]), __uint_as_float(b[e]), c, 0, 0, 0);
-    return c;
+      asm volatile("v_mfma_f32_16x16x4_f32 %0, %1, %2, %0" : "+a"(acc) : "v"(a[e]), "v"(b[e]));
   }
 }
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
-// exp(l - top), 1 where both are the same infinity.  expf, not the fast form: its error does not grow
-// with the distance from the maximum, and the tile's K products cost far more.
-__device__ __forceinline__ float exp_off(float l, float top) { return l == top ? 1.f : expf(l - top); }
+// exp(x) for x <= 0: off by |x| 2^-24 of itself, which in sum_v exp(l_v - top) comes to at most
+// log(V) 2^-24 of the sum (the mean distance from the maximum under the softmax is at most log V).
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+// exp(l - top), 1 where both are the same infinity.
+__device__ __forceinline__ float exp_off(float l, float top) { return l == top ? 1.f : fast_exp(l - top); }
 
 }  // namespace
 
@@ -70,23 +77,34 @@ struct VocabTile {
   int tiles_a, tiles_b;
 };
 
-// Workgroup: a BM x BN tile of C, WA x WB waves, each BM/WA x BN/WB.  Per step 128 bytes of every
-// row of both operands are copied straight into one of two LDS buffers (16-byte segment sg of row
-// R in slot sg ^ (R % 8), so the 16 rows of a fragment read hit different banks); the next step's
-// copies are issued before the current one is multiplied.  Rows past the end read as 0.
+// Workgroup: a BM x BN tile of C, WA x WB waves, each BM/WA x BN/WB.  The contraction runs in steps of
+// 128 bytes of every row (a whole cache line: 64-byte pieces halved the L2's throughput), double
+// buffered in LDS, each step multiplied in two halves.  While a half is multiplied (its operands
+// already in registers) the wave reads the next half's operands from LDS; once a step's second half
+// is in registers everywhere (the step's one barrier), the copies of the step after next go straight
+// into its buffer and have the rest of this step and half of the next one to land.  16-byte segment sg
+// of row R lies in place sg ^ (R % 8) of its 128 bytes: any eight neighbouring lanes of an operand read
+// cover all banks once.  Rows past the end of a matrix read as 0; past the last step the copies repeat
+// it, which nothing reads.
 template <typename T, int BM, int BN, int WA, int WB, int EPI>
-__global__ __launch_bounds__(64 * WA * WB) void k_nt(VocabTile t) {
+__global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
   constexpr int kWaves = WA * WB;
   constexpr int FA = BM / WA / 16, FB = BN / WB / 16;
   constexpr int kBlocks = (BM + BN) / 8;                  // 1 KB copies (8 rows) per step
   static_assert(kBlocks % kWaves == 0 && BM % 8 == 0, "whole copies per wave");
   constexpr int kMine = kBlocks / kWaves;
-  __shared__ __align__(16) uint8_t s_buf[2][(BM + BN) * 128];
+  constexpr int kStep = (BM + BN) * 128;
+  __shared__ __align__(16) uint8_t s_buf[2 * kStep];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane & 15, g = lane >> 4;
   const int wa = wave / WB, wb = wave % WB;
-  const int ta = blockIdx.x / t.tiles_b, tb = blockIdx.x % t.tiles_b;
+  // Workgroups go to the eight XCDs in turn; each XCD takes a contiguous run of tiles with the B tiles
+  // innermost, so the A rows of a run are fetched into one L2 only.
+  const int per_xcd = (t.tiles_a * t.tiles_b + 7) / 8;
+  const int tile = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per_xcd || tile >= t.tiles_a * t.tiles_b) return;
+  const int ta = tile / t.tiles_b, tb = tile % t.tiles_b;
   const int64_t a0 = (int64_t)ta * BM, b0 = (int64_t)tb * BN;
   const int64_t ra = min((int64_t)BM, t.rows_a - a0), rb = min((int64_t)BN, t.rows_b - b0);
   const __amdgpu_buffer_rsrc_t rs_a =
@@ -96,79 +114,128 @@ __global__ __launch_bounds__(64 * WA * WB) void k_nt(VocabTile t) {
   uint32_t off[kMine];
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
-    const int blk = wave * kMine + i;
-    const int R = blk * 8 + (lane >> 3), sg = (lane & 7) ^ (R & 7);
+    const int R = (wave * kMine + i) * 8 + (lane >> 3), sg = (lane & 7) ^ (R & 7);
     off[i] = (uint32_t)(((R < BM ? R * t.lda : (R - BM) * t.ldb)) * sizeof(T)) + 16 * sg;
   }
-  auto stage = [&](int step, int buf) {
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int blk = wave * kMine + i;
-      const uint32_t voff = off[i];
-      if (blk * 8 < BM)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, (lds_ptr_t)(s_buf[buf] + blk * 1024), 16, voff, step * 128, 0, 0);
-      else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, (lds_ptr_t)(s_buf[buf] + blk * 1024), 16, voff, step * 128, 0, 0);
-    }
+  const int steps = (int)(t.k * sizeof(T) / 128);
+  // this wave's copy i of a step
+  auto copy = [&](int step, int buf, int i) {
+    const int koff = min(step, steps - 1) * 128;
+    const int blk = wave * kMine + i;
+    const uint32_t voff = off[i];
+    if (blk * 8 < BM)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, (lds_ptr_t)(s_buf + buf * kStep + blk * 1024), 16, voff, koff, 0, 0);
+    else
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, (lds_ptr_t)(s_buf + buf * kStep + blk * 1024), 16, voff, koff, 0, 0);
   };
+  int at_a[2], at_b[2];                                   // operand offsets of the two halves
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int at = c * 128 + ((4 * h + g) ^ (c & 7)) * 16;
+    at_a[h] = wa * FA * 2048 + at;
+    at_b[h] = BM * 128 + wb * FB * 2048 + at;
+  }
   v4f acc[FA][FB];
 #pragma unroll
   for (int i = 0; i < FA; ++i)
 #pragma unroll
     for (int j = 0; j < FB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  auto compute = [&](int buf) {
+  v4u fa[2][FA], fb[2][FB];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) copy(r, r, i);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((kMine & 15) | ((kMine >> 4) << 14) | 0xF70);   // step 0 has landed
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < FA; ++i) fa[0][i] = *reinterpret_cast<const v4u*>(s_buf + at_a[0] + i * 2048);
+#pragma unroll
+  for (int j = 0; j < FB; ++j) fb[0][j] = *reinterpret_cast<const v4u*>(s_buf + at_b[0] + j * 2048);
+  for (int s = 0; s < steps; ++s) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      v4u fa[FA], fb[FB];
-      const int slot = (4 * h + g) ^ (c & 7);
+      // FA groups of FB products; ahead of each group its share of the reads and copies
+      const uint8_t* next = s_buf + ((s + h) & 1) * kStep;
 #pragma unroll
-      for (int i = 0; i < FA; ++i)
-        fa[i] = *reinterpret_cast<const v4u*>(s_buf[buf] + ((wa * FA + i) * 16 + c) * 128 + slot * 16);
+      for (int i = 0; i < FA; ++i) {
+        fa[h ^ 1][i] = *reinterpret_cast<const v4u*>(next + at_a[h ^ 1] + i * 2048);
 #pragma unroll
-      for (int j = 0; j < FB; ++j)
-        fb[j] = *reinterpret_cast<const v4u*>(s_buf[buf] + (BM + (wb * FB + j) * 16 + c) * 128 + slot * 16);
+        for (int j = i * FB / FA; j < (i + 1) * FB / FA; ++j)
+          fb[h ^ 1][j] = *reinterpret_cast<const v4u*>(next + at_b[h ^ 1] + j * 2048);
+        if (h == 1) {
 #pragma unroll
-      for (int i = 0; i < FA; ++i)
+          for (int k = i * kMine / FA; k < (i + 1) * kMine / FA; ++k) copy(s + 2, s & 1, k);
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < FB; ++j) acc[i][j] = mma<T>(fa[i], fb[j], acc[i][j]);
+        for (int j = 0; j < FB; ++j) mma<T>(acc[i][j], fa[h][i], fb[h][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (h == 0) {
+        // this wave holds the step's second half, and its copies of the next step have landed
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x70);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+      }
     }
-  };
-  const int steps = (int)(t.k * sizeof(T) / 128);
-  stage(0, 0);
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-  for (int s = 0; s < steps; ++s) {
-    if (s + 1 < steps) stage(s + 1, (s + 1) & 1);
-    compute(s & 1);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
   }
+  __builtin_amdgcn_s_waitcnt(0);                           // no copy outlives its buffer
+  settle();
+#pragma unroll
+  for (int i = 0; i < FA; ++i)
+#pragma unroll
+    for (int j = 0; j < FB; ++j) asm volatile("" : "+a"(acc[i][j]));   // read only after settle()
 
   const int64_t va = a0 + wa * FA * 16 + 4 * g;            // this lane's first A row
   const int64_t nb = b0 + wb * FB * 16 + c;                // its first B row
   if constexpr (EPI == kLoss) {
-    __shared__ float2 s_red[WA][BN];
+    // The pairs of the tile's waves take over the operand buffers.  (They are not an array of their own:
+    // with two arrays in LDS the compiler no longer knows that an operand read cannot meet a copy in
+    // flight and waits for every copy before every read, which doubled the time.)
+    __syncthreads();                                       // every wave's copies have landed
+    float2(*s_red)[BN] = reinterpret_cast<float2(*)[BN]>(s_buf);
+    static_assert(WA * BN * sizeof(float2) <= sizeof(s_buf), "the pairs fit");
+    const bool whole = a0 + BM <= t.V;                     // no row past the vocabulary
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
       const int64_t tok = nb + 16 * j;
       const int64_t tgt = tok < t.N ? t.target[tok] : -1;
-      float top = -INFINITY;
+      // this lane has the target's logit if it lies 16 i + e past the lane's first row
+      const int d = tgt >= va && tgt < va + FA * 16 && tgt < t.V ? (int)(tgt - va) : 4;
+      float top = -INFINITY, mine = 0.f;
 #pragma unroll
       for (int i = 0; i < FA; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int64_t v = va + 16 * i + e;
-          if (v < t.V) top = fmaxf(top, acc[i][j][e]);
-          if (v == tgt && v < t.V) t.tlogit[tok] = acc[i][j][e];
+          if (!whole && va + 16 * i + e >= t.V) acc[i][j][e] = -INFINITY;
+          top = fmaxf(top, acc[i][j][e]);
         }
+      if (__ballot((d & 12) == 0)) {
+#pragma unroll
+        for (int i = 0; i < FA; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (d == 16 * i + e) mine = acc[i][j][e];
+        if ((d & 12) == 0) t.tlogit[tok] = mine;
+      }
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       float sum = 0.f;
+      if (__ballot(!(fabsf(top) < INFINITY))) {            // an infinity: exp_off's cases
 #pragma unroll
-      for (int i = 0; i < FA; ++i)
+        for (int i = 0; i < FA; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (va + 16 * i + e < t.V) sum += exp_off(acc[i][j][e], top);
+          for (int e = 0; e < 4; ++e)
+            if (va + 16 * i + e < t.V) sum += exp_off(acc[i][j][e], top);
+      } else {
+#pragma unroll
+        for (int i = 0; i < FA; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum += fast_exp(acc[i][j][e] - top);
+      }
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
       if (g == 0) s_red[wa][(wb * FB + j) * 16 + c] = make_float2(top, sum);
@@ -289,7 +356,8 @@ __global__ __launch_bounds__(256) void k_transpose_pad(const T* __restrict__ in,
 
 namespace {
 
-constexpr int kTileA = 128, kTileB = 128;
+constexpr int kWA = 2, kWB = 4;
+constexpr int kTileA = 256, kTileB = 256;
 constexpr int64_t kPieceRows = 8192;         // vocabulary entries per piece of the gradient, less where N
                                              // tokens of it would be over 2^27 values
 
@@ -301,7 +369,7 @@ template <typename T, int EPI>
 void launch_nt(VocabTile& t, int64_t cover_a, int64_t cover_b, hipStream_t s) {
   t.tiles_a = tiles(cover_a, kTileA);
   t.tiles_b = tiles(cover_b, kTileB);
-  hipLaunchKernelGGL((k_nt<T, kTileA, kTileB, 2, 2, EPI>), dim3(t.tiles_a * t.tiles_b), dim3(256), 0, s, t);
+  hipLaunchKernelGGL((k_nt<T, kTileA, kTileB, kWA, kWB, EPI>), dim3((t.tiles_a * t.tiles_b + 7) / 8 * 8), dim3(64 * kWA * kWB), 0, s, t);
 }
 
 struct LossPlan {
