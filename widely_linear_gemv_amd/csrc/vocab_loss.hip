@@ -7,12 +7,13 @@
 // cores does all the work; what differs is what happens to a finished tile:
 //   logits   A = W, B = h: each tile is reduced on chip to a (maximum, sum of exponentials) pair
 //            per token, and the target's logit is picked out; no logit is stored.
-//   p        the same product again for a piece of the vocabulary: p is rounded to the inputs' dtype
-//            and stored twice, as [token][v] and as [v][token] (the two products below contract v
-//            and the token).  For bf16 inputs this rounding (2^-8 of each p) adds about as much to
-//            dh and dW as their own final rounding to bf16.
-//   dh       A = W^T piece, B = p: fp32 sums over the pieces, rounded once at the end.
+//   p        the same product again for a piece of the vocabulary: p [token][v] is rounded to the
+//            inputs' dtype and stored.  For bf16 inputs this rounding (2^-8 of each p) adds about as
+//            much to dh and dW as their own final rounding to bf16.
+//   dh       A = W^T, B = p: fp32 sums over the pieces, rounded once at the end.
 //   dW       A = h^T, B = p^T: rows of the piece, rounded once.
+// Transposed operands are read from the matrix as it lies in memory: rows of the contraction are
+// copied into LDS and transposed on the way into registers, so no transposed copy is made.
 // Sums are fp32; a C tile has the A rows in its accumulator rows, so a lane holds four consecutive
 // vocabulary entries (or hidden columns) of one token (or vocabulary row).
 #include <algorithm>
@@ -24,7 +25,10 @@ namespace f2i {
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef __attribute__((address_space(3))) v4s* lds_v4s_t;
 
 namespace {
 
@@ -58,8 +62,8 @@ __device__ __forceinline__ float exp_off(float l, float top) { return l == top ?
 // What the epilogues need.
 struct VocabTile {
   int64_t rows_a, rows_b;       // rows of A and B
-  int64_t k;                    // contraction (a multiple of 128 bytes of T)
-  int64_t lda, ldb;
+  int64_t k;                    // contraction
+  int64_t lda, ldb;             // row pitch in memory (of a transposed operand: of its contraction rows)
   const void* a;
   const void* b;
   const int64_t* target;        // [N]
@@ -68,32 +72,86 @@ struct VocabTile {
   float2* part;                 // [row tile of A][N] (kLoss)
   float* tlogit;                // [N] (kLoss)
   void* p;                      // [N][ldp] (kGrad)
-  void* pt;                     // [ldp][ldt] (kGrad)
-  float* acc;                   // [rows_b][rows_a] fp32 running sums (kHidden)
+  float* acc;                   // [splits][rows_b][rows_a] fp32 running sums (kHidden)
   void* out;                    // [rows_b][rows_a] (kHidden on the last piece, kWeight)
   int64_t v0, V;                // first vocabulary entry of A, vocabulary size
-  int64_t N, ldp, ldt;
+  int64_t N, ldp;
   int first, last;              // piece
   int tiles_a, tiles_b;
+  int splits;                   // of the contraction (kHidden; 1 otherwise)
+};
+
+// ds_read_b64_tr_b16: of 16 lanes, lane 4 i + q gives the address of columns 4 q .. 4 q + 3 of
+// contraction row i, and lane l gets column l of the four rows.  (The restrict-qualified argument gives
+// the read alias information; without any the compiler takes it to meet the copies in flight and waits
+// for all of them first.)
+__device__ __forceinline__ v2u read_transposed(lds_v4s_t __restrict p) {
+  return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p));
+}
+
+// One side of the product in LDS: ROWS rows by 128 bytes of contraction, 16-byte pieces permuted so that
+// the lanes of an operand read cover all banks evenly.
+//   Plain: row R at 128 R, its segment sg in place sg ^ (R % 8).
+//   TRANS: contraction rows of ROWS elements as in memory; 16 columns of contraction row k (32 bytes of
+//   bf16, 64 of fp32) lie in place unit ^ f(k), f(k) = k % 4 + 4 (k / 8 % 4) for bf16, k / 4 % 4 for
+//   fp32: the sixteen (four) contraction rows of one read differ in f.
+template <typename T, int ROWS, bool TRANS>
+struct Side {
+  static constexpr int kUnit = 16 * sizeof(T);            // bytes of 16 columns
+  static constexpr int kUnits = ROWS / 16;
+  __device__ static int f(int k) {
+    return (sizeof(T) == 2 ? (k & 3) | (((k >> 3) & 3) << 2) : (k >> 2) & 3) & (kUnits - 1);
+  }
+  // Offset in memory (from the tile's first row, or the step's first contraction row and the tile's
+  // first column) of the 16 bytes that lane `lane` of 1 KB copy `blk` brings.
+  __device__ static uint32_t source(int blk, int lane, int64_t ld) {
+    if constexpr (!TRANS) {
+      const int R = blk * 8 + (lane >> 3), sg = (lane & 7) ^ (R & 7);
+      return (uint32_t)(R * ld * sizeof(T)) + 16 * sg;
+    } else {
+      constexpr int kRow = ROWS * sizeof(T);
+      const int pos = blk * 1024 + lane * 16, k = pos / kRow, in = pos % kRow;
+      return (uint32_t)(k * ld * sizeof(T)) + ((in / kUnit) ^ f(k)) * kUnit + in % kUnit;
+    }
+  }
+  // The lane's operand of 16-row fragment `frag` in half h of a step, at `base`.
+  __device__ static __forceinline__ v4u read(const uint8_t* base, int frag, int h, int c, int g) {
+    if constexpr (!TRANS) {
+      return *reinterpret_cast<const v4u*>(base + (frag * 16 + c) * 128 + ((4 * h + g) ^ (c & 7)) * 16);
+    } else if constexpr (sizeof(T) == 2) {
+      constexpr int kRow = ROWS * 2;
+      const int k = 8 * g + (c >> 2);
+      const uint8_t* p = base + k * kRow + ((frag ^ f(k)) * kUnit) + (c & 3) * 8 + h * 32 * kRow;
+      const v2u lo = read_transposed((lds_v4s_t)p), hi = read_transposed((lds_v4s_t)(p + 4 * kRow));
+      return v4u{lo[0], lo[1], hi[0], hi[1]};
+    } else {
+      constexpr int kRow = ROWS * 4;
+      const uint8_t* p = base + (16 * h + 4 * g) * kRow + ((frag ^ (g & (kUnits - 1))) * kUnit) + c * 4;
+      return v4u{*reinterpret_cast<const uint32_t*>(p), *reinterpret_cast<const uint32_t*>(p + kRow),
+                 *reinterpret_cast<const uint32_t*>(p + 2 * kRow), *reinterpret_cast<const uint32_t*>(p + 3 * kRow)};
+    }
+  }
 };
 
 // Workgroup: a BM x BN tile of C, WA x WB waves, each BM/WA x BN/WB.  The contraction runs in steps of
-// 128 bytes of every row (a whole cache line: 64-byte pieces halved the L2's throughput), double
-// buffered in LDS, each step multiplied in two halves.  While a half is multiplied (its operands
-// already in registers) the wave reads the next half's operands from LDS; once a step's second half
-// is in registers everywhere (the step's one barrier), the copies of the step after next go straight
-// into its buffer and have the rest of this step and half of the next one to land.  16-byte segment sg
-// of row R lies in place sg ^ (R % 8) of its 128 bytes: any eight neighbouring lanes of an operand read
-// cover all banks once.  Rows past the end of a matrix read as 0; past the last step the copies repeat
-// it, which nothing reads.
+// 128 bytes (64 bf16, 32 fp32) of every row -- whole cache lines: 64-byte pieces halved the L2's
+// throughput -- double buffered in LDS, each step multiplied in two halves.  While a half is multiplied
+// (its operands already in registers) the wave reads the next half's operands from LDS; once a step's
+// second half is in registers everywhere (the step's one barrier), the copies of the step after next
+// go straight into its buffer and have the rest of this step and half of the next one to land.  Rows
+// past the end of a matrix read as 0; past the last step the copies repeat it, which nothing reads.
 template <typename T, int BM, int BN, int WA, int WB, int EPI>
 __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
   constexpr int kWaves = WA * WB;
   constexpr int FA = BM / WA / 16, FB = BN / WB / 16;
-  constexpr int kBlocks = (BM + BN) / 8;                  // 1 KB copies (8 rows) per step
-  static_assert(kBlocks % kWaves == 0 && BM % 8 == 0, "whole copies per wave");
+  constexpr int kBlocks = (BM + BN) / 8;                  // 1 KB copies per step
+  static_assert(BM / 8 % kWaves == 0 && BN / 8 % kWaves == 0, "whole copies per wave and side");
   constexpr int kMine = kBlocks / kWaves;
   constexpr int kStep = (BM + BN) * 128;
+  constexpr int kDeep = 128 / sizeof(T);                  // contraction per step
+  using SideA = Side<T, BM, (EPI == kHidden || EPI == kWeight)>;
+  using SideB = Side<T, BN, EPI == kWeight>;
+  constexpr bool kTransA = EPI == kHidden || EPI == kWeight, kTransB = EPI == kWeight;
   __shared__ __align__(16) uint8_t s_buf[2 * kStep];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -101,93 +159,100 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
   const int wa = wave / WB, wb = wave % WB;
   // Workgroups go to the eight XCDs in turn; each XCD takes a contiguous run of tiles with the B tiles
   // innermost, so the A rows of a run are fetched into one L2 only.
+  const int split = blockIdx.y;
   const int per_xcd = (t.tiles_a * t.tiles_b + 7) / 8;
   const int tile = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
   if ((int)(blockIdx.x >> 3) >= per_xcd || tile >= t.tiles_a * t.tiles_b) return;
   const int ta = tile / t.tiles_b, tb = tile % t.tiles_b;
   const int64_t a0 = (int64_t)ta * BM, b0 = (int64_t)tb * BN;
-  const int64_t ra = min((int64_t)BM, t.rows_a - a0), rb = min((int64_t)BN, t.rows_b - b0);
-  const __amdgpu_buffer_rsrc_t rs_a =
-      range_rsrc(static_cast<const T*>(t.a) + a0 * t.lda, max(ra, (int64_t)0) * t.lda * sizeof(T));
-  const __amdgpu_buffer_rsrc_t rs_b =
-      range_rsrc(static_cast<const T*>(t.b) + b0 * t.ldb, max(rb, (int64_t)0) * t.ldb * sizeof(T));
+  const int all_steps = (int)((t.k + kDeep - 1) / kDeep);
+  const int per_split = (all_steps + t.splits - 1) / t.splits;
+  const int step0 = split * per_split, steps = min(per_split, all_steps - step0);
+  // the part of an operand that step `step` copies, and the lanes' offsets in it
+  auto part = [&](const void* m, int64_t row0, int64_t rows, int64_t ld, bool trans, int step) {
+    const T* p = static_cast<const T*>(m);
+    if (trans) {
+      const int64_t k = (int64_t)step * kDeep;
+      return range_rsrc(p + k * ld, max(t.k - k, (int64_t)0) * ld * (int64_t)sizeof(T));
+    }
+    return range_rsrc(p + row0 * ld, max(rows - row0, (int64_t)0) * ld * (int64_t)sizeof(T));
+  };
+  // Copy i of this wave is 1 KB number i kWaves + wave of the step; the first kCopiesA are A's.
+  constexpr int kCopiesA = BM / 8 / kWaves;
   uint32_t off[kMine];
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
-    const int R = (wave * kMine + i) * 8 + (lane >> 3), sg = (lane & 7) ^ (R & 7);
-    off[i] = (uint32_t)(((R < BM ? R * t.lda : (R - BM) * t.ldb)) * sizeof(T)) + 16 * sg;
+    const int blk = i * kWaves + wave;
+    off[i] = i < kCopiesA ? SideA::source(blk, lane, t.lda) + (kTransA ? (uint32_t)(a0 * sizeof(T)) : 0)
+                          : SideB::source(blk - BM / 8, lane, t.ldb) + (kTransB ? (uint32_t)(b0 * sizeof(T)) : 0);
   }
-  const int steps = (int)(t.k * sizeof(T) / 128);
-  // this wave's copy i of a step
-  auto copy = [&](int step, int buf, int i) {
-    const int koff = min(step, steps - 1) * 128;
-    const int blk = wave * kMine + i;
-    const uint32_t voff = off[i];
-    if (blk * 8 < BM)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, (lds_ptr_t)(s_buf + buf * kStep + blk * 1024), 16, voff, koff, 0, 0);
-    else
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, (lds_ptr_t)(s_buf + buf * kStep + blk * 1024), 16, voff, koff, 0, 0);
-  };
-  int at_a[2], at_b[2];                                   // operand offsets of the two halves
+  auto copy = [&](__amdgpu_buffer_rsrc_t rs_a, __amdgpu_buffer_rsrc_t rs_b, int step, int buf, int from, int to) {
+    const int ka = kTransA ? 0 : step * 128, kb = kTransB ? 0 : step * 128;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int at = c * 128 + ((4 * h + g) ^ (c & 7)) * 16;
-    at_a[h] = wa * FA * 2048 + at;
-    at_b[h] = BM * 128 + wb * FB * 2048 + at;
-  }
+    for (int i = 0; i < kMine; ++i) {
+      if (i < from || i >= to) continue;
+      const uint32_t voff = off[i];
+      uint8_t* to_lds = s_buf + buf * kStep + (i * kWaves + wave) * 1024;
+      if (i < kCopiesA) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, (lds_ptr_t)to_lds, 16, voff, ka, 0, 0);
+      else __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, (lds_ptr_t)to_lds, 16, voff, kb, 0, 0);
+    }
+  };
   v4f acc[FA][FB];
 #pragma unroll
   for (int i = 0; i < FA; ++i)
 #pragma unroll
     for (int j = 0; j < FB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  v4u fa[2][FA], fb[2][FB];
+  if (steps > 0) {
+    v4u fa[2][FA], fb[2][FB];
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < 2; ++r) {
+      const int step = step0 + min(r, steps - 1);
+      copy(part(t.a, a0, t.rows_a, t.lda, kTransA, step), part(t.b, b0, t.rows_b, t.ldb, kTransB, step), step, r, 0, kMine);
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((kMine & 15) | ((kMine >> 4) << 14) | 0xF70);   // step 0 has landed
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) copy(r, r, i);
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((kMine & 15) | ((kMine >> 4) << 14) | 0xF70);   // step 0 has landed
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+    for (int i = 0; i < FA; ++i) fa[0][i] = SideA::read(s_buf, wa * FA + i, 0, c, g);
 #pragma unroll
-  for (int i = 0; i < FA; ++i) fa[0][i] = *reinterpret_cast<const v4u*>(s_buf + at_a[0] + i * 2048);
+    for (int j = 0; j < FB; ++j) fb[0][j] = SideB::read(s_buf + BM * 128, wb * FB + j, 0, c, g);
+    for (int s = 0; s < steps; ++s) {
 #pragma unroll
-  for (int j = 0; j < FB; ++j) fb[0][j] = *reinterpret_cast<const v4u*>(s_buf + at_b[0] + j * 2048);
-  for (int s = 0; s < steps; ++s) {
+      for (int h = 0; h < 2; ++h) {
+        // FA groups of FB products; ahead of each group its share of the reads and copies
+        const uint8_t* next = s_buf + ((s + h) & 1) * kStep;
+        const int after = step0 + min(s + 2, steps - 1);
+        const __amdgpu_buffer_rsrc_t rs_a = part(t.a, a0, t.rows_a, t.lda, kTransA, after);
+        const __amdgpu_buffer_rsrc_t rs_b = part(t.b, b0, t.rows_b, t.ldb, kTransB, after);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      // FA groups of FB products; ahead of each group its share of the reads and copies
-      const uint8_t* next = s_buf + ((s + h) & 1) * kStep;
+        for (int i = 0; i < FA; ++i) {
+          fa[h ^ 1][i] = SideA::read(next, wa * FA + i, h ^ 1, c, g);
 #pragma unroll
-      for (int i = 0; i < FA; ++i) {
-        fa[h ^ 1][i] = *reinterpret_cast<const v4u*>(next + at_a[h ^ 1] + i * 2048);
+          for (int j = i * FB / FA; j < (i + 1) * FB / FA; ++j)
+            fb[h ^ 1][j] = SideB::read(next + BM * 128, wb * FB + j, h ^ 1, c, g);
+          if (h == 1) copy(rs_a, rs_b, after, s & 1, i * kMine / FA, (i + 1) * kMine / FA);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = i * FB / FA; j < (i + 1) * FB / FA; ++j)
-          fb[h ^ 1][j] = *reinterpret_cast<const v4u*>(next + at_b[h ^ 1] + j * 2048);
-        if (h == 1) {
-#pragma unroll
-          for (int k = i * kMine / FA; k < (i + 1) * kMine / FA; ++k) copy(s + 2, s & 1, k);
+          for (int j = 0; j < FB; ++j) mma<T>(acc[i][j], fa[h][i], fb[h][j]);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int j = 0; j < FB; ++j) mma<T>(acc[i][j], fa[h][i], fb[h][j]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (h == 0) {
-        // this wave holds the step's second half, and its copies of the next step have landed
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x70);
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
+        if (h == 0) {
+          // this wave holds the step's second half, and its copies of the next step have landed
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_s_waitcnt(0x70);
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+        }
       }
     }
+    __builtin_amdgcn_s_waitcnt(0);                         // no copy outlives its buffer
+    settle();
+#pragma unroll
+    for (int i = 0; i < FA; ++i)
+#pragma unroll
+      for (int j = 0; j < FB; ++j) asm volatile("" : "+a"(acc[i][j]));   // read only after settle()
   }
-  __builtin_amdgcn_s_waitcnt(0);                           // no copy outlives its buffer
-  settle();
-#pragma unroll
-  for (int i = 0; i < FA; ++i)
-#pragma unroll
-    for (int j = 0; j < FB; ++j) asm volatile("" : "+a"(acc[i][j]));   // read only after settle()
 
   const int64_t va = a0 + wa * FA * 16 + 4 * g;            // this lane's first A row
   const int64_t nb = b0 + wb * FB * 16 + c;                // its first B row
@@ -252,34 +317,31 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
     }
   } else if constexpr (EPI == kGrad) {
     T* __restrict__ p = static_cast<T*>(t.p);
-    T* __restrict__ pt = static_cast<T*>(t.pt);
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
       const int64_t tok = nb + 16 * j;
-      if (tok >= t.ldt) continue;
-      const int64_t tgt = tok < t.N ? t.target[tok] : -1;
+      if (tok >= t.N) continue;
+      const int64_t tgt = t.target[tok];
       const bool live = tgt >= 0 && tgt < t.V;
       const float lse = live ? t.lse[tok] : 0.f, gi = live ? t.g[tok] : 0.f;
+      const int64_t away = tgt - t.v0 - va;                // the target lies this far past the lane's first row
+      const int d = live && away >= 0 && away < FA * 16 ? (int)away : -1;
 #pragma unroll
       for (int i = 0; i < FA; ++i) {
         const int64_t r = va + 16 * i;                     // row within the piece
         if (r >= t.ldp) continue;
-        T o[4];
+        float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int64_t v = t.v0 + r + e;
-          float x = 0.f;
-          if (live && v < t.V && r + e < t.rows_a) x = gi * (expf(acc[i][j][e] - lse) - (v == tgt ? 1.f : 0.f));
-          store_out(o, e, x);
-          pt[(r + e) * t.ldt + tok] = o[e];
+          const float soft = sizeof(T) == 2 ? fast_exp(acc[i][j][e] - lse) : expf(acc[i][j][e] - lse);
+          x[e] = live && r + e < t.rows_a ? gi * (soft - (d == 16 * i + e ? 1.f : 0.f)) : 0.f;
         }
-        if (tok < t.N) {
-          if constexpr (sizeof(T) == 2)
-            *reinterpret_cast<uint2*>(p + tok * t.ldp + r) =
-                make_uint2(o[0] | ((uint32_t)o[1] << 16), o[2] | ((uint32_t)o[3] << 16));
-          else
-            *reinterpret_cast<v4f*>(p + tok * t.ldp + r) = v4f{o[0], o[1], o[2], o[3]};
-        }
+        if constexpr (sizeof(T) == 2)
+          *reinterpret_cast<uint2*>(p + tok * t.ldp + r) =
+              make_uint2(f32_to_bf16_rne(x[0]) | ((uint32_t)f32_to_bf16_rne(x[1]) << 16),
+                         f32_to_bf16_rne(x[2]) | ((uint32_t)f32_to_bf16_rne(x[3]) << 16));
+        else
+          *reinterpret_cast<v4f*>(p + tok * t.ldp + r) = v4f{x[0], x[1], x[2], x[3]};
       }
     }
   } else {
@@ -295,9 +357,10 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
         const int64_t at = rowb * t.rows_a + col;
         v4f v = acc[i][j];
         if constexpr (EPI == kHidden) {
-          if (!t.first) v += *reinterpret_cast<const v4f*>(t.acc + at);
-          if (!t.last) {
-            *reinterpret_cast<v4f*>(t.acc + at) = v;
+          float* sum = t.acc + (int64_t)split * t.rows_b * t.rows_a + at;
+          if (!t.first) v += *reinterpret_cast<const v4f*>(sum);
+          if (!t.last || t.splits > 1) {
+            *reinterpret_cast<v4f*>(sum) = v;
             continue;
           }
         }
@@ -337,79 +400,112 @@ __global__ __launch_bounds__(256) void k_loss_join(const float2* __restrict__ pa
   }
 }
 
-// out [cols][ldo] = in [rows][cols] transposed, columns rows..ldo-1 zeroed.
+// out = the sum of the splits' running sums, in order, rounded once.
 template <typename T>
-__global__ __launch_bounds__(256) void k_transpose_pad(const T* __restrict__ in, T* __restrict__ out, int64_t rows,
-                                                       int64_t cols, int64_t ldo) {
-  __shared__ T s[64][65];
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  const int64_t c0 = (int64_t)blockIdx.x * 64, r0 = (int64_t)blockIdx.y * 64;
+__global__ __launch_bounds__(256) void k_hidden_join(const float* __restrict__ acc, T* __restrict__ out, int64_t n,
+                                                     int splits) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;       // n is a multiple of 64
+  if (i >= n) return;
+  v4f v = *reinterpret_cast<const v4f*>(acc + i);
+  for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const v4f*>(acc + s * n + i);
 #pragma unroll
-  for (int j = 0; j < 64; j += 4) {
-    const int64_t rr = r0 + ty + j;
-    s[ty + j][tx] = rr < rows ? in[rr * cols + c0 + tx] : T(0);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < 64; j += 4) out[(c0 + ty + j) * ldo + r0 + tx] = s[tx][ty + j];
+  for (int e = 0; e < 4; ++e) store_out(out, i + e, v[e]);
 }
 
 namespace {
 
-constexpr int kWA = 2, kWB = 4;
-constexpr int kTileA = 256, kTileB = 256;
+constexpr int kCUs = 256;
 constexpr int64_t kPieceRows = 8192;         // vocabulary entries per piece of the gradient, less where N
                                              // tokens of it would be over 2^27 values
+
+// Tile shapes, largest first, with the time of a tile of each per element of C relative to the first:
+// smaller tiles read LDS (and the L2) more often for the same products.
+struct TileShape {
+  int a, b;
+  float cost;
+};
+constexpr TileShape kTiles[] = {{256, 256, 1.f}, {256, 128, 1.25f}, {128, 128, 1.5f}, {128, 64, 2.f}};
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
 int tiles(int64_t rows, int tile) { return (int)((rows + tile - 1) / tile); }
 
-template <typename T, int EPI>
-void launch_nt(VocabTile& t, int64_t cover_a, int64_t cover_b, hipStream_t s) {
-  t.tiles_a = tiles(cover_a, kTileA);
-  t.tiles_b = tiles(cover_b, kTileB);
-  hipLaunchKernelGGL((k_nt<T, kTileA, kTileB, kWA, kWB, EPI>), dim3((t.tiles_a * t.tiles_b + 7) / 8 * 8), dim3(64 * kWA * kWB), 0, s, t);
+// Shape and splits of the contraction with the least rounds of workgroups over the device: cover_a x
+// cover_b elements of C, and splits up to `most` (each worth at least 16 steps, and costing a pass over
+// its sums that weighs like two).
+struct NtPlan {
+  int shape, splits;
+};
+NtPlan nt_plan(int64_t cover_a, int64_t cover_b, int64_t steps, int most) {
+  NtPlan best{0, 1};
+  double least = 0;
+  for (int k = 0; k < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++k)
+    for (int s = 1; s <= most && (s == 1 || steps / s >= 16); ++s) {
+      const int64_t wgs = (int64_t)tiles(cover_a, kTiles[k].a) * tiles(cover_b, kTiles[k].b) * s;
+      const double rounds = (double)((wgs + kCUs - 1) / kCUs);
+      const double cost = rounds * kTiles[k].a * kTiles[k].b * kTiles[k].cost * ((double)steps / s + (s > 1 ? 4 : 2));
+      if ((k == 0 && s == 1) || cost < least) {
+        least = cost;
+        best = NtPlan{k, s};
+      }
+    }
+  return best;
 }
 
+template <typename T, int EPI>
+void launch_nt(VocabTile& t, const NtPlan& plan, int64_t cover_a, int64_t cover_b, hipStream_t s) {
+  t.tiles_a = tiles(cover_a, kTiles[plan.shape].a);
+  t.tiles_b = tiles(cover_b, kTiles[plan.shape].b);
+  t.splits = plan.splits;
+  const dim3 grid((t.tiles_a * t.tiles_b + 7) / 8 * 8, plan.splits);
+  switch (plan.shape) {
+    case 0: hipLaunchKernelGGL((k_nt<T, 256, 256, 2, 4, EPI>), grid, dim3(512), 0, s, t); break;
+    case 1: hipLaunchKernelGGL((k_nt<T, 256, 128, 4, 2, EPI>), grid, dim3(512), 0, s, t); break;
+    case 2: hipLaunchKernelGGL((k_nt<T, 128, 128, 2, 2, EPI>), grid, dim3(256), 0, s, t); break;
+    default: hipLaunchKernelGGL((k_nt<T, 128, 64, 2, 2, EPI>), grid, dim3(256), 0, s, t); break;
+  }
+}
+
+int64_t steps_of(int64_t k, int elem) { return (k * elem + 127) / 128; }
+
 struct LossPlan {
+  NtPlan nt;
   size_t part, tlogit, total;
 };
-LossPlan loss_plan(int64_t N, int64_t V) {
+LossPlan loss_plan(int64_t N, int64_t V, int64_t K, int elem) {
   LossPlan p;
+  p.nt = nt_plan(V, N, steps_of(K, elem), 1);
   p.part = 0;
-  p.tlogit = up256((size_t)tiles(V, kTileA) * N * sizeof(float2));
+  p.tlogit = up256((size_t)tiles(V, kTiles[p.nt.shape].a) * N * sizeof(float2));
   p.total = p.tlogit + up256((size_t)N * 4);
   return p;
 }
 
 struct GradPlan {
-  int64_t piece, ldt;
+  int64_t piece;
   int pieces;
-  size_t p, pt, wt, ht, acc, total;
+  NtPlan hidden;
+  size_t p, acc, total;
 };
 GradPlan grad_plan(int64_t N, int64_t V, int64_t K, int elem) {
   GradPlan g;
-  const int64_t most = std::max<int64_t>(256, std::min<int64_t>(kPieceRows, (int64_t(1) << 27) / N / 256 * 256));
+  const int64_t fit = std::min((int64_t(1) << 27) / N, (int64_t(1) << 30) / (K * elem)) / 256 * 256;
+  const int64_t most = std::max<int64_t>(256, std::min<int64_t>(kPieceRows, fit));
   g.pieces = (int)((V + most - 1) / most);
-  g.piece = (V + g.pieces - 1) / g.pieces;
-  g.piece = (g.piece + 255) / 256 * 256;
+  g.piece = ((V + g.pieces - 1) / g.pieces + 255) / 256 * 256;
   g.pieces = (int)((V + g.piece - 1) / g.piece);
-  g.ldt = up64(N);
+  g.hidden = nt_plan(K, N, steps_of(std::min(g.piece, V), elem), 8);
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
   g.p = take((size_t)N * g.piece * elem);
-  g.pt = take((size_t)g.piece * g.ldt * elem);
-  g.wt = take((size_t)K * g.piece * elem);
-  g.ht = take((size_t)K * g.ldt * elem);
-  g.acc = take(g.pieces > 1 ? (size_t)N * K * 4 : 0);
+  g.acc = take(g.pieces > 1 || g.hidden.splits > 1 ? (size_t)g.hidden.splits * N * K * 4 : 0);
   g.total = at;
   return g;
 }
 
 template <typename T>
 hipError_t loss_t(const VocabArgs& a, hipStream_t s) {
-  const LossPlan p = loss_plan(a.N, a.V);
+  const LossPlan p = loss_plan(a.N, a.V, a.K, sizeof(T));
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   VocabTile t{};
   t.a = a.W; t.b = a.h;
@@ -419,7 +515,7 @@ hipError_t loss_t(const VocabArgs& a, hipStream_t s) {
   t.part = reinterpret_cast<float2*>(ws + p.part);
   t.tlogit = reinterpret_cast<float*>(ws + p.tlogit);
   t.V = a.V; t.N = a.N;
-  launch_nt<T, kLoss>(t, a.V, a.N, s);
+  launch_nt<T, kLoss>(t, p.nt, a.V, a.N, s);
   hipLaunchKernelGGL(k_loss_join, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, t.part, t.tlogit, a.target, a.N, a.V,
                      t.tiles_a, a.loss, a.lse_out);
   return hipGetLastError();
@@ -430,43 +526,38 @@ hipError_t grad_t(const VocabArgs& a, hipStream_t s) {
   const GradPlan q = grad_plan(a.N, a.V, a.K, sizeof(T));
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   T* p = reinterpret_cast<T*>(ws + q.p);
-  T* pt = reinterpret_cast<T*>(ws + q.pt);
-  T* wt = reinterpret_cast<T*>(ws + q.wt);
-  T* ht = reinterpret_cast<T*>(ws + q.ht);
+  float* acc = reinterpret_cast<float*>(ws + q.acc);
   const T* W = static_cast<const T*>(a.W);
-  const T* h = static_cast<const T*>(a.h);
-  if (a.dW)
-    hipLaunchKernelGGL((k_transpose_pad<T>), dim3((unsigned)(a.K / 64), (unsigned)(q.ldt / 64)), dim3(256), 0, s, h, ht,
-                       a.N, a.K, q.ldt);
   for (int k = 0; k < q.pieces; ++k) {
     const int64_t v0 = k * q.piece, rows = std::min(q.piece, a.V - v0), ldp = up64(rows);
     VocabTile t{};
-    t.a = W + v0 * a.K; t.b = h;
+    t.a = W + v0 * a.K; t.b = a.h;
     t.rows_a = rows; t.rows_b = a.N;
     t.k = t.lda = t.ldb = a.K;
     t.target = a.target; t.lse = a.lse; t.g = a.g;
-    t.p = p; t.pt = pt; t.ldp = ldp; t.ldt = q.ldt;
+    t.p = p; t.ldp = ldp;
     t.v0 = v0; t.V = a.V; t.N = a.N;
-    launch_nt<T, kGrad>(t, ldp, q.ldt, s);
+    launch_nt<T, kGrad>(t, nt_plan(ldp, a.N, steps_of(a.K, sizeof(T)), 1), ldp, a.N, s);
     if (a.dh) {
-      hipLaunchKernelGGL((k_transpose_pad<T>), dim3((unsigned)(a.K / 64), (unsigned)(ldp / 64)), dim3(256), 0, s,
-                         W + v0 * a.K, wt, rows, a.K, ldp);
       VocabTile d{};
-      d.a = wt; d.b = p;
+      d.a = W + v0 * a.K; d.b = p;
       d.rows_a = a.K; d.rows_b = a.N;
-      d.k = d.lda = d.ldb = ldp;
-      d.acc = reinterpret_cast<float*>(ws + q.acc);
+      d.k = rows; d.lda = a.K; d.ldb = ldp;
+      d.acc = acc;
       d.out = a.dh;
       d.first = k == 0; d.last = k == q.pieces - 1;
-      launch_nt<T, kHidden>(d, a.K, a.N, s);
+      launch_nt<T, kHidden>(d, q.hidden, a.K, a.N, s);
+      if (d.last && q.hidden.splits > 1)
+        hipLaunchKernelGGL((k_hidden_join<T>), dim3((unsigned)((a.N * a.K / 4 + 255) / 256)), dim3(256), 0, s, acc,
+                           static_cast<T*>(a.dh), a.N * a.K, q.hidden.splits);
     }
     if (a.dW) {
       VocabTile d{};
-      d.a = ht; d.b = pt;
+      d.a = a.h; d.b = p;
       d.rows_a = a.K; d.rows_b = rows;
-      d.k = d.lda = d.ldb = q.ldt;
+      d.k = a.N; d.lda = a.K; d.ldb = ldp;
       d.out = static_cast<T*>(a.dW) + v0 * a.K;
-      launch_nt<T, kWeight>(d, a.K, rows, s);
+      launch_nt<T, kWeight>(d, nt_plan(a.K, rows, steps_of(a.N, sizeof(T)), 1), a.K, rows, s);
     }
   }
   return hipGetLastError();
@@ -475,9 +566,7 @@ hipError_t grad_t(const VocabArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t vocab_loss_workspace_bytes(int64_t N, int64_t V, int64_t K, int bf16) {
-  (void)K;
-  (void)bf16;
-  return loss_plan(N, V).total;
+  return loss_plan(N, V, K, bf16 ? 2 : 4).total;
 }
 size_t vocab_loss_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int bf16) {
   return grad_plan(N, V, K, bf16 ? 2 : 4).total;
