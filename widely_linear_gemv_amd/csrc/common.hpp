@@ -257,7 +257,9 @@ struct LoraReduceItem {
   const void* x;        // [N][K]
   const void* W;        // [L][r][ldw]
   float* part;          // [chunk][N][rp]
-  float* joined;        // [N][rp] (k_reduce_join)
+  float* joined;        // [N][rp] or null (k_reduce_join)
+  void* groups;         // operand groups [tile][step][lane] or null (k_reduce_join)
+  const float* alpha;   // [L]
   int64_t K, ldw;
   int chunk;
 };
@@ -266,8 +268,9 @@ struct LoraReduceGroup {
 };
 struct LoraExpandItem {
   const float* part;    // [nchunk][N][rp]
+  const void* groups;   // [tile][step][lane], where k_reduce_join has made them
   const void* W;        // [L][M][r]
-  const float* alpha;   // null: the partial sums are scaled already
+  const float* alpha;   // [L]
   const void* base;
   void* y;
   int64_t M;
@@ -275,6 +278,11 @@ struct LoraExpandItem {
 };
 struct LoraExpandGroup {
   LoraExpandItem items[kMaxLoraItems];
+};
+struct LoraTranspose {
+  const void* in;       // [L][R][C]
+  void* out;            // [L][C][ldo]
+  int64_t R, C, ldo;
 };
 struct LoraOuterItem {
   const void* x;        // [N][C]
