@@ -257,8 +257,8 @@ struct LoraReduceItem {
   const void* x;        // [N][K]
   const void* W;        // [L][r][ldw]
   float* part;          // [chunk][N][rp]
-  float* joined;        // [N][rp] or null (k_reduce_join)
-  void* groups;         // operand groups [tile][step][lane] or null (k_reduce_join)
+  void* factors;        // k_outer's operands or null (k_reduce_join)
+  void* groups;         // k_expand's operands [tile][step][lane] or null (k_reduce_join)
   const float* alpha;   // [L]
   int64_t K, ldw;
   int chunk;
@@ -286,7 +286,7 @@ struct LoraTranspose {
 };
 struct LoraOuterItem {
   const void* x;        // [N][C]
-  const float* factor;  // [N][rp]
+  const void* factors;  // [block of 32 bf16, 16 fp32 rows][rank tile][part][lane]
   float* out;           // [split][L][r][C] (rank_major) or [split][L][C][r]
   int64_t C;
   int rank_major;

@@ -22,33 +22,12 @@
 // fp32 inputs use the fp32 matrix instruction throughout.
 #include <algorithm>
 
-#include "common.hpp"
+#include "tiles.hpp"
 
 namespace f2i {
 
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 namespace {
-
-// One 16-byte operand per lane (row or column lane & 15, contraction group lane >> 4).
-template <typename T> struct Mma;
-template <> struct Mma<uint16_t> {
-  static constexpr int kGroup = 8;     // contraction elements per lane and step
-  __device__ static v4f run(v4u a, v4u b, v4f c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
-  }
-};
-template <> struct Mma<float> {
-  static constexpr int kGroup = 4;
-  __device__ static v4f run(v4u a, v4u b, v4f c) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[e]), __uint_as_float(b[e]), c, 0, 0, 0);
-    return c;
-  }
-};
 
 // kGroup consecutive elements at p; elements at or past `have` read as 0.  VEC: p is 16-byte
 // aligned and `have` is a multiple of kGroup (or <= 0).
@@ -122,6 +101,9 @@ struct Segments {
 };
 
 constexpr int kRows = 16;              // rows of x per tile
+// Parts that the fp32 factors of the outer sums are split into (their results are fp32).
+template <typename T>
+constexpr int kFactorParts = sizeof(T) == 4 ? 1 : 3;
 // Parts that h is split into for adapters of type T and outputs of type YT.
 template <typename T, typename YT>
 constexpr int expand_parts() { return sizeof(T) == 4 ? 1 : (sizeof(YT) == 2 ? 2 : 3); }
@@ -141,7 +123,7 @@ __global__ __launch_bounds__(64 * kReduceWaves) void k_reduce(LoraReduceGroup gr
                                                               const int32_t* __restrict__ seg_adapter, int S, int L,
                                                               int N, int r, int Q) {
   constexpr int G = Mma<T>::kGroup, kStep = 4 * G;
-  constexpr int U = RT * TR > 8 || RT > 4 ? 1 : 2;
+  constexpr int U = TR > 1 || RT > 4 ? 1 : (RT > 2 ? 2 : 4);   // steps loaded together
   constexpr int kTile = kRows * TR;
   __shared__ __align__(16) float s_part[kReduceWaves][kTile][RT * 16 + 4];
   const LoraReduceItem& it = grp.items[blockIdx.z];
@@ -201,17 +183,21 @@ __global__ __launch_bounds__(64 * kReduceWaves) void k_reduce(LoraReduceGroup gr
     for (int64_t k = k0; k < kend; k += 2 * U * kStep) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        if (k + (h + 1) * U * kStep < kend) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          load_x(k + ((h + 1) * U + u) * kStep, xs[h ^ 1][u]);
-          load_w(k + ((h + 1) * U + u) * kStep, ws[h ^ 1][u]);
+          for (int u = 0; u < U; ++u) {
+            load_x(k + ((h + 1) * U + u) * kStep, xs[h ^ 1][u]);
+            load_w(k + ((h + 1) * U + u) * kStep, ws[h ^ 1][u]);
+          }
         }
+        if (h == 0 || k + U * kStep < kend) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int t = 0; t < RT; ++t)
+            for (int t = 0; t < RT; ++t)
 #pragma unroll
-            for (int v = 0; v < TR; ++v) acc[t][v] = Mma<T>::run(ws[h][u][t], xs[h][u][v], acc[t][v]);
+              for (int v = 0; v < TR; ++v) acc[t][v] = Mma<T>::run(ws[h][u][t], xs[h][u][v], acc[t][v]);
+        }
       }
     }
     // C: lane holds ranks 16 t + 4 g .. + 3 of row 16 v + c
@@ -281,43 +267,84 @@ __device__ __forceinline__ void join_chunks(const float* __restrict__ part, int6
   }
 }
 
-// For each 16-row tile: the chunks' partial sums joined and scaled by the row's alpha, written as
-// fp32 rows [N][rp] (item.joined) and / or as k_expand's operand groups [tile][step][lane]
-// (item.groups), each optional.  Rows without an adapter give 0.  One wave per tile.
+// The chunks' partial sums joined and scaled by the row's alpha, as operands of the products that
+// read them; rows without an adapter give 0.  blockIdx.z picks the form, one wave per 64 operands:
+//   0  item.groups, k_expand's: [16-row tile][step][lane], ranks along the contraction
+//   1  item.factors, k_outer's: [block of 4 G rows][rank tile][part][lane], rows along the contraction
 template <typename T>
 __global__ __launch_bounds__(256) void k_reduce_join(LoraReduceGroup grp, const int32_t* __restrict__ seg_start,
                                                      const int32_t* __restrict__ seg_adapter, int S, int L, int N,
-                                                     int rp, int parts) {
+                                                     int r, int rp, int parts, int row_blocks) {
   constexpr int G = Mma<T>::kGroup;
   const LoraReduceItem& it = grp.items[blockIdx.y];
-  const int lane = threadIdx.x & (kWave - 1), c = lane & 15;
-  const int gpp = rp / G;
-  const int steps = (parts * gpp + 3) / 4;
-  const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);   // (tile, step)
-  const int tile = unit / steps, st = unit % steps;
-  const int t0 = tile * kRows;
-  if (t0 >= N) return;
-  const int grpi = st * 4 + (lane >> 4), part = grpi / gpp, k = (grpi % gpp) * G, row = t0 + c;
-  Segments segs(seg_start, seg_adapter, S, L, t0, min(t0 + kRows, N), 0, 1, lane);
-  int own = -1;
-  for (int lo, hi, a; segs.next(lo, hi, a);)
-    if (row >= lo && row < hi) own = a;
-  float v[G];
+  const int lane = threadIdx.x & (kWave - 1), c = lane & 15, g = lane >> 4;
+  const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int nchunk = (int)((it.K + it.chunk - 1) / it.chunk);
+  const int64_t pitch = (int64_t)N * rp;
+  if (blockIdx.z == 0) {
+    const int gpp = rp / G, steps = (parts * gpp + 3) / 4;
+    const int tile = unit / steps, st = unit % steps;
+    const int t0 = tile * kRows;
+    if (!it.groups || t0 >= N) return;
+    const int grpi = st * 4 + g, part = grpi / gpp, k = (grpi % gpp) * G, row = t0 + c;
+    Segments segs(seg_start, seg_adapter, S, L, t0, min(t0 + kRows, N), 0, 1, lane);
+    int own = -1;
+    for (int lo, hi, a; segs.next(lo, hi, a);)
+      if (row >= lo && row < hi) own = a;
+    float v[G];
 #pragma unroll
-  for (int j = 0; j < G; ++j) v[j] = 0.f;
-  if (own >= 0 && part < parts) {
-    const float al = it.alpha[own];
-    join_chunks<G>(it.part, (int64_t)row * rp + k, (int64_t)N * rp, (int)((it.K + it.chunk - 1) / it.chunk), v);
+    for (int j = 0; j < G; ++j) v[j] = 0.f;
+    if (own >= 0 && part < parts) {
+      const float al = it.alpha[own];
+      join_chunks<G>(it.part, (int64_t)row * rp + k, pitch, nchunk, v);
 #pragma unroll
-    for (int j = 0; j < G; ++j) v[j] *= al;
+      for (int j = 0; j < G; ++j) v[j] *= al;
+    }
+    static_cast<v4u*>(it.groups)[((int64_t)tile * steps + st) * 64 + lane] =
+        part < parts ? operand_group<T>(v, part) : v4u{0, 0, 0, 0};
+  } else {
+    const int rts = rp / 16, rb = unit / rts, rt = unit % rts;
+    if (!it.factors || rb >= row_blocks) return;
+    const int row0 = rb * 4 * G, rank = rt * 16 + c;
+    int own[G];
+#pragma unroll
+    for (int e = 0; e < G; ++e) own[e] = -1;
+    if (row0 < N) {
+      Segments segs(seg_start, seg_adapter, S, L, row0, min(row0 + 4 * G, N), 0, 1, lane);
+      for (int lo, hi, a; segs.next(lo, hi, a);) {
+#pragma unroll
+        for (int e = 0; e < G; ++e)
+          if (row0 + g * G + e >= lo && row0 + g * G + e < hi) own[e] = a;
+      }
+    }
+    const __amdgpu_buffer_rsrc_t rs = range_rsrc(it.part, pitch * nchunk * 4);
+    float v[G], al[G];
+#pragma unroll
+    for (int e = 0; e < G; ++e) {
+      v[e] = 0.f;
+      al[e] = own[e] >= 0 ? it.alpha[own[e]] : 0.f;
+    }
+    for (int ch = 0; ch < nchunk; ch += 2) {
+      float w[2][G];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < G; ++e) {
+          const bool ok = own[e] >= 0 && rank < r && ch + u < nchunk;
+          w[u][e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+              rs, ok ? (uint32_t)(((ch + u) * pitch + (int64_t)(row0 + g * G + e) * rp + rank) * 4) : kNoLoad, 0, 0));
+        }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < G; ++e) v[e] += w[u][e];
+    }
+#pragma unroll
+    for (int e = 0; e < G; ++e) v[e] = own[e] >= 0 ? v[e] * al[e] : 0.f;
+#pragma unroll
+    for (int p = 0; p < kFactorParts<T>; ++p)
+      static_cast<v4u*>(it.factors)[((int64_t)unit * kFactorParts<T> + p) * 64 + lane] = operand_group<T>(v, p);
   }
-  if (it.joined && part == 0 && row < N) {
-#pragma unroll
-    for (int j = 0; j < G; j += 4)
-      *reinterpret_cast<v4f*>(it.joined + (int64_t)row * rp + k + j) = v4f{v[j], v[j + 1], v[j + 2], v[j + 3]};
-  }
-  if (it.groups) static_cast<v4u*>(it.groups)[((int64_t)tile * steps + st) * 64 + lane] =
-      part < parts ? operand_group<T>(v, part) : v4u{0, 0, 0, 0};
 }
 
 // ------------------------------------------------------------------------------ expand ----
@@ -328,8 +355,10 @@ __global__ __launch_bounds__(256) void k_reduce_join(LoraReduceGroup grp, const 
 // the partial sums (few rows: one launch less).  base is loaded first of all, so that it arrives while
 // the segments, the groups and the adapter do.
 //
-// Row i of output fragment f of a 64-output group is output 16 (i / 4) + 4 f + i % 4, so that the
-// accumulators of a lane over the four fragments are 16 consecutive outputs of one row.
+// The outputs of a wave's 64 are dealt to the rows i of its four output fragments f so that a lane's
+// accumulators make whole 16-byte pieces of one row of y: output 16 f + i for fp32 (each piece of a lane
+// 64 bytes on), 16 (i / 4) + 4 f + i % 4 for bf16 (its two pieces side by side).  Each is the faster
+// one for its type (bf16 59.6 against 62.2 us beside gate/up, fp32 7.8 against 8.9 us at 389 x 1408).
 template <typename T, typename YT, int TF, bool READY, bool WVEC>
 __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32_t* __restrict__ seg_start,
                                                 const int32_t* __restrict__ seg_adapter, int S, int L, int N, int r,
@@ -351,7 +380,10 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
   const int steps = (kParts * gpp + 3) / 4;
   const YT* base = static_cast<const YT*>(it.base);
   YT* y = static_cast<YT*>(it.y);
-  const bool yvec = (M * sizeof(YT)) % 16 == 0 && o0 + 16 * g + 16 <= M;
+  // 16-byte pieces of whole rows (M is even: a group of 64 outputs that M cuts short goes one by one)
+  const bool yvec = (M * sizeof(YT)) % 16 == 0 && o0 + 64 <= M;
+  auto output = [](int f, int i) { return sizeof(YT) == 4 ? 16 * f + i : 16 * (i >> 2) + 4 * f + (i & 3); };
+  auto piece = [&](int i) { return sizeof(YT) == 4 ? 16 * i + 4 * g : 16 * g + 8 * i; };   // first output of a piece
   v4u old[TF][kBase];
 #pragma unroll
   for (int t = 0; t < TF; ++t)
@@ -359,7 +391,7 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
       const int64_t row = min(t0 + 16 * t + c, t1 - 1);
 #pragma unroll
       for (int i = 0; i < kBase; ++i)
-        old[t][i] = *reinterpret_cast<const v4u*>(base + row * M + o0 + 16 * g + i * (16 / kBase));
+        old[t][i] = *reinterpret_cast<const v4u*>(base + row * M + o0 + piece(i));
     }
 
   Segments segs(seg_start, seg_adapter, S, L, t0, t1, q, Q, lane);
@@ -408,7 +440,7 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
       v4u wa[4], hb[TF];
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
-        const int o = 16 * (c >> 2) + 4 * f + (c & 3);
+        const int o = output(f, c);
         if constexpr (WVEC) {
           wa[f] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
               rs_w, have > 0 ? (uint32_t)((o * r + k) * sizeof(T)) : kNoLoad, 0, 0));
@@ -427,13 +459,13 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
     for (int t = 0; t < TF; ++t) {
       const int row = t0 + 16 * t + c;
       if (row < lo || row >= hi) continue;
-      const int64_t off = (int64_t)row * M + o0 + 16 * g;
+      const int64_t off = (int64_t)row * M + o0;
       if (yvec) {
         if constexpr (sizeof(YT) == 4) {
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
             const v4f b = __builtin_bit_cast(v4f, old[t][f]);
-            *reinterpret_cast<v4f*>(y + off + 4 * f) =
+            *reinterpret_cast<v4f*>(y + off + piece(f)) =
                 v4f{b[0] + acc[f][t][0], b[1] + acc[f][t][1], b[2] + acc[f][t][2], b[3] + acc[f][t][3]};
           }
         } else {
@@ -447,7 +479,7 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
               o[w] = (uint32_t)f32_to_bf16_rne(bf16_lo(old[t][h][w]) + d[e]) |
                      ((uint32_t)f32_to_bf16_rne(bf16_hi(old[t][h][w]) + d[e + 1]) << 16);
             }
-            *reinterpret_cast<v4u*>(y + off + 8 * h) = o;
+            *reinterpret_cast<v4u*>(y + off + piece(h)) = o;
           }
         }
       } else {
@@ -455,8 +487,8 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
         for (int f = 0; f < 4; ++f)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (o0 + 16 * g + 4 * f + e < M) {
-              const int64_t i = off + 4 * f + e;
+            if (o0 + output(f, 4 * g + e) < M) {
+              const int64_t i = off + output(f, 4 * g + e);
               float b;
               if constexpr (sizeof(YT) == 4) b = base[i]; else b = bf16_lo(base[i]);
               store_out(y, i, b + acc[f][t][e]);
@@ -496,76 +528,117 @@ __global__ __launch_bounds__(256) void k_transpose(LoraTranspose ta, LoraTranspo
 
 // --------------------------------------------------------------------------- outer sums ----
 
-// dA (dB): for adapter a, columns of x (dy) and 16 ranks, the sum over the adapter's rows of
-// factor[row][rank] * x[row][col], all fp32.  Workgroup: 128 columns (two per lane) x 16 ranks x the
-// rows [split * span, (split + 1) * span); its four waves take every fourth row and join in LDS in
-// wave order.  The factor is wave-uniform: it arrives over scalar loads.  Splits are joined in order
-// by k_outer_join (splits > 1), so the result never depends on scheduling.
-template <typename T>
+// dA (dB): for adapter a, the sum over the adapter's rows of factor[row][rank] * x[row][col].
+// Workgroup: 256 columns (64 per wave) x RT tiles of 16 ranks (up to four: two workgroups share the
+// columns of ranks over 64) x the rows [split * span, (split + 1) * span).  Steps
+// of 64 bf16 (32 fp32) rows are copied into LDS as they lie, double buffered, and transposed on the
+// way into registers (A operand: columns; B operand: the factors, made by k_reduce_join with rows along
+// the contraction).  Rows of other segments are neither copied (zeros stand for them) nor counted (their
+// factors are masked), so a NaN in another request's row cannot reach the sum.  Splits are joined in
+// order by k_outer_join (splits > 1), so the result never depends on scheduling.
+template <typename T, int RT>
 __global__ __launch_bounds__(256) void k_outer(LoraOuterGroup grp, const int32_t* __restrict__ seg_start,
                                                const int32_t* __restrict__ seg_adapter, int S, int L, int N, int r,
-                                               int rp, int splits, int span) {
-  __shared__ float s_sum[4][128][17];
-  const int half = blockIdx.z & 1;
-  const LoraOuterItem& it = grp.items[half];
+                                               int rts, int splits, int span) {
+  constexpr int G = Mma<T>::kGroup, kDeep = 8 * G;         // rows per step
+  constexpr int kParts = kFactorParts<T>;
+  using X = Side<T, 256, true>;
+  __shared__ __align__(16) uint8_t s_x[2 * 256 * 128];
+  const LoraOuterItem& it = grp.items[blockIdx.z & 1];
   const int a = (int)(blockIdx.z >> 1);
   const int64_t C = it.C;
-  const int64_t c0 = (int64_t)blockIdx.x * 128;
+  const int64_t c0 = (int64_t)blockIdx.x * 256;
   if (c0 >= C) return;
-  const int rt = blockIdx.y / splits, split = blockIdx.y % splits;
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int c = lane & 15, g = lane >> 4;
+  const int split = blockIdx.y % splits, rt0 = blockIdx.y / splits * RT;
   const int t0 = split * span, t1 = min(t0 + span, N);
-  const T* __restrict__ x = static_cast<const T*>(it.x);
-  const float* __restrict__ fac = it.factor + rt * 16;
-  const T* __restrict__ xc = x + min(c0 + 2 * lane, C - 2);      // C is even: a pair never straddles the end
-  constexpr int kDeep = 4;                                 // rows whose loads are in flight together
-  float acc[2][16];
+  uint32_t off[8];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) acc[0][k] = acc[1][k] = 0.f;
+  for (int i = 0; i < 8; ++i) off[i] = X::source(i * 4 + wave, lane, C) + (uint32_t)(c0 * sizeof(T));
+  v4f acc[4][RT];
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[f][t] = v4f{0.f, 0.f, 0.f, 0.f};
+
   Segments segs(seg_start, seg_adapter, S, L, t0, t1, 0, 1, lane);
   int lo, hi, who;
   while (segs.next(lo, hi, who)) {
     if (who != a) continue;
-    for (int row0 = lo + wave; row0 < hi; row0 += 4 * kDeep) {
-      float v[kDeep][2];
+    const int first = lo / kDeep * kDeep;                  // steps start at multiples of kDeep
+    auto copy = [&](int row0, int buf) {
+      const __amdgpu_buffer_rsrc_t rs = range_rsrc(static_cast<const T*>(it.x) + (int64_t)row0 * C,
+                                                   (int64_t)max(min(kDeep, hi - row0), 0) * C * (int64_t)sizeof(T));
 #pragma unroll
-      for (int d = 0; d < kDeep; ++d) {                    // rows past the segment repeat its last one
-        const int64_t row = min(row0 + 4 * d, hi - 1);
-        if constexpr (sizeof(T) == 4) {
-          const float2 w = *reinterpret_cast<const float2*>(xc + row * C);
-          v[d][0] = w.x;
-          v[d][1] = w.y;
-        } else {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(xc + row * C);
-          v[d][0] = bf16_lo(w);
-          v[d][1] = bf16_hi(w);
+      for (int i = 0; i < 8; ++i) {
+        const int row = row0 + ((i * 4 + wave) * 1024 + lane * 16) / (256 * (int)sizeof(T));
+        const uint32_t voff = row >= lo && row < hi ? off[i] : kNoLoad;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(s_x + buf * 32768 + (i * 4 + wave) * 1024), 16, voff, 0, 0, 0);
+      }
+    };
+    copy(first, 0);
+    for (int row0 = first, buf = 0; row0 < hi; row0 += kDeep, buf ^= 1) {
+      v4u fb[2][RT * kParts];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < RT * kParts; ++t)
+          fb[h][t] = static_cast<const v4u*>(it.factors)[(((int64_t)(row0 / (4 * G) + h) * rts + rt0) * kParts + t) * 64 + lane];
+      __builtin_amdgcn_s_waitcnt(0);                       // this wave's copies (and factors) have landed
+      __syncthreads();                                     // everyone's have, and the other buffer is free
+      if (row0 + kDeep < hi) copy(row0 + kDeep, buf ^ 1);
+      if (row0 < lo || row0 + kDeep > hi) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = row0 + 4 * G * h + G * g;        // this lane's G rows
+          uint32_t keep[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            if constexpr (sizeof(T) == 4) {
+              keep[w] = row + w >= lo && row + w < hi ? 0xFFFFFFFFu : 0u;
+            } else {
+              keep[w] = (row + 2 * w >= lo && row + 2 * w < hi ? 0xFFFFu : 0u) |
+                        (row + 2 * w + 1 >= lo && row + 2 * w + 1 < hi ? 0xFFFF0000u : 0u);
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < RT * kParts; ++t)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) fb[h][t][w] &= keep[w];
         }
       }
 #pragma unroll
-      for (int d = 0; d < kDeep; ++d) {
-        if (row0 + 4 * d >= hi) break;
-        const float* __restrict__ f = fac + (int64_t)(row0 + 4 * d) * rp;
+      for (int h = 0; h < 2; ++h) {
+        v4u fa[4];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          acc[0][k] = fmaf(v[d][0], f[k], acc[0][k]);
-          acc[1][k] = fmaf(v[d][1], f[k], acc[1][k]);
-        }
+        for (int f = 0; f < 4; ++f) fa[f] = X::read(s_x + buf * 32768, wave * 4 + f, h, c, g);
+#pragma unroll
+        for (int t = 0; t < RT * kParts; ++t)
+#pragma unroll
+          for (int f = 0; f < 4; ++f) acc[f][t / kParts] = Mma<T>::run(fa[f], fb[h][t], acc[f][t / kParts]);
       }
     }
+    __syncthreads();                                       // before the next segment's first copy
   }
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    s_sum[wave][2 * lane][k] = acc[0][k];
-    s_sum[wave][2 * lane + 1][k] = acc[1][k];
-  }
-  __syncthreads();
+
+  // C: lane holds columns 4 g .. + 3 of fragment f at rank 16 (rt0 + t) + c
   float* __restrict__ out = it.out + ((int64_t)split * L + a) * r * C;
-  for (int e = threadIdx.x; e < 128 * 16; e += 256) {
-    const int col = it.rank_major ? e % 128 : e / 16, k = it.rank_major ? e / 128 : e % 16;
-    const int rank = rt * 16 + k;
-    if (c0 + col >= C || rank >= r) continue;
-    const float v = ((s_sum[0][col][k] + s_sum[1][col][k]) + s_sum[2][col][k]) + s_sum[3][col][k];
-    out[it.rank_major ? (int64_t)rank * C + c0 + col : (c0 + col) * r + rank] = v;
+#pragma unroll
+  for (int f = 0; f < 4; ++f) {
+    const int64_t col = c0 + wave * 64 + 16 * f + 4 * g;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int rank = 16 * (rt0 + t) + c;
+      if (rank >= r) continue;
+      if (it.rank_major) {
+        if (col < C) *reinterpret_cast<v4f*>(out + (int64_t)rank * C + col) = acc[f][t];   // C = 2m: whole pieces
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < C) out[(col + e) * r + rank] = acc[f][t][e];
+      }
+    }
   }
 }
 
@@ -602,7 +675,8 @@ int segment_shares(int N, int S) {
 }
 
 // Row tiles per workgroup of k_reduce: an adapter of rank over 32 is several times the bytes of 16 rows
-// of x, so long segments take 64 rows to one read of it.
+// of x, so long segments take 64 rows to one read of it.  (For smaller ranks 64 rows measured no faster:
+// rank 32, 2048 x 4096, two projections 22.5 us with 16 rows, 24.3 with 64.)
 int reduce_rows(int N, int S, int r) { return segment_shares(N, S) == 1 && N >= 256 && r > 32 ? 4 : 1; }
 
 // Contraction chunk of k_reduce: small enough that the launch has about 2048 workgroups, at least
@@ -610,7 +684,7 @@ int reduce_rows(int N, int S, int r) { return segment_shares(N, S) == 1 && N >= 
 int reduce_chunk(int64_t K, int N, int S, int r, int items) {
   const int tile = kRows * reduce_rows(N, S, r);
   const int64_t wgs = (int64_t)((N + tile - 1) / tile) * segment_shares(N, S) * items;
-  const int64_t want = std::max<int64_t>(1, 2048 / wgs);
+  const int64_t want = std::max<int64_t>(1, XW / wgs);
   const int64_t chunk = (K + want - 1) / want;
   return (int)std::max<int64_t>(256, (chunk + 255) / 256 * 256);
 }
@@ -632,17 +706,13 @@ void launch_reduce(const LoraReduceGroup& grp, int count, bool vec, const int32_
   int most = 1;
   for (int k = 0; k < count; ++k) most = std::max(most, chunks(grp.items[k].K, grp.items[k].chunk));
   const dim3 grid((N + tile - 1) / tile * Q, most, count);
-  switch (rank_tiles(r)) {
-    case 1: reduce_vec<T, 1, 1>(grp, vec, grid, ss, sa, S, L, N, r, Q, st); break;
-    case 2: reduce_vec<T, 2, 1>(grp, vec, grid, ss, sa, S, L, N, r, Q, st); break;
-    case 4:
-      if (tr == 4) reduce_vec<T, 4, 4>(grp, vec, grid, ss, sa, S, L, N, r, Q, st);
-      else reduce_vec<T, 4, 1>(grp, vec, grid, ss, sa, S, L, N, r, Q, st);
-      break;
-    default:
-      if (tr == 4) reduce_vec<T, 8, 4>(grp, vec, grid, ss, sa, S, L, N, r, Q, st);
-      else reduce_vec<T, 8, 1>(grp, vec, grid, ss, sa, S, L, N, r, Q, st);
-      break;
+  switch (rank_tiles(r) * 8 + tr) {
+    case 9: reduce_vec<T, 1, 1>(grp, vec, grid, ss, sa, S, L, N, r, Q, st); break;
+    case 17: reduce_vec<T, 2, 1>(grp, vec, grid, ss, sa, S, L, N, r, Q, st); break;
+    case 33: reduce_vec<T, 4, 1>(grp, vec, grid, ss, sa, S, L, N, r, Q, st); break;
+    case 36: reduce_vec<T, 4, 4>(grp, vec, grid, ss, sa, S, L, N, r, Q, st); break;
+    case 65: reduce_vec<T, 8, 1>(grp, vec, grid, ss, sa, S, L, N, r, Q, st); break;
+    default: reduce_vec<T, 8, 4>(grp, vec, grid, ss, sa, S, L, N, r, Q, st); break;
   }
 }
 
@@ -688,11 +758,13 @@ void launch_expand_y(const LoraExpandGroup& grp, int count, int y_bf16, const in
 }
 
 template <typename T>
-void launch_join(const LoraReduceGroup& grp, int count, int y_bf16, const int32_t* ss, const int32_t* sa, int S, int L,
-                 int N, int r, hipStream_t st) {
+void launch_join(const LoraReduceGroup& grp, int count, int y_bf16, bool factors, const int32_t* ss, const int32_t* sa,
+                 int S, int L, int N, int r, hipStream_t st) {
   const int units = (N + kRows - 1) / kRows * group_steps(r, sizeof(T), y_bf16);
-  hipLaunchKernelGGL((k_reduce_join<T>), dim3((units + 3) / 4, count), dim3(256), 0, st, grp, ss, sa, S, L, N,
-                     16 * rank_tiles(r), sizeof(T) == 4 ? 1 : (y_bf16 ? 2 : 3));
+  const int row_blocks = factors ? (N + 8 * Mma<T>::kGroup - 1) / (8 * Mma<T>::kGroup) * 2 : 0;
+  hipLaunchKernelGGL((k_reduce_join<T>), dim3((std::max(units, row_blocks * rank_tiles(r)) + 3) / 4, count, factors ? 2 : 1),
+                     dim3(256), 0, st, grp, ss, sa, S, L, N, r, 16 * rank_tiles(r), sizeof(T) == 4 ? 1 : (y_bf16 ? 2 : 3),
+                     row_blocks);
 }
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -716,25 +788,30 @@ hipError_t lora_t(const LoraArgs& p, const LoraItem* items, int count, hipStream
                                   chunks(K, chunk)};
   }
   launch_reduce<T>(red, count, true, p.seg_start, p.seg_adapter, p.S, p.L, p.N, p.r, st);
-  if (ready) launch_join<T>(red, count, p.y_bf16, p.seg_start, p.seg_adapter, p.S, p.L, p.N, p.r, st);
+  if (ready) launch_join<T>(red, count, p.y_bf16, false, p.seg_start, p.seg_adapter, p.S, p.L, p.N, p.r, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   launch_expand_y<T>(exp, count, p.y_bf16, p.seg_start, p.seg_adapter, p.S, p.L, p.N, p.r, st);
   return hipGetLastError();
 }
 
-// Row ranges of k_outer: enough workgroups for the device when there are few adapters and columns,
-// at least 64 rows each.
-int outer_splits(int64_t N, int64_t C, int r, int L) {
-  const int64_t wgs = (C + 127) / 128 * ((r + 15) / 16) * L * 2;
-  const int64_t want = std::max<int64_t>(1, 1024 / wgs);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(want, N / 64));
+// Row ranges of k_outer: enough workgroups for the device when there are few adapters and columns, at
+// least two steps each.
+int outer_splits(int64_t N, int64_t C, int L, int elem) {
+  const int64_t wgs = (C + 255) / 256 * L * 2, step = 128 / elem;
+  const int64_t want = std::max<int64_t>(1, 512 / wgs);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(want, N / (2 * step)));
+}
+// Bytes of one item's factors: row blocks of 4 G rows in whole steps.
+size_t factor_bytes(int64_t N, int r, int elem) {
+  const int64_t step = 128 / elem;
+  return (size_t)((N + step - 1) / step) * 2 * rank_tiles(r) * (elem == 4 ? 1 : 3) * 1024;
 }
 
 struct BackwardPlan {
   int rp, chunk_x, chunk_y, splits, span;
   int64_t K, M, Mp;
-  size_t part_x, part_y, joined, groups, bt, at, outer_a, outer_b, total;
+  size_t part_x, part_y, fac_x, fac_y, groups, bt, at, outer_a, outer_b, total;
 };
 
 BackwardPlan backward_plan(int64_t N, int64_t m, int64_t n, int r, int L, int S, int elem) {
@@ -745,13 +822,16 @@ BackwardPlan backward_plan(int64_t N, int64_t m, int64_t n, int r, int L, int S,
   b.Mp = (b.M + 63) / 64 * 64;
   b.chunk_x = reduce_chunk(b.K, (int)N, S, r, 2);
   b.chunk_y = reduce_chunk(b.M, (int)N, S, r, 2);
-  b.splits = outer_splits(N, std::max(b.K, b.M), r, L);
-  b.span = (int)((N + b.splits - 1) / b.splits);
+  const int step = 128 / elem;
+  b.splits = outer_splits(N, std::max(b.K, b.M), L, elem);
+  b.span = (int)(((N + b.splits - 1) / b.splits + step - 1) / step * step);
+  b.splits = (int)((N + b.span - 1) / b.span);
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
   b.part_x = take((size_t)chunks(b.K, b.chunk_x) * N * b.rp * 4);
   b.part_y = take((size_t)chunks(b.M, b.chunk_y) * N * b.rp * 4);
-  b.joined = take((size_t)2 * N * b.rp * 4);
+  b.fac_x = take(factor_bytes(N, r, elem));
+  b.fac_y = take(factor_bytes(N, r, elem));
   b.groups = take(group_bytes(N, r, elem, 0));           // an fp32 dx has the most parts
   b.bt = take((size_t)L * r * b.Mp * elem);
   b.at = take((size_t)L * b.K * r * elem);
@@ -761,12 +841,18 @@ BackwardPlan backward_plan(int64_t N, int64_t m, int64_t n, int r, int L, int S,
   return b;
 }
 
+template <typename T, int RT>
+void launch_outer(const LoraOuterGroup& out, const BackwardPlan& b, const LoraBackwardArgs& p, hipStream_t st) {
+  const int rts = rank_tiles(p.r);
+  const dim3 grid((unsigned)((std::max(b.K, b.M) + 255) / 256), b.splits * (rts / RT), 2 * p.L);
+  hipLaunchKernelGGL((k_outer<T, RT>), grid, dim3(256), 0, st, out, p.seg_start, p.seg_adapter, p.S, p.L, p.N, p.r, rts,
+                     b.splits, b.span);
+}
+
 template <typename T>
 hipError_t lora_backward_t(const LoraBackwardArgs& p, hipStream_t st) {
   const BackwardPlan b = backward_plan(p.N, p.m, p.n, p.r, p.L, p.S, sizeof(T));
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
-  float* h = reinterpret_cast<float*>(ws + b.joined);
-  float* dh = h + (size_t)p.N * b.rp;
   T* Bt = reinterpret_cast<T*>(ws + b.bt);
   T* At = reinterpret_cast<T*>(ws + b.at);
   const dim3 block(256);
@@ -778,10 +864,10 @@ hipError_t lora_backward_t(const LoraBackwardArgs& p, hipStream_t st) {
   const bool ready = ready_groups(p.N, p.S);
   float* part_y = reinterpret_cast<float*>(ws + b.part_y);
   LoraReduceGroup red;
-  red.items[0] = LoraReduceItem{p.x, p.A, reinterpret_cast<float*>(ws + b.part_x), h, nullptr, p.alpha, b.K, b.K, b.chunk_x};
-  red.items[1] = LoraReduceItem{p.dy, Bt, part_y, dh, p.dx && ready ? ws + b.groups : nullptr, p.alpha, b.M, b.Mp, b.chunk_y};
+  red.items[0] = LoraReduceItem{p.x, p.A, reinterpret_cast<float*>(ws + b.part_x), ws + b.fac_x, nullptr, p.alpha, b.K, b.K, b.chunk_x};
+  red.items[1] = LoraReduceItem{p.dy, Bt, part_y, ws + b.fac_y, p.dx && ready ? ws + b.groups : nullptr, p.alpha, b.M, b.Mp, b.chunk_y};
   launch_reduce<T>(red, 2, vec, p.seg_start, p.seg_adapter, p.S, p.L, p.N, p.r, st);
-  launch_join<T>(red, 2, p.dx_bf16, p.seg_start, p.seg_adapter, p.S, p.L, p.N, p.r, st);
+  launch_join<T>(red, 2, p.dx_bf16, true, p.seg_start, p.seg_adapter, p.S, p.L, p.N, p.r, st);
   if (p.dx) {
     LoraExpandGroup exp;
     exp.items[0] = LoraExpandItem{part_y, ws + b.groups, At, p.alpha, p.dx_base, p.dx, b.K, chunks(b.M, b.chunk_y)};
@@ -790,10 +876,11 @@ hipError_t lora_backward_t(const LoraBackwardArgs& p, hipStream_t st) {
   LoraOuterGroup out;
   float* da = b.splits > 1 ? reinterpret_cast<float*>(ws + b.outer_a) : p.dA;
   float* db = b.splits > 1 ? reinterpret_cast<float*>(ws + b.outer_b) : p.dB;
-  out.items[0] = LoraOuterItem{p.x, dh, da, b.K, 1};
-  out.items[1] = LoraOuterItem{p.dy, h, db, b.M, 0};
-  hipLaunchKernelGGL((k_outer<T>), dim3((unsigned)((std::max(b.K, b.M) + 127) / 128), (p.r + 15) / 16 * b.splits, 2 * p.L),
-                     block, 0, st, out, p.seg_start, p.seg_adapter, p.S, p.L, p.N, p.r, b.rp, b.splits, b.span);
+  out.items[0] = LoraOuterItem{p.x, ws + b.fac_y, da, b.K, 1};
+  out.items[1] = LoraOuterItem{p.dy, ws + b.fac_x, db, b.M, 0};
+  if (p.r <= 16) launch_outer<T, 1>(out, b, p, st);
+  else if (p.r <= 32) launch_outer<T, 2>(out, b, p, st);
+  else launch_outer<T, 4>(out, b, p, st);
   if (b.splits > 1) {
     const int64_t na = (int64_t)p.L * p.r * b.K, nb = (int64_t)p.L * p.r * b.M;
     hipLaunchKernelGGL(k_outer_join, dim3((unsigned)((std::max(na, nb) + 511) / 512), 2), block, 0, st, out, p.dA, p.dB,
