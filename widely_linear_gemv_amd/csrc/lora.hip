@@ -217,6 +217,107 @@ __global__ __launch_bounds__(64 * kReduceWaves) void k_reduce(LoraReduceGroup gr
   }
 }
 
+// k_reduce for long segments and small ranks: the same work with both operands copied straight into LDS,
+// 128 contiguous bytes of a row at a time (register loads in operand layout fetch 64, and kept fewer
+// bytes in flight).  Each wave has a ring of RING steps of its own for its quarter of the chunk, so no
+// barrier is needed until the waves join.
+template <typename T, int RT, int RING>
+__global__ __launch_bounds__(64 * kReduceWaves, 1) void k_reduce_ring(LoraReduceGroup grp,
+                                                                      const int32_t* __restrict__ seg_start,
+                                                                      const int32_t* __restrict__ seg_adapter, int S,
+                                                                      int L, int N, int r) {
+  constexpr int kDeep = 128 / sizeof(T);                   // contraction per step
+  constexpr int kCopies = 2 + 2 * RT, kStage = kCopies * 1024;
+  constexpr int rp = RT * 16;
+  static_assert(kCopies * (RING - 1) < 64, "the copies in flight can be counted");
+  constexpr int kFlight = kCopies * (RING - 1);
+  __shared__ __align__(16) uint8_t s_ring[kReduceWaves * RING * kStage];
+  static_assert(sizeof(s_ring) >= sizeof(float) * kReduceWaves * kRows * (rp + 4), "the waves' sums fit");
+  using X = Side<T, kRows, false>;
+  using Y = Side<T, rp, false>;
+  const LoraReduceItem& it = grp.items[blockIdx.z];
+  const int chunk = blockIdx.y;
+  if ((int64_t)chunk * it.chunk >= it.K) return;
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int c = lane & 15, g = lane >> 4;
+  const int t0 = blockIdx.x * kRows, t1 = min(t0 + kRows, N);
+  const int64_t K = it.K;
+  const int64_t k0 = (int64_t)chunk * it.chunk + (int64_t)wave * (it.chunk / kReduceWaves);
+  const int64_t kend = min(k0 + it.chunk / kReduceWaves, K);
+  const int steps = (int)max((kend - k0 + kDeep - 1) / kDeep, (int64_t)0);
+  const __amdgpu_buffer_rsrc_t rs_x =
+      range_rsrc(static_cast<const T*>(it.x) + (int64_t)t0 * K, (int64_t)(t1 - t0) * K * sizeof(T));
+  uint32_t off_x[2], off_w[2 * RT];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) off_x[i] = X::source(i, lane, K) + (uint32_t)(k0 * sizeof(T));
+#pragma unroll
+  for (int i = 0; i < 2 * RT; ++i) off_w[i] = Y::source(i, lane, it.ldw) + (uint32_t)(k0 * sizeof(T));
+  // contraction of this lane's 16 bytes within a step: at or past kend it reads as 0
+  const int64_t mine = k0 + (((lane & 7) ^ ((lane >> 3) & 7)) * 16) / (int)sizeof(T);
+  uint8_t* ring = s_ring + wave * RING * kStage;
+
+  Segments segs(seg_start, seg_adapter, S, L, t0, t1, 0, 1, lane);
+  int lo, hi, a;
+  while (segs.next(lo, hi, a)) {
+    const __amdgpu_buffer_rsrc_t rs_w = range_rsrc(static_cast<const T*>(it.W) + (int64_t)a * r * it.ldw,
+                                                   (int64_t)r * it.ldw * sizeof(T));
+    auto copy = [&](int step) {
+      uint8_t* to = ring + (step & (RING - 1)) * kStage;
+      const bool in = mine + (int64_t)step * kDeep < kend;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t voff = in ? off_x[i] + step * 128 : kNoLoad;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_x, (lds_ptr_t)(to + i * 1024), 16, voff, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * RT; ++i) {
+        const uint32_t voff = in ? off_w[i] + step * 128 : kNoLoad;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_w, (lds_ptr_t)(to + 2048 + i * 1024), 16, voff, 0, 0, 0);
+      }
+    };
+    v4f acc[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < RING; ++s) copy(s);
+    for (int s = 0; s < steps; ++s) {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt((kFlight & 15) | ((kFlight >> 4) << 14) | 0xF70);   // step s has landed
+      asm volatile("" ::: "memory");
+      const uint8_t* from = ring + (s & (RING - 1)) * kStage;
+      v4u xs[2], ws[2][RT];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        xs[h] = X::read(from, 0, h, c, g);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) ws[h][t] = Y::read(from + 2048, t, h, c, g);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[t] = Mma<T>::run(ws[h][t], xs[h], acc[t]);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0xC07F);                  // the step's reads are done: its place is free
+      asm volatile("" ::: "memory");
+      copy(s + RING);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();                                       // no copy of any wave is left in the ring
+    float(*s_part)[kRows][rp + 4] = reinterpret_cast<float(*)[kRows][rp + 4]>(s_ring);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) *reinterpret_cast<v4f*>(&s_part[wave][c][t * 16 + 4 * g]) = acc[t];
+    __syncthreads();
+    for (int e = threadIdx.x; e < (hi - lo) * rp; e += 64 * kReduceWaves) {
+      const int row = lo + e / rp, k = e % rp;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kReduceWaves; ++w) v += s_part[w][row - t0][k];
+      it.part[((int64_t)chunk * N + row) * rp + k] = k < r ? v : 0.f;
+    }
+    __syncthreads();
+  }
+}
+
 // One lane's operand group for k_expand from G sums: part `part` of the bf16 split (hi, then what is
 // left, then what is left of that), or the fp32 values.
 template <typename T>
@@ -356,9 +457,9 @@ __global__ __launch_bounds__(256) void k_reduce_join(LoraReduceGroup grp, const 
 // the segments, the groups and the adapter do.
 //
 // The outputs of a wave's 64 are dealt to the rows i of its four output fragments f so that a lane's
-// accumulators make whole 16-byte pieces of one row of y: output 16 f + i for fp32 (each piece of a lane
-// 64 bytes on), 16 (i / 4) + 4 f + i % 4 for bf16 (its two pieces side by side).  Each is the faster
-// one for its type (bf16 59.6 against 62.2 us beside gate/up, fp32 7.8 against 8.9 us at 389 x 1408).
+// accumulators make whole 16-byte pieces of one row of y: output 16 f + i for fp32, 16 (i / 4) + 4 f +
+// i % 4 for bf16.  With long segments workgroups are ordered with the outputs innermost, so those that
+// run together read and write whole rows (beside gate/up, 2048 rows: 47.2 us, rows innermost 55.4).
 template <typename T, typename YT, int TF, bool READY, bool WVEC>
 __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32_t* __restrict__ seg_start,
                                                 const int32_t* __restrict__ seg_adapter, int S, int L, int N, int r,
@@ -372,9 +473,15 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
   const int64_t M = it.M;
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane & 15, g = lane >> 4;
-  const int64_t o_block = (int64_t)blockIdx.y * 256, o0 = o_block + wave * 64;
+  uint32_t row_block = blockIdx.x, out_block = blockIdx.y;
+  if constexpr (READY) {                                   // dispatch order: outputs innermost
+    const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x;
+    row_block = block / gridDim.y;
+    out_block = block - row_block * gridDim.y;
+  }
+  const int64_t o_block = (int64_t)out_block * 256, o0 = o_block + wave * 64;
   if (o_block >= M) return;
-  const int t0 = (int)(blockIdx.x / Q) * kTile, q = blockIdx.x % Q;
+  const int t0 = (int)(row_block / Q) * kTile, q = row_block % Q;
   const int t1 = min(t0 + kTile, N);
   const int gpp = rp / G;                                  // operand groups per part
   const int steps = (kParts * gpp + 3) / 4;
@@ -434,8 +541,11 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
     for (int f = 0; f < 4; ++f)
 #pragma unroll
       for (int t = 0; t < TF; ++t) acc[f][t] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int st = 0; st < steps; ++st) {
-      const int grpi = st * 4 + g, k = (grpi % gpp) * G;
+    // Whole steps of ranks (rp >= 4 G) are multiplied with each part of h in turn, the adapter loaded
+    // once; a rank of under 4 G shares one step between the parts.
+    const int passes = gpp % 4 == 0 ? kParts : 1, wsteps = gpp % 4 == 0 ? gpp / 4 : steps;
+    for (int ws = 0; ws < wsteps; ++ws) {
+      const int grpi = ws * 4 + g, k = (grpi % gpp) * G;
       const int have = grpi < kParts * gpp ? r - k : 0;
       v4u wa[4], hb[TF];
 #pragma unroll
@@ -448,12 +558,14 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
           wa[f] = load_group<T, false>(Wa + min((int64_t)o, M - 1 - o0) * r + k, have);
         }
       }
+      for (int p = 0; p < passes; ++p) {
 #pragma unroll
-      for (int t = 0; t < TF; ++t) hb[t] = groups[(min(t, tiles_here - 1) * steps + st) * 64 + lane];
+        for (int t = 0; t < TF; ++t) hb[t] = groups[(min(t, tiles_here - 1) * steps + p * wsteps + ws) * 64 + lane];
 #pragma unroll
-      for (int f = 0; f < 4; ++f)
+        for (int f = 0; f < 4; ++f)
 #pragma unroll
-        for (int t = 0; t < TF; ++t) acc[f][t] = Mma<T>::run(wa[f], hb[t], acc[f][t]);
+          for (int t = 0; t < TF; ++t) acc[f][t] = Mma<T>::run(wa[f], hb[t], acc[f][t]);
+      }
     }
 #pragma unroll
     for (int t = 0; t < TF; ++t) {
@@ -476,8 +588,7 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
             for (int w = 0; w < 4; ++w) {
               const v4f& d = acc[2 * h + (w >> 1)][t];
               const int e = 2 * (w & 1);
-              o[w] = (uint32_t)f32_to_bf16_rne(bf16_lo(old[t][h][w]) + d[e]) |
-                     ((uint32_t)f32_to_bf16_rne(bf16_hi(old[t][h][w]) + d[e + 1]) << 16);
+              o[w] = pack_bf16(bf16_lo(old[t][h][w]) + d[e], bf16_hi(old[t][h][w]) + d[e + 1]);
             }
             *reinterpret_cast<v4u*>(y + off + piece(h)) = o;
           }
@@ -679,12 +790,17 @@ int segment_shares(int N, int S) {
 // rank 32, 2048 x 4096, two projections 22.5 us with 16 rows, 24.3 with 64.)
 int reduce_rows(int N, int S, int r) { return segment_shares(N, S) == 1 && N >= 256 && r > 32 ? 4 : 1; }
 
-// Contraction chunk of k_reduce: small enough that the launch has about 2048 workgroups, at least
-// 256 elements (each wave then runs two bf16 steps), a multiple of 256.
-int reduce_chunk(int64_t K, int N, int S, int r, int items) {
+// Whether k_reduce_ring runs: long segments and small ranks (above, operands from registers with 64 rows
+// to a workgroup), whole 16-byte pieces in every row.
+bool reduce_ring(int N, int S, int r, bool vec) { return vec && segment_shares(N, S) == 1 && N >= 256 && r <= 32; }
+
+// Contraction chunk: small enough that the launch has about 1024 workgroups (k_reduce) or one per CU
+// (k_reduce_ring, whose rings keep the bytes in flight: 2048 x 4096 for two projections at rank 32
+// 15.0 us, with 512 workgroups 17.0, with 1024 20.1), at least 256 elements, a multiple of 256.
+int reduce_chunk(int64_t K, int N, int S, int r, bool vec, int items) {
   const int tile = kRows * reduce_rows(N, S, r);
   const int64_t wgs = (int64_t)((N + tile - 1) / tile) * segment_shares(N, S) * items;
-  const int64_t want = std::max<int64_t>(1, XW / wgs);
+  const int64_t want = std::max<int64_t>(1, (reduce_ring(N, S, r, vec) ? 256 : 1024) / wgs);
   const int64_t chunk = (K + want - 1) / want;
   return (int)std::max<int64_t>(256, (chunk + 255) / 256 * 256);
 }
@@ -705,6 +821,12 @@ void launch_reduce(const LoraReduceGroup& grp, int count, bool vec, const int32_
   const int Q = segment_shares(N, S), tr = reduce_rows(N, S, r), tile = kRows * tr;
   int most = 1;
   for (int k = 0; k < count; ++k) most = std::max(most, chunks(grp.items[k].K, grp.items[k].chunk));
+  if (reduce_ring(N, S, r, vec)) {
+    const dim3 grid((N + kRows - 1) / kRows, most, count), block(64 * kReduceWaves);
+    if (r <= 16) hipLaunchKernelGGL((k_reduce_ring<T, 1, 4>), grid, block, 0, st, grp, ss, sa, S, L, N, r);
+    else hipLaunchKernelGGL((k_reduce_ring<T, 2, 4>), grid, block, 0, st, grp, ss, sa, S, L, N, r);
+    return;
+  }
   const dim3 grid((N + tile - 1) / tile * Q, most, count);
   switch (rank_tiles(r) * 8 + tr) {
     case 9: reduce_vec<T, 1, 1>(grp, vec, grid, ss, sa, S, L, N, r, Q, st); break;
@@ -741,12 +863,16 @@ void expand_tf(const LoraExpandGroup& grp, int count, const int32_t* ss, const i
     hipLaunchKernelGGL((k_expand<T, YT, TF, READY, false>), grid, dim3(256), lds, st, grp, ss, sa, S, L, N, r, rp, Q);
 }
 
-// Rows per workgroup of k_expand: 16 for few rows or short segments, 32 otherwise (an adapter fragment
-// then serves two row tiles, and four waves a SIMD still fit).
+// Rows per workgroup of k_expand: 32 where that still leaves 2048 workgroups (an adapter fragment then
+// serves two row tiles), 16 otherwise.  Beside gate/up, 2048 rows: 47.2 us with 32, 50.8 with 16, 48.6
+// with 64; 389 fp32 rows of 1408: 5.6 us with 16, 7.6 with 32.
 template <typename T, typename YT>
 void launch_expand(const LoraExpandGroup& grp, int count, const int32_t* ss, const int32_t* sa, int S, int L, int N,
                    int r, hipStream_t st) {
-  if (ready_groups(N, S)) expand_tf<T, YT, 2, true>(grp, count, ss, sa, S, L, N, r, 1, st);
+  int64_t wgs = 0;
+  for (int k = 0; k < count; ++k) wgs += (int64_t)((N + 31) / 32) * ((grp.items[k].M + 255) / 256);
+  if (ready_groups(N, S) && wgs >= 2048) expand_tf<T, YT, 2, true>(grp, count, ss, sa, S, L, N, r, 1, st);
+  else if (ready_groups(N, S)) expand_tf<T, YT, 1, true>(grp, count, ss, sa, S, L, N, r, 1, st);
   else expand_tf<T, YT, 1, false>(grp, count, ss, sa, S, L, N, r, segment_shares(N, S), st);
 }
 
@@ -774,7 +900,7 @@ size_t lora_part_floats(int64_t K, int chunk, int64_t N, int r) { return (size_t
 template <typename T>
 hipError_t lora_t(const LoraArgs& p, const LoraItem* items, int count, hipStream_t st) {
   const int64_t K = 2 * p.m;
-  const int chunk = reduce_chunk(K, p.N, p.S, p.r, count);
+  const int chunk = reduce_chunk(K, p.N, p.S, p.r, true, count);
   const size_t part = up256(lora_part_floats(K, chunk, p.N, p.r) * 4), groups = up256(group_bytes(p.N, p.r, sizeof(T), p.y_bf16));
   const bool ready = ready_groups(p.N, p.S);
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
@@ -820,8 +946,9 @@ BackwardPlan backward_plan(int64_t N, int64_t m, int64_t n, int r, int L, int S,
   b.K = 2 * m;
   b.M = 2 * n;
   b.Mp = (b.M + 63) / 64 * 64;
-  b.chunk_x = reduce_chunk(b.K, (int)N, S, r, 2);
-  b.chunk_y = reduce_chunk(b.M, (int)N, S, r, 2);
+  const bool vec = b.M * elem % 16 == 0;
+  b.chunk_x = reduce_chunk(b.K, (int)N, S, r, vec, 2);
+  b.chunk_y = reduce_chunk(b.M, (int)N, S, r, vec, 2);
   const int step = 128 / elem;
   b.splits = outer_splits(N, std::max(b.K, b.M), L, elem);
   b.span = (int)(((N + b.splits - 1) / b.splits + step - 1) / step * step);
@@ -895,7 +1022,7 @@ size_t lora_workspace_bytes(int count, int64_t N, int64_t m, int r, int64_t S) {
   size_t most = 0;
   for (int items : {std::min(count, kMaxLoraItems), count % kMaxLoraItems}) {
     if (items < 1) continue;
-    const int chunk = reduce_chunk(2 * m, (int)N, (int)S, r, items);
+    const int chunk = reduce_chunk(2 * m, (int)N, (int)S, r, true, items);
     // the operand groups of fp32 outputs (three parts) are the largest
     const size_t groups = std::max(group_bytes(N, r, 2, 0), group_bytes(N, r, 4, 0));
     most = std::max(most, items * (up256(lora_part_floats(2 * m, chunk, N, r) * 4) +

@@ -13,6 +13,13 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 typedef __attribute__((address_space(3))) v4s* lds_v4s_t;
 
+// Two fp32 values as a pair of bf16, each rounded to nearest even (one instruction).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2bf));
+}
+
 // One 16-byte operand per lane (row or column lane & 15, contraction group lane >> 4).
 template <typename T> struct Mma;
 template <> struct Mma<uint16_t> {

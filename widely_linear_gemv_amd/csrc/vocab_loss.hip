@@ -279,8 +279,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
         }
         if constexpr (sizeof(T) == 2)
           *reinterpret_cast<uint2*>(p + tok * t.ldp + r) =
-              make_uint2(f32_to_bf16_rne(x[0]) | ((uint32_t)f32_to_bf16_rne(x[1]) << 16),
-                         f32_to_bf16_rne(x[2]) | ((uint32_t)f32_to_bf16_rne(x[3]) << 16));
+              make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
         else
           *reinterpret_cast<v4f*>(p + tok * t.ldp + r) = v4f{x[0], x[1], x[2], x[3]};
       }
@@ -307,8 +306,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
         }
         if constexpr (sizeof(T) == 2)
           *reinterpret_cast<uint2*>(out + at) =
-              make_uint2(f32_to_bf16_rne(v[0]) | ((uint32_t)f32_to_bf16_rne(v[1]) << 16),
-                         f32_to_bf16_rne(v[2]) | ((uint32_t)f32_to_bf16_rne(v[3]) << 16));
+              make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
         else
           *reinterpret_cast<v4f*>(out + at) = v;
       }
