@@ -131,7 +131,7 @@ def test_workspace_sizes_of_refused_shapes_are_zero():
     assert f2.fairy2i_vocab_loss_workspace_bytes(4, 100, 63, f2.BF16) == 0
     assert f2.fairy2i_vocab_loss_backward_workspace_bytes(1 << 20, 1 << 20, 64, f2.F32) == 0
     assert f2.fairy2i_lora_workspace_bytes(3, 16, 2048, 16, 16) > 0
-    assert f2.fairy2i_clip_grads_workspace_bytes([5, 0, 9000]) == 16 + 8 * 3
+    assert f2.fairy2i_clip_grads_workspace_bytes([5, 0, 9000]) == 16 + 32 * 3 + 8 * 3
 
 
 # ---- binding ----

@@ -9,6 +9,7 @@ every call raises -- there is no fallback implementation.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import functools
@@ -645,18 +646,22 @@ def fairy2i_gemm_noalloc(packed: torch.Tensor, scales: torch.Tensor, x: torch.Te
 # These calls take stream= too (_on_stream adds it): they run, and allocate what the caller gives no
 # tensor for, on that stream of the operands' device.
 
+_FLOATS = {torch.float32, torch.bfloat16}
+_HERE_SCOPE = contextlib.nullcontext()
+
+
 def _scope(t, stream):
     """Context of a call on t's device and the given stream, or the device's current one.  What the
     call allocates then belongs to the stream that uses it."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
-        return contextlib.nullcontext()                 # the argument checks refuse it
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+        return _HERE_SCOPE                              # the argument checks refuse it
     if stream is not None:
         if stream.device != t.device:
             raise ValueError(f"stream: on {stream.device}, the operands are on {t.device}")
         return torch.cuda.stream(stream)
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         return torch.cuda.device(t.device)
-    return contextlib.nullcontext()
+    return _HERE_SCOPE
 
 
 def _on_stream(fn):
@@ -668,6 +673,26 @@ def _on_stream(fn):
         with _scope(first[0] if isinstance(first, list) and first else first, stream):
             return fn(first, *args, **kwargs)
     return call
+
+
+def _fits(t, dtype, shape, dev):
+    """Whether t is what a call needs: a contiguous tensor of this dtype and shape on GPU number dev.
+    The calls test all their arguments with it at once; only if one fails does the matching _refuse_
+    function look for the reason (its checks in their fixed order) and raise."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == dev)
+
+
+def _room(workspace, nbytes, dev):
+    """(pointer, bytes, tensor) of the call's workspace: allocated when None, checked otherwise."""
+    if workspace is None:
+        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+    else:
+        _workspace(workspace, nbytes, dev)
+        _gpu((workspace, "workspace"))
+        if workspace.device != dev:
+            raise ValueError(f"workspace: on {workspace.device}, the other operands are on {dev}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def _workspace(workspace, nbytes, dev):
@@ -734,14 +759,44 @@ def fairy2i_lora_grouped(x: torch.Tensor, items, seg_start: torch.Tensor, seg_ad
     seg_adapter[s] (int32 on the GPU); y = base + alpha B A x on its rows, other rows of y are not
     written.  Returns the list of y."""
     items = list(items)
+    arr = (LoraItem * max(len(items), 1))()
+    ys = []
+    try:
+        dt, dev = x.dtype, x.get_device()
+        N, two_m = x.shape
+        S, = seg_adapter.shape
+        L, r, _ = items[0][0].shape
+        ydt = items[0][3].dtype
+        good = (dt in _FLOATS and ydt in _FLOATS and dev >= 0 and two_m % 2 == 0 and x.is_contiguous() and S > 0
+                and _fits(seg_adapter, torch.int32, (S,), dev) and _fits(seg_start, torch.int32, (S + 1,), dev))
+        for k, (A, B, alpha, base, y) in enumerate(items):
+            two_n = B.shape[1]
+            here = base.data_ptr()
+            there = here if y is None or y is base else y.data_ptr()
+            good = (good and two_n % 2 == 0 and _fits(A, dt, (L, r, two_m), dev) and _fits(B, dt, (L, two_n, r), dev)
+                    and _fits(alpha, torch.float32, (L,), dev) and _fits(base, ydt, (N, two_n), dev)
+                    and (there == here or abs(there - here) >= N * two_n * ydt.itemsize)
+                    and (y is None or y is base or _fits(y, ydt, (N, two_n), dev)))
+            arr[k] = (A.data_ptr(), B.data_ptr(), alpha.data_ptr(), here, there, two_n // 2)
+            ys.append(base if y is None else y)
+    except (AttributeError, IndexError, TypeError, ValueError):
+        good = False
+    if not good:
+        _refuse_lora(x, items, seg_start, seg_adapter, workspace)
+    ws, nbytes, keep = _room(workspace, fairy2i_lora_workspace_bytes(len(items), N, two_m // 2, r, S), x.device)
+    _check(lib().fairy2i_lora_grouped(arr, len(items), x.data_ptr(), _DTYPE[dt], N, two_m // 2, L, r, seg_start.data_ptr(),
+                                      seg_adapter.data_ptr(), S, _DTYPE[ydt], ws, nbytes, _stream()))
+    return ys
+
+
+def _refuse_lora(x, items, seg_start, seg_adapter, workspace):
+    """Raises for the first argument of fairy2i_lora_grouped that does not fit."""
     if not items:
         raise ValueError("fairy2i_lora_grouped: no items")
     _check_x(x)
     N, two_m = x.shape
     S = _check_segments(seg_start, seg_adapter)
-    arr = (LoraItem * len(items))()
     named = [(x, "x"), (seg_start, "seg_start"), (seg_adapter, "seg_adapter")]
-    ys = []
     for k, (A, B, alpha, base, y) in enumerate(items):
         name = f"items[{k}]." if len(items) > 1 else ""
         Lk, rk, two_n = _check_adapters(x, A, B, alpha, name)
@@ -756,15 +811,11 @@ def fairy2i_lora_grouped(x: torch.Tensor, items, seg_start: torch.Tensor, seg_ad
             raise ValueError(f"{name}base: dtype {base.dtype}, items[0] has {items[0][3].dtype}")
         if _overlap(y, base):
             raise ValueError(f"{name}y: overlaps base without being base")
-        arr[k] = LoraItem(A.data_ptr(), B.data_ptr(), alpha.data_ptr(), base.data_ptr(), y.data_ptr(), two_n // 2)
         named += [(A, name + "A"), (B, name + "B"), (alpha, name + "alpha"), (base, name + "base"), (y, name + "y")]
-        ys.append(y)
-    workspace = _workspace(workspace, fairy2i_lora_workspace_bytes(len(items), N, two_m // 2, r, S), x.device)
+    if workspace is not None:
+        _workspace(workspace, fairy2i_lora_workspace_bytes(len(items), N, two_m // 2, r, S), x.device)
     _gpu(*named, (workspace, "workspace"))
-    _check(lib().fairy2i_lora_grouped(arr, len(items), _ptr(x), _DTYPE[x.dtype], N, two_m // 2, L, r, _ptr(seg_start),
-                                      _ptr(seg_adapter), S, _DTYPE[ys[0].dtype], _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), _stream()))
-    return ys
+    raise ValueError("fairy2i_lora: the arguments do not fit together")
 
 
 def fairy2i_lora(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, alpha: torch.Tensor, seg_start: torch.Tensor,
@@ -785,6 +836,40 @@ def fairy2i_lora_backward(dy: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B:
     """Gradient of fairy2i_lora.  dy [N][2n] (x's dtype); dx_base [N][2m] is the gradient through the
     shared projection: dx = dx_base + A^T dh on rows with an adapter (dx None: in place; dx_base None:
     no dx).  Returns (dx or None, dA fp32 [L][r][2m], dB fp32 [L][2n][r])."""
+    f32 = torch.float32
+    out = dx_base if dx is None else dx
+    try:
+        dt, dev = x.dtype, x.get_device()
+        N, two_m = x.shape
+        S, = seg_adapter.shape
+        L, r, _ = A.shape
+        two_n = B.shape[1]
+        good = (dt in _FLOATS and dev >= 0 and two_m % 2 == 0 and two_n % 2 == 0 and x.is_contiguous() and S > 0
+                and _fits(dy, dt, (N, two_n), dev) and _fits(A, dt, (L, r, two_m), dev) and _fits(B, dt, (L, two_n, r), dev)
+                and _fits(alpha, f32, (L,), dev) and _fits(seg_adapter, torch.int32, (S,), dev)
+                and _fits(seg_start, torch.int32, (S + 1,), dev)
+                and (dA is None or _fits(dA, f32, (L, r, two_m), dev)) and (dB is None or _fits(dB, f32, (L, two_n, r), dev))
+                and (dx is None if dx_base is None else
+                     dx_base.dtype in _FLOATS and _fits(dx_base, dx_base.dtype, (N, two_m), dev)
+                     and (out is dx_base or _fits(out, dx_base.dtype, (N, two_m), dev) and not _overlap(out, dx_base))))
+    except (AttributeError, IndexError, TypeError, ValueError):
+        good = False
+    if not good:
+        _refuse_lora_backward(dy, x, A, B, alpha, seg_start, seg_adapter, dx_base, dx, dA, dB, workspace)
+    dA = torch.empty((L, r, two_m), dtype=f32, device=x.device) if dA is None else dA
+    dB = torch.empty((L, two_n, r), dtype=f32, device=x.device) if dB is None else dB
+    ws, nbytes, keep = _room(workspace, fairy2i_lora_backward_workspace_bytes(N, two_m // 2, two_n // 2, L, r, S, _DTYPE[dt]),
+                             x.device)
+    _check(lib().fairy2i_lora_backward(dy.data_ptr(), x.data_ptr(), _DTYPE[dt], N, two_m // 2, A.data_ptr(), B.data_ptr(),
+                                       alpha.data_ptr(), L, r, two_n // 2, seg_start.data_ptr(), seg_adapter.data_ptr(), S,
+                                       None if out is None else dx_base.data_ptr(), None if out is None else out.data_ptr(),
+                                       F32 if out is None else _DTYPE[out.dtype], dA.data_ptr(), dB.data_ptr(), ws, nbytes,
+                                       _stream()))
+    return out, dA, dB
+
+
+def _refuse_lora_backward(dy, x, A, B, alpha, seg_start, seg_adapter, dx_base, dx, dA, dB, workspace):
+    """Raises for the first argument of fairy2i_lora_backward that does not fit."""
     _check_x(x)
     N, two_m = x.shape
     S = _check_segments(seg_start, seg_adapter)
@@ -798,21 +883,12 @@ def fairy2i_lora_backward(dy: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B:
         _check_plain(dx, "dx", (dx_base.dtype,), (N, two_m))
         if _overlap(dx, dx_base):
             raise ValueError("dx: overlaps dx_base without being dx_base")
-    if dA is None:
-        dA = torch.empty((L, r, two_m), dtype=torch.float32, device=x.device)
-    if dB is None:
-        dB = torch.empty((L, two_n, r), dtype=torch.float32, device=x.device)
-    _check_plain(dA, "dA", (torch.float32,), (L, r, two_m))
-    _check_plain(dB, "dB", (torch.float32,), (L, two_n, r))
-    nbytes = fairy2i_lora_backward_workspace_bytes(N, two_m // 2, two_n // 2, L, r, S, _DTYPE[x.dtype])
-    workspace = _workspace(workspace, nbytes, x.device)
+    for t, name, shape in ((dA, "dA", (L, r, two_m)), (dB, "dB", (L, two_n, r))):
+        if t is not None:
+            _check_plain(t, name, (torch.float32,), shape)
     _gpu((x, "x"), (dy, "dy"), (A, "A"), (B, "B"), (alpha, "alpha"), (seg_start, "seg_start"),
          (seg_adapter, "seg_adapter"), (dx_base, "dx_base"), (dx, "dx"), (dA, "dA"), (dB, "dB"), (workspace, "workspace"))
-    _check(lib().fairy2i_lora_backward(_ptr(dy), _ptr(x), _DTYPE[x.dtype], N, two_m // 2, _ptr(A), _ptr(B), _ptr(alpha),
-                                       L, r, two_n // 2, _ptr(seg_start), _ptr(seg_adapter), S, _ptr(dx_base), _ptr(dx),
-                                       F32 if dx is None else _DTYPE[dx.dtype], _ptr(dA), _ptr(dB), _ptr(workspace),
-                                       workspace.numel() * workspace.element_size(), _stream()))
-    return dx, dA, dB
+    raise ValueError("fairy2i_lora_backward: the arguments do not fit together")
 
 
 def _check_head(h, W, target):
@@ -840,14 +916,18 @@ def fairy2i_vocab_loss(h: torch.Tensor, W: torch.Tensor, target: torch.Tensor, *
     """Per-token cross entropy of the vocabulary projection l = h W^T, h [N][K], W [V][K], without
     storing l: (loss, lse) fp32 [N].  Tokens whose target (int64) is outside [0, V) get loss 0."""
     N, V, K = _check_head(h, W, target)
-    loss = torch.empty((N,), dtype=torch.float32, device=h.device) if loss is None else loss
-    lse = torch.empty((N,), dtype=torch.float32, device=h.device) if lse is None else lse
-    _check_plain(loss, "loss", (torch.float32,), (N,))
-    _check_plain(lse, "lse", (torch.float32,), (N,))
-    workspace = _workspace(workspace, fairy2i_vocab_loss_workspace_bytes(N, V, K, _DTYPE[h.dtype]), h.device)
-    _gpu((h, "h"), (W, "W"), (target, "target"), (loss, "loss"), (lse, "lse"), (workspace, "workspace"))
-    _check(lib().fairy2i_vocab_loss(_ptr(h), _ptr(W), _DTYPE[h.dtype], N, V, K, _ptr(target), _ptr(loss), _ptr(lse),
-                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream()))
+    f32 = torch.float32
+    if loss is not None:
+        _check_plain(loss, "loss", (f32,), (N,))
+    if lse is not None:
+        _check_plain(lse, "lse", (f32,), (N,))
+    _gpu((h, "h"), (W, "W"), (target, "target"), (loss, "loss"), (lse, "lse"))
+    loss = torch.empty((N,), dtype=f32, device=h.device) if loss is None else loss
+    lse = torch.empty((N,), dtype=f32, device=h.device) if lse is None else lse
+    code = _DTYPE[h.dtype]
+    ws, nbytes, keep = _room(workspace, fairy2i_vocab_loss_workspace_bytes(N, V, K, code), h.device)
+    _check(lib().fairy2i_vocab_loss(h.data_ptr(), W.data_ptr(), code, N, V, K, target.data_ptr(), loss.data_ptr(),
+                                    lse.data_ptr(), ws, nbytes, _stream()))
     return loss, lse
 
 
@@ -869,17 +949,17 @@ def fairy2i_vocab_loss_backward(h: torch.Tensor, W: torch.Tensor, target: torch.
         raise ValueError("fairy2i_vocab_loss_backward: nothing to compute")
     if (dh is not None and not want_dh) or (dW is not None and not want_dW):
         raise ValueError("an output was given for a gradient that is not wanted")
-    if want_dh:
-        dh = torch.empty_like(h) if dh is None else dh
+    if dh is not None:
         _check_plain(dh, "dh", (h.dtype,), (N, K))
-    if want_dW:
-        dW = torch.empty_like(W) if dW is None else dW
+    if dW is not None:
         _check_plain(dW, "dW", (h.dtype,), (V, K))
-    workspace = _workspace(workspace, fairy2i_vocab_loss_backward_workspace_bytes(N, V, K, _DTYPE[h.dtype]), h.device)
-    _gpu((h, "h"), (W, "W"), (target, "target"), (lse, "lse"), (g, "g"), (dh, "dh"), (dW, "dW"), (workspace, "workspace"))
-    _check(lib().fairy2i_vocab_loss_backward(_ptr(h), _ptr(W), _DTYPE[h.dtype], N, V, K, _ptr(target), _ptr(lse),
-                                             _ptr(g), _ptr(dh), _ptr(dW), _ptr(workspace),
-                                             workspace.numel() * workspace.element_size(), _stream()))
+    _gpu((h, "h"), (W, "W"), (target, "target"), (lse, "lse"), (g, "g"), (dh, "dh"), (dW, "dW"))
+    dh = torch.empty_like(h) if want_dh and dh is None else dh
+    dW = torch.empty_like(W) if want_dW and dW is None else dW
+    code = _DTYPE[h.dtype]
+    ws, nbytes, keep = _room(workspace, fairy2i_vocab_loss_backward_workspace_bytes(N, V, K, code), h.device)
+    _check(lib().fairy2i_vocab_loss_backward(h.data_ptr(), W.data_ptr(), code, N, V, K, target.data_ptr(), lse.data_ptr(),
+                                             g.data_ptr(), _ptr(dh), _ptr(dW), ws, nbytes, _stream()))
     return dh, dW
 
 
@@ -893,10 +973,40 @@ def fairy2i_clip_grads(grads, max_norm: float, *, out=None, norm=None, workspace
     """Global norm of a list of gradients (fp32 or bf16 each, on one GPU) and clipping to max_norm:
     each gradient times min(1, max_norm / (norm + 1e-6)), in place or into the list `out`.  Returns
     the norm, fp32 [1]."""
-    grads = list(grads)
+    Tensor, n = torch.Tensor, len(grads)
+    outs = grads if out is None else list(out)
+    if not n or len(outs) != n or not max_norm >= 0 or not all(isinstance(t, Tensor) for t in (*grads, *outs)):
+        _refuse_clip(grads, outs, max_norm, norm)
+    # a stack's adapters are hundreds of tensors: each property is read once, in a loop of its own
+    ptrs, counts, dtypes = list(map(Tensor.data_ptr, grads)), list(map(Tensor.numel, grads)), [t.dtype for t in grads]
+    dev = grads[0].get_device()
+    good = (dev >= 0 and set(dtypes) <= _FLOATS and all(map(Tensor.is_contiguous, grads))
+            and set(map(Tensor.get_device, grads)) == {dev} and (norm is None or _fits(norm, torch.float32, (1,), dev)))
+    to = ptrs
+    if out is not None:
+        to = list(map(Tensor.data_ptr, outs))
+        good = (good and [t.dtype for t in outs] == dtypes and all(map(Tensor.is_contiguous, outs))
+                and set(map(Tensor.get_device, outs)) == {dev} and list(map(Tensor.numel, outs)) == counts
+                and all(a == b or abs(a - b) >= c * d.itemsize
+                        for a, b, c, d in zip(ptrs, to, counts, dtypes)))
+    if not good:
+        _refuse_clip(grads, outs, max_norm, norm)
+    numel = array.array("q", counts)
+    codes = array.array("i", [_DTYPE[d] for d in dtypes])
+    address = lambda a, kind: ctypes.cast(a.buffer_info()[0], ctypes.POINTER(kind))
+    from_, to_ = array.array("Q", ptrs), array.array("Q", to)
+    norm = torch.empty((1,), dtype=torch.float32, device=grads[0].device) if norm is None else norm
+    sizes = address(numel, _I64)
+    ws, nbytes, keep = _room(workspace, lib().fairy2i_clip_grads_workspace_bytes(n, sizes), norm.device)
+    _check(lib().fairy2i_clip_grads(n, address(from_, _P), None if out is None else address(to_, _P), sizes,
+                                    address(codes, _INT), max_norm, norm.data_ptr(), ws, nbytes, _stream()))
+    return norm
+
+
+def _refuse_clip(grads, outs, max_norm, norm):
+    """Raises for the first argument of fairy2i_clip_grads that does not fit."""
     if not grads:
         raise ValueError("fairy2i_clip_grads: no gradients")
-    outs = grads if out is None else list(out)
     if len(outs) != len(grads):
         raise ValueError(f"out: {len(outs)} outputs for {len(grads)} gradients")
     for k, (g, o) in enumerate(zip(grads, outs)):
@@ -904,21 +1014,16 @@ def fairy2i_clip_grads(grads, max_norm: float, *, out=None, norm=None, workspace
         _dtype(g, f"grads[{k}]", torch.float32, torch.bfloat16)
         _on_gpu(g, f"grads[{k}]")
         if o is not g:
-            _check_plain(o, f"out[{k}]", (g.dtype,), g.shape)
+            _tensor(o, f"out[{k}]")
+            _dtype(o, f"out[{k}]", g.dtype)
+            if o.numel() != g.numel():
+                raise ValueError(f"out[{k}]: {o.numel()} elements, its gradient has {g.numel()}")
+            _on_gpu(o, f"out[{k}]")
             if _overlap(o, g):
                 raise ValueError(f"out[{k}]: overlaps its gradient without being it")
-    dev = grads[0].device
-    norm = torch.empty((1,), dtype=torch.float32, device=dev) if norm is None else norm
-    _check_plain(norm, "norm", (torch.float32,), (1,))
     if not max_norm >= 0:
         raise ValueError(f"max_norm: {max_norm}, need at least 0")
-    n = len(grads)
-    numel = (_I64 * n)(*[g.numel() for g in grads])
-    workspace = _workspace(workspace, int(lib().fairy2i_clip_grads_workspace_bytes(n, numel)), dev)
-    _gpu(*[(g, f"grads[{k}]") for k, g in enumerate(grads)], *[(o, f"out[{k}]") for k, o in enumerate(outs)],
-         (norm, "norm"), (workspace, "workspace"))
-    _check(lib().fairy2i_clip_grads(n, (_P * n)(*[g.data_ptr() for g in grads]),
-                                    None if out is None else (_P * n)(*[o.data_ptr() for o in outs]), numel,
-                                    (_INT * n)(*[_DTYPE[g.dtype] for g in grads]), max_norm, _ptr(norm),
-                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream()))
-    return norm
+    if norm is not None:
+        _check_plain(norm, "norm", (torch.float32,), (1,))
+    _gpu(*[(g, f"grads[{k}]") for k, g in enumerate(grads)], *[(o, f"out[{k}]") for k, o in enumerate(outs)], (norm, "norm"))
+    raise ValueError("fairy2i_clip_grads: the arguments do not fit together")

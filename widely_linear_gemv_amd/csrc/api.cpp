@@ -813,7 +813,7 @@ static int64_t clip_total_pieces(int count, const int64_t* numel) {
 
 size_t fairy2i_clip_grads_workspace_bytes(int count, const int64_t* numel) {
   if (count < 0 || (count > 0 && !numel)) return 0;
-  return 16 + (size_t)clip_total_pieces(count, numel) * sizeof(double);
+  return 16 + (size_t)count * sizeof(f2i::ClipItem) + (size_t)clip_total_pieces(count, numel) * sizeof(double);
 }
 
 int fairy2i_clip_grads(int count, const void* const* grads, void* const* out, const int64_t* numel, const int* dtypes,
@@ -834,37 +834,35 @@ int fairy2i_clip_grads(int count, const void* const* grads, void* const* out, co
   }
   if (!aligned(norm, 4)) return fail(FAIRY2I_ERR_ALIGN, "norm needs 4-byte alignment");
   if (int s = check_workspace(workspace, workspace_bytes, fairy2i_clip_grads_workspace_bytes(count, numel))) return s;
+  // workspace: coefficient, table (8-byte entries), partial sums
   float* coef = static_cast<float*>(workspace);
-  double* part = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + 16);
+  f2i::ClipItem* table = reinterpret_cast<f2i::ClipItem*>(static_cast<uint8_t*>(workspace) + 16);
+  double* part = reinterpret_cast<double*>(table + count);
   int64_t pieces = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t at = 0;
-    for (int k = 0; k < count;) {
-      f2i::ClipGroup grp;
-      grp.count = 0;
-      grp.piece0 = at;
-      int64_t blocks = 0;
-      for (; k < count && grp.count < f2i::kMaxClipItems; ++k) {
-        if (numel[k] == 0) continue;
-        const int64_t p = f2i::clip_pieces(numel[k]);
-        if (grp.count > 0 && blocks + p >= (int64_t(1) << 24)) break;       // 2^32 work-items a launch
-        void* o = out ? out[k] : const_cast<void*>(grads[k]);
-        grp.items[grp.count++] = f2i::ClipItem{grads[k], o, numel[k], (int)blocks, dtypes[k] == FAIRY2I_BF16,
-                                               aligned(grads[k], 16) && aligned(o, 16)};
-        blocks += p;
-      }
-      if (grp.count == 0) continue;
-      const hipError_t e = pass == 0 ? f2i::launch_clip_square(grp, (int)blocks, part, stream)
-                                     : f2i::launch_clip_scale(grp, (int)blocks, coef, stream);
-      if (e != hipSuccess) return hip_status(e, "gradient clipping launch");
-      at += blocks;
+  int items = 0;
+  hipError_t e = hipSuccess;
+  for (int k = 0; k < count;) {
+    f2i::ClipGroup grp;
+    grp.count = 0;
+    for (; k < count && grp.count < f2i::kMaxClipItems; ++k) {
+      if (numel[k] == 0) continue;
+      void* o = out ? out[k] : const_cast<void*>(grads[k]);
+      const int flags = (dtypes[k] == FAIRY2I_BF16 ? f2i::kClipBf16 : 0) |
+                        (aligned(grads[k], 16) && aligned(o, 16) ? f2i::kClipVec : 0);
+      grp.items[grp.count++] = f2i::ClipItem{grads[k], o, pieces, (uint16_t)f2i::clip_tail(numel[k]), (uint16_t)flags};
+      pieces += f2i::clip_pieces(numel[k]);
     }
-    if (pass == 0) {
-      pieces = at;
-      const hipError_t e = f2i::launch_clip_norm(part, pieces, max_norm, norm, coef, stream);
-      if (e != hipSuccess) return hip_status(e, "gradient norm launch");
-    }
+    if (grp.count == 0) continue;
+    e = f2i::launch_clip_table(grp, table + items, stream);
+    if (e != hipSuccess) return hip_status(e, "gradient clipping launch");
+    items += grp.count;
   }
+  e = f2i::launch_clip_square(table, items, pieces, part, stream);
+  if (e != hipSuccess) return hip_status(e, "gradient norm launch");
+  e = f2i::launch_clip_norm(part, pieces, max_norm, norm, coef, stream);
+  if (e != hipSuccess) return hip_status(e, "gradient norm launch");
+  e = f2i::launch_clip_scale(table, items, pieces, coef, stream);
+  if (e != hipSuccess) return hip_status(e, "gradient clipping launch");
   return ok();
 }
 

@@ -7,7 +7,9 @@
 // result never depends on scheduling) into the norm and c, k_scale multiplies.  The norm must be
 // known before the first write, so the gradients are read twice; the second time they come from
 // the Infinity Cache as far as they fit.  In place with c = 1 nothing is written.
-#include "common.hpp"
+#include <algorithm>
+
+#include "tiles.hpp"
 
 namespace f2i {
 
@@ -15,14 +17,31 @@ namespace {
 
 constexpr int kPiece = 8192;       // elements per workgroup
 
-// Tensor of workgroup `block`: the last one whose first piece is at or before it.
-__device__ __forceinline__ int find_tensor(const ClipGroup& g, int block) {
-  int lo = 0, hi = g.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (g.items[mid].first_piece <= block) lo = mid; else hi = mid - 1;
+// Piece `piece` among all: the last tensor whose first piece is at or before it (64 entries of the table
+// are compared at a time), its first element and its elements.
+struct Piece {
+  const void* g;
+  void* out;
+  int64_t i0;
+  int n;
+  bool bf16, vec;
+};
+__device__ __forceinline__ Piece find_piece(const ClipItem* __restrict__ table, int count, int64_t pieces, int64_t piece) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int lo = 0, len = count;
+  while (len > 1) {
+    const int stride = (len + kWave - 1) / kWave;
+    const int at = lo + lane * stride;
+    const uint64_t before = __ballot(at < lo + len && table[min(at, count - 1)].first_piece <= piece);
+    const int k = 63 - __builtin_clzll(before | 1);
+    lo += k * stride;
+    len = min(stride, len - k * stride);
   }
-  return lo;
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  const ClipItem it = table[lo];
+  const int64_t last = (lo + 1 < count ? table[lo + 1].first_piece : pieces) - 1;
+  return Piece{it.g, it.out, (piece - it.first_piece) * kPiece, piece == last ? (int)it.tail : kPiece,
+               (it.flags & kClipBf16) != 0, (it.flags & kClipVec) != 0};
 }
 
 __device__ __forceinline__ double sq(float v) { return (double)v * (double)v; }
@@ -41,39 +60,60 @@ __device__ __forceinline__ double block_sum(double v, double* s_wave) {
 
 }  // namespace
 
-__global__ __launch_bounds__(256) void k_square(ClipGroup grp, double* __restrict__ part) {
-  __shared__ double s_wave[4];
-  const int k = find_tensor(grp, blockIdx.x);
-  const ClipItem& it = grp.items[k];
-  const int64_t i0 = (int64_t)(blockIdx.x - it.first_piece) * kPiece;
-  const int n = (int)min((int64_t)kPiece, it.numel - i0);
-  double v = 0.0;
-  if (it.bf16) {
-    const uint16_t* __restrict__ p = static_cast<const uint16_t*>(it.g) + i0;
-    int i = threadIdx.x;
-    if (it.vec) {
-      for (i = threadIdx.x * 8; i + 8 <= n; i += 256 * 8) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p + i);
-        v += sq(bf16_lo(w.x)) + sq(bf16_hi(w.x)) + sq(bf16_lo(w.y)) + sq(bf16_hi(w.y));
-        v += sq(bf16_lo(w.z)) + sq(bf16_hi(w.z)) + sq(bf16_lo(w.w)) + sq(bf16_hi(w.w));
-      }
-      i = (n & ~7) + threadIdx.x;
+// The table of tensors comes in the kernel arguments, 120 entries to a launch, and is kept in the
+// workspace: the passes over the data then run as one launch each, and their thousands of workgroups
+// read it from the L2 (arguments lie in host memory: reading the table there took longer than the data).
+__global__ __launch_bounds__(64) void k_table(ClipGroup grp, ClipItem* __restrict__ table) {
+  for (int k = threadIdx.x; k < grp.count; k += 64) table[k] = grp.items[k];
+}
+
+// The 16-byte pieces of an aligned tensor's piece, kPiece / 256 elements to a thread: every load is issued
+// before the first is used; elements past the last whole 16 bytes (all, where the tensor is not aligned)
+// go one by one.
+template <typename T>
+struct Chunk {
+  static constexpr int kEach = 16 / sizeof(T), kLoads = kPiece / (256 * kEach);
+  uint4 w[kLoads];
+  int whole;
+  __device__ __forceinline__ void load(const T* p, int n, bool vec) {
+    whole = vec ? n / kEach * kEach : 0;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = j * 256 + threadIdx.x;
+      w[j] = i * kEach < whole ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
     }
-    for (; i < n; i += 256) v += sq(bf16_lo(p[i]));
-  } else {
-    const float* __restrict__ p = static_cast<const float*>(it.g) + i0;
-    int i = threadIdx.x;
-    if (it.vec) {
-      for (i = threadIdx.x * 4; i + 4 <= n; i += 256 * 4) {
-        const float4 w = *reinterpret_cast<const float4*>(p + i);
-        v += (sq(w.x) + sq(w.y)) + (sq(w.z) + sq(w.w));
-      }
-      i = (n & ~3) + threadIdx.x;
-    }
-    for (; i < n; i += 256) v += sq(p[i]);
   }
+};
+__device__ __forceinline__ float value(float v) { return v; }
+__device__ __forceinline__ float value(uint16_t v) { return bf16_lo(v); }
+
+template <typename T>
+__device__ __forceinline__ double squares(const T* __restrict__ p, int n, bool vec) {
+  Chunk<T> q;
+  q.load(p, n, vec);
+  double v = 0.0;
+#pragma unroll
+  for (int j = 0; j < Chunk<T>::kLoads; ++j) {
+    const uint32_t e[4] = {q.w[j].x, q.w[j].y, q.w[j].z, q.w[j].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) v += sq(__uint_as_float(e[i]));
+      else v += sq(bf16_lo(e[i])) + sq(bf16_hi(e[i]));
+    }
+  }
+#pragma unroll 4
+  for (int i = q.whole + threadIdx.x; i < n; i += 256) v += sq(value(p[i]));
+  return v;
+}
+
+__global__ __launch_bounds__(256) void k_square(const ClipItem* __restrict__ table, int count, int64_t pieces,
+                                                int64_t piece0, double* __restrict__ part) {
+  __shared__ double s_wave[4];
+  const Piece q = find_piece(table, count, pieces, piece0 + blockIdx.x);
+  const double v = q.bf16 ? squares(static_cast<const uint16_t*>(q.g) + q.i0, q.n, q.vec)
+                          : squares(static_cast<const float*>(q.g) + q.i0, q.n, q.vec);
   const double t = block_sum<256>(v, s_wave);
-  if (threadIdx.x == 0) part[grp.piece0 + blockIdx.x] = t;
+  if (threadIdx.x == 0) part[piece0 + blockIdx.x] = t;
 }
 
 // coef[0] = c (fp32).
@@ -91,48 +131,50 @@ __global__ __launch_bounds__(1024) void k_norm(const double* __restrict__ part, 
   }
 }
 
-__global__ __launch_bounds__(256) void k_scale(ClipGroup grp, const float* __restrict__ coef) {
-  const int k = find_tensor(grp, blockIdx.x);
-  const ClipItem& it = grp.items[k];
-  const float c = *coef;
-  if (c == 1.f && it.out == it.g) return;
-  const int64_t i0 = (int64_t)(blockIdx.x - it.first_piece) * kPiece;
-  const int n = (int)min((int64_t)kPiece, it.numel - i0);
-  if (it.bf16) {
-    const uint16_t* p = static_cast<const uint16_t*>(it.g) + i0;
-    uint16_t* o = static_cast<uint16_t*>(it.out) + i0;
-    int i = threadIdx.x;
-    if (it.vec) {
-      for (i = threadIdx.x * 8; i + 8 <= n; i += 256 * 8) {
-        uint4 w = *reinterpret_cast<const uint4*>(p + i);
-        uint32_t* e = &w.x;
+template <typename T>
+__device__ __forceinline__ void scaled(const T* p, T* o, int n, bool vec, float c) {
+  Chunk<T> q;
+  q.load(p, n, vec);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          e[j] = (uint32_t)f32_to_bf16_rne(c * bf16_lo(e[j])) | ((uint32_t)f32_to_bf16_rne(c * bf16_hi(e[j])) << 16);
-        *reinterpret_cast<uint4*>(o + i) = w;
-      }
-      i = (n & ~7) + threadIdx.x;
+  for (int j = 0; j < Chunk<T>::kLoads; ++j) {
+    const int at = j * 256 + threadIdx.x;
+    if (at * Chunk<T>::kEach >= q.whole) break;
+    uint32_t e[4] = {q.w[j].x, q.w[j].y, q.w[j].z, q.w[j].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) e[i] = __float_as_uint(c * __uint_as_float(e[i]));
+      else e[i] = pack_bf16(c * bf16_lo(e[i]), c * bf16_hi(e[i]));
     }
-    for (; i < n; i += 256) o[i] = f32_to_bf16_rne(c * bf16_lo(p[i]));
-  } else {
-    const float* p = static_cast<const float*>(it.g) + i0;
-    float* o = static_cast<float*>(it.out) + i0;
-    int i = threadIdx.x;
-    if (it.vec) {
-      for (i = threadIdx.x * 4; i + 4 <= n; i += 256 * 4) {
-        const float4 w = *reinterpret_cast<const float4*>(p + i);
-        *reinterpret_cast<float4*>(o + i) = make_float4(c * w.x, c * w.y, c * w.z, c * w.w);
-      }
-      i = (n & ~3) + threadIdx.x;
-    }
-    for (; i < n; i += 256) o[i] = c * p[i];
+    reinterpret_cast<uint4*>(o)[at] = make_uint4(e[0], e[1], e[2], e[3]);
   }
+#pragma unroll 4
+  for (int i = q.whole + threadIdx.x; i < n; i += 256) store_out(o, i, c * value(p[i]));
+}
+
+__global__ __launch_bounds__(256) void k_scale(const ClipItem* __restrict__ table, int count, int64_t pieces,
+                                               int64_t piece0, const float* __restrict__ coef) {
+  const float c = *coef;
+  const Piece q = find_piece(table, count, pieces, piece0 + blockIdx.x);
+  if (c == 1.f && q.out == q.g) return;
+  if (q.bf16) scaled(static_cast<const uint16_t*>(q.g) + q.i0, static_cast<uint16_t*>(q.out) + q.i0, q.n, q.vec, c);
+  else scaled(static_cast<const float*>(q.g) + q.i0, static_cast<float*>(q.out) + q.i0, q.n, q.vec, c);
 }
 
 int64_t clip_pieces(int64_t numel) { return (numel + kPiece - 1) / kPiece; }
+int clip_tail(int64_t numel) { return (int)(numel - (clip_pieces(numel) - 1) * kPiece); }
 
-hipError_t launch_clip_square(const ClipGroup& grp, int pieces, double* part, hipStream_t s) {
-  hipLaunchKernelGGL(k_square, dim3(pieces), dim3(256), 0, s, grp, part);
+hipError_t launch_clip_table(const ClipGroup& grp, ClipItem* table, hipStream_t s) {
+  hipLaunchKernelGGL(k_table, dim3(1), dim3(64), 0, s, grp, table);
+  return hipGetLastError();
+}
+
+// 2^23 pieces to a launch (2^32 work-items are too many for one).
+constexpr int64_t kLaunchPieces = int64_t(1) << 23;
+
+hipError_t launch_clip_square(const ClipItem* table, int count, int64_t pieces, double* part, hipStream_t s) {
+  for (int64_t p = 0; p < pieces; p += kLaunchPieces)
+    hipLaunchKernelGGL(k_square, dim3((unsigned)std::min(kLaunchPieces, pieces - p)), dim3(256), 0, s, table, count, pieces,
+                       p, part);
   return hipGetLastError();
 }
 
@@ -141,8 +183,10 @@ hipError_t launch_clip_norm(const double* part, int64_t pieces, float max_norm, 
   return hipGetLastError();
 }
 
-hipError_t launch_clip_scale(const ClipGroup& grp, int pieces, const float* coef, hipStream_t s) {
-  hipLaunchKernelGGL(k_scale, dim3(pieces), dim3(256), 0, s, grp, coef);
+hipError_t launch_clip_scale(const ClipItem* table, int count, int64_t pieces, const float* coef, hipStream_t s) {
+  for (int64_t p = 0; p < pieces; p += kLaunchPieces)
+    hipLaunchKernelGGL(k_scale, dim3((unsigned)std::min(kLaunchPieces, pieces - p)), dim3(256), 0, s, table, count, pieces,
+                       p, coef);
   return hipGetLastError();
 }
 

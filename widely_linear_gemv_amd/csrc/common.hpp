@@ -320,21 +320,22 @@ hipError_t launch_vocab_loss(const VocabArgs& a, hipStream_t s);
 hipError_t launch_vocab_loss_backward(const VocabArgs& a, hipStream_t s);
 
 // ---- gradient clipping (clip.hip) ----
-constexpr int kMaxClipItems = 100;    // tensors per launch; the table travels in the kernel arguments
+constexpr int kMaxClipItems = 120;    // tensors per launch; the table travels in the kernel arguments
+constexpr int kClipBf16 = 1, kClipVec = 2;   // flags; vec: gradient and output 16-byte aligned
 struct ClipItem {
   const void* g;
   void* out;
-  int64_t numel;
-  int first_piece;        // of the launch
-  uint8_t bf16, vec;      // vec: g and out 16-byte aligned
+  int64_t first_piece;
+  uint16_t tail, flags;   // elements of the last piece
 };
 struct ClipGroup {
   int count;
-  int64_t piece0;         // the launch's first piece among all pieces
   ClipItem items[kMaxClipItems];
 };
 int64_t clip_pieces(int64_t numel);
-hipError_t launch_clip_square(const ClipGroup& grp, int pieces, double* part, hipStream_t s);
+int clip_tail(int64_t numel);
+hipError_t launch_clip_table(const ClipGroup& grp, ClipItem* table, hipStream_t s);
+hipError_t launch_clip_square(const ClipItem* table, int count, int64_t pieces, double* part, hipStream_t s);
 hipError_t launch_clip_norm(const double* part, int64_t pieces, float max_norm, float* norm, float* coef, hipStream_t s);
-hipError_t launch_clip_scale(const ClipGroup& grp, int pieces, const float* coef, hipStream_t s);
+hipError_t launch_clip_scale(const ClipItem* table, int count, int64_t pieces, const float* coef, hipStream_t s);
 }  // namespace f2i
