@@ -424,8 +424,11 @@ int fairy2i_lora_backward(const void* dy, const void* x, int x_dtype, int64_t N,
  *   target  int64 [N]; a target outside [0, V) (-100, say) marks a token that does not count: its
  *           loss is 0.
  *   loss, lse  out, fp32 [N].
- * Sums are fp32 with a running maximum.  workspace: fairy2i_vocab_loss_workspace_bytes(...) bytes,
- * 16-byte aligned; calls that share one must not overlap. */
+ * Sums are fp32 with a running maximum.  fp32 operands are multiplied as three bf16 parts each, which
+ * hold them exactly; the products left out are under 2^-23 of |h W|.  A NaN or infinity in a row of h
+ * stays in that token's loss and lse (fp32: an infinity as NaN).
+ * workspace: fairy2i_vocab_loss_workspace_bytes(...) bytes, 16-byte aligned; calls that share one must
+ * not overlap. */
 size_t fairy2i_vocab_loss_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype);
 int fairy2i_vocab_loss(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K, const int64_t* target,
                        float* loss, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
@@ -434,7 +437,9 @@ int fairy2i_vocab_loss(const void* h, const void* W, int x_dtype, int64_t N, int
  *     p_iv = g_i (exp(l_iv - lse_i) - [v = target_i])   (0 for tokens that do not count)
  *     dh_i = sum_v p_iv W_v        dW_v = sum_i p_iv h_i
  * in pieces of the vocabulary, whose logits are computed again; p is held in x_dtype between the two
- * products, sums are fp32 and each output is rounded once.
+ * products (bf16: apart from the scale of g_i, which is applied to the fp32 sums of dh and, unless all
+ * g are equal, costs dW one rounding of h more), sums are fp32 and each output is rounded once.  A
+ * token with g_i = 0 adds nothing, whatever its logits.
  *   dh [N][K], dW [V][K], x_dtype; either may be NULL (not computed: a frozen W needs no dW). */
 size_t fairy2i_vocab_loss_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype);
 int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K,

@@ -1,12 +1,14 @@
 """Vocabulary cross entropy (fairy2i_vocab_loss) and its gradient against the formulas in 64 bits.
 
 Tolerances from the arithmetic, with u the inputs' unit roundoff (finfo.eps / 2):
-  logit   d_iv = (K + 8) 2^-24 sum_k |h_ik W_vk|                  (fp32 sums of exact or once-rounded products)
+  logit   d_iv = (K + 8) 2^-24 sum_k |h_ik W_vk|                  (fp32 sums of exact products), for fp32
+          operands 2^-23 of the same sum more                    (products of their smallest parts left out)
   lse     max_v d_iv + 2^-18 + 2^-22 |lse|                        (exponentials and their sum: 64 roundings)
   loss    lse's + d_it + 2^-23 (|lse| + |loss|)
   p       |p| (u + d_iv + lse's + 2^-20) + 2^-23 |g| at the target (one rounding to the inputs' dtype)
   dh, dW  the p's errors through the product, (V + 16) or (N + 16) 2^-24 of the absolute terms for the
-          fp32 sums, and u of the result."""
+          fp32 sums, and u of the result; for bf16 dW one rounding (u) of its other operand more, which
+          is h times the g's own factor."""
 import math
 
 import pytest
@@ -37,14 +39,14 @@ def reference(c):
     N, K = h.shape
     V = W.shape[0]
     z = h @ W.t()
-    d = (K + 8) * E24 * (h.abs() @ W.abs().t())
+    d = (K + 8) * E24 * (h.abs() @ W.abs().t()) + (2.0 ** -23 * (h.abs() @ W.abs().t()) if c["h"].dtype == torch.float32 else 0.0)
     lse = torch.logsumexp(z, 1)
     dl = d.max(1).values + 2.0 ** -18 + 2.0 ** -22 * lse.abs()
     ok = (t >= 0) & (t < V)
     at = t.clamp(0, V - 1)
-    row = torch.arange(N)
-    loss = torch.where(ok, lse - z[row, at], torch.zeros(N, dtype=torch.float64))
-    dloss = torch.where(ok, dl + d[row, at] + 2.0 ** -23 * (lse.abs() + loss.abs()), torch.zeros(N, dtype=torch.float64))
+    row = torch.arange(N, device=z.device)
+    loss = torch.where(ok, lse - z[row, at], torch.zeros_like(lse))
+    dloss = torch.where(ok, dl + d[row, at] + 2.0 ** -23 * (lse.abs() + loss.abs()), torch.zeros_like(lse))
     return z, d, lse, dl, loss, dloss, ok, at
 
 
@@ -53,17 +55,17 @@ def grad_reference(c):
     h, W = c["h"].double(), c["W"].double()
     N, V = z.shape
     u = torch.finfo(c["h"].dtype).eps / 2
-    row = torch.arange(N)
-    g = torch.where(ok, c["g"].double(), torch.zeros(N, dtype=torch.float64))
+    row = torch.arange(N, device=z.device)
+    g = torch.where(ok, c["g"].double(), torch.zeros_like(lse))
     soft = (z - lse[:, None]).exp()
     p = soft.clone()
     p[row, at] -= 1.0
     p = p * g[:, None]
-    ep = g[:, None] * soft * (d + dl[:, None] + 2.0 ** -20) + u * p.abs()
-    ep[row, at] += 2.0 ** -23 * g
+    ep = g.abs()[:, None] * soft * (d + dl[:, None] + 2.0 ** -20) + u * p.abs()
+    ep[row, at] += 2.0 ** -23 * g.abs()
     dh, dW = p @ W, p.t() @ h
     bh = ep @ W.abs() + (V + 16) * E24 * (p.abs() @ W.abs()) + u * dh.abs()
-    bW = ep.t() @ h.abs() + (N + 16) * E24 * (p.abs().t() @ h.abs()) + u * dW.abs()
+    bW = ep.t() @ h.abs() + ((N + 16) * E24 + (u if u > E24 else 0.0)) * (p.abs().t() @ h.abs()) + u * dW.abs()
     return dh, bh, dW, bW
 
 
@@ -113,6 +115,81 @@ def test_wide_logits(dt):
     _, _, wl, bl, wo, bo, _, _ = reference(c)
     close(lse, wl, bl, "lse")
     close(loss, wo, bo, "loss")
+
+
+# one size for each tile shape that the gradient's and the loss's products may take, with two pieces
+LARGE = [(2048, 16384, 64), (2048, 9000, 192), (1000, 8200, 256), (600, 12000, 1024)]
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("size", LARGE, ids=lambda s: "N%d-V%d-K%d" % s)
+def test_large_tiles(size, dt):
+    """Sizes that fill the device with larger tiles; the 64-bit reference runs on the GPU."""
+    dev = device()
+    _, d = make(*size, dt, 15, dev)
+    announce("vocab large", size, dt)
+    loss, lse = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"])
+    dh, dW = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"])
+    _, _, wl, bl, wo, bo, _, _ = (x.cpu() for x in reference(d))
+    close(lse, wl, bl, "lse")
+    close(loss, wo, bo, "loss")
+    wh, bh, wW, bW = (x.cpu() for x in grad_reference(d))
+    close(dh, wh, bh, "dh")
+    close(dW, wW, bW, "dW")
+
+
+@pytest.mark.parametrize("kind", ["mean", "two", "random"])
+def test_rounding_is_not_common_to_all_values(kind):
+    """bf16: the part of dh's and dW's error along dh and dW themselves, which a rounding shared by all
+    values (of -g at the targets, say) would make up to 2^-8.  Independent roundings of N K >= 2^17
+    values of at most 2^-8 each leave under 2^-8 * 6 / 2^8.5 along any fixed direction (six standard
+    deviations); 2^-12 allows for values of unequal size.  The one rounding that is alike for all tokens
+    is that of the target's entry, -(1 - p): -1 is a bf16 value, so the rounded entry is off by at most
+    its distance from it, p, which adds at most sum_i |g_i| p_i |<W_t, dh_i>| / |dh|^2 along dh (with h
+    and dW in their place along dW)."""
+    dev = device()
+    N, V, K = 300, 2000, 512
+    c, d = make(N, V, K, torch.bfloat16, 16, dev, ignored=0.1)
+    g = {"mean": torch.full((N,), 1 / 261.0), "two": torch.where(torch.arange(N) % 2 == 0, 1 / 261.0, 0.7 / 261.0),
+         "random": c["g"]}[kind]
+    c["g"], d["g"] = g, g.to(dev)
+    announce("vocab common rounding", kind)
+    _, lse = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"])
+    dh, dW = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"])
+    wh, _, wW, _ = grad_reference(c)
+    z, _, l64, _, _, _, ok, at = reference(c)
+    h, W = c["h"].double(), c["W"].double()
+    p = torch.where(ok, c["g"].double() * (z[torch.arange(N), at] - l64).exp(), torch.zeros(N, dtype=torch.float64))
+    alike = {"dh": p * (W[at] * wh).sum(1).abs(), "dW": p * (h * wW[at]).sum(1).abs()}
+    for got, want, name in ((dh, wh, "dh"), (dW, wW, "dW")):
+        err = got.double().cpu() - want
+        along = ((err * want).sum() / (want * want).sum()).item()
+        assert abs(along) <= 2.0 ** -12 + (alike[name].sum() / (want * want).sum()).item(), (name, along)
+    if kind == "two":                                       # each half by itself
+        for half in (0, 1):
+            err, want = (dh.double().cpu() - wh)[half::2], wh[half::2]
+            room = 2.0 ** -12 + (alike["dh"][half::2].sum() / (want * want).sum()).item()
+            assert abs(((err * want).sum() / (want * want).sum()).item()) <= room, half
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_weights_of_every_kind(dt):
+    """g of both signs, zero, tiny and huge (zero in the first token), against the formula."""
+    dev = device()
+    N, V, K = 40, 500, 128
+    c, d = make(N, V, K, dt, 17, dev, ignored=0.1)
+    g = torch.randn(N, generator=torch.Generator().manual_seed(4)) * 10.0 ** torch.linspace(-6, 6, N)
+    g[0] = 0.0
+    c["g"], d["g"] = g, g.to(dev)
+    announce("vocab weights", dt)
+    _, lse = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"])
+    dh, dW = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"])
+    wh, bh, wW, bW = grad_reference(c)
+    close(dh, wh, bh, "dh")
+    close(dW, wW, bW, "dW")
+    d["h"][0] = float("nan")                                # g = 0: adds nothing
+    dh2, _ = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"], want_dW=False)
+    assert torch.equal(dh2, dh)
 
 
 def test_no_token_counts():

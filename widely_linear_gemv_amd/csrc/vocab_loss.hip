@@ -8,10 +8,16 @@
 //   logits   A = W, B = h: each tile is reduced on chip to a (maximum, sum of exponentials) pair
 //            per token, and the target's logit is picked out; no logit is stored.
 //   p        the same product again for a piece of the vocabulary: p [token][v] is rounded to the
-//            inputs' dtype and stored.  For bf16 inputs this rounding (2^-8 of each p) adds about as
-//            much to dh and dW as their own final rounding to bf16.
+//            inputs' dtype and stored.
 //   dh       A = W^T, B = p: fp32 sums over the pieces, rounded once at the end.
 //   dW       A = h^T, B = p^T: rows of the piece, rounded once.
+// For bf16 inputs the rounding of p (2^-8) must not be the same for all of a token's or of a batch's
+// entries, as it would be for the entries -g_i of the targets, which dominate both results: they would
+// be off by up to 2^-8 together.  So g_i is taken apart as G m_i s_i with G the first token's |g|, s_i a
+// power of two with g_i's sign and 1 <= m_i < 2: p is stored as s_i (softmax - [target]), whose rounding
+// depends on the softmax alone; dh_i is scaled by G m_i and dW by G in fp32; and dW's other operand is
+// m_i h_i (h itself where all g are equal, as for a mean).  Then the roundings of p, and of m_i h_i, are
+// independent from value to value and add about as much to dh and dW as their own final rounding.
 // Transposed operands are read from the matrix as it lies in memory: rows of the contraction are
 // copied into LDS and transposed on the way into registers, so no transposed copy is made.
 // Sums are fp32; a C tile has the A rows in its accumulator rows, so a lane holds four consecutive
@@ -31,15 +37,8 @@ enum { kLoss = 0, kGrad = 1, kHidden = 2, kWeight = 3 };
 // accumulation registers: left to itself the compiler moves the 256 of a 128 x 128 wave tile about,
 // which cost a third of the time.  (Consecutive calls use different accumulators, and settle()
 // separates the last one from whatever reads them.)
-template <typename T>
 __device__ __forceinline__ void mma(v4f& acc, const v4u& a, const v4u& b) {
-  if constexpr (sizeof(T) == 2) {
-    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      asm volatile("v_mfma_f32_16x16x4_f32 %0, %1, %2, %0" : "+a"(acc) : "v"(a[e]), "v"(b[e]));
-  }
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
 __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
@@ -61,7 +60,9 @@ struct VocabTile {
   const void* b;
   const int64_t* target;        // [N]
   const float* lse;             // [N] (kGrad)
-  const float* g;               // [N] (kGrad)
+  const float* g;               // [N] factor of p (kGrad)
+  const float* row_scale;       // [N] factor of dh's rows, or null (kHidden)
+  const float* all_scale;       // [1] factor of dW, or null (kWeight)
   float2* part;                 // [row tile of A][N] (kLoss)
   float* tlogit;                // [N] (kLoss)
   void* p;                      // [N][ldp] (kGrad)
@@ -73,6 +74,137 @@ struct VocabTile {
   int tiles_a, tiles_b;
   int splits;                   // of the contraction (kHidden; 1 otherwise)
 };
+
+// What happens to a finished tile (above).
+template <typename T, int BM, int BN, int WA, int WB, int FA, int FB, int EPI>
+__device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], uint8_t* s_buf, int64_t a0, int64_t b0,
+                                       int ta, int split) {
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int c = lane & 15, g = lane >> 4;
+  const int wa = wave / WB, wb = wave % WB;
+  const int64_t va = a0 + wa * FA * 16 + 4 * g;            // this lane's first A row
+  const int64_t nb = b0 + wb * FB * 16 + c;                // its first B row
+  if constexpr (EPI == kLoss) {
+    // The pairs of the tile's waves take over the operand buffers.  (They are not an array of their own:
+    // with two arrays in LDS the compiler no longer knows that an operand read cannot meet a copy in
+    // flight and waits for every copy before every read, which doubled the time.)
+    __syncthreads();                                       // every wave's copies have landed
+    float2(*s_red)[BN] = reinterpret_cast<float2(*)[BN]>(s_buf);
+    static_assert(WA * BN * sizeof(float2) <= (BM + BN) * 128, "the pairs fit");
+    const bool whole = a0 + BM <= t.V;                     // no row past the vocabulary
+#pragma unroll
+    for (int j = 0; j < FB; ++j) {
+      const int64_t tok = nb + 16 * j;
+      const int64_t tgt = tok < t.N ? t.target[tok] : -1;
+      // this lane has the target's logit if it lies 16 i + e past the lane's first row
+      const int d = tgt >= va && tgt < va + FA * 16 && tgt < t.V ? (int)(tgt - va) : 4;
+      float top = -INFINITY, mine = 0.f;
+#pragma unroll
+      for (int i = 0; i < FA; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (!whole && va + 16 * i + e >= t.V) acc[i][j][e] = -INFINITY;
+          top = fmaxf(top, acc[i][j][e]);
+        }
+      if (__ballot((d & 12) == 0)) {
+#pragma unroll
+        for (int i = 0; i < FA; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (d == 16 * i + e) mine = acc[i][j][e];
+        if ((d & 12) == 0) t.tlogit[tok] = mine;
+      }
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      float sum = 0.f;
+      if (__ballot(!(fabsf(top) < INFINITY))) {            // an infinity: exp_off's cases
+#pragma unroll
+        for (int i = 0; i < FA; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (va + 16 * i + e < t.V) sum += exp_off(acc[i][j][e], top);
+      } else {
+#pragma unroll
+        for (int i = 0; i < FA; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum += fast_exp(acc[i][j][e] - top);
+      }
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      if (g == 0) s_red[wa][(wb * FB + j) * 16 + c] = make_float2(top, sum);
+    }
+    __syncthreads();
+    for (int k = tid; k < BN; k += 64 * WA * WB) {
+      if (b0 + k >= t.N) continue;
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < WA; ++w) top = fmaxf(top, s_red[w][k].x);
+#pragma unroll
+      for (int w = 0; w < WA; ++w) sum += s_red[w][k].y * exp_off(s_red[w][k].x, top);
+      t.part[(int64_t)ta * t.N + b0 + k] = make_float2(top, sum);
+    }
+  } else if constexpr (EPI == kGrad) {
+    T* __restrict__ p = static_cast<T*>(t.p);
+#pragma unroll
+    for (int j = 0; j < FB; ++j) {
+      const int64_t tok = nb + 16 * j;
+      if (tok >= t.N) continue;
+      const int64_t tgt = t.target[tok];
+      const float gi = tgt >= 0 && tgt < t.V ? t.g[tok] : 0.f;
+      const bool live = gi != 0.f;                         // other tokens give 0 whatever their logits are
+      const float lse = live ? t.lse[tok] : 0.f;
+      const int64_t away = tgt - t.v0 - va;                // the target lies this far past the lane's first row
+      const int d = live && away >= 0 && away < FA * 16 ? (int)away : -1;
+#pragma unroll
+      for (int i = 0; i < FA; ++i) {
+        const int64_t r = va + 16 * i;                     // row within the piece
+        if (r >= t.ldp) continue;
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float soft = sizeof(T) == 2 ? fast_exp(acc[i][j][e] - lse) : expf(acc[i][j][e] - lse);
+          x[e] = live && r + e < t.rows_a ? gi * (soft - (d == 16 * i + e ? 1.f : 0.f)) : 0.f;
+        }
+        if constexpr (sizeof(T) == 2)
+          *reinterpret_cast<uint2*>(p + tok * t.ldp + r) =
+              make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        else
+          *reinterpret_cast<v4f*>(p + tok * t.ldp + r) = v4f{x[0], x[1], x[2], x[3]};
+      }
+    }
+  } else {
+    T* __restrict__ out = static_cast<T*>(t.out);
+    const float all = EPI == kWeight && t.all_scale ? *t.all_scale : 1.f;
+#pragma unroll
+    for (int j = 0; j < FB; ++j) {
+      const int64_t rowb = nb + 16 * j;
+      if (rowb >= t.rows_b) continue;
+      const float scale = EPI == kHidden && t.row_scale ? t.row_scale[rowb] : all;
+#pragma unroll
+      for (int i = 0; i < FA; ++i) {
+        const int64_t col = va + 16 * i;
+        if (col >= t.rows_a) continue;                     // rows_a is a multiple of 64
+        const int64_t at = rowb * t.rows_a + col;
+        v4f v = acc[i][j];
+        if constexpr (EPI == kHidden) {
+          float* sum = t.acc + (int64_t)split * t.rows_b * t.rows_a + at;
+          if (!t.first) v += *reinterpret_cast<const v4f*>(sum);
+          if (!t.last || t.splits > 1) {
+            *reinterpret_cast<v4f*>(sum) = v;
+            continue;
+          }
+        }
+        v *= scale;
+        if constexpr (sizeof(T) == 2)
+          *reinterpret_cast<uint2*>(out + at) =
+              make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        else
+          *reinterpret_cast<v4f*>(out + at) = v;
+      }
+    }
+  }
+}
 
 // Workgroup: a BM x BN tile of C, WA x WB waves, each BM/WA x BN/WB.  The contraction runs in steps of
 // 128 bytes (64 bf16, 32 fp32) of every row -- whole cache lines: 64-byte pieces halved the L2's
@@ -175,7 +307,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
           if (h == 1) copy(rs_a, rs_b, after, s & 1, i * kMine / FA, (i + 1) * kMine / FA);
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int j = 0; j < FB; ++j) mma<T>(acc[i][j], fa[h][i], fb[h][j]);
+          for (int j = 0; j < FB; ++j) mma(acc[i][j], fa[h][i], fb[h][j]);
           __builtin_amdgcn_sched_barrier(0);
         }
         if (h == 0) {
@@ -195,123 +327,178 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
       for (int j = 0; j < FB; ++j) asm volatile("" : "+a"(acc[i][j]));   // read only after settle()
   }
 
-  const int64_t va = a0 + wa * FA * 16 + 4 * g;            // this lane's first A row
-  const int64_t nb = b0 + wb * FB * 16 + c;                // its first B row
-  if constexpr (EPI == kLoss) {
-    // The pairs of the tile's waves take over the operand buffers.  (They are not an array of their own:
-    // with two arrays in LDS the compiler no longer knows that an operand read cannot meet a copy in
-    // flight and waits for every copy before every read, which doubled the time.)
-    __syncthreads();                                       // every wave's copies have landed
-    float2(*s_red)[BN] = reinterpret_cast<float2(*)[BN]>(s_buf);
-    static_assert(WA * BN * sizeof(float2) <= sizeof(s_buf), "the pairs fit");
-    const bool whole = a0 + BM <= t.V;                     // no row past the vocabulary
-#pragma unroll
-    for (int j = 0; j < FB; ++j) {
-      const int64_t tok = nb + 16 * j;
-      const int64_t tgt = tok < t.N ? t.target[tok] : -1;
-      // this lane has the target's logit if it lies 16 i + e past the lane's first row
-      const int d = tgt >= va && tgt < va + FA * 16 && tgt < t.V ? (int)(tgt - va) : 4;
-      float top = -INFINITY, mine = 0.f;
-#pragma unroll
-      for (int i = 0; i < FA; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (!whole && va + 16 * i + e >= t.V) acc[i][j][e] = -INFINITY;
-          top = fmaxf(top, acc[i][j][e]);
-        }
-      if (__ballot((d & 12) == 0)) {
-#pragma unroll
-        for (int i = 0; i < FA; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (d == 16 * i + e) mine = acc[i][j][e];
-        if ((d & 12) == 0) t.tlogit[tok] = mine;
-      }
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      float sum = 0.f;
-      if (__ballot(!(fabsf(top) < INFINITY))) {            // an infinity: exp_off's cases
-#pragma unroll
-        for (int i = 0; i < FA; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (va + 16 * i + e < t.V) sum += exp_off(acc[i][j][e], top);
-      } else {
-#pragma unroll
-        for (int i = 0; i < FA; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum += fast_exp(acc[i][j][e] - top);
-      }
-      sum += __shfl_xor(sum, 16);
-      sum += __shfl_xor(sum, 32);
-      if (g == 0) s_red[wa][(wb * FB + j) * 16 + c] = make_float2(top, sum);
+  finish<T, BM, BN, WA, WB, FA, FB, EPI>(t, acc, s_buf, a0, b0, ta, split);
+}
+
+// The same product for fp32 operands, on the bf16 matrix instructions: every value is cut into three bf16
+// parts of 8 bits each (x = x1 + x2 + x3 exactly: each part is the leading half of what is left), and of
+// the nine products of two values' parts the six largest are summed; the other three are under 2^-23 of
+// |a b| together, within the rounding of the fp32 sums.  Six bf16 products take 96 cycles of a SIMD for
+// 16 x 16 x 32, the fp32 instructions 256.
+//
+// Workgroup and waves as k_nt.  Steps of 32 along the contraction: while step s is multiplied from one of
+// two LDS buffers, each thread cuts its 16-byte pieces of step s + 1 and writes the three parts to the
+// other, and loads those of step s + 3 into the registers that this frees (a whole step ahead of their
+// use); one barrier a step.
+//   Plain operand: a part's row R is 64 bytes, its 16-byte segment sg in place sg ^ (R / 2 % 4).
+//   Transposed: rows of the contraction as in Side<bf16, ROWS, true>.
+template <int ROWS, bool TRANS, int THREADS>
+struct SplitSide {
+  static constexpr int kPart = ROWS * 64;                 // bytes of one part of a step
+  static constexpr int kPieces = ROWS * 8 / THREADS;      // 16-byte pieces of a thread
+  static_assert(ROWS * 8 % THREADS == 0, "whole pieces per thread");
+  using Bf = Side<uint16_t, ROWS, true>;
+  __device__ static uint32_t source(int i, int tid, int64_t ld) {
+    const int u = i * THREADS + tid;
+    if constexpr (TRANS) return (uint32_t)((u / (ROWS / 4)) * ld * 4) + (u % (ROWS / 4)) * 16;
+    else return (uint32_t)((u / 8) * ld * 4) + (u % 8) * 16;
+  }
+  __device__ static int place(int i, int tid) {
+    const int u = i * THREADS + tid;
+    if constexpr (TRANS) {
+      const int k = u / (ROWS / 4), q = u % (ROWS / 4);
+      return k * ROWS * 2 + ((q >> 2) ^ Bf::f(k)) * 32 + (q & 3) * 8;
+    } else {
+      const int R = u / 8, q = u % 8;
+      return R * 64 + ((q >> 1) ^ ((R >> 1) & 3)) * 16 + (q & 1) * 8;
     }
-    __syncthreads();
-    for (int k = tid; k < BN; k += 64 * kWaves) {
-      if (b0 + k >= t.N) continue;
-      float top = -INFINITY, sum = 0.f;
+  }
+  __device__ static __forceinline__ v4u read(const uint8_t* part, int frag, int c, int g) {
+    if constexpr (TRANS) return Bf::read(part, frag, 0, c, g);
+    else return *reinterpret_cast<const v4u*>(part + (frag * 16 + c) * 64 + ((g ^ ((c >> 1) & 3)) * 16));
+  }
+};
+
+// Four fp32 values cut into parts, two bf16 to a word: out[p] holds part p.  (Of an infinity NaN is left,
+// so that its products are NaN.)
+__device__ __forceinline__ void cut(const v4u& x, v2u (&out)[3]) {
+  float f[4];
 #pragma unroll
-      for (int w = 0; w < WA; ++w) top = fmaxf(top, s_red[w][k].x);
+  for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(x[e]);
 #pragma unroll
-      for (int w = 0; w < WA; ++w) sum += s_red[w][k].y * exp_off(s_red[w][k].x, top);
-      t.part[(int64_t)ta * t.N + b0 + k] = make_float2(top, sum);
+  for (int p = 0; p < 3; ++p) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t a = __float_as_uint(f[2 * h]), b = __float_as_uint(f[2 * h + 1]);
+      out[p][h] = __builtin_amdgcn_perm(b, a, 0x07060302u);    // the leading halves
     }
-  } else if constexpr (EPI == kGrad) {
-    T* __restrict__ p = static_cast<T*>(t.p);
+    if (p < 2) {
 #pragma unroll
-    for (int j = 0; j < FB; ++j) {
-      const int64_t tok = nb + 16 * j;
-      if (tok >= t.N) continue;
-      const int64_t tgt = t.target[tok];
-      const bool live = tgt >= 0 && tgt < t.V;
-      const float lse = live ? t.lse[tok] : 0.f, gi = live ? t.g[tok] : 0.f;
-      const int64_t away = tgt - t.v0 - va;                // the target lies this far past the lane's first row
-      const int d = live && away >= 0 && away < FA * 16 ? (int)away : -1;
-#pragma unroll
-      for (int i = 0; i < FA; ++i) {
-        const int64_t r = va + 16 * i;                     // row within the piece
-        if (r >= t.ldp) continue;
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float soft = sizeof(T) == 2 ? fast_exp(acc[i][j][e] - lse) : expf(acc[i][j][e] - lse);
-          x[e] = live && r + e < t.rows_a ? gi * (soft - (d == 16 * i + e ? 1.f : 0.f)) : 0.f;
-        }
-        if constexpr (sizeof(T) == 2)
-          *reinterpret_cast<uint2*>(p + tok * t.ldp + r) =
-              make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-        else
-          *reinterpret_cast<v4f*>(p + tok * t.ldp + r) = v4f{x[0], x[1], x[2], x[3]};
-      }
-    }
-  } else {
-    T* __restrict__ out = static_cast<T*>(t.out);
-#pragma unroll
-    for (int j = 0; j < FB; ++j) {
-      const int64_t rowb = nb + 16 * j;
-      if (rowb >= t.rows_b) continue;
-#pragma unroll
-      for (int i = 0; i < FA; ++i) {
-        const int64_t col = va + 16 * i;
-        if (col >= t.rows_a) continue;                     // rows_a is a multiple of 64
-        const int64_t at = rowb * t.rows_a + col;
-        v4f v = acc[i][j];
-        if constexpr (EPI == kHidden) {
-          float* sum = t.acc + (int64_t)split * t.rows_b * t.rows_a + at;
-          if (!t.first) v += *reinterpret_cast<const v4f*>(sum);
-          if (!t.last || t.splits > 1) {
-            *reinterpret_cast<v4f*>(sum) = v;
-            continue;
-          }
-        }
-        if constexpr (sizeof(T) == 2)
-          *reinterpret_cast<uint2*>(out + at) =
-              make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-        else
-          *reinterpret_cast<v4f*>(out + at) = v;
+      for (int e = 0; e < 4; ++e) {
+        f[e] -= __uint_as_float(__float_as_uint(f[e]) & 0xFFFF0000u);
       }
     }
   }
+}
+
+template <int BM, int BN, int WA, int WB, int EPI>
+__global__ __launch_bounds__(64 * WA * WB, 1) void k_nt_split(VocabTile t) {
+  constexpr int kThreads = 64 * WA * WB;
+  constexpr int FA = BM / WA / 16, FB = BN / WB / 16;
+  constexpr bool kTransA = EPI == kHidden || EPI == kWeight, kTransB = EPI == kWeight;
+  using SideA = SplitSide<BM, kTransA, kThreads>;
+  using SideB = SplitSide<BN, kTransB, kThreads>;
+  constexpr int kStep = 3 * (BM + BN) * 64;
+  constexpr int PA = SideA::kPieces, PB = SideB::kPieces;
+  __shared__ __align__(16) uint8_t s_buf[2 * kStep];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int c = lane & 15, g = lane >> 4;
+  const int wa = wave / WB, wb = wave % WB;
+  const int split = blockIdx.y;
+  const int per_xcd = (t.tiles_a * t.tiles_b + 7) / 8;    // as k_nt
+  const int tile = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per_xcd || tile >= t.tiles_a * t.tiles_b) return;
+  const int ta = tile / t.tiles_b, tb = tile % t.tiles_b;
+  const int64_t a0 = (int64_t)ta * BM, b0 = (int64_t)tb * BN;
+  const int all_steps = (int)((t.k + 31) / 32);
+  const int per_split = (all_steps + t.splits - 1) / t.splits;
+  const int step0 = split * per_split, steps = min(per_split, all_steps - step0);
+  auto part = [&](const void* m, int64_t row0, int64_t rows, int64_t ld, bool trans, int step) {
+    const float* p = static_cast<const float*>(m);
+    const int64_t from = trans ? (int64_t)step * 32 : row0, all = trans ? t.k : rows;
+    return range_rsrc(p + from * ld, max(all - from, (int64_t)0) * ld * 4);
+  };
+  uint32_t off_a[PA], off_b[PB];
+#pragma unroll
+  for (int i = 0; i < PA; ++i) off_a[i] = SideA::source(i, tid, t.lda) + (kTransA ? (uint32_t)(a0 * 4) : 0);
+#pragma unroll
+  for (int i = 0; i < PB; ++i) off_b[i] = SideB::source(i, tid, t.ldb) + (kTransB ? (uint32_t)(b0 * 4) : 0);
+  v4u raw_a[2][PA], raw_b[2][PB];
+  auto load = [&](int step, v4u (&to_a)[PA], v4u (&to_b)[PB]) {
+    step = step0 + min(step, steps - 1);
+    const __amdgpu_buffer_rsrc_t rs_a = part(t.a, a0, t.rows_a, t.lda, kTransA, step);
+    const __amdgpu_buffer_rsrc_t rs_b = part(t.b, b0, t.rows_b, t.ldb, kTransB, step);
+    const int ka = kTransA ? 0 : step * 128, kb = kTransB ? 0 : step * 128;
+#pragma unroll
+    for (int i = 0; i < PA; ++i) to_a[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rs_a, off_a[i], ka, 0));
+#pragma unroll
+    for (int i = 0; i < PB; ++i) to_b[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rs_b, off_b[i], kb, 0));
+  };
+  auto store = [&](int buf, const v4u (&from_a)[PA], const v4u (&from_b)[PB], int i) {   // piece i of A, or i - PA of B
+    uint8_t* base = s_buf + buf * kStep;
+    v2u o[3];
+    if (i < PA) {
+      cut(from_a[i < PA ? i : 0], o);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) *reinterpret_cast<v2u*>(base + p * SideA::kPart + SideA::place(i, tid)) = o[p];
+    } else {
+      cut(from_b[i < PA ? 0 : i - PA], o);
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        *reinterpret_cast<v2u*>(base + 3 * SideA::kPart + p * SideB::kPart + SideB::place(i - PA, tid)) = o[p];
+    }
+  };
+  v4f acc[FA][FB];
+#pragma unroll
+  for (int i = 0; i < FA; ++i)
+#pragma unroll
+    for (int j = 0; j < FB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  if (steps > 0) {
+    load(0, raw_a[0], raw_b[0]);
+    load(1, raw_a[1], raw_b[1]);
+#pragma unroll
+    for (int i = 0; i < PA + PB; ++i) store(0, raw_a[0], raw_b[0], i);
+    load(2, raw_a[0], raw_b[0]);
+    __syncthreads();
+    for (int s0 = 0; s0 < steps; s0 += 2) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int s = s0 + h;
+        if (s >= steps) break;
+        const uint8_t* from = s_buf + h * kStep;
+        v4u fa[3][FA], fb[3][FB];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+#pragma unroll
+          for (int i = 0; i < FA; ++i) fa[p][i] = SideA::read(from + p * SideA::kPart, wa * FA + i, c, g);
+#pragma unroll
+          for (int j = 0; j < FB; ++j) fb[p][j] = SideB::read(from + 3 * SideA::kPart + p * SideB::kPart, wb * FB + j, c, g);
+        }
+        // the six products, smallest parts first; the next step's pieces are cut between them
+        constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+        for (int q = 0; q < 6; ++q) {
+#pragma unroll
+          for (int i = 0; i < FA; ++i)
+#pragma unroll
+            for (int j = 0; j < FB; ++j) mma(acc[i][j], fa[kA[q]][i], fb[kB[q]][j]);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int i = q * (PA + PB) / 6; i < (q + 1) * (PA + PB) / 6; ++i) store(h ^ 1, raw_a[h ^ 1], raw_b[h ^ 1], i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        load(s + 3, raw_a[h ^ 1], raw_b[h ^ 1]);
+        __syncthreads();
+      }
+    }
+    settle();
+#pragma unroll
+    for (int i = 0; i < FA; ++i)
+#pragma unroll
+      for (int j = 0; j < FB; ++j) asm volatile("" : "+a"(acc[i][j]));   // read only after settle()
+  }
+  finish<float, BM, BN, WA, WB, FA, FB, EPI>(t, acc, s_buf, a0, b0, ta, split);
 }
 
 // Joins the tiles' pairs in order (one wave per token) into lse, and the loss from the target's logit.
@@ -339,16 +526,68 @@ __global__ __launch_bounds__(256) void k_loss_join(const float2* __restrict__ pa
   }
 }
 
-// out = the sum of the splits' running sums, in order, rounded once.
+// out = the sum of the splits' running sums, in order, times the row's factor (if any), rounded once.
 template <typename T>
-__global__ __launch_bounds__(256) void k_hidden_join(const float* __restrict__ acc, T* __restrict__ out, int64_t n,
-                                                     int splits) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;       // n is a multiple of 64
+__global__ __launch_bounds__(256) void k_hidden_join(const float* __restrict__ acc, const float* __restrict__ row_scale,
+                                                     T* __restrict__ out, int64_t n, int64_t K, int splits) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;       // n and K are multiples of 64
   if (i >= n) return;
   v4f v = *reinterpret_cast<const v4f*>(acc + i);
   for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const v4f*>(acc + s * n + i);
+  if (row_scale) v *= row_scale[i / K];
 #pragma unroll
   for (int e = 0; e < 4; ++e) store_out(out, i + e, v[e]);
+}
+
+// The parts of g (above), one wave per token: s_i (0 for tokens that do not count or have g = 0), G m_i,
+// and m_i h_i where `scaled` is given.  G is |g| of the first token that counts and has a finite g other
+// than 0 (1 if none has); every wave finds it for itself, 64 tokens at a time.  A g that is not finite
+// is its own s_i, so that it reaches its outputs.
+__global__ __launch_bounds__(256) void k_grad_scales(const float* __restrict__ g, const int64_t* __restrict__ target,
+                                                     int64_t N, int64_t V, const uint16_t* __restrict__ h, int64_t K,
+                                                     float* __restrict__ s, float* __restrict__ row, float* __restrict__ all,
+                                                     uint16_t* __restrict__ scaled) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
+  if (i >= N) return;
+  float G = 1.f;
+  for (int64_t t0 = 0; t0 < N; t0 += kWave) {
+    const int64_t t = min(t0 + lane, N - 1);
+    const float v = fabsf(g[t]);
+    const uint64_t good = __ballot(target[t] >= 0 && target[t] < V && v > 0.f && v < INFINITY);
+    if (good) {
+      G = __shfl(v, __builtin_ctzll(good));
+      break;
+    }
+  }
+  const float gi = g[i], ratio = fabsf(gi) / G;
+  const bool live = target[i] >= 0 && target[i] < V && gi != 0.f;
+  float si = 0.f, m = 1.f;
+  if (live) {
+    if (ratio >= 0x1p-100f && ratio < 0x1p100f) {
+      const uint32_t top = __float_as_uint(ratio) & 0x7F800000u;           // 2^floor(log2(ratio))
+      m = ratio / __uint_as_float(top);
+      si = copysignf(__uint_as_float(top), gi);
+    } else {
+      si = gi / G;                                                         // extreme or not finite: as it is
+    }
+  }
+  if (lane == 0) {
+    s[i] = si;
+    row[i] = G * m;
+    if (i == 0) *all = G;
+  }
+  if (scaled) {
+    const uint16_t* __restrict__ from = h + i * K;
+    uint16_t* __restrict__ to = scaled + i * K;
+    for (int64_t k = lane * 8; k < K; k += kWave * 8) {
+      uint4 w = *reinterpret_cast<const uint4*>(from + k);
+      uint32_t* e = &w.x;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] = pack_bf16(m * bf16_lo(e[j]), m * bf16_hi(e[j]));
+      *reinterpret_cast<uint4*>(to + k) = w;
+    }
+  }
 }
 
 namespace {
@@ -357,33 +596,38 @@ constexpr int kCUs = 256;
 constexpr int64_t kPieceRows = 8192;         // vocabulary entries per piece of the gradient, less where N
                                              // tokens of it would be over 2^27 values
 
-// Tile shapes, largest first, with the time of a tile of each per element of C relative to the first:
-// smaller tiles read LDS (and the L2) more often for the same products.
+// Tile shapes, largest first, with the time of a tile of each per element of C relative to the first that
+// the type has (2048 x 32000 x 4096, every shape in turn).  Smaller tiles read LDS and the L2 more often
+// for the same products, but fill the device where there are few.
 struct TileShape {
   int a, b;
-  float cost;
+  float bf16, fp32;
 };
-constexpr TileShape kTiles[] = {{256, 256, 1.f}, {256, 128, 1.25f}, {128, 128, 1.5f}, {128, 64, 2.f}};
+constexpr TileShape kTiles[] = {{256, 256, 1.f, 0.f}, {256, 128, 1.15f, 1.f}, {128, 128, 1.3f, 1.1f}, {128, 64, 1.7f, 1.25f}};
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 int64_t up64(int64_t v) { return (v + 63) / 64 * 64; }
 int tiles(int64_t rows, int tile) { return (int)((rows + tile - 1) / tile); }
 
 // Shape and splits of the contraction with the least rounds of workgroups over the device: cover_a x
-// cover_b elements of C, and splits up to `most` (each worth at least 16 steps, and costing a pass over
-// its sums that weighs like two).
+// cover_b elements of C, and splits up to `most`, each worth at least 16 steps.  What follows a tile's
+// steps is counted in steps: 2 for an epilogue, 28 where the tile's fp32 sums are read and written
+// (`sums`: a later piece adds to them, or splits are joined afterwards; 0.5 MB for a 256 x 256 tile at a
+// CU's share of HBM).
 struct NtPlan {
   int shape, splits;
 };
-NtPlan nt_plan(int64_t cover_a, int64_t cover_b, int64_t steps, int most) {
-  NtPlan best{0, 1};
+NtPlan nt_plan(int64_t cover_a, int64_t cover_b, int64_t steps, int elem, int most, bool sums) {
+  const int first = elem == 2 ? 0 : 1;                     // three parts of a 256 x 256 step are over LDS
+  NtPlan best{first, 1};
   double least = 0;
-  for (int k = 0; k < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++k)
+  for (int k = first; k < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++k)
     for (int s = 1; s <= most && (s == 1 || steps / s >= 16); ++s) {
       const int64_t wgs = (int64_t)tiles(cover_a, kTiles[k].a) * tiles(cover_b, kTiles[k].b) * s;
       const double rounds = (double)((wgs + kCUs - 1) / kCUs);
-      const double cost = rounds * kTiles[k].a * kTiles[k].b * kTiles[k].cost * ((double)steps / s + (s > 1 ? 4 : 2));
-      if ((k == 0 && s == 1) || cost < least) {
+      const double tile = kTiles[k].a * kTiles[k].b * (elem == 2 ? kTiles[k].bf16 : kTiles[k].fp32);
+      const double cost = rounds * tile * ((double)steps / s + (sums ? 28 : s > 1 ? 14 : 2));
+      if ((k == first && s == 1) || cost < least) {
         least = cost;
         best = NtPlan{k, s};
       }
@@ -397,11 +641,19 @@ void launch_nt(VocabTile& t, const NtPlan& plan, int64_t cover_a, int64_t cover_
   t.tiles_b = tiles(cover_b, kTiles[plan.shape].b);
   t.splits = plan.splits;
   const dim3 grid((t.tiles_a * t.tiles_b + 7) / 8 * 8, plan.splits);
-  switch (plan.shape) {
-    case 0: hipLaunchKernelGGL((k_nt<T, 256, 256, 2, 4, EPI>), grid, dim3(512), 0, s, t); break;
-    case 1: hipLaunchKernelGGL((k_nt<T, 256, 128, 4, 2, EPI>), grid, dim3(512), 0, s, t); break;
-    case 2: hipLaunchKernelGGL((k_nt<T, 128, 128, 2, 2, EPI>), grid, dim3(256), 0, s, t); break;
-    default: hipLaunchKernelGGL((k_nt<T, 128, 64, 2, 2, EPI>), grid, dim3(256), 0, s, t); break;
+  if constexpr (sizeof(T) == 2) {
+    switch (plan.shape) {
+      case 0: hipLaunchKernelGGL((k_nt<T, 256, 256, 2, 4, EPI>), grid, dim3(512), 0, s, t); break;
+      case 1: hipLaunchKernelGGL((k_nt<T, 256, 128, 4, 2, EPI>), grid, dim3(512), 0, s, t); break;
+      case 2: hipLaunchKernelGGL((k_nt<T, 128, 128, 2, 2, EPI>), grid, dim3(256), 0, s, t); break;
+      default: hipLaunchKernelGGL((k_nt<T, 128, 64, 2, 2, EPI>), grid, dim3(256), 0, s, t); break;
+    }
+  } else {
+    switch (plan.shape) {
+      case 1: hipLaunchKernelGGL((k_nt_split<256, 128, 4, 2, EPI>), grid, dim3(512), 0, s, t); break;
+      case 2: hipLaunchKernelGGL((k_nt_split<128, 128, 2, 4, EPI>), grid, dim3(512), 0, s, t); break;
+      default: hipLaunchKernelGGL((k_nt_split<128, 64, 4, 2, EPI>), grid, dim3(512), 0, s, t); break;
+    }
   }
 }
 
@@ -413,7 +665,7 @@ struct LossPlan {
 };
 LossPlan loss_plan(int64_t N, int64_t V, int64_t K, int elem) {
   LossPlan p;
-  p.nt = nt_plan(V, N, steps_of(K, elem), 1);
+  p.nt = nt_plan(V, N, steps_of(K, elem), elem, 1, false);
   p.part = 0;
   p.tlogit = up256((size_t)tiles(V, kTiles[p.nt.shape].a) * N * sizeof(float2));
   p.total = p.tlogit + up256((size_t)N * 4);
@@ -424,7 +676,7 @@ struct GradPlan {
   int64_t piece;
   int pieces;
   NtPlan hidden;
-  size_t p, acc, total;
+  size_t p, acc, scales, scaled, total;
 };
 GradPlan grad_plan(int64_t N, int64_t V, int64_t K, int elem) {
   GradPlan g;
@@ -433,11 +685,13 @@ GradPlan grad_plan(int64_t N, int64_t V, int64_t K, int elem) {
   g.pieces = (int)((V + most - 1) / most);
   g.piece = ((V + g.pieces - 1) / g.pieces + 255) / 256 * 256;
   g.pieces = (int)((V + g.piece - 1) / g.piece);
-  g.hidden = nt_plan(K, N, steps_of(std::min(g.piece, V), elem), 8);
+  g.hidden = nt_plan(K, N, steps_of(std::min(g.piece, V), elem), elem, 8, g.pieces > 1);
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
   g.p = take((size_t)N * g.piece * elem);
   g.acc = take(g.pieces > 1 || g.hidden.splits > 1 ? (size_t)g.hidden.splits * N * K * 4 : 0);
+  g.scales = take(elem == 2 ? ((size_t)2 * N + 1) * 4 : 0);
+  g.scaled = take(elem == 2 ? (size_t)N * K * 2 : 0);
   g.total = at;
   return g;
 }
@@ -467,36 +721,51 @@ hipError_t grad_t(const VocabArgs& a, hipStream_t s) {
   T* p = reinterpret_cast<T*>(ws + q.p);
   float* acc = reinterpret_cast<float*>(ws + q.acc);
   const T* W = static_cast<const T*>(a.W);
+  const float* factor = a.g;
+  const float *row_scale = nullptr, *all_scale = nullptr;
+  const void* h = a.h;
+  if constexpr (sizeof(T) == 2) {
+    float* s_i = reinterpret_cast<float*>(ws + q.scales);
+    uint16_t* scaled = a.dW ? reinterpret_cast<uint16_t*>(ws + q.scaled) : nullptr;
+    hipLaunchKernelGGL(k_grad_scales, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a.g, a.target, a.N, a.V,
+                       static_cast<const uint16_t*>(a.h), a.K, s_i, s_i + a.N, s_i + 2 * a.N, scaled);
+    factor = s_i;
+    row_scale = s_i + a.N;
+    all_scale = s_i + 2 * a.N;
+    h = scaled;
+  }
   for (int k = 0; k < q.pieces; ++k) {
     const int64_t v0 = k * q.piece, rows = std::min(q.piece, a.V - v0), ldp = up64(rows);
     VocabTile t{};
     t.a = W + v0 * a.K; t.b = a.h;
     t.rows_a = rows; t.rows_b = a.N;
     t.k = t.lda = t.ldb = a.K;
-    t.target = a.target; t.lse = a.lse; t.g = a.g;
+    t.target = a.target; t.lse = a.lse; t.g = factor;
     t.p = p; t.ldp = ldp;
     t.v0 = v0; t.V = a.V; t.N = a.N;
-    launch_nt<T, kGrad>(t, nt_plan(ldp, a.N, steps_of(a.K, sizeof(T)), 1), ldp, a.N, s);
+    launch_nt<T, kGrad>(t, nt_plan(ldp, a.N, steps_of(a.K, sizeof(T)), sizeof(T), 1, false), ldp, a.N, s);
     if (a.dh) {
       VocabTile d{};
       d.a = W + v0 * a.K; d.b = p;
       d.rows_a = a.K; d.rows_b = a.N;
       d.k = rows; d.lda = a.K; d.ldb = ldp;
       d.acc = acc;
+      d.row_scale = row_scale;
       d.out = a.dh;
       d.first = k == 0; d.last = k == q.pieces - 1;
       launch_nt<T, kHidden>(d, q.hidden, a.K, a.N, s);
       if (d.last && q.hidden.splits > 1)
         hipLaunchKernelGGL((k_hidden_join<T>), dim3((unsigned)((a.N * a.K / 4 + 255) / 256)), dim3(256), 0, s, acc,
-                           static_cast<T*>(a.dh), a.N * a.K, q.hidden.splits);
+                           row_scale, static_cast<T*>(a.dh), a.N * a.K, a.K, q.hidden.splits);
     }
     if (a.dW) {
       VocabTile d{};
-      d.a = a.h; d.b = p;
+      d.a = h; d.b = p;
+      d.all_scale = all_scale;
       d.rows_a = a.K; d.rows_b = rows;
       d.k = a.N; d.lda = a.K; d.ldb = ldp;
       d.out = static_cast<T*>(a.dW) + v0 * a.K;
-      launch_nt<T, kWeight>(d, nt_plan(a.K, rows, steps_of(a.N, sizeof(T)), 1), a.K, rows, s);
+      launch_nt<T, kWeight>(d, nt_plan(a.K, rows, steps_of(a.N, sizeof(T)), sizeof(T), 1, false), a.K, rows, s);
     }
   }
   return hipGetLastError();
