@@ -72,6 +72,10 @@ CASES = [  # N, K, M, r, L, spans, ids
     (130, 1408, 130, 40, 2, [0, 65, 130], [1, 0]),
     (257, 256, 320, 128, 3, [0, 100, 101, 257], [2, 1, 0]),
     (200, 11008, 192, 64, 2, [0, 200], [1]),
+    (300, 384, 514, 16, 3, [0, 100, 101, 290], [2, 0, 1]),             # long segments and small ranks
+    (513, 256, 1006, 24, 4, [0, 37, 260, 261, 513], [1, 3, -1, 0]),
+    (1100, 128, 15104, 8, 2, [0, 600, 1100], [1, 0]),                   # two row tiles a workgroup
+    (700, 1280, 256, 48, 2, [5, 333, 700], [0, 1]),
 ]
 
 

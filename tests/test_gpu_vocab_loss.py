@@ -118,7 +118,8 @@ def test_wide_logits(dt):
 
 
 # one size for each tile shape that the gradient's and the loss's products may take, with two pieces
-LARGE = [(2048, 16384, 64), (2048, 9000, 192), (1000, 8200, 256), (600, 12000, 1024)]
+LARGE = [(2048, 16384, 64), (2048, 9000, 192), (1000, 8200, 256), (600, 12000, 1024), (2048, 2000, 4096),
+         (1024, 2000, 4096), (256, 8192, 2048), (64, 4000, 4096), (4096, 1000, 4096)]
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
