@@ -207,13 +207,14 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
 }
 
 // Workgroup: a BM x BN tile of C, WA x WB waves, each BM/WA x BN/WB.  The contraction runs in steps of
-// 128 bytes (64 bf16, 32 fp32) of every row -- whole cache lines: 64-byte pieces halved the L2's
-// throughput -- double buffered in LDS, each step multiplied in two halves.  While a half is multiplied
+// 128 bytes (64 values) of every row -- whole cache lines: 64-byte pieces halved the L2's throughput --
+// in NB buffers in LDS (two; four where one workgroup a CU streams W past few tokens and needs the bytes
+// in flight), each step multiplied in two halves.  While a half is multiplied
 // (its operands already in registers) the wave reads the next half's operands from LDS; once a step's
-// second half is in registers everywhere (the step's one barrier), the copies of the step after next
-// go straight into its buffer and have the rest of this step and half of the next one to land.  Rows
+// second half is in registers everywhere (the step's one barrier), the copies of step s + NB go straight
+// into its buffer and have NB - 1.5 steps to land.  Rows
 // past the end of a matrix read as 0; past the last step the copies repeat it, which nothing reads.
-template <typename T, int BM, int BN, int WA, int WB, int EPI>
+template <typename T, int BM, int BN, int WA, int WB, int EPI, int NB = 2>
 __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
   constexpr int kWaves = WA * WB;
   constexpr int FA = BM / WA / 16, FB = BN / WB / 16;
@@ -225,7 +226,12 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
   using SideA = Side<T, BM, (EPI == kHidden || EPI == kWeight)>;
   using SideB = Side<T, BN, EPI == kWeight>;
   constexpr bool kTransA = EPI == kHidden || EPI == kWeight, kTransB = EPI == kWeight;
-  __shared__ __align__(16) uint8_t s_buf[2 * kStep];
+  // waits until at most `steps` steps' copies of this wave are in flight (and for its LDS reads: lgkm 0)
+  constexpr auto wait = [](int steps, int lgkm) {
+    return (steps * kMine & 15) | ((steps * kMine >> 4) << 14) | 0x70 | (lgkm << 8);
+  };
+  static_assert((NB - 1) * kMine < 64 && (NB & (NB - 1)) == 0, "the copies in flight can be counted");
+  __shared__ __align__(16) uint8_t s_buf[NB * kStep];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane & 15, g = lane >> 4;
@@ -278,12 +284,12 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
   if (steps > 0) {
     v4u fa[2][FA], fb[2][FB];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < NB; ++r) {
       const int step = step0 + min(r, steps - 1);
       copy(part(t.a, a0, t.rows_a, t.lda, kTransA, step), part(t.b, b0, t.rows_b, t.ldb, kTransB, step), step, r, 0, kMine);
     }
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((kMine & 15) | ((kMine >> 4) << 14) | 0xF70);   // step 0 has landed
+    __builtin_amdgcn_s_waitcnt(wait(NB - 1, 15));          // step 0 has landed
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 #pragma unroll
@@ -294,8 +300,8 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         // FA groups of FB products; ahead of each group its share of the reads and copies
-        const uint8_t* next = s_buf + ((s + h) & 1) * kStep;
-        const int after = step0 + min(s + 2, steps - 1);
+        const uint8_t* next = s_buf + ((s + h) & (NB - 1)) * kStep;
+        const int after = step0 + min(s + NB, steps - 1);
         const __amdgpu_buffer_rsrc_t rs_a = part(t.a, a0, t.rows_a, t.lda, kTransA, after);
         const __amdgpu_buffer_rsrc_t rs_b = part(t.b, b0, t.rows_b, t.ldb, kTransB, after);
 #pragma unroll
@@ -304,7 +310,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
 #pragma unroll
           for (int j = i * FB / FA; j < (i + 1) * FB / FA; ++j)
             fb[h ^ 1][j] = SideB::read(next + BM * 128, wb * FB + j, h ^ 1, c, g);
-          if (h == 1) copy(rs_a, rs_b, after, s & 1, i * kMine / FA, (i + 1) * kMine / FA);
+          if (h == 1) copy(rs_a, rs_b, after, s & (NB - 1), i * kMine / FA, (i + 1) * kMine / FA);
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int j = 0; j < FB; ++j) mma(acc[i][j], fa[h][i], fb[h][j]);
@@ -313,7 +319,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
         if (h == 0) {
           // this wave holds the step's second half, and its copies of the next step have landed
           asm volatile("" ::: "memory");
-          __builtin_amdgcn_s_waitcnt(0x70);
+          __builtin_amdgcn_s_waitcnt(wait(NB - 2, 0));
           __builtin_amdgcn_s_barrier();
           asm volatile("" ::: "memory");
         }
@@ -338,8 +344,9 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
 //
 // Workgroup and waves as k_nt.  Steps of 32 along the contraction: while step s is multiplied from one of
 // two LDS buffers, each thread cuts its 16-byte pieces of step s + 1 and writes the three parts to the
-// other, and loads those of step s + 3 into the registers that this frees (a whole step ahead of their
-// use); one barrier a step.
+// other between the products, and then loads those of step s + 2 into the registers
+// that this frees; one barrier a step.  (A second set of registers, loaded a step earlier, spilled: dW of
+// 2048 x 32000 x 4096 3390 us against 3150.)
 //   Plain operand: a part's row R is 64 bytes, its 16-byte segment sg in place sg ^ (R / 2 % 4).
 //   Transposed: rows of the contraction as in Side<bf16, ROWS, true>.
 template <int ROWS, bool TRANS, int THREADS>
@@ -424,26 +431,26 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt_split(VocabTile t) {
   for (int i = 0; i < PA; ++i) off_a[i] = SideA::source(i, tid, t.lda) + (kTransA ? (uint32_t)(a0 * 4) : 0);
 #pragma unroll
   for (int i = 0; i < PB; ++i) off_b[i] = SideB::source(i, tid, t.ldb) + (kTransB ? (uint32_t)(b0 * 4) : 0);
-  v4u raw_a[2][PA], raw_b[2][PB];
-  auto load = [&](int step, v4u (&to_a)[PA], v4u (&to_b)[PB]) {
+  v4u raw_a[PA], raw_b[PB];
+  auto load = [&](int step) {
     step = step0 + min(step, steps - 1);
     const __amdgpu_buffer_rsrc_t rs_a = part(t.a, a0, t.rows_a, t.lda, kTransA, step);
     const __amdgpu_buffer_rsrc_t rs_b = part(t.b, b0, t.rows_b, t.ldb, kTransB, step);
     const int ka = kTransA ? 0 : step * 128, kb = kTransB ? 0 : step * 128;
 #pragma unroll
-    for (int i = 0; i < PA; ++i) to_a[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rs_a, off_a[i], ka, 0));
+    for (int i = 0; i < PA; ++i) raw_a[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rs_a, off_a[i], ka, 0));
 #pragma unroll
-    for (int i = 0; i < PB; ++i) to_b[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rs_b, off_b[i], kb, 0));
+    for (int i = 0; i < PB; ++i) raw_b[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rs_b, off_b[i], kb, 0));
   };
-  auto store = [&](int buf, const v4u (&from_a)[PA], const v4u (&from_b)[PB], int i) {   // piece i of A, or i - PA of B
+  auto store = [&](int buf, int i) {                      // piece i of A, or i - PA of B
     uint8_t* base = s_buf + buf * kStep;
     v2u o[3];
     if (i < PA) {
-      cut(from_a[i < PA ? i : 0], o);
+      cut(raw_a[i < PA ? i : 0], o);
 #pragma unroll
       for (int p = 0; p < 3; ++p) *reinterpret_cast<v2u*>(base + p * SideA::kPart + SideA::place(i, tid)) = o[p];
     } else {
-      cut(from_b[i < PA ? 0 : i - PA], o);
+      cut(raw_b[i < PA ? 0 : i - PA], o);
 #pragma unroll
       for (int p = 0; p < 3; ++p)
         *reinterpret_cast<v2u*>(base + 3 * SideA::kPart + p * SideB::kPart + SideB::place(i - PA, tid)) = o[p];
@@ -455,11 +462,10 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt_split(VocabTile t) {
 #pragma unroll
     for (int j = 0; j < FB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   if (steps > 0) {
-    load(0, raw_a[0], raw_b[0]);
-    load(1, raw_a[1], raw_b[1]);
+    load(0);
 #pragma unroll
-    for (int i = 0; i < PA + PB; ++i) store(0, raw_a[0], raw_b[0], i);
-    load(2, raw_a[0], raw_b[0]);
+    for (int i = 0; i < PA + PB; ++i) store(0, i);
+    load(1);
     __syncthreads();
     for (int s0 = 0; s0 < steps; s0 += 2) {
 #pragma unroll
@@ -485,10 +491,10 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt_split(VocabTile t) {
             for (int j = 0; j < FB; ++j) mma(acc[i][j], fa[kA[q]][i], fb[kB[q]][j]);
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int i = q * (PA + PB) / 6; i < (q + 1) * (PA + PB) / 6; ++i) store(h ^ 1, raw_a[h ^ 1], raw_b[h ^ 1], i);
+          for (int i = q * (PA + PB) / 5; i < min(q + 1, 5) * (PA + PB) / 5; ++i) store(h ^ 1, i);
+          if (q == 4) load(s + 2);
           __builtin_amdgcn_sched_barrier(0);
         }
-        load(s + 3, raw_a[h ^ 1], raw_b[h ^ 1]);
         __syncthreads();
       }
     }
@@ -646,7 +652,12 @@ void launch_nt(VocabTile& t, const NtPlan& plan, int64_t cover_a, int64_t cover_
       case 0: hipLaunchKernelGGL((k_nt<T, 256, 256, 2, 4, EPI>), grid, dim3(512), 0, s, t); break;
       case 1: hipLaunchKernelGGL((k_nt<T, 256, 128, 4, 2, EPI>), grid, dim3(512), 0, s, t); break;
       case 2: hipLaunchKernelGGL((k_nt<T, 128, 128, 2, 2, EPI>), grid, dim3(256), 0, s, t); break;
-      default: hipLaunchKernelGGL((k_nt<T, 128, 64, 2, 2, EPI>), grid, dim3(256), 0, s, t); break;
+      default:
+        if ((EPI == kLoss || EPI == kGrad) && t.tiles_a * t.tiles_b <= kCUs)
+          hipLaunchKernelGGL((k_nt<T, 128, 64, 2, 2, EPI, EPI == kLoss || EPI == kGrad ? 4 : 2>), grid, dim3(256), 0, s, t);
+        else
+          hipLaunchKernelGGL((k_nt<T, 128, 64, 2, 2, EPI>), grid, dim3(256), 0, s, t);
+        break;
     }
   } else {
     switch (plan.shape) {
