@@ -314,6 +314,7 @@ __global__ __launch_bounds__(64 * kReduceWaves, 1) void k_reduce_ring(LoraReduce
       for (int w = 0; w < kReduceWaves; ++w) v += s_part[w][row - t0][k];
       it.part[((int64_t)chunk * N + row) * rp + k] = k < r ? v : 0.f;
     }
+    __builtin_amdgcn_s_waitcnt(0);                         // only copies are counted from here on
     __syncthreads();
   }
 }
