@@ -394,7 +394,8 @@ typedef struct {
 
 /* fairy2i_lora for `count` projections that read the same x (q, k and v; gate and up) and share N,
  * m, L, r, the segments and the dtypes, eight to a launch.  items is a HOST array, read during the
- * call only.  workspace: fairy2i_lora_workspace_bytes with the same count. */
+ * call only; no item's y overlaps x or another item's y or base (two sets of adapters on one output are
+ * two calls).  workspace: fairy2i_lora_workspace_bytes with the same count. */
 int fairy2i_lora_grouped(const fairy2i_lora_item* items, int count, const void* x, int x_dtype, int64_t N, int64_t m,
                          int64_t L, int r, const int32_t* seg_start, const int32_t* seg_adapter, int64_t S, int y_dtype,
                          void* workspace, size_t workspace_bytes, hipStream_t stream);
@@ -404,10 +405,11 @@ int fairy2i_lora_grouped(const fairy2i_lora_item* items, int count, const void* 
  *     dA_a = sum_i dh_i x_i^T        dB_a = sum_i alpha_a dy_i (A_a x_i)^T     (rows i of adapter a)
  *   dy           [N][2n], x's dtype.
  *   dx_base, dx  [N][2m], dx_dtype FAIRY2I_F32 or FAIRY2I_BF16: dx_base is the gradient through
- *                the shared projection and dx may be dx_base; both NULL: dx is not computed.  Rows
- *                without an adapter are not written.
+ *                the shared projection and dx may be dx_base (but overlaps neither x nor dy); both
+ *                NULL: dx is not computed.  Rows without an adapter are not written.
  *   dA, dB       out, fp32 [L][r][2m] and [L][2n][r]; zero for an adapter that no row uses.  An
- *                adapter of several segments gets the sum over all of them.
+ *                adapter of several segments gets the sum over all of them.  They overlap no other
+ *                argument.
  * The sums over rows run in a fixed order, so results do not depend on scheduling.  Other arguments
  * as fairy2i_lora; x here is the x of the forward call. */
 size_t fairy2i_lora_backward_workspace_bytes(int64_t N, int64_t m, int64_t n, int64_t L, int r, int64_t S, int x_dtype);
@@ -440,7 +442,8 @@ int fairy2i_vocab_loss(const void* h, const void* W, int x_dtype, int64_t N, int
  * products (bf16: apart from the scale of g_i, which is applied to the fp32 sums of dh and, unless all
  * g are equal, costs dW one rounding of h more), sums are fp32 and each output is rounded once.  A
  * token with g_i = 0 adds nothing, whatever its logits.
- *   dh [N][K], dW [V][K], x_dtype; either may be NULL (not computed: a frozen W needs no dW). */
+ *   dh [N][K], dW [V][K], x_dtype, overlapping none of h, W and each other; either may be NULL (not
+ *   computed: a frozen W needs no dW). */
 size_t fairy2i_vocab_loss_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype);
 int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K,
                                 const int64_t* target, const float* lse, const float* g, void* dh, void* dW,
@@ -451,7 +454,8 @@ int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64
  *   grads, out, numel, dtypes  HOST arrays of count device pointers, sizes and dtypes (FAIRY2I_F32 or
  *           FAIRY2I_BF16 per tensor), read during the call only; tensors need their element's
  *           alignment only (16 bytes run faster).  out NULL: in place; out[k] is grads[k] or does not
- *           overlap any gradient.  A tensor of 0 elements is skipped (its pointers may be NULL).
+ *           overlap any gradient; no two outputs overlap, so no tensor is listed twice in place.  A
+ *           tensor of 0 elements is skipped (its pointers may be NULL).
  *   max_norm  >= 0; INFINITY computes the norm alone and leaves in-place gradients as they are.
  *   norm    out, fp32 [1].  Not finite if a gradient is not finite: c is then 0 or NaN.
  * Squares and sums are fp64 in a fixed order; c is applied in fp32 and each output rounded once.

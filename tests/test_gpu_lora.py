@@ -204,6 +204,30 @@ def test_backward(case, dt, ydt):
     assert again is d["dx_base"] and torch.equal(again, dx)
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N", [40, 300])
+def test_gradients_of_requests_do_not_mix(dt, N):
+    """NaN and infinity in the rows of one adapter, and in rows without any, reach no other gradient."""
+    dev = device()
+    K, M, r, L = 256, 130, 16, 3
+    spans, ids = [0, N // 3, N // 2, N - 5], [0, 1, 2]              # the last five rows: none
+    c, d = make(N, K, M, r, L, spans, ids, dt, torch.float32, 91, dev)
+    args = lambda e: [e[k] for k in ("dy", "x", "A", "B", "alpha", "seg_start", "seg_adapter")]
+    announce("lora gradient isolation", dt, N)
+    dx, dA, dB = f2.fairy2i_lora_backward(*args(d), dx_base=d["dx_base"], dx=d["dx_base"].clone())
+    bad = {k: v.clone() for k, v in d.items()}
+    for name in ("x", "dy"):
+        bad[name][N // 3] = float("nan")                             # adapter 1's first row
+        bad[name][N // 2 - 1] = float("inf")                         # and its last
+        bad[name][N - 3] = float("nan")
+    dx2, dA2, dB2 = f2.fairy2i_lora_backward(*args(bad), dx_base=d["dx_base"], dx=d["dx_base"].clone())
+    for a in (0, 2):
+        assert torch.equal(dA2[a], dA[a]) and torch.equal(dB2[a], dB[a]), a
+    assert not torch.isfinite(dA2[1]).any() and not torch.isfinite(dB2[1]).any()
+    rows = [i for i in range(N) if i not in (N // 3, N // 2 - 1)]
+    assert torch.equal(dx2[rows], dx[rows])
+
+
 def test_backward_against_differences():
     """d/dt of sum(y * dy) along a random direction of (x, A, B), by central differences of the
     forward call.  Truncation is exactly zero for the cubic's odd part up to t^2 |dA dB dx| terms:

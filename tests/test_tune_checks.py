@@ -16,6 +16,7 @@ import widely_linear_gemv_amd as f2
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 1 << 20          # a 16-byte aligned, never dereferenced address
 ODD = FAKE + 2
+Y, Z, Q = (FAKE + (k << 20) for k in (1, 2, 3))      # outputs, apart from the inputs
 S = None
 
 
@@ -28,8 +29,8 @@ def L():
 
 
 def lora_args(**kw):
-    a = dict(x=FAKE, x_dtype=1, N=4, m=64, A=FAKE, B=FAKE, alpha=FAKE, L=2, r=8, n=32, ss=FAKE, sa=FAKE, S=2, base=FAKE,
-             y=FAKE, y_dtype=0, ws=FAKE, wsb=1 << 30, st=S)
+    a = dict(x=FAKE, x_dtype=1, N=4, m=64, A=FAKE, B=FAKE, alpha=FAKE, L=2, r=8, n=32, ss=FAKE, sa=FAKE, S=2, base=Y,
+             y=Y, y_dtype=0, ws=FAKE, wsb=1 << 30, st=S)
     a.update(kw)
     return list(a.values())
 
@@ -43,6 +44,7 @@ def lora_args(**kw):
     (dict(S=0), 2), (dict(S=(1 << 20) + 1), 2),
     (dict(x=ODD), 5), (dict(A=ODD), 5), (dict(B=FAKE + 8), 5), (dict(base=ODD), 5), (dict(y=ODD), 5), (dict(ss=ODD), 5),
     (dict(ws=FAKE + 8), 5), (dict(ws=None), 6), (dict(wsb=8), 6),
+    (dict(y=FAKE, base=FAKE), 2), (dict(y=Y + 16), 2),                          # y on x; y on part of base
 ])
 def test_lora_errors(L, kw, status):
     assert L.fairy2i_lora(*lora_args(**kw)) == status
@@ -50,20 +52,27 @@ def test_lora_errors(L, kw, status):
 
 
 def test_lora_grouped_errors(L):
-    items = (f2.LoraItem * 2)(f2.LoraItem(FAKE, FAKE, FAKE, FAKE, FAKE, 32), f2.LoraItem(FAKE, FAKE, FAKE, FAKE, None, 32))
+    items = (f2.LoraItem * 2)(f2.LoraItem(FAKE, FAKE, FAKE, Y, Y, 32), f2.LoraItem(FAKE, FAKE, FAKE, Y, None, 32))
     call = lambda it, count: L.fairy2i_lora_grouped(it, count, FAKE, 1, 4, 64, 2, 8, FAKE, FAKE, 2, 0, FAKE, 1 << 30, S)
     assert call(None, 1) == 1
     assert call(items, 0) == 2
     assert call(items, 2) == 1 and "item 1" in f2.fairy2i_last_error()
-    items[1].y, items[1].n = FAKE, 0
+    items[1].y, items[1].n = Y, 0
     assert call(items, 2) == 2
     items[1].n, items[1].B = 32, ODD
     assert call(items, 2) == 5
+    items[1].B = FAKE
+    assert call(items, 2) == 2 and "overlaps" in f2.fairy2i_last_error()       # both write one y
+    items[1].base = items[1].y = Z
+    items[0].base = items[0].y = Z + 64
+    assert call(items, 2) == 2                                                  # some bytes in common
+    items[0].base, items[0].y = Z, Y
+    assert call(items, 2) == 2                                                  # item 1's y is item 0's base
 
 
 def back_args(**kw):
     a = dict(dy=FAKE, x=FAKE, x_dtype=1, N=4, m=64, A=FAKE, B=FAKE, alpha=FAKE, L=2, r=8, n=32, ss=FAKE, sa=FAKE, S=2,
-             dxb=FAKE, dx=FAKE, dx_dtype=0, dA=FAKE, dB=FAKE, ws=FAKE, wsb=1 << 40, st=S)
+             dxb=Y, dx=Y, dx_dtype=0, dA=Q, dB=Z, ws=FAKE, wsb=1 << 40, st=S)
     a.update(kw)
     return list(a.values())
 
@@ -72,7 +81,8 @@ def back_args(**kw):
     (dict(dy=None), 1), (dict(x=None), 1), (dict(dA=None), 1), (dict(dB=None), 1), (dict(dx=None), 1), (dict(dxb=None), 1),
     (dict(x_dtype=2), 4), (dict(dx_dtype=2), 4), (dict(N=0), 2), (dict(m=96), 2), (dict(n=0), 2), (dict(L=0), 2),
     (dict(r=129), 2), (dict(S=0), 2), (dict(dy=ODD), 5), (dict(dA=FAKE + 4), 5), (dict(dx=ODD), 5), (dict(ws=None), 6),
-    (dict(wsb=64), 6),
+    (dict(wsb=64), 6), (dict(dx=FAKE, dxb=FAKE), 2), (dict(dx=Y + 64), 2), (dict(dy=Y), 2),
+    (dict(dA=FAKE), 2), (dict(dB=FAKE), 2), (dict(dA=Z + 64), 2), (dict(dB=Y), 2),
 ])
 def test_lora_backward_errors(L, kw, status):
     assert L.fairy2i_lora_backward(*back_args(**kw)) == status
@@ -85,7 +95,7 @@ def loss_args(**kw):
 
 
 def grad_args(**kw):
-    a = dict(h=FAKE, W=FAKE, dt=1, N=4, V=100, K=64, t=FAKE, lse=FAKE, g=FAKE, dh=FAKE, dW=FAKE, ws=FAKE, wsb=1 << 40, st=S)
+    a = dict(h=FAKE, W=FAKE, dt=1, N=4, V=100, K=64, t=FAKE, lse=FAKE, g=FAKE, dh=Y, dW=Z, ws=FAKE, wsb=1 << 40, st=S)
     a.update(kw)
     return list(a.values())
 
@@ -102,7 +112,8 @@ def test_vocab_loss_errors(L, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", SIZES + [(dict(lse=None), 1), (dict(g=None), 1), (dict(dh=None, dW=None), 1),
-                                               (dict(dh=ODD), 5), (dict(dW=ODD), 5), (dict(g=ODD), 5)])
+                                               (dict(dh=ODD), 5), (dict(dW=ODD), 5), (dict(g=ODD), 5),
+                                               (dict(dh=FAKE), 2), (dict(dW=FAKE), 2), (dict(dh=Z + 64), 2)])
 def test_vocab_loss_backward_errors(L, kw, status):
     assert L.fairy2i_vocab_loss_backward(*grad_args(**kw)) == status
 
@@ -122,6 +133,13 @@ def test_clip_errors(L):
     assert c(g=ptrs(FAKE + 2, FAKE)) == 5           # fp32 needs 4 bytes
     assert c(g=ptrs(FAKE, FAKE + 1)) == 5           # bf16 needs 2
     assert c(ws=None) == 6 and c(wsb=16) == 6
+    # 8 fp32 and 8 bf16 values: 32 and 16 bytes
+    assert c() == 2 and "twice" in f2.fairy2i_last_error()
+    assert c(g=ptrs(FAKE, FAKE + 28)) == 2 and c(g=ptrs(FAKE + 12, FAKE)) == 2
+    assert c(g=ptrs(FAKE, Z), o=ptrs(Y, Y)) == 2                    # one output for two gradients
+    assert c(g=ptrs(FAKE, Z), o=ptrs(Z, Y)) == 2                    # written over the other gradient
+    assert c(g=ptrs(FAKE, Z), o=ptrs(FAKE + 16, Y)) == 2            # over part of its own
+    assert c(g=ptrs(FAKE, FAKE), o=ptrs(FAKE, Y)) == 2              # read by the second, clipped by the first
 
 
 def test_workspace_sizes_of_refused_shapes_are_zero():
@@ -227,17 +245,17 @@ if torch.cuda.device_count() != 0:
     sys.exit(0)
 import widely_linear_gemv_amd as f2
 L = f2.lib()
-P = 1 << 20
+P, Q = 1 << 20, 1 << 21
 W = 1 << 40
-items = (f2.LoraItem * 1)(f2.LoraItem(P, P, P, P, P, 32))
+items = (f2.LoraItem * 1)(f2.LoraItem(P, P, P, Q, Q, 32))
 one = lambda t, v: (t * 1)(v)
 out = {}
 for name, call in {
-    "lora": lambda: L.fairy2i_lora(P, 1, 4, 64, P, P, P, 2, 8, 32, P, P, 2, P, P, 0, P, W, None),
+    "lora": lambda: L.fairy2i_lora(P, 1, 4, 64, P, P, P, 2, 8, 32, P, P, 2, Q, Q, 0, P, W, None),
     "grouped": lambda: L.fairy2i_lora_grouped(items, 1, P, 0, 4, 64, 2, 8, P, P, 2, 0, P, W, None),
-    "backward": lambda: L.fairy2i_lora_backward(P, P, 1, 4, 64, P, P, P, 2, 8, 32, P, P, 2, P, P, 1, P, P, P, W, None),
+    "backward": lambda: L.fairy2i_lora_backward(P, P, 1, 4, 64, P, P, P, 2, 8, 32, P, P, 2, Q, Q, 1, 2 * Q, 3 * Q, P, W, None),
     "loss": lambda: L.fairy2i_vocab_loss(P, P, 1, 4, 100, 64, P, P, P, P, W, None),
-    "loss_backward": lambda: L.fairy2i_vocab_loss_backward(P, P, 0, 4, 100, 64, P, P, P, P, P, P, W, None),
+    "loss_backward": lambda: L.fairy2i_vocab_loss_backward(P, P, 0, 4, 100, 64, P, P, P, Q, 2 * Q, P, W, None),
     "clip": lambda: L.fairy2i_clip_grads(1, one(ctypes.c_void_p, P), None, one(ctypes.c_int64, 8), one(ctypes.c_int, 0), 1.0,
                                          P, P, W, None),
 }.items():

@@ -975,20 +975,20 @@ def fairy2i_clip_grads(grads, max_norm: float, *, out=None, norm=None, workspace
     the norm, fp32 [1]."""
     Tensor, n = torch.Tensor, len(grads)
     outs = grads if out is None else list(out)
-    if not n or len(outs) != n or not max_norm >= 0 or not all(isinstance(t, Tensor) for t in (*grads, *outs)):
-        _refuse_clip(grads, outs, max_norm, norm)
     # a stack's adapters are hundreds of tensors: each property is read once, in a loop of its own
-    ptrs, counts, dtypes = list(map(Tensor.data_ptr, grads)), list(map(Tensor.numel, grads)), [t.dtype for t in grads]
-    dev = grads[0].get_device()
-    good = (dev >= 0 and set(dtypes) <= _FLOATS and all(map(Tensor.is_contiguous, grads))
-            and set(map(Tensor.get_device, grads)) == {dev} and (norm is None or _fits(norm, torch.float32, (1,), dev)))
-    to = ptrs
-    if out is not None:
-        to = list(map(Tensor.data_ptr, outs))
-        good = (good and [t.dtype for t in outs] == dtypes and all(map(Tensor.is_contiguous, outs))
-                and set(map(Tensor.get_device, outs)) == {dev} and list(map(Tensor.numel, outs)) == counts
-                and all(a == b or abs(a - b) >= c * d.itemsize
-                        for a, b, c, d in zip(ptrs, to, counts, dtypes)))
+    try:
+        ptrs, counts, dtypes = list(map(Tensor.data_ptr, grads)), list(map(Tensor.numel, grads)), [t.dtype for t in grads]
+        dev = grads[0].get_device()
+        good = (max_norm >= 0 and dev >= 0 and set(dtypes) <= _FLOATS and all(map(Tensor.is_contiguous, grads))
+                and set(map(Tensor.get_device, grads)) == {dev} and (norm is None or _fits(norm, torch.float32, (1,), dev)))
+        to = ptrs
+        if out is not None:
+            to = list(map(Tensor.data_ptr, outs))
+            good = (good and [t.dtype for t in outs] == dtypes and all(map(Tensor.is_contiguous, outs))
+                    and set(map(Tensor.get_device, outs)) == {dev} and list(map(Tensor.numel, outs)) == counts
+                    and all(a == b or abs(a - b) >= c * d.itemsize for a, b, c, d in zip(ptrs, to, counts, dtypes)))
+    except (IndexError, TypeError):
+        good = False
     if not good:
         _refuse_clip(grads, outs, max_norm, norm)
     numel = array.array("q", counts)

@@ -6,7 +6,9 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <memory>
 #include <mutex>
+#include <new>
 
 #include "common.hpp"
 
@@ -649,6 +651,12 @@ int check_workspace(const void* workspace, size_t have, size_t need) {
   return FAIRY2I_OK;
 }
 
+// Whether two ranges of device memory share bytes (a NULL one shares none).
+bool overlap(const void* p, uint64_t p_bytes, const void* q, uint64_t q_bytes) {
+  const uint64_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + q_bytes && b < a + p_bytes;
+}
+
 int check_lora_n(int64_t n) {
   if (n < 1 || n > kMaxLoraSide) return fail(FAIRY2I_ERR_SHAPE, "n = %lld out of range", (long long)n);
   return FAIRY2I_OK;
@@ -698,6 +706,18 @@ int fairy2i_lora_grouped(const fairy2i_lora_item* items, int count, const void* 
     if (!aligned(items[k].A, 16) || !aligned(items[k].B, 16) || !aligned(items[k].base, 16) || !aligned(items[k].y, 16) ||
         !aligned(items[k].alpha, 4))
       return fail(FAIRY2I_ERR_ALIGN, "item %d: A, B, base and y need 16-byte alignment, alpha 4", k);
+  // every item's y is written while the others' inputs are read
+  const uint64_t ye = y_dtype == FAIRY2I_BF16 ? 2 : 4, xe = x_dtype == FAIRY2I_BF16 ? 2 : 4;
+  for (int k = 0; k < count; ++k) {
+    const uint64_t yb = (uint64_t)N * 2 * items[k].n * ye;
+    if (overlap(items[k].y, yb, x, (uint64_t)N * 2 * m * xe) || (items[k].y != items[k].base && overlap(items[k].y, yb, items[k].base, yb)))
+      return fail(FAIRY2I_ERR_SHAPE, "item %d: y overlaps x, or base without being base", k);
+    for (int j = 0; j < count; ++j) {
+      const uint64_t ob = (uint64_t)N * 2 * items[j].n * ye;
+      if (j != k && (overlap(items[k].y, yb, items[j].y, ob) || overlap(items[k].y, yb, items[j].base, ob)))
+        return fail(FAIRY2I_ERR_SHAPE, "y of item %d overlaps y or base of item %d", k, j);
+    }
+  }
   if (int s = check_workspace(workspace, workspace_bytes, f2i::lora_workspace_bytes(count, N, m, r, S))) return s;
   const f2i::LoraArgs args{x, x_dtype == FAIRY2I_BF16, y_dtype == FAIRY2I_BF16, (int)N, (int)S, (int)L, r, m,
                            seg_start, seg_adapter, workspace};
@@ -743,6 +763,20 @@ int fairy2i_lora_backward(const void* dy, const void* x, int x_dtype, int64_t N,
       !aligned(dx_base, 16) || !aligned(dA, 16) || !aligned(dB, 16) || !aligned(alpha, 4) || !aligned(seg_start, 4) ||
       !aligned(seg_adapter, 4))
     return fail(FAIRY2I_ERR_ALIGN, "dy, x, A, B, dx_base, dx, dA and dB need 16-byte alignment, alpha and the segments 4");
+  const uint64_t xe = x_dtype == FAIRY2I_BF16 ? 2 : 4, de = dx_dtype == FAIRY2I_BF16 ? 2 : 4;
+  const uint64_t dx_bytes = (uint64_t)N * 2 * m * de;
+  if (overlap(dx, dx_bytes, x, (uint64_t)N * 2 * m * xe) || overlap(dx, dx_bytes, dy, (uint64_t)N * 2 * n * xe) ||
+      (dx != dx_base && overlap(dx, dx_bytes, dx_base, dx_bytes)))
+    return fail(FAIRY2I_ERR_SHAPE, "dx overlaps x, dy, or dx_base without being dx_base");
+  // dA and dB are written while the other gradients' inputs are read
+  const struct { const void* p; uint64_t bytes; } all[] = {
+      {dA, (uint64_t)L * r * 2 * m * 4}, {dB, (uint64_t)L * 2 * n * r * 4}, {dx, dx_bytes}, {dx_base, dx_bytes},
+      {A, (uint64_t)L * r * 2 * m * xe}, {B, (uint64_t)L * 2 * n * r * xe}, {x, (uint64_t)N * 2 * m * xe},
+      {dy, (uint64_t)N * 2 * n * xe}};
+  for (int k = 0; k < 2; ++k)
+    for (int j = k + 1; j < 8; ++j)
+      if (overlap(all[k].p, all[k].bytes, all[j].p, all[j].bytes))
+        return fail(FAIRY2I_ERR_SHAPE, "%s overlaps an input or another gradient", k ? "dB" : "dA");
   if (int s = check_workspace(workspace, workspace_bytes,
                               f2i::lora_backward_workspace_bytes(N, m, n, r, (int)L, S, x_dtype == FAIRY2I_BF16)))
     return s;
@@ -796,6 +830,10 @@ int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64
   if (!aligned(h, 16) || !aligned(W, 16) || !aligned(dh, 16) || !aligned(dW, 16) || !aligned(target, 8) ||
       !aligned(lse, 4) || !aligned(g, 4))
     return fail(FAIRY2I_ERR_ALIGN, "h, W, dh and dW need 16-byte alignment, target 8, lse and g 4");
+  const uint64_t xe = x_dtype == FAIRY2I_BF16 ? 2 : 4, hb = (uint64_t)N * K * xe, wb = (uint64_t)V * K * xe;
+  if (overlap(dh, hb, h, hb) || overlap(dh, hb, W, wb) || overlap(dW, wb, h, hb) || overlap(dW, wb, W, wb) ||
+      overlap(dh, hb, dW, wb))
+    return fail(FAIRY2I_ERR_SHAPE, "dh and dW must not overlap h, W or each other");
   if (int s = check_workspace(workspace, workspace_bytes, fairy2i_vocab_loss_backward_workspace_bytes(N, V, K, x_dtype)))
     return s;
   f2i::VocabArgs a{};
@@ -804,7 +842,24 @@ int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64
   return hip_status(f2i::launch_vocab_loss_backward(a, stream), "vocabulary loss backward launch");
 }
 
-static int64_t clip_total_pieces(int count, const int64_t* numel) {
+static // A range of device memory that clipping reads or writes.
+struct Span {
+  uint64_t lo, hi;
+  bool written;
+};
+// Whether a written range shares bytes with any other range.
+bool written_twice(Span* spans, int64_t count) {
+  std::sort(spans, spans + count, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  uint64_t read = 0, written = 0;                // where the ranges up to here end
+  for (int64_t k = 0; k < count; ++k) {
+    const Span& s = spans[k];
+    if (s.lo < written || (s.written && s.lo < read)) return true;
+    (s.written ? written : read) = std::max(s.written ? written : read, s.hi);
+  }
+  return false;
+}
+
+int64_t clip_total_pieces(int count, const int64_t* numel) {
   int64_t pieces = 0;
   for (int k = 0; k < count; ++k)
     if (numel[k] > 0) pieces += f2i::clip_pieces(numel[k]);
@@ -834,6 +889,20 @@ int fairy2i_clip_grads(int count, const void* const* grads, void* const* out, co
   }
   if (!aligned(norm, 4)) return fail(FAIRY2I_ERR_ALIGN, "norm needs 4-byte alignment");
   if (int s = check_workspace(workspace, workspace_bytes, fairy2i_clip_grads_workspace_bytes(count, numel))) return s;
+  {
+    std::unique_ptr<Span[]> spans(new (std::nothrow) Span[2 * (size_t)count]);
+    if (!spans) return fail(FAIRY2I_ERR_SHAPE, "count = %d: no host memory", count);
+    int64_t n = 0;
+    for (int k = 0; k < count; ++k) {
+      if (numel[k] == 0) continue;
+      const uint64_t bytes = (uint64_t)numel[k] * (dtypes[k] == FAIRY2I_BF16 ? 2 : 4);
+      const uint64_t g = reinterpret_cast<uintptr_t>(grads[k]), o = out ? reinterpret_cast<uintptr_t>(out[k]) : g;
+      spans[n++] = Span{o, o + bytes, true};
+      if (o != g) spans[n++] = Span{g, g + bytes, false};
+    }
+    if (written_twice(spans.get(), n))
+      return fail(FAIRY2I_ERR_SHAPE, "a tensor is listed twice, or an output overlaps another output or a gradient");
+  }
   // workspace: coefficient, table (8-byte entries), partial sums
   float* coef = static_cast<float*>(workspace);
   f2i::ClipItem* table = reinterpret_cast<f2i::ClipItem*>(static_cast<uint8_t*>(workspace) + 16);
