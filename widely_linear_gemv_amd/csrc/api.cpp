@@ -657,6 +657,23 @@ bool overlap(const void* p, uint64_t p_bytes, const void* q, uint64_t q_bytes) {
   return p && q && a < b + q_bytes && b < a + p_bytes;
 }
 
+// A range of device memory that clipping reads or writes.
+struct Span {
+  uint64_t lo, hi;
+  bool written;
+};
+// Whether a written range shares bytes with any other range.
+bool written_twice(Span* spans, int64_t count) {
+  std::sort(spans, spans + count, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  uint64_t read = 0, written = 0;                // where the ranges up to here end
+  for (int64_t k = 0; k < count; ++k) {
+    const Span& s = spans[k];
+    if (s.lo < written || (s.written && s.lo < read)) return true;
+    (s.written ? written : read) = std::max(s.written ? written : read, s.hi);
+  }
+  return false;
+}
+
 int check_lora_n(int64_t n) {
   if (n < 1 || n > kMaxLoraSide) return fail(FAIRY2I_ERR_SHAPE, "n = %lld out of range", (long long)n);
   return FAIRY2I_OK;
@@ -842,24 +859,7 @@ int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64
   return hip_status(f2i::launch_vocab_loss_backward(a, stream), "vocabulary loss backward launch");
 }
 
-static // A range of device memory that clipping reads or writes.
-struct Span {
-  uint64_t lo, hi;
-  bool written;
-};
-// Whether a written range shares bytes with any other range.
-bool written_twice(Span* spans, int64_t count) {
-  std::sort(spans, spans + count, [](const Span& a, const Span& b) { return a.lo < b.lo; });
-  uint64_t read = 0, written = 0;                // where the ranges up to here end
-  for (int64_t k = 0; k < count; ++k) {
-    const Span& s = spans[k];
-    if (s.lo < written || (s.written && s.lo < read)) return true;
-    (s.written ? written : read) = std::max(s.written ? written : read, s.hi);
-  }
-  return false;
-}
-
-int64_t clip_total_pieces(int count, const int64_t* numel) {
+static int64_t clip_total_pieces(int count, const int64_t* numel) {
   int64_t pieces = 0;
   for (int k = 0; k < count; ++k)
     if (numel[k] > 0) pieces += f2i::clip_pieces(numel[k]);
