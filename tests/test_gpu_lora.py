@@ -204,6 +204,25 @@ def test_backward(case, dt, ydt):
     assert again is d["dx_base"] and torch.equal(again, dx)
 
 
+@pytest.mark.parametrize("N", [2, 100])
+@pytest.mark.parametrize("ydt", [torch.bfloat16, torch.float32])
+def test_h_past_the_largest_bf16(N, ydt):
+    """h = (2^128 - 2^120) + 1.5 2^119 fits fp32 but not bf16: y = 2^-100 h is finite.  Off by at most 2^-16 h
+    (its parts), the rounding of the fp32 sum and of y, which are under 2^-23 and u of y."""
+    dev = device()
+    K, M = 128, 64
+    x = torch.zeros((N, K), dtype=torch.bfloat16)
+    x[:, 0], x[:, 1] = 2.0 ** 127 * (2 - 2.0 ** -7), 1.5 * 2.0 ** 119
+    A, B = torch.zeros((1, 1, K), dtype=torch.bfloat16), torch.full((1, M, 1), 2.0 ** -100, dtype=torch.bfloat16)
+    A[0, 0, :2] = 1.0
+    announce("lora h past bf16", N, ydt)
+    y = f2.fairy2i_lora(x.to(dev), A.to(dev), B.to(dev), torch.ones(1, device=dev),
+                        torch.tensor([0, N], dtype=torch.int32, device=dev), torch.zeros(1, dtype=torch.int32, device=dev),
+                        base=torch.zeros((N, M), dtype=ydt, device=dev))
+    want = torch.full((N, M), (2.0 ** 127 * (2 - 2.0 ** -7) + 1.5 * 2.0 ** 119) * 2.0 ** -100, dtype=torch.float64)
+    close(y, want, want * (2.0 ** -16 + 2.0 ** -23 + unit(ydt)), "y")
+
+
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("N", [40, 300])
 def test_gradients_of_requests_do_not_mix(dt, N):

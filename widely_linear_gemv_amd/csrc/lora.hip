@@ -26,29 +26,22 @@
 
 namespace f2i {
 
-
 namespace {
 
-// kGroup consecutive elements at p; elements at or past `have` read as 0.  VEC: p is 16-byte
-// aligned and `have` is a multiple of kGroup (or <= 0).
-template <typename T, bool VEC>
+// kGroup consecutive elements at p, one by one; elements at or past `have` read as 0.
+template <typename T>
 __device__ __forceinline__ v4u load_group(const T* __restrict__ p, int64_t have) {
   constexpr int G = Mma<T>::kGroup;
-  if constexpr (VEC) {
-    if (have <= 0) return v4u{0, 0, 0, 0};
-    return *reinterpret_cast<const v4u*>(p);
-  } else {
-    uint32_t e[G];
+  uint32_t e[G];
 #pragma unroll
-    for (int k = 0; k < G; ++k) {
-      e[k] = 0;
-      if (k < have) {
-        if constexpr (sizeof(T) == 2) e[k] = p[k]; else e[k] = __float_as_uint(p[k]);
-      }
+  for (int k = 0; k < G; ++k) {
+    e[k] = 0;
+    if (k < have) {
+      if constexpr (sizeof(T) == 2) e[k] = p[k]; else e[k] = __float_as_uint(p[k]);
     }
-    if constexpr (G == 8) return v4u{e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16)};
-    else return v4u{e[0], e[1], e[2], e[3]};
   }
+  if constexpr (G == 8) return v4u{e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16)};
+  else return v4u{e[0], e[1], e[2], e[3]};
 }
 
 // The segments that meet rows [t0, t1), have rows and an adapter, and are this workgroup's share
@@ -151,7 +144,7 @@ __global__ __launch_bounds__(64 * kReduceWaves) void k_reduce(LoraReduceGroup gr
         const uint32_t voff = kk < kend ? (uint32_t)((row * K + kk) * sizeof(T)) : kNoLoad;
         o[t] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rs_x, voff, 0, 0));
       } else {
-        o[t] = load_group<T, false>(x + min(row, (int64_t)(t1 - t0 - 1)) * K + kk, kend - kk);
+        o[t] = load_group<T>(x + min(row, (int64_t)(t1 - t0 - 1)) * K + kk, kend - kk);
       }
     }
   };
@@ -219,14 +212,14 @@ __global__ __launch_bounds__(64 * kReduceWaves) void k_reduce(LoraReduceGroup gr
 
 // k_reduce for long segments and small ranks: the same work with both operands copied straight into LDS,
 // 128 contiguous bytes of a row at a time (register loads in operand layout fetch 64, and kept fewer
-// bytes in flight).  Each wave has a ring of RING steps of its own for its quarter of the chunk, so no
+// bytes in flight).  Each wave has a ring of four steps of its own for its quarter of the chunk, so no
 // barrier is needed until the waves join.
-template <typename T, int RT, int RING>
+template <typename T, int RT>
 __global__ __launch_bounds__(64 * kReduceWaves, 1) void k_reduce_ring(LoraReduceGroup grp,
                                                                       const int32_t* __restrict__ seg_start,
                                                                       const int32_t* __restrict__ seg_adapter, int S,
                                                                       int L, int N, int r) {
-  constexpr int kDeep = 128 / sizeof(T);                   // contraction per step
+  constexpr int kDeep = 128 / sizeof(T), RING = 4;         // contraction per step, steps in the ring
   constexpr int kCopies = 2 + 2 * RT, kStage = kCopies * 1024;
   constexpr int rp = RT * 16;
   static_assert(kCopies * (RING - 1) < 64, "the copies in flight can be counted");
@@ -319,8 +312,8 @@ __global__ __launch_bounds__(64 * kReduceWaves, 1) void k_reduce_ring(LoraReduce
   }
 }
 
-// One lane's operand group for k_expand from G sums: part `part` of the bf16 split (hi, then what is
-// left, then what is left of that), or the fp32 values.
+// One lane's operand group for k_expand from G sums: part `part` of the bf16 split (the leading 8 bits,
+// then what is left, then what is left of that), or the fp32 values.
 template <typename T>
 __device__ __forceinline__ v4u operand_group(const float (&h)[Mma<T>::kGroup], int part) {
   v4u o;
@@ -331,13 +324,15 @@ __device__ __forceinline__ v4u operand_group(const float (&h)[Mma<T>::kGroup], i
     uint32_t b[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float v = h[j];
-      uint32_t w = f32_to_bf16_rne(v);
-      // a part that is not finite carries everything: the later parts are 0, not inf - inf
-      for (int p = 0; p < part; ++p) {
-        const float hi = __uint_as_float(w << 16);
-        v = isfinite(hi) ? v - hi : 0.f;
+      // The first part is cut off, not rounded: a value past the largest bf16 would round to infinity.
+      // One that is not finite is carried by the first part alone (not inf - inf).
+      const bool finite = isfinite(h[j]);
+      const uint32_t top = finite ? __float_as_uint(h[j]) >> 16 : (uint32_t)f32_to_bf16_rne(h[j]);
+      float v = finite ? h[j] - __uint_as_float(top << 16) : 0.f;
+      uint32_t w = top;
+      for (int p = 1; p <= part; ++p) {
         w = f32_to_bf16_rne(v);
+        v -= __uint_as_float(w << 16);
       }
       b[j] = w;
     }
@@ -556,7 +551,7 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
           wa[f] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
               rs_w, have > 0 ? (uint32_t)((o * r + k) * sizeof(T)) : kNoLoad, 0, 0));
         } else {
-          wa[f] = load_group<T, false>(Wa + min((int64_t)o, M - 1 - o0) * r + k, have);
+          wa[f] = load_group<T>(Wa + min((int64_t)o, M - 1 - o0) * r + k, have);
         }
       }
       for (int p = 0; p < passes; ++p) {
@@ -824,8 +819,8 @@ void launch_reduce(const LoraReduceGroup& grp, int count, bool vec, const int32_
   for (int k = 0; k < count; ++k) most = std::max(most, chunks(grp.items[k].K, grp.items[k].chunk));
   if (reduce_ring(N, S, r, vec)) {
     const dim3 grid((N + kRows - 1) / kRows, most, count), block(64 * kReduceWaves);
-    if (r <= 16) hipLaunchKernelGGL((k_reduce_ring<T, 1, 4>), grid, block, 0, st, grp, ss, sa, S, L, N, r);
-    else hipLaunchKernelGGL((k_reduce_ring<T, 2, 4>), grid, block, 0, st, grp, ss, sa, S, L, N, r);
+    if (r <= 16) hipLaunchKernelGGL((k_reduce_ring<T, 1>), grid, block, 0, st, grp, ss, sa, S, L, N, r);
+    else hipLaunchKernelGGL((k_reduce_ring<T, 2>), grid, block, 0, st, grp, ss, sa, S, L, N, r);
     return;
   }
   const dim3 grid((N + tile - 1) / tile * Q, most, count);
