@@ -441,7 +441,8 @@ int fairy2i_vocab_loss(const void* h, const void* W, int x_dtype, int64_t N, int
  * in pieces of the vocabulary, whose logits are computed again; p is held in x_dtype between the two
  * products (bf16: apart from the scale of g_i, which is applied to the fp32 sums of dh and, unless all
  * g are equal, costs dW one rounding of h more), sums are fp32 and each output is rounded once.  A
- * token with g_i = 0 adds nothing, whatever its logits.
+ * token that does not count or has g_i = 0 adds nothing, whatever its row of h holds (padding may hold
+ * NaN).
  *   dh [N][K], dW [V][K], x_dtype, overlapping none of h, W and each other; either may be NULL (not
  *   computed: a frozen W needs no dW). */
 size_t fairy2i_vocab_loss_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype);

@@ -203,6 +203,28 @@ def test_no_token_counts():
     assert not loss.any() and not dh.any() and not dW.any() and torch.isfinite(lse).all()
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N", [20, 300])
+def test_padding_reaches_no_gradient(dt, N):
+    """Whatever lies in rows of h that do not count (target -100, or g = 0): dh and dW are the same."""
+    dev = device()
+    c, d = make(N, 700, 128, dt, 23, dev, ignored=0.0)
+    d["t"][N - 6:] = -100
+    d["g"][3] = 0.0
+    d["h"][N - 6:] = 0.0
+    _, lse = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"])
+    announce("vocab padding", dt, N)
+    dh, dW = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"])
+    bad = d["h"].clone()
+    bad[N - 6:N - 3] = float("nan")
+    bad[N - 3:] = float("inf")
+    bad[3] = float("nan")
+    loss2, lse2 = f2.fairy2i_vocab_loss(bad, d["W"], d["t"])
+    assert not loss2[N - 6:].any()
+    dh2, dW2 = f2.fairy2i_vocab_loss_backward(bad, d["W"], d["t"], lse2, d["g"])
+    assert torch.equal(dh2, dh) and torch.equal(dW2, dW)
+
+
 def test_bad_rows_stay_apart():
     """A NaN row and an infinite one: their own loss and dh only; NaN in a row that does not count
     reaches no gradient."""

@@ -28,7 +28,6 @@
 
 namespace f2i {
 
-
 namespace {
 
 enum { kLoss = 0, kGrad = 1, kHidden = 2, kWeight = 3 };
@@ -214,8 +213,9 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
 // second half is in registers everywhere (the step's one barrier), the copies of step s + NB go straight
 // into its buffer and have NB - 1.5 steps to land.  Rows
 // past the end of a matrix read as 0; past the last step the copies repeat it, which nothing reads.
-template <typename T, int BM, int BN, int WA, int WB, int EPI, int NB = 2>
+template <int BM, int BN, int WA, int WB, int EPI, int NB = 2>
 __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
+  using T = uint16_t;
   constexpr int kWaves = WA * WB;
   constexpr int FA = BM / WA / 16, FB = BN / WB / 16;
   constexpr int kBlocks = (BM + BN) / 8;                  // 1 KB copies per step
@@ -545,54 +545,66 @@ __global__ __launch_bounds__(256) void k_hidden_join(const float* __restrict__ a
   for (int e = 0; e < 4; ++e) store_out(out, i + e, v[e]);
 }
 
-// The parts of g (above), one wave per token: s_i (0 for tokens that do not count or have g = 0), G m_i,
-// and m_i h_i where `scaled` is given.  G is |g| of the first token that counts and has a finite g other
-// than 0 (1 if none has); every wave finds it for itself, 64 tokens at a time.  A g that is not finite
-// is its own s_i, so that it reaches its outputs.
+// bf16: the parts of g (above), one wave per token: s_i (0 for tokens that do not count or have g = 0),
+// G m_i, and m_i h_i where `scaled` is given.  G is |g| of the first token that counts and has a finite g
+// other than 0 (1 if none has); every wave finds it for itself, 64 tokens at a time.  A g that is not
+// finite is its own s_i, so that it reaches its outputs.
+// Rows of `scaled` are 0 for tokens that do not count or have g = 0: padding may hold anything, and p = 0
+// times a NaN would be one in every row of dW.  fp32 needs the copy for this alone.
+template <typename T>
 __global__ __launch_bounds__(256) void k_grad_scales(const float* __restrict__ g, const int64_t* __restrict__ target,
-                                                     int64_t N, int64_t V, const uint16_t* __restrict__ h, int64_t K,
+                                                     int64_t N, int64_t V, const T* __restrict__ h, int64_t K,
                                                      float* __restrict__ s, float* __restrict__ row, float* __restrict__ all,
-                                                     uint16_t* __restrict__ scaled) {
+                                                     T* __restrict__ scaled) {
+  constexpr int kEach = 16 / sizeof(T);
   const int lane = threadIdx.x & (kWave - 1);
   const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
   if (i >= N) return;
-  float G = 1.f;
-  for (int64_t t0 = 0; t0 < N; t0 += kWave) {
-    const int64_t t = min(t0 + lane, N - 1);
-    const float v = fabsf(g[t]);
-    const uint64_t good = __ballot(target[t] >= 0 && target[t] < V && v > 0.f && v < INFINITY);
-    if (good) {
-      G = __shfl(v, __builtin_ctzll(good));
-      break;
-    }
-  }
-  const float gi = g[i], ratio = fabsf(gi) / G;
+  const float gi = g[i];
   const bool live = target[i] >= 0 && target[i] < V && gi != 0.f;
-  float si = 0.f, m = 1.f;
-  if (live) {
-    if (ratio >= 0x1p-100f && ratio < 0x1p100f) {
-      const uint32_t top = __float_as_uint(ratio) & 0x7F800000u;           // 2^floor(log2(ratio))
-      m = ratio / __uint_as_float(top);
-      si = copysignf(__uint_as_float(top), gi);
-    } else {
-      si = gi / G;                                                         // extreme or not finite: as it is
+  float m = 1.f;
+  if constexpr (sizeof(T) == 2) {
+    float G = 1.f;
+    for (int64_t t0 = 0; t0 < N; t0 += kWave) {
+      const int64_t t = min(t0 + lane, N - 1);
+      const float v = fabsf(g[t]);
+      const uint64_t good = __ballot(target[t] >= 0 && target[t] < V && v > 0.f && v < INFINITY);
+      if (good) {
+        G = __shfl(v, __builtin_ctzll(good));
+        break;
+      }
+    }
+    const float ratio = fabsf(gi) / G;
+    float si = 0.f;
+    if (live) {
+      if (ratio >= 0x1p-100f && ratio < 0x1p100f) {
+        const uint32_t top = __float_as_uint(ratio) & 0x7F800000u;         // 2^floor(log2(ratio))
+        m = ratio / __uint_as_float(top);
+        si = copysignf(__uint_as_float(top), gi);
+      } else {
+        si = gi / G;                                                       // extreme or not finite: as it is
+      }
+    }
+    if (lane == 0) {
+      s[i] = si;
+      row[i] = G * m;
+      if (i == 0) *all = G;
     }
   }
-  if (lane == 0) {
-    s[i] = si;
-    row[i] = G * m;
-    if (i == 0) *all = G;
-  }
-  if (scaled) {
-    const uint16_t* __restrict__ from = h + i * K;
-    uint16_t* __restrict__ to = scaled + i * K;
-    for (int64_t k = lane * 8; k < K; k += kWave * 8) {
-      uint4 w = *reinterpret_cast<const uint4*>(from + k);
-      uint32_t* e = &w.x;
+  if (!scaled) return;
+  const T* __restrict__ from = h + i * K;
+  T* __restrict__ to = scaled + i * K;
+  for (int64_t k = lane * kEach; k < K; k += kWave * kEach) {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (live) {
+      w = *reinterpret_cast<const uint4*>(from + k);
+      if constexpr (sizeof(T) == 2) {
+        uint32_t* e = &w.x;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) e[j] = pack_bf16(m * bf16_lo(e[j]), m * bf16_hi(e[j]));
-      *reinterpret_cast<uint4*>(to + k) = w;
+        for (int j = 0; j < 4; ++j) e[j] = pack_bf16(m * bf16_lo(e[j]), m * bf16_hi(e[j]));
+      }
     }
+    *reinterpret_cast<uint4*>(to + k) = w;
   }
 }
 
@@ -649,14 +661,14 @@ void launch_nt(VocabTile& t, const NtPlan& plan, int64_t cover_a, int64_t cover_
   const dim3 grid((t.tiles_a * t.tiles_b + 7) / 8 * 8, plan.splits);
   if constexpr (sizeof(T) == 2) {
     switch (plan.shape) {
-      case 0: hipLaunchKernelGGL((k_nt<T, 256, 256, 2, 4, EPI>), grid, dim3(512), 0, s, t); break;
-      case 1: hipLaunchKernelGGL((k_nt<T, 256, 128, 4, 2, EPI>), grid, dim3(512), 0, s, t); break;
-      case 2: hipLaunchKernelGGL((k_nt<T, 128, 128, 2, 2, EPI>), grid, dim3(256), 0, s, t); break;
+      case 0: hipLaunchKernelGGL((k_nt<256, 256, 2, 4, EPI>), grid, dim3(512), 0, s, t); break;
+      case 1: hipLaunchKernelGGL((k_nt<256, 128, 4, 2, EPI>), grid, dim3(512), 0, s, t); break;
+      case 2: hipLaunchKernelGGL((k_nt<128, 128, 2, 2, EPI>), grid, dim3(256), 0, s, t); break;
       default:
         if ((EPI == kLoss || EPI == kGrad) && t.tiles_a * t.tiles_b <= kCUs)
-          hipLaunchKernelGGL((k_nt<T, 128, 64, 2, 2, EPI, EPI == kLoss || EPI == kGrad ? 4 : 2>), grid, dim3(256), 0, s, t);
+          hipLaunchKernelGGL((k_nt<128, 64, 2, 2, EPI, EPI == kLoss || EPI == kGrad ? 4 : 2>), grid, dim3(256), 0, s, t);
         else
-          hipLaunchKernelGGL((k_nt<T, 128, 64, 2, 2, EPI>), grid, dim3(256), 0, s, t);
+          hipLaunchKernelGGL((k_nt<128, 64, 2, 2, EPI>), grid, dim3(256), 0, s, t);
         break;
     }
   } else {
@@ -702,7 +714,7 @@ GradPlan grad_plan(int64_t N, int64_t V, int64_t K, int elem) {
   g.p = take((size_t)N * g.piece * elem);
   g.acc = take(g.pieces > 1 || g.hidden.splits > 1 ? (size_t)g.hidden.splits * N * K * 4 : 0);
   g.scales = take(elem == 2 ? ((size_t)2 * N + 1) * 4 : 0);
-  g.scaled = take(elem == 2 ? (size_t)N * K * 2 : 0);
+  g.scaled = take((size_t)N * K * elem);
   g.total = at;
   return g;
 }
@@ -734,17 +746,16 @@ hipError_t grad_t(const VocabArgs& a, hipStream_t s) {
   const T* W = static_cast<const T*>(a.W);
   const float* factor = a.g;
   const float *row_scale = nullptr, *all_scale = nullptr;
-  const void* h = a.h;
-  if constexpr (sizeof(T) == 2) {
-    float* s_i = reinterpret_cast<float*>(ws + q.scales);
-    uint16_t* scaled = a.dW ? reinterpret_cast<uint16_t*>(ws + q.scaled) : nullptr;
-    hipLaunchKernelGGL(k_grad_scales, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a.g, a.target, a.N, a.V,
-                       static_cast<const uint16_t*>(a.h), a.K, s_i, s_i + a.N, s_i + 2 * a.N, scaled);
+  float* s_i = reinterpret_cast<float*>(ws + q.scales);
+  T* h = a.dW ? reinterpret_cast<T*>(ws + q.scaled) : nullptr;
+  if (sizeof(T) == 2) {
     factor = s_i;
     row_scale = s_i + a.N;
     all_scale = s_i + 2 * a.N;
-    h = scaled;
   }
+  if (sizeof(T) == 2 || h)
+    hipLaunchKernelGGL((k_grad_scales<T>), dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a.g, a.target, a.N, a.V,
+                       static_cast<const T*>(a.h), a.K, s_i, s_i + a.N, s_i + 2 * a.N, h);
   for (int k = 0; k < q.pieces; ++k) {
     const int64_t v0 = k * q.piece, rows = std::min(q.piece, a.V - v0), ldp = up64(rows);
     VocabTile t{};
