@@ -21,6 +21,7 @@
 // that take neighbouring places of the contraction, so the matrix cores still run at the bf16 rate.
 // fp32 inputs use the fp32 matrix instruction throughout.
 #include <algorithm>
+#include <type_traits>
 
 #include "tiles.hpp"
 
@@ -28,20 +29,24 @@ namespace f2i {
 
 namespace {
 
+// A loaded group of which only the first `have` elements count: the others as 0.  (Whole words: `have` is
+// even for bf16, or at least the kGroup.)
+template <typename T>
+__device__ __forceinline__ v4u first_of(v4u w, int64_t have) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k * (4 / (int)sizeof(T)) >= have) w[k] = 0;
+  return w;
+}
+
 // kGroup consecutive elements at p, one by one; elements at or past `have` read as 0.
 template <typename T>
 __device__ __forceinline__ v4u load_group(const T* __restrict__ p, int64_t have) {
-  constexpr int G = Mma<T>::kGroup;
-  uint32_t e[G];
+  static_assert(sizeof(T) == 2, "fp32 rows hold whole words");
+  uint32_t e[8];
 #pragma unroll
-  for (int k = 0; k < G; ++k) {
-    e[k] = 0;
-    if (k < have) {
-      if constexpr (sizeof(T) == 2) e[k] = p[k]; else e[k] = __float_as_uint(p[k]);
-    }
-  }
-  if constexpr (G == 8) return v4u{e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16)};
-  else return v4u{e[0], e[1], e[2], e[3]};
+  for (int k = 0; k < 8; ++k) e[k] = k < have ? p[k] : 0;
+  return v4u{e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16)};
 }
 
 // The segments that meet rows [t0, t1), have rows and an adapter, and are this workgroup's share
@@ -101,6 +106,9 @@ constexpr int kFactorParts = sizeof(T) == 4 ? 1 : 3;
 template <typename T, typename YT>
 constexpr int expand_parts() { return sizeof(T) == 4 ? 1 : (sizeof(YT) == 2 ? 2 : 3); }
 constexpr int kReduceWaves = 4;
+// How an output's ranks lie in memory: whole 16-byte groups, whole words (read as groups, the words past
+// the last rank set to 0), or neither (an odd rank of bf16: element by element).
+enum { kGroups = 0, kWords = 1, kHalfWords = 2 };
 
 }  // namespace
 
@@ -110,7 +118,9 @@ constexpr int kReduceWaves = 4;
 // four waves take a quarter of the chunk each and join in LDS.  Output: fp32 partial sums
 // part[chunk][row][rp], each (chunk, row) written by exactly one workgroup (the one whose segment
 // holds the row); rows without an adapter are not written.  Loads are range-checked buffer loads, all of
-// U steps issued before the first product, and U more while those are multiplied.
+// U steps issued before the first product, and U more while those are multiplied.  VEC: rows of x are
+// whole 16-byte groups; else a group may reach into the next row (rows are even: whole words) and the
+// words past the row's end, whatever they are, count as 0.
 template <typename T, int RT, int TR, bool VEC>
 __global__ __launch_bounds__(64 * kReduceWaves) void k_reduce(LoraReduceGroup grp, const int32_t* __restrict__ seg_start,
                                                               const int32_t* __restrict__ seg_adapter, int S, int L,
@@ -140,12 +150,9 @@ __global__ __launch_bounds__(64 * kReduceWaves) void k_reduce(LoraReduceGroup gr
 #pragma unroll
     for (int t = 0; t < TR; ++t) {
       const int64_t row = 16 * t + c;
-      if constexpr (VEC) {
-        const uint32_t voff = kk < kend ? (uint32_t)((row * K + kk) * sizeof(T)) : kNoLoad;
-        o[t] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rs_x, voff, 0, 0));
-      } else {
-        o[t] = load_group<T>(x + min(row, (int64_t)(t1 - t0 - 1)) * K + kk, kend - kk);
-      }
+      const uint32_t voff = kk < kend ? (uint32_t)((row * K + kk) * sizeof(T)) : kNoLoad;
+      o[t] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rs_x, voff, 0, 0));
+      if constexpr (!VEC) o[t] = first_of<T>(o[t], kend - kk);
     }
   };
 
@@ -456,7 +463,7 @@ __global__ __launch_bounds__(256) void k_reduce_join(LoraReduceGroup grp, const 
 // accumulators make whole 16-byte pieces of one row of y: output 16 f + i for fp32, 16 (i / 4) + 4 f +
 // i % 4 for bf16.  With long segments workgroups are ordered with the outputs innermost, so those that
 // run together read and write whole rows (beside gate/up, 2048 rows: 47.2 us, rows innermost 55.4).
-template <typename T, typename YT, int TF, bool READY, bool WVEC>
+template <typename T, typename YT, int TF, bool READY, int RANKS>
 __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32_t* __restrict__ seg_start,
                                                 const int32_t* __restrict__ seg_adapter, int S, int L, int N, int r,
                                                 int rp, int Q) {
@@ -547,9 +554,10 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
         const int o = output(f, c);
-        if constexpr (WVEC) {
+        if constexpr (RANKS != kHalfWords) {
           wa[f] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(
               rs_w, have > 0 ? (uint32_t)((o * r + k) * sizeof(T)) : kNoLoad, 0, 0));
+          if constexpr (RANKS == kWords) wa[f] = first_of<T>(wa[f], have);
         } else {
           wa[f] = load_group<T>(Wa + min((int64_t)o, M - 1 - o0) * r + k, have);
         }
@@ -853,10 +861,13 @@ void expand_tf(const LoraExpandGroup& grp, int count, const int32_t* ss, const i
   for (int k = 0; k < count; ++k) most = std::max(most, grp.items[k].M);
   const int tile = kRows * TF;
   const dim3 grid((N + tile - 1) / tile * Q, (unsigned)((most + 255) / 256), count);
-  if (r % Mma<T>::kGroup == 0)
-    hipLaunchKernelGGL((k_expand<T, YT, TF, READY, true>), grid, dim3(256), lds, st, grp, ss, sa, S, L, N, r, rp, Q);
-  else
-    hipLaunchKernelGGL((k_expand<T, YT, TF, READY, false>), grid, dim3(256), lds, st, grp, ss, sa, S, L, N, r, rp, Q);
+  auto run = [&](auto ranks) {
+    hipLaunchKernelGGL((k_expand<T, YT, TF, READY, decltype(ranks)::value>), grid, dim3(256), lds, st, grp, ss, sa, S, L, N, r,
+                       rp, Q);
+  };
+  if (r % Mma<T>::kGroup == 0) run(std::integral_constant<int, kGroups>());
+  else if (sizeof(T) == 4 || r % 2 == 0) run(std::integral_constant<int, kWords>());
+  else if constexpr (sizeof(T) == 2) run(std::integral_constant<int, kHalfWords>());
 }
 
 // Rows per workgroup of k_expand: 32 where that still leaves 2048 workgroups (an adapter fragment then
