@@ -490,8 +490,10 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
   const int steps = (kParts * gpp + 3) / 4;
   const YT* base = static_cast<const YT*>(it.base);
   YT* y = static_cast<YT*>(it.y);
-  // 16-byte pieces of whole rows (M is even: a group of 64 outputs that M cuts short goes one by one)
-  const bool yvec = (M * sizeof(YT)) % 16 == 0 && o0 + 64 <= M;
+  // A lane's 16-byte pieces of a row of y (rows are even, so pieces are at least 4-byte aligned, which is
+  // what the vector memory instructions need); 64 outputs that M cuts short go one by one.
+  typedef v4u __attribute__((aligned(4))) piece_t;
+  const bool yvec = o0 + 64 <= M;
   auto output = [](int f, int i) { return sizeof(YT) == 4 ? 16 * f + i : 16 * (i >> 2) + 4 * f + (i & 3); };
   auto piece = [&](int i) { return sizeof(YT) == 4 ? 16 * i + 4 * g : 16 * g + 8 * i; };   // first output of a piece
   v4u old[TF][kBase];
@@ -501,7 +503,7 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
       const int64_t row = min(t0 + 16 * t + c, t1 - 1);
 #pragma unroll
       for (int i = 0; i < kBase; ++i)
-        old[t][i] = *reinterpret_cast<const v4u*>(base + row * M + o0 + piece(i));
+        old[t][i] = *reinterpret_cast<const piece_t*>(base + row * M + o0 + piece(i));
     }
 
   Segments segs(seg_start, seg_adapter, S, L, t0, t1, q, Q, lane);
@@ -581,8 +583,8 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
             const v4f b = __builtin_bit_cast(v4f, old[t][f]);
-            *reinterpret_cast<v4f*>(y + off + piece(f)) =
-                v4f{b[0] + acc[f][t][0], b[1] + acc[f][t][1], b[2] + acc[f][t][2], b[3] + acc[f][t][3]};
+            *reinterpret_cast<piece_t*>(y + off + piece(f)) = __builtin_bit_cast(
+                v4u, v4f{b[0] + acc[f][t][0], b[1] + acc[f][t][1], b[2] + acc[f][t][2], b[3] + acc[f][t][3]});
           }
         } else {
 #pragma unroll
@@ -594,7 +596,7 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
               const int e = 2 * (w & 1);
               o[w] = pack_bf16(bf16_lo(old[t][h][w]) + d[e], bf16_hi(old[t][h][w]) + d[e + 1]);
             }
-            *reinterpret_cast<v4u*>(y + off + piece(h)) = o;
+            *reinterpret_cast<piece_t*>(y + off + piece(h)) = o;
           }
         }
       } else {
