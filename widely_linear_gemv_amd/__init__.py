@@ -13,6 +13,7 @@ import array
 import contextlib
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -968,6 +969,9 @@ def fairy2i_clip_grads_workspace_bytes(numels) -> int:
     return int(lib().fairy2i_clip_grads_workspace_bytes(len(numels), (_I64 * len(numels))(*numels)))
 
 
+_dtype_of = operator.attrgetter("dtype")
+
+
 @_on_stream
 def fairy2i_clip_grads(grads, max_norm: float, *, out=None, norm=None, workspace=None) -> torch.Tensor:
     """Global norm of a list of gradients (fp32 or bf16 each, on one GPU) and clipping to max_norm:
@@ -977,22 +981,22 @@ def fairy2i_clip_grads(grads, max_norm: float, *, out=None, norm=None, workspace
     outs = grads if out is None else list(out)
     # a stack's adapters are hundreds of tensors: each property is read once, in a loop of its own
     try:
-        ptrs, counts, dtypes = list(map(Tensor.data_ptr, grads)), list(map(Tensor.numel, grads)), [t.dtype for t in grads]
+        ptrs, counts, dtypes = list(map(Tensor.data_ptr, grads)), list(map(Tensor.numel, grads)), list(map(_dtype_of, grads))
         dev = grads[0].get_device()
         good = (max_norm >= 0 and dev >= 0 and set(dtypes) <= _FLOATS and all(map(Tensor.is_contiguous, grads))
                 and set(map(Tensor.get_device, grads)) == {dev} and (norm is None or _fits(norm, torch.float32, (1,), dev)))
         to = ptrs
         if out is not None:
             to = list(map(Tensor.data_ptr, outs))
-            good = (good and [t.dtype for t in outs] == dtypes and all(map(Tensor.is_contiguous, outs))
-                    and set(map(Tensor.get_device, outs)) == {dev} and list(map(Tensor.numel, outs)) == counts
-                    and all(a == b or abs(a - b) >= c * d.itemsize for a, b, c, d in zip(ptrs, to, counts, dtypes)))
-    except (IndexError, TypeError):
+            good = (good and list(map(_dtype_of, outs)) == dtypes and all(map(Tensor.is_contiguous, outs))
+                    and set(map(Tensor.get_device, outs)) == {dev} and list(map(Tensor.numel, outs)) == counts)
+    except (AttributeError, IndexError, TypeError):
         good = False
     if not good:
         _refuse_clip(grads, outs, max_norm, norm)
     numel = array.array("q", counts)
-    codes = array.array("i", [_DTYPE[d] for d in dtypes])
+    one = dtypes.count(dtypes[0]) == n
+    codes = array.array("i", [_DTYPE[dtypes[0]]]) * n if one else array.array("i", [_DTYPE[d] for d in dtypes])
     address = lambda a, kind: ctypes.cast(a.buffer_info()[0], ctypes.POINTER(kind))
     from_, to_ = array.array("Q", ptrs), array.array("Q", to)
     norm = torch.empty((1,), dtype=torch.float32, device=grads[0].device) if norm is None else norm
