@@ -7,6 +7,9 @@
 // result never depends on scheduling) into the norm and c, k_scale multiplies.  The norm must be
 // known before the first write, so the gradients are read twice; the second time they come from
 // the Infinity Cache as far as they fit.  In place with c = 1 nothing is written.
+// Bound by memory: 448 fp32 tensors of 44032 to 88064 elements (145 MB) take k_square 44 us (3.3 TB/s; a
+// library sum over 1 GiB reads 3.9) and k_scale 48 us (6.0 TB/s read and written, part of it from the
+// Infinity Cache).
 #include <algorithm>
 
 #include "tiles.hpp"

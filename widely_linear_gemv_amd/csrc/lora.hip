@@ -114,6 +114,10 @@ enum { kGroups = 0, kWords = 1, kHalfWords = 2 };
 
 // ------------------------------------------------------------------------------ reduce ----
 
+// Bound by latency for few rows (one row of 4096, rank 16: 3.9 us; 16 rows with an adapter each, three
+// projections, 6 MB of adapters: 5.4 us), so the contraction is cut into chunks until some
+// 1024 workgroups load at once and every wave has its loads in flight together.
+//
 // Workgroup: 16 TR rows x one chunk of the contraction x the tile's segments s with s % Q == q; its
 // four waves take a quarter of the chunk each and join in LDS.  Output: fp32 partial sums
 // part[chunk][row][rp], each (chunk, row) written by exactly one workgroup (the one whose segment
@@ -220,7 +224,9 @@ __global__ __launch_bounds__(64 * kReduceWaves) void k_reduce(LoraReduceGroup gr
 // k_reduce for long segments and small ranks: the same work with both operands copied straight into LDS,
 // 128 contiguous bytes of a row at a time (register loads in operand layout fetch 64, and kept fewer
 // bytes in flight).  Each wave has a ring of four steps of its own for its quarter of the chunk, so no
-// barrier is needed until the waves join.
+// barrier is needed until the waves join.  Bound by x from HBM and the adapters from the L2: 2048 x 4096
+// bf16 at rank 32, two projections, 15.0 us (from registers 22.5); dy and x of the gradient at rank 16
+// 12.6 us for 33.6 MB, 2.7 TB/s.
 template <typename T, int RT>
 __global__ __launch_bounds__(64 * kReduceWaves, 1) void k_reduce_ring(LoraReduceGroup grp,
                                                                       const int32_t* __restrict__ seg_start,
@@ -375,6 +381,8 @@ __device__ __forceinline__ void join_chunks(const float* __restrict__ part, int6
 // read them; rows without an adapter give 0.  blockIdx.z picks the form, one wave per 64 operands:
 //   0  item.groups, k_expand's: [16-row tile][step][lane], ranks along the contraction
 //   1  item.factors, k_outer's: [block of 4 G rows][rank tile][part][lane], rows along the contraction
+// A launch of its own pays where every workgroup of a row tile in k_expand would join the same sums: 4.8 us
+// for 2048 rows of two projections at rank 32.
 template <typename T>
 __global__ __launch_bounds__(256) void k_reduce_join(LoraReduceGroup grp, const int32_t* __restrict__ seg_start,
                                                      const int32_t* __restrict__ seg_adapter, int S, int L, int N,
@@ -460,9 +468,13 @@ __global__ __launch_bounds__(256) void k_reduce_join(LoraReduceGroup grp, const 
 // the segments, the groups and the adapter do.
 //
 // The outputs of a wave's 64 are dealt to the rows i of its four output fragments f so that a lane's
-// accumulators make whole 16-byte pieces of one row of y: output 16 f + i for fp32, 16 (i / 4) + 4 f +
-// i % 4 for bf16.  With long segments workgroups are ordered with the outputs innermost, so those that
-// run together read and write whole rows (beside gate/up, 2048 rows: 47.2 us, rows innermost 55.4).
+// accumulators make whole 16-byte pieces of one row of y: output 16 f + i for fp32, 32 (f / 2) +
+// 8 (i / 4) + 4 (f % 2) + i % 4 for bf16 (one instruction then covers 64 contiguous bytes of each row).  With long segments workgroups are ordered with the outputs innermost, so those that
+// run together read and write whole rows (beside gate/up, 2048 rows: 46 us, rows innermost 55).
+//
+// Bound by HBM: base is read and y written once.  Beside gate/up, 2048 x 11008 bf16 twice: 180 MB in 46 us,
+// 3.9 TB/s, where a copy of 1 GiB reaches 5.2.  (Stores and loads past the caches: 48.5 and 55 us.)  One
+// row and one adapter, 4096 outputs, is latency: 7 us, three dependent loads deep.
 template <typename T, typename YT, int TF, bool READY, int RANKS>
 __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32_t* __restrict__ seg_start,
                                                 const int32_t* __restrict__ seg_adapter, int S, int L, int N, int r,
@@ -494,8 +506,8 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
   // what the vector memory instructions need); 64 outputs that M cuts short go one by one.
   typedef v4u __attribute__((aligned(4))) piece_t;
   const bool yvec = o0 + 64 <= M;
-  auto output = [](int f, int i) { return sizeof(YT) == 4 ? 16 * f + i : 16 * (i >> 2) + 4 * f + (i & 3); };
-  auto piece = [&](int i) { return sizeof(YT) == 4 ? 16 * i + 4 * g : 16 * g + 8 * i; };   // first output of a piece
+  auto output = [](int f, int i) { return sizeof(YT) == 4 ? 16 * f + i : 32 * (f >> 1) + 8 * (i >> 2) + 4 * (f & 1) + (i & 3); };
+  auto piece = [&](int i) { return sizeof(YT) == 4 ? 16 * i + 4 * g : 32 * i + 8 * g; };   // first output of a piece
   v4u old[TF][kBase];
 #pragma unroll
   for (int t = 0; t < TF; ++t)
@@ -618,7 +630,8 @@ __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32
 // --------------------------------------------------------------------- adapter transposes ----
 
 // Copies of the adapter matrices with their axes exchanged, for the gradient's two products:
-// in [L][R][C] -> out [L][C][ldo], columns R..ldo-1 zeroed.  blockIdx.y picks the matrix.
+// in [L][R][C] -> out [L][C][ldo], columns R..ldo-1 zeroed.  blockIdx.y picks the matrix.  Launch-bound
+// (3.6 us for one adapter of 4096 x 16); the adapters are a fraction of the rows that meet them.
 template <typename T>
 __global__ __launch_bounds__(256) void k_transpose(LoraTranspose ta, LoraTranspose tb) {
   __shared__ T s[32][33];
@@ -652,7 +665,9 @@ __global__ __launch_bounds__(256) void k_transpose(LoraTranspose ta, LoraTranspo
 // way into registers (A operand: columns; B operand: the factors, made by k_reduce_join with rows along
 // the contraction).  Rows of other segments are neither copied (zeros stand for them) nor counted (their
 // factors are masked), so a NaN in another request's row cannot reach the sum.  Splits are joined in
-// order by k_outer_join (splits > 1), so the result never depends on scheduling.
+// order by k_outer_join (splits > 1), so the result never depends on scheduling.  2048 x 4096 bf16 twice at
+// rank 16: 12.5 us for 33.6 MB (2.7 TB/s; register operands, read two bytes at a time, took 20.2), and 5 us
+// for the join of 16 splits.
 template <typename T, int RT>
 __global__ __launch_bounds__(256) void k_outer(LoraOuterGroup grp, const int32_t* __restrict__ seg_start,
                                                const int32_t* __restrict__ seg_adapter, int S, int L, int N, int r,
@@ -873,8 +888,8 @@ void expand_tf(const LoraExpandGroup& grp, int count, const int32_t* ss, const i
 }
 
 // Rows per workgroup of k_expand: 32 where that still leaves 2048 workgroups (an adapter fragment then
-// serves two row tiles), 16 otherwise.  Beside gate/up, 2048 rows: 47.2 us with 32, 50.8 with 16, 48.6
-// with 64; 389 fp32 rows of 1408: 5.6 us with 16, 7.6 with 32.
+// serves two row tiles), 16 otherwise.  Beside gate/up, 2048 rows: 47 us with 32, 51 with 16, 49 with
+// 64; 389 fp32 rows of 1408: 5.6 us with 16, 7.6 with 32.
 template <typename T, typename YT>
 void launch_expand(const LoraExpandGroup& grp, int count, const int32_t* ss, const int32_t* sa, int S, int L, int N,
                    int r, hipStream_t st) {

@@ -213,6 +213,11 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
 // second half is in registers everywhere (the step's one barrier), the copies of step s + NB go straight
 // into its buffer and have NB - 1.5 steps to land.  Rows
 // past the end of a matrix read as 0; past the last step the copies repeat it, which nothing reads.
+//
+// Bound by the matrix cores for many tokens: 2048 x 32000 x 4096 takes 400-480 us as logits (1342-1119
+// TFLOP/s: the clock falls under the power limit in a run of such calls; the card's best library product
+// reaches 1399 at 8192^3), 431-451 as p, 460-488 as dh and 464-498 as dW.  For 24 tokens by W from HBM:
+// 262 MB in 59 us, 4.4 TB/s (two buffers 64 us).
 template <int BM, int BN, int WA, int WB, int EPI, int NB = 2>
 __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
   using T = uint16_t;
@@ -346,7 +351,12 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
 // two LDS buffers, each thread cuts its 16-byte pieces of step s + 1 and writes the three parts to the
 // other between the products, and then loads those of step s + 2 into the registers
 // that this frees; one barrier a step.  (A second set of registers, loaded a step earlier, spilled: dW of
-// 2048 x 32000 x 4096 3390 us against 3150.)
+// 2048 x 32000 x 4096 3390 us against 3150.  Operands of the next step read between the products, or each
+// piece's load issued right after its cut, changed nothing: 2228-2350 us either way.)
+//
+// Bound by the matrix cores: 2048 x 32000 x 4096 takes 2.23-2.36 ms as logits, six bf16 products at
+// 1445-1365 TFLOP/s; p 2.3-2.4 ms, dh 2.3-2.4, dW 2.5-2.6.  263 x 5003 x 1088: 30-33 us each, 200 tiles of
+// 128 x 64 on 256 CUs.
 //   Plain operand: a part's row R is 64 bytes, its 16-byte segment sg in place sg ^ (R / 2 % 4).
 //   Transposed: rows of the contraction as in Side<bf16, ROWS, true>.
 template <int ROWS, bool TRANS, int THREADS>
@@ -507,7 +517,8 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt_split(VocabTile t) {
   finish<float, BM, BN, WA, WB, FA, FB, EPI>(t, acc, s_buf, a0, b0, ta, split);
 }
 
-// Joins the tiles' pairs in order (one wave per token) into lse, and the loss from the target's logit.
+// Joins the tiles' pairs in order (one wave per token) into lse, and the loss from the target's logit:
+// launch-bound (4.6 us for 24 tokens, 5.2 for 2048).
 __global__ __launch_bounds__(256) void k_loss_join(const float2* __restrict__ part, const float* __restrict__ tlogit,
                                                    const int64_t* __restrict__ target, int64_t N, int64_t V, int tiles,
                                                    float* __restrict__ loss, float* __restrict__ lse) {
@@ -550,7 +561,8 @@ __global__ __launch_bounds__(256) void k_hidden_join(const float* __restrict__ a
 // other than 0 (1 if none has); every wave finds it for itself, 64 tokens at a time.  A g that is not
 // finite is its own s_i, so that it reaches its outputs.
 // Rows of `scaled` are 0 for tokens that do not count or have g = 0: padding may hold anything, and p = 0
-// times a NaN would be one in every row of dW.  fp32 needs the copy for this alone.
+// times a NaN would be one in every row of dW.  fp32 needs the copy for this alone.  8 us for 2048 x 4096
+// bf16, of a step's 1770; fp32 13 us of 9310.
 template <typename T>
 __global__ __launch_bounds__(256) void k_grad_scales(const float* __restrict__ g, const int64_t* __restrict__ target,
                                                      int64_t N, int64_t V, const T* __restrict__ h, int64_t K,
