@@ -193,6 +193,25 @@ def test_weights_of_every_kind(dt):
     assert torch.equal(dh2, dh)
 
 
+def test_long_padding_in_front():
+    """The first token that counts lies past the ones that are searched for a common factor of g: the
+    gradients of the others, equal g and different ones, are the formula's."""
+    dev = device()
+    N, V, K = 4400, 60, 64
+    for kind in ("equal", "different"):
+        c, d = make(N, V, K, torch.bfloat16, 31, dev, ignored=0.0)
+        c["t"][:4300] = -100
+        if kind == "equal":
+            c["g"] = torch.full((N,), 0.01)
+        d["t"], d["g"] = c["t"].to(dev), c["g"].to(dev)
+        announce("vocab padding in front", kind)
+        _, lse = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"])
+        dh, dW = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"])
+        wh, bh, wW, bW = grad_reference(c)
+        close(dh, wh, bh, "dh")
+        close(dW, wW, bW, "dW")
+
+
 def test_no_token_counts():
     dev = device()
     c, d = make(9, 100, 64, torch.bfloat16, 7, dev)

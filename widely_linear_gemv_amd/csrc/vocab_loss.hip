@@ -558,11 +558,13 @@ __global__ __launch_bounds__(256) void k_hidden_join(const float* __restrict__ a
 
 // bf16: the parts of g (above), one wave per token: s_i (0 for tokens that do not count or have g = 0),
 // G m_i, and m_i h_i where `scaled` is given.  G is |g| of the first token that counts and has a finite g
-// other than 0 (1 if none has); every wave finds it for itself, 64 tokens at a time.  A g that is not
-// finite is its own s_i, so that it reaches its outputs.
+// other than 0; every wave finds it for itself, 64 tokens at a time, among the first 4096 (with a longer
+// run of padding in front G is 1: equal g then cost dW the rounding that different ones do).  A g that is
+// not finite is its own s_i, so that it reaches its outputs.
 // Rows of `scaled` are 0 for tokens that do not count or have g = 0: padding may hold anything, and p = 0
 // times a NaN would be one in every row of dW.  fp32 needs the copy for this alone.  8 us for 2048 x 4096
 // bf16, of a step's 1770; fp32 13 us of 9310.
+constexpr int kScanned = 4096;
 template <typename T>
 __global__ __launch_bounds__(256) void k_grad_scales(const float* __restrict__ g, const int64_t* __restrict__ target,
                                                      int64_t N, int64_t V, const T* __restrict__ h, int64_t K,
@@ -577,7 +579,7 @@ __global__ __launch_bounds__(256) void k_grad_scales(const float* __restrict__ g
   float m = 1.f;
   if constexpr (sizeof(T) == 2) {
     float G = 1.f;
-    for (int64_t t0 = 0; t0 < N; t0 += kWave) {
+    for (int64_t t0 = 0; t0 < min(N, (int64_t)kScanned); t0 += kWave) {
       const int64_t t = min(t0 + lane, N - 1);
       const float v = fabsf(g[t]);
       const uint64_t good = __ballot(target[t] >= 0 && target[t] < V && v > 0.f && v < INFINITY);
