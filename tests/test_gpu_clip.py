@@ -92,6 +92,19 @@ def test_norm_alone_and_zero():
     assert f2.fairy2i_clip_grads(g, 1.0).item() == 0.0
 
 
+def test_norm_alone_of_bad_gradients():
+    """max_norm infinite changes nothing, whatever the norm is."""
+    dev = device()
+    for bad in (math.inf, -math.inf, math.nan):
+        g = [torch.randn(9000, device=dev), torch.randn(33, device=dev).bfloat16()]
+        g[1][7] = bad
+        before = [t.clone() for t in g]
+        announce("clip norm alone", bad)
+        norm = f2.fairy2i_clip_grads(g, math.inf).item()
+        assert not math.isfinite(norm)
+        assert torch.equal(g[0], before[0]) and torch.equal(g[1].view(torch.int16), before[1].view(torch.int16))
+
+
 def test_stream_and_graph():
     dev = device()
     grads = grads_of([9000, 77, 20000], [torch.float32, torch.bfloat16], 5, dev)

@@ -130,7 +130,7 @@ __global__ __launch_bounds__(1024) void k_norm(const double* __restrict__ part, 
     const double nrm = sqrt(t);
     const double c = (double)max_norm / (nrm + 1e-6);
     *norm = (float)nrm;
-    *coef = (float)(c > 1.0 ? 1.0 : c);        // NaN stays
+    *coef = max_norm == INFINITY || c > 1.0 ? 1.f : (float)c;      // NaN stays, but for the norm alone
   }
 }
 
