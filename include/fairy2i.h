@@ -425,7 +425,7 @@ int fairy2i_lora_backward(const void* dy, const void* x, int x_dtype, int64_t N,
  *           64 <= K <= 65536; 1 <= N <= 2^20, 1 <= V <= 2^24, N V <= 2^36.
  *   target  int64 [N]; a target outside [0, V) (-100, say) marks a token that does not count: its
  *           loss is 0.
- *   loss, lse  out, fp32 [N].
+ *   loss, lse  out, fp32 [N], overlapping nothing else.
  * Sums are fp32 with a running maximum.  fp32 operands are multiplied as three bf16 parts each, which
  * hold them exactly; the products left out are under 2^-23 of |h W|.  A NaN or infinity in a row of h
  * stays in that token's loss and lse (fp32: an infinity as NaN).

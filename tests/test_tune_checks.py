@@ -89,7 +89,7 @@ def test_lora_backward_errors(L, kw, status):
 
 
 def loss_args(**kw):
-    a = dict(h=FAKE, W=FAKE, dt=1, N=4, V=100, K=64, t=FAKE, loss=FAKE, lse=FAKE, ws=FAKE, wsb=1 << 30, st=S)
+    a = dict(h=FAKE, W=FAKE, dt=1, N=4, V=100, K=64, t=FAKE, loss=Y, lse=Z, ws=FAKE, wsb=1 << 30, st=S)
     a.update(kw)
     return list(a.values())
 
@@ -106,7 +106,8 @@ SIZES = [(dict(N=0), 2), (dict(V=0), 2), (dict(K=0), 2), (dict(K=96), 2), (dict(
 
 
 @pytest.mark.parametrize("kw,status", SIZES + [(dict(h=None), 1), (dict(W=None), 1), (dict(t=None), 1), (dict(loss=None), 1),
-                                               (dict(lse=None), 1), (dict(loss=ODD), 5)])
+                                               (dict(lse=None), 1), (dict(loss=ODD), 5), (dict(loss=Z + 12), 2),
+                                               (dict(lse=FAKE), 2), (dict(t=Y), 2)])
 def test_vocab_loss_errors(L, kw, status):
     assert L.fairy2i_vocab_loss(*loss_args(**kw)) == status
 
@@ -254,7 +255,7 @@ for name, call in {
     "lora": lambda: L.fairy2i_lora(P, 1, 4, 64, P, P, P, 2, 8, 32, P, P, 2, Q, Q, 0, P, W, None),
     "grouped": lambda: L.fairy2i_lora_grouped(items, 1, P, 0, 4, 64, 2, 8, P, P, 2, 0, P, W, None),
     "backward": lambda: L.fairy2i_lora_backward(P, P, 1, 4, 64, P, P, P, 2, 8, 32, P, P, 2, Q, Q, 1, 2 * Q, 3 * Q, P, W, None),
-    "loss": lambda: L.fairy2i_vocab_loss(P, P, 1, 4, 100, 64, P, P, P, P, W, None),
+    "loss": lambda: L.fairy2i_vocab_loss(P, P, 1, 4, 100, 64, P, Q, 2 * Q, P, W, None),
     "loss_backward": lambda: L.fairy2i_vocab_loss_backward(P, P, 0, 4, 100, 64, P, P, P, Q, 2 * Q, P, W, None),
     "clip": lambda: L.fairy2i_clip_grads(1, one(ctypes.c_void_p, P), None, one(ctypes.c_int64, 8), one(ctypes.c_int, 0), 1.0,
                                          P, P, W, None),

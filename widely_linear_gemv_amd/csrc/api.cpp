@@ -826,6 +826,11 @@ int fairy2i_vocab_loss(const void* h, const void* W, int x_dtype, int64_t N, int
   if (int s = check_vocab_sizes(N, V, K)) return s;
   if (!aligned(h, 16) || !aligned(W, 16) || !aligned(target, 8) || !aligned(loss, 4) || !aligned(lse, 4))
     return fail(FAIRY2I_ERR_ALIGN, "h and W need 16-byte alignment, target 8, loss and lse 4");
+  const uint64_t xe = x_dtype == FAIRY2I_BF16 ? 2 : 4, ob = (uint64_t)N * 4;
+  if (overlap(loss, ob, lse, ob) || overlap(loss, ob, target, (uint64_t)N * 8) || overlap(lse, ob, target, (uint64_t)N * 8) ||
+      overlap(loss, ob, h, (uint64_t)N * K * xe) || overlap(lse, ob, h, (uint64_t)N * K * xe) ||
+      overlap(loss, ob, W, (uint64_t)V * K * xe) || overlap(lse, ob, W, (uint64_t)V * K * xe))
+    return fail(FAIRY2I_ERR_SHAPE, "loss and lse must not overlap h, W, target or each other");
   if (int s = check_workspace(workspace, workspace_bytes, fairy2i_vocab_loss_workspace_bytes(N, V, K, x_dtype))) return s;
   f2i::VocabArgs a{};
   a.h = h; a.W = W; a.target = target; a.N = N; a.V = V; a.K = K; a.bf16 = x_dtype == FAIRY2I_BF16;
