@@ -214,9 +214,9 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
 // into its buffer and have NB - 1.5 steps to land.  Rows
 // past the end of a matrix read as 0; past the last step the copies repeat it, which nothing reads.
 //
-// Bound by the matrix cores for many tokens: 2048 x 32000 x 4096 takes 400-480 us as logits (1342-1119
-// TFLOP/s: the clock falls under the power limit in a run of such calls; the card's best library product
-// reaches 1399 at 8192^3), 431-451 as p, 460-488 as dh and 464-498 as dW.  For 24 tokens by W from HBM:
+// Bound by the matrix cores under the power limit for many tokens: 2048 x 32000 x 4096 takes 400-480 us as
+// logits (1342-1119 TFLOP/s; the card's best library product reaches 1399 at 8192^3; on zeros the same
+// launch takes 365), 431-451 as p, 460-488 as dh and 464-498 as dW.  For 24 tokens by W from HBM:
 // 262 MB in 59 us, 4.4 TB/s (two buffers 64 us).
 template <int BM, int BN, int WA, int WB, int EPI, int NB = 2>
 __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
@@ -354,9 +354,10 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
 // 2048 x 32000 x 4096 3390 us against 3150.  Operands of the next step read between the products, or each
 // piece's load issued right after its cut, changed nothing: 2228-2350 us either way.)
 //
-// Bound by the matrix cores: 2048 x 32000 x 4096 takes 2.23-2.36 ms as logits, six bf16 products at
-// 1445-1365 TFLOP/s; p 2.3-2.4 ms, dh 2.3-2.4, dW 2.5-2.6.  263 x 5003 x 1088: 30-33 us each, 200 tiles of
-// 128 x 64 on 256 CUs.
+// Bound by the matrix cores under the power limit: 2048 x 32000 x 4096 takes 2.23-2.39 ms as logits, six
+// bf16 products at 1445-1345 TFLOP/s (on zeros 2.02); p 2.3-2.5 ms, dh 2.3-2.5, dW 2.5-2.7.  263 x 5003 x
+// 1088: 30-33 us each, 200 tiles of 128 x 64 on 256 CUs; a step takes 0.66 us, of which the products alone
+// would be 0.32 and loads without anything else 0.32 (without cuts 0.47, without loads 0.51).
 //   Plain operand: a part's row R is 64 bytes, its 16-byte segment sg in place sg ^ (R / 2 % 4).
 //   Transposed: rows of the contraction as in Side<bf16, ROWS, true>.
 template <int ROWS, bool TRANS, int THREADS>
