@@ -666,8 +666,8 @@ __global__ __launch_bounds__(256) void k_transpose(LoraTranspose ta, LoraTranspo
 // the contraction).  Rows of other segments are neither copied (zeros stand for them) nor counted (their
 // factors are masked), so a NaN in another request's row cannot reach the sum.  Splits are joined in
 // order by k_outer_join (splits > 1), so the result never depends on scheduling.  2048 x 4096 bf16 twice at
-// rank 16: 12.5 us for 33.6 MB (2.7 TB/s; register operands, read two bytes at a time, took 20.2), and 5 us
-// for the join of 16 splits.
+// rank 16: 12.5 us for 33.6 MB (2.7 TB/s; register operands, read two bytes at a time, took 20.2), and 4 us
+// for the join of 8 splits.
 template <typename T, int RT>
 __global__ __launch_bounds__(256) void k_outer(LoraOuterGroup grp, const int32_t* __restrict__ seg_start,
                                                const int32_t* __restrict__ seg_adapter, int S, int L, int N, int r,
@@ -945,11 +945,11 @@ hipError_t lora_t(const LoraArgs& p, const LoraItem* items, int count, hipStream
   return hipGetLastError();
 }
 
-// Row ranges of k_outer: enough workgroups for the device when there are few adapters and columns, at
-// least two steps each.
+// Row ranges of k_outer: one workgroup a CU when there are few adapters and columns, at least two steps
+// each.  (Two a CU: k_outer the same 12 us at 2048 x 4096 and rank 16, its join 5.0 us instead of 4.0.)
 int outer_splits(int64_t N, int64_t C, int L, int elem) {
   const int64_t wgs = (C + 255) / 256 * L * 2, step = 128 / elem;
-  const int64_t want = std::max<int64_t>(1, 512 / wgs);
+  const int64_t want = std::max<int64_t>(1, 256 / wgs);
   return (int)std::max<int64_t>(1, std::min<int64_t>(want, N / (2 * step)));
 }
 // Bytes of one item's factors: row blocks of 4 G rows in whole steps.
