@@ -235,6 +235,10 @@ def test_clip_binding():
     raises("max_norm", f, [g], math.nan)
     raises("norm", f, [g], 1.0, norm=torch.zeros(2))
     raises("GPU", f, [g], 1.0)
+    raises("GPU", f, grads=[g], max_norm=1.0)               # by name
+    raises("max_norm", f, max_norm=-1.0, grads=[g])
+    with pytest.raises(TypeError, match="grads"):
+        f(max_norm=1.0)
 
 
 CHILD = r'''

@@ -667,8 +667,13 @@ def _scope(t, stream):
 
 def _on_stream(fn):
     """Runs fn(first, ...) in the _scope of its first tensor and its stream argument."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kwargs):
+    def call(*args, stream=None, **kwargs):
+        if not args and name not in kwargs:
+            return fn(**kwargs)                         # raises for the missing argument
+        first, args = (args[0], args[1:]) if args else (kwargs.pop(name), args)
         if not isinstance(first, torch.Tensor) and first is not None:
             first = list(first)
         with _scope(first[0] if isinstance(first, list) and first else first, stream):
