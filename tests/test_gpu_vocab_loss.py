@@ -354,3 +354,40 @@ def test_vocabulary_offsets_past_32_bits(dt):
         # two or three non-zero terms of size <= 12, each rounded once, and the result
         assert abs(dh[i, 0].item() - (mean - l)) <= 2 * u * 12 + u * abs(mean - l) + 2.0 ** -14
         assert not dh[i, 1:].any()
+
+
+def wide_weights(kind, N):
+    """Finite g whose quotients pass fp32's range or fall under it, the first counting one often tiny."""
+    g = torch.linspace(0.5, 1.5, N)
+    if kind == "small first":
+        g[0], g[1] = 1e-20, 1e20
+    elif kind == "subnormal first":
+        g[0] = 8e-40
+    elif kind == "decayed":
+        g = 0.9 ** torch.arange(N - 1, -1, -1, dtype=torch.float64)
+    elif kind == "large first":
+        g[0], g[2], g[3] = 1e20, -1e-20, 1e-30
+    elif kind == "all of fp32":
+        g = 10.0 ** torch.linspace(-37, 37, N, dtype=torch.float64)[torch.randperm(N, generator=torch.Generator().manual_seed(1))]
+    return g.float()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kind", ["small first", "subnormal first", "decayed", "large first", "all of fp32"])
+def test_weights_of_any_size(kind, dt):
+    """Finite weights give the formula's gradients however far apart they lie.  Beside the bounds above, a value
+    under fp32's and bf16's normal range may be held as 0: an output (2^-126), a value of p (2^-126 times |W| or
+    |h| and, for bf16, a factor under 4 that is applied afterwards), a term of dW's sums (2^-126, a factor
+    under 2)."""
+    dev = device()
+    N, V, K = (1200 if kind == "decayed" else 60), 300, 128
+    c, d = make(N, V, K, dt, 37, dev, ignored=0.0)
+    c["g"] = wide_weights(kind, N)
+    d["g"] = c["g"].to(dev)
+    announce("vocab weights of any size", kind, dt)
+    _, lse = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"])
+    dh, dW = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"])
+    wh, bh, wW, bW = grad_reference(c)
+    tiny = 2.0 ** -126
+    close(dh, wh, bh + tiny + 4 * tiny * c["W"].double().abs().sum(0), "dh")
+    close(dW, wW, bW + (1 + 2 * N) * tiny + 4 * tiny * c["h"].double().abs().sum(0), "dW")

@@ -13,11 +13,14 @@
 //   dW       A = h^T, B = p^T: rows of the piece, rounded once.
 // For bf16 inputs the rounding of p (2^-8) must not be the same for all of a token's or of a batch's
 // entries, as it would be for the entries -g_i of the targets, which dominate both results: they would
-// be off by up to 2^-8 together.  So g_i is taken apart as G m_i s_i with G the first token's |g|, s_i a
-// power of two with g_i's sign and 1 <= m_i < 2: p is stored as s_i (softmax - [target]), whose rounding
-// depends on the softmax alone; dh_i is scaled by G m_i and dW by G in fp32; and dW's other operand is
-// m_i h_i (h itself where all g are equal, as for a mean).  Then the roundings of p, and of m_i h_i, are
-// independent from value to value and add about as much to dh and dW as their own final rounding.
+// be off by up to 2^-8 together.  So g_i is taken apart as G m_i s_i with 1 <= G < 2 the significand of the
+// first token's |g|, s_i a power of two with g_i's sign and 1 <= m_i < 2: p is stored as
+// s_i (softmax - [target]), whose rounding depends on the softmax alone; dh_i is scaled by G m_i and dW by G
+// in fp32; and dW's other operand is m_i h_i (h itself where all g are equal, as for a mean).  Then the
+// roundings of p, and of m_i h_i, are independent from value to value and add about as much to dh and dW as
+// their own final rounding.  No part leaves fp32's range: p and the sums keep g's own size to within a
+// factor of 4, but for |g_i| under 2^-60, where s_i stays at 2^-60 (or p would lose its small values) and m_i
+// takes the rest.
 // Transposed operands are read from the matrix as it lies in memory: rows of the contraction are
 // copied into LDS and transposed on the way into registers, so no transposed copy is made.
 // Sums are fp32; a C tile has the A rows in its accumulator rows, so a lane holds four consecutive
@@ -558,8 +561,9 @@ __global__ __launch_bounds__(256) void k_hidden_join(const float* __restrict__ a
 }
 
 // bf16: the parts of g (above), one wave per token: s_i (0 for tokens that do not count or have g = 0),
-// G m_i, and m_i h_i where `scaled` is given.  G is |g| of the first token that counts and has a finite g
-// other than 0; every wave finds it for itself, 64 tokens at a time, among the first 4096 (with a longer
+// G m_i, and m_i h_i where `scaled` is given.  G is the significand of |g| of the first token that counts and
+// has a finite g other than 0 (any number in [1, 2) would do; this one makes m_i 1 where all g are equal);
+// every wave finds it for itself, 64 tokens at a time, among the first 4096 (with a longer
 // run of padding in front G is 1: equal g then cost dW the rounding that different ones do).  A g that is
 // not finite is its own s_i, so that it reaches its outputs.
 // Rows of `scaled` are 0 for tokens that do not count or have g = 0: padding may hold anything, and p = 0
@@ -585,19 +589,19 @@ __global__ __launch_bounds__(256) void k_grad_scales(const float* __restrict__ g
       const float v = fabsf(g[t]);
       const uint64_t good = __ballot(target[t] >= 0 && target[t] < V && v > 0.f && v < INFINITY);
       if (good) {
-        G = __shfl(v, __builtin_ctzll(good));
+        G = __uint_as_float((__float_as_uint(__shfl(v, __builtin_ctzll(good))) & 0x007FFFFFu) | 0x3F800000u);
         break;
       }
     }
-    const float ratio = fabsf(gi) / G;
     float si = 0.f;
     if (live) {
-      if (ratio >= 0x1p-100f && ratio < 0x1p100f) {
-        const uint32_t top = __float_as_uint(ratio) & 0x7F800000u;         // 2^floor(log2(ratio))
-        m = ratio / __uint_as_float(top);
-        si = copysignf(__uint_as_float(top), gi);
+      const float ratio = fabsf(gi) / G;
+      if (ratio < INFINITY) {
+        const float top = fmaxf(__uint_as_float(__float_as_uint(ratio) & 0x7F800000u), 0x1p-60f);   // 2^floor(log2(ratio))
+        m = ratio / top;
+        si = copysignf(top, gi);
       } else {
-        si = gi / G;                                                       // extreme or not finite: as it is
+        si = gi;
       }
     }
     if (lane == 0) {
