@@ -391,3 +391,55 @@ def test_weights_of_any_size(kind, dt):
     tiny = 2.0 ** -126
     close(dh, wh, bh + tiny + 4 * tiny * c["W"].double().abs().sum(0), "dh")
     close(dW, wW, bW + (1 + 2 * N) * tiny + 4 * tiny * c["h"].double().abs().sum(0), "dW")
+
+
+@pytest.mark.parametrize("kind", ["equal", "different"])
+def test_target_entry_shifts_no_row(kind):
+    """bf16, target probabilities of 0.2 to 0.7 (a head that has learnt): dh_i is mostly the target's entry
+    -g_i (1 - p) times W_t, and row t of dW the same times h_i, so a rounding of that entry would move a whole
+    row by up to u = 2^-8 of itself.  The part of a row's error along W_t (h_i) is held to independent
+    roundings of at most u each -- of the row's own values, of p's other entries, and for dW of m_i h_i --
+    which together pass 6 times the root of their squares' sum with a probability under 2 e^-18, plus what
+    fp32 costs the softmax and the sums."""
+    dev = device()
+    N, V, K, u = 256, 2000, 1024, 2.0 ** -8
+    gen = torch.Generator().manual_seed(43)
+    W = torch.randn(V, K, generator=gen) * K ** -0.5
+    t = torch.randperm(V, generator=gen)[:N]
+    prob = torch.rand(N, generator=gen) * 0.5 + 0.2
+    h = W[t] / (W[t] ** 2).sum(1, keepdim=True) * (V * prob / (1 - prob)).log()[:, None]
+    g = torch.full((N,), 1.0 / N) if kind == "equal" else (torch.rand(N, generator=gen) + 0.5) / N
+    c = {"h": h.bfloat16(), "W": W.bfloat16(), "t": t, "g": g}
+    d = {k: v.to(dev) for k, v in c.items()}
+    announce("vocab target entry", kind)
+    _, lse = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"])
+    dh, dW = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"])
+    z, dz, lse64, dl, _, _, _, at = reference(c)
+    h, W, row = c["h"].double(), c["W"].double(), torch.arange(N)
+    soft = (z - lse64[:, None]).exp()
+    assert 0.15 < soft[row, at].min() and soft[row, at].max() < 0.75
+    p = soft.clone()
+    p[row, at] -= 1.0
+    p = p * g.double()[:, None]
+    ep = g.double()[:, None] * soft * (dz + dl[:, None] + 2.0 ** -20)          # fp32's part of p's error
+    ep[row, at] += 2.0 ** -23 * g.double()
+    rest = p.clone()
+    rest[row, at] = 0.0
+    Wt = W[at]
+    want = p @ W
+    cross = (W @ Wt.t()).t()                                                    # <W_v, W_t> [N][V]
+    got = ((dh.double().cpu() - want) * Wt).sum(1).abs()
+    chance = ((u * want * Wt) ** 2).sum(1) + ((u * rest * cross) ** 2).sum(1)
+    sums = (V + 16) * E24 * ((p.abs() @ W.abs()) * Wt.abs()).sum(1)
+    over = (got - 6 * chance.sqrt() - (ep * cross.abs()).sum(1) - sums) / (Wt ** 2).sum(1) / g.double()
+    assert over.max() <= 0, ("dh", over.max().item(), (over > 0).sum().item())
+    want = (p.t() @ h)[at]                                                      # rows t of dW
+    mine = p[row, at]
+    cross = h @ h.t()                                                           # <h_j, h_i>
+    others = rest.t()[at]                                                       # p_jt [row t][j]
+    got = ((dW.double().cpu()[at] - want) * h).sum(1).abs()
+    chance = ((u * want * h) ** 2).sum(1) + ((u * others * cross) ** 2).sum(1) \
+        + ((u * mine[:, None] * h * h) ** 2).sum(1) + ((u * others) ** 2 @ (h * h) * (h * h)).sum(1)
+    sums = (N + 16) * E24 * (((p.abs().t() @ h.abs())[at]) * h.abs()).sum(1)
+    over = (got - 6 * chance.sqrt() - (ep.t()[at] * cross.abs()).sum(1) - sums) / (h ** 2).sum(1) / g.double()
+    assert over.max() <= 0, ("dW", over.max().item(), (over > 0).sum().item())

@@ -11,16 +11,19 @@
 //            inputs' dtype and stored.
 //   dh       A = W^T, B = p: fp32 sums over the pieces, rounded once at the end.
 //   dW       A = h^T, B = p^T: rows of the piece, rounded once.
-// For bf16 inputs the rounding of p (2^-8) must not be the same for all of a token's or of a batch's
-// entries, as it would be for the entries -g_i of the targets, which dominate both results: they would
-// be off by up to 2^-8 together.  So g_i is taken apart as G m_i s_i with 1 <= G < 2 the significand of the
-// first token's |g|, s_i a power of two with g_i's sign and 1 <= m_i < 2: p is stored as
-// s_i (softmax - [target]), whose rounding depends on the softmax alone; dh_i is scaled by G m_i and dW by G
-// in fp32; and dW's other operand is m_i h_i (h itself where all g are equal, as for a mean).  Then the
-// roundings of p, and of m_i h_i, are independent from value to value and add about as much to dh and dW as
-// their own final rounding.  No part leaves fp32's range: p and the sums keep g's own size to within a
-// factor of 4, but for |g_i| under 2^-60, where s_i stays at 2^-60 (or p would lose its small values) and m_i
-// takes the rest.
+// For bf16 inputs the rounding of p (2^-8) must not move whole rows: the entry -g_i (1 - p_t) of a token's
+// target t dominates dh_i and row t of dW, so its rounding would be all of a row's values' at once (and,
+// where all g are equal, every row's).  So p is stored in units in which that entry is a power of two: with
+// f_i = 1 - softmax_t, g_i f_i is taken apart as G m_i s_i with 1 <= G < 2 the significand of the first
+// token's |g|, s_i a power of two with g_i's sign and 1/2 < m_i <= 1; p holds -s_i for the target and
+// s_i softmax / f_i elsewhere, dh_i is scaled by G m_i and dW by G in fp32, and dW's other operand is m_i h_i
+// (h itself to within f_i where all g are equal, as for a mean).  Then the roundings, of p's other entries
+// and of m_i h_i, are independent from value to value.  Target probabilities of 0.2 to 0.7, 256 tokens, 2000 x
+// 1024: dh 0.00166 off 64 bits (2-norm), as much as its own final rounding; dW 0.0024, final rounding 0.0017.
+// (Where f_i is under 2^-16, mostly rounding itself, it is left in p: the target's entry is then
+// -s_i (1 - softmax_t).)
+// No part leaves fp32's range: p and the sums keep g's own size to within a factor of 4, but for |g_i| f_i
+// under 2^-60, where s_i stays at 2^-60 (or p would lose its small values) and m_i takes the rest.
 // Transposed operands are read from the matrix as it lies in memory: rows of the contraction are
 // copied into LDS and transposed on the way into registers, so no transposed copy is made.
 // Sums are fp32; a C tile has the A rows in its accumulator rows, so a lane holds four consecutive
@@ -61,8 +64,9 @@ struct VocabTile {
   const void* a;
   const void* b;
   const int64_t* target;        // [N]
-  const float* lse;             // [N] (kGrad)
-  const float* g;               // [N] factor of p (kGrad)
+  const float* lse;             // [N] (kGrad; bf16: with log f_i added)
+  const float* g;               // [N] factor of p (kGrad; bf16: s_i)
+  const float* at_target;       // [N] p over that factor at the target (kGrad, bf16)
   const float* row_scale;       // [N] factor of dh's rows, or null (kHidden)
   const float* all_scale;       // [1] factor of dW, or null (kWeight)
   float2* part;                 // [row tile of A][N] (kLoss)
@@ -156,6 +160,8 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
       const float gi = tgt >= 0 && tgt < t.V ? t.g[tok] : 0.f;
       const bool live = gi != 0.f;                         // other tokens give 0 whatever their logits are
       const float lse = live ? t.lse[tok] : 0.f;
+      float at_target = 0.f;
+      if constexpr (sizeof(T) == 2) at_target = live ? t.at_target[tok] : 0.f;
       const int64_t away = tgt - t.v0 - va;                // the target lies this far past the lane's first row
       const int d = live && away >= 0 && away < FA * 16 ? (int)away : -1;
 #pragma unroll
@@ -165,8 +171,11 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
         float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float soft = sizeof(T) == 2 ? fast_exp(acc[i][j][e] - lse) : expf(acc[i][j][e] - lse);
-          x[e] = live && r + e < t.rows_a ? gi * (soft - (d == 16 * i + e ? 1.f : 0.f)) : 0.f;
+          const bool target = d == 16 * i + e;
+          float v;
+          if constexpr (sizeof(T) == 2) v = target ? at_target : fast_exp(acc[i][j][e] - lse);
+          else v = expf(acc[i][j][e] - lse) - (target ? 1.f : 0.f);
+          x[e] = live && r + e < t.rows_a ? gi * v : 0.f;
         }
         if constexpr (sizeof(T) == 2)
           *reinterpret_cast<uint2*>(p + tok * t.ldp + r) =
@@ -560,27 +569,33 @@ __global__ __launch_bounds__(256) void k_hidden_join(const float* __restrict__ a
   for (int e = 0; e < 4; ++e) store_out(out, i + e, v[e]);
 }
 
-// bf16: the parts of g (above), one wave per token: s_i (0 for tokens that do not count or have g = 0),
-// G m_i, and m_i h_i where `scaled` is given.  G is the significand of |g| of the first token that counts and
-// has a finite g other than 0 (any number in [1, 2) would do; this one makes m_i 1 where all g are equal);
-// every wave finds it for itself, 64 tokens at a time, among the first 4096 (with a longer
-// run of padding in front G is 1: equal g then cost dW the rounding that different ones do).  A g that is
-// not finite is its own s_i, so that it reaches its outputs.
+// bf16: the parts of g f (above), one wave per token: s_i (0 for tokens that do not count or have g = 0),
+// G m_i, p's target entry over s_i, lse_i + log f_i, and m_i h_i where `scaled` is given.  f_i comes from the
+// target's logit, made here (off by as much as the product's own).  G is the significand of |g| of the first
+// token that counts and has a finite g other than 0 (any number in [1, 2) would do; this one makes m_i 1 to
+// within f_i where all g are equal); every wave finds it for itself, 64 tokens at a time, among the first 4096
+// (with a longer run of padding in front G is 1: equal g then cost dW the rounding that different ones do).  A
+// g that is not finite is its own s_i, so that it reaches its outputs.
 // Rows of `scaled` are 0 for tokens that do not count or have g = 0: padding may hold anything, and p = 0
-// times a NaN would be one in every row of dW.  fp32 needs the copy for this alone.  8 us for 2048 x 4096
-// bf16, of a step's 1770; fp32 13 us of 9310.
+// times a NaN would be one in every row of dW.  fp32 needs the copy for this alone.  13 us for 2048 x 4096
+// bf16 (8 without the target's logits), of a step's 1890; fp32 13 us of 9310.
 constexpr int kScanned = 4096;
+constexpr float kLeastRest = 0x1p-16f;       // f_i under which it stays in p
+struct GradScales {                          // [N] each, but for all [1]
+  float *s, *row, *at_target, *lse, *all;
+};
 template <typename T>
 __global__ __launch_bounds__(256) void k_grad_scales(const float* __restrict__ g, const int64_t* __restrict__ target,
-                                                     int64_t N, int64_t V, const T* __restrict__ h, int64_t K,
-                                                     float* __restrict__ s, float* __restrict__ row, float* __restrict__ all,
-                                                     T* __restrict__ scaled) {
+                                                     int64_t N, int64_t V, const T* __restrict__ h,
+                                                     const T* __restrict__ W, const float* __restrict__ lse, int64_t K,
+                                                     GradScales out, T* __restrict__ scaled) {
   constexpr int kEach = 16 / sizeof(T);
   const int lane = threadIdx.x & (kWave - 1);
   const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
   if (i >= N) return;
   const float gi = g[i];
-  const bool live = target[i] >= 0 && target[i] < V && gi != 0.f;
+  const int64_t tgt = target[i];
+  const bool live = tgt >= 0 && tgt < V && gi != 0.f;
   float m = 1.f;
   if constexpr (sizeof(T) == 2) {
     float G = 1.f;
@@ -593,21 +608,45 @@ __global__ __launch_bounds__(256) void k_grad_scales(const float* __restrict__ g
         break;
       }
     }
-    float si = 0.f;
+    float si = 0.f, at_target = 0.f, base = 0.f;
     if (live) {
-      const float ratio = fabsf(gi) / G;
+      const T* __restrict__ hi = h + i * K;
+      const T* __restrict__ wt = W + tgt * K;
+      float logit = 0.f;
+      for (int64_t k = lane * kEach; k < K; k += kWave * kEach) {
+        const v4u a = *reinterpret_cast<const v4u*>(hi + k), b = *reinterpret_cast<const v4u*>(wt + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          logit = fmaf(bf16_lo(a[j]), bf16_lo(b[j]), logit);
+          logit = fmaf(bf16_hi(a[j]), bf16_hi(b[j]), logit);
+        }
+      }
+      logit = wave_sum(logit);
+      base = lse[i];
+      float f = -expm1f(logit - base);
+      const bool apart = f >= kLeastRest;                                  // not a NaN either
+      at_target = apart ? -1.f : -f;
+      if (apart) base += logf(f);
+      else f = 1.f;
+      const float ratio = fabsf(gi) * f / G;
       if (ratio < INFINITY) {
-        const float top = fmaxf(__uint_as_float(__float_as_uint(ratio) & 0x7F800000u), 0x1p-60f);   // 2^floor(log2(ratio))
+        float top = fmaxf(__uint_as_float(__float_as_uint(ratio) & 0x7F800000u), 0x1p-60f);   // 2^floor(log2(ratio))
         m = ratio / top;
+        if (m > 1.f && top < 0x1p127f) {
+          m *= 0.5f;
+          top *= 2.f;
+        }
         si = copysignf(top, gi);
       } else {
         si = gi;
       }
     }
     if (lane == 0) {
-      s[i] = si;
-      row[i] = G * m;
-      if (i == 0) *all = G;
+      out.s[i] = si;
+      out.row[i] = G * m;
+      out.at_target[i] = at_target;
+      out.lse[i] = base;
+      if (i == 0) *out.all = G;
     }
   }
   if (!scaled) return;
@@ -732,7 +771,7 @@ GradPlan grad_plan(int64_t N, int64_t V, int64_t K, int elem) {
   auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
   g.p = take((size_t)N * g.piece * elem);
   g.acc = take(g.pieces > 1 || g.hidden.splits > 1 ? (size_t)g.hidden.splits * N * K * 4 : 0);
-  g.scales = take(elem == 2 ? ((size_t)2 * N + 1) * 4 : 0);
+  g.scales = take(elem == 2 ? ((size_t)4 * N + 1) * 4 : 0);
   g.scaled = take((size_t)N * K * elem);
   g.total = at;
   return g;
@@ -763,25 +802,27 @@ hipError_t grad_t(const VocabArgs& a, hipStream_t s) {
   T* p = reinterpret_cast<T*>(ws + q.p);
   float* acc = reinterpret_cast<float*>(ws + q.acc);
   const T* W = static_cast<const T*>(a.W);
-  const float* factor = a.g;
-  const float *row_scale = nullptr, *all_scale = nullptr;
-  float* s_i = reinterpret_cast<float*>(ws + q.scales);
+  const float *factor = a.g, *lse = a.lse, *at_target = nullptr, *row_scale = nullptr, *all_scale = nullptr;
+  float* sc = reinterpret_cast<float*>(ws + q.scales);
+  const GradScales out{sc, sc + a.N, sc + 2 * a.N, sc + 3 * a.N, sc + 4 * a.N};
   T* h = a.dW ? reinterpret_cast<T*>(ws + q.scaled) : nullptr;
   if (sizeof(T) == 2) {
-    factor = s_i;
-    row_scale = s_i + a.N;
-    all_scale = s_i + 2 * a.N;
+    factor = out.s;
+    lse = out.lse;
+    at_target = out.at_target;
+    row_scale = out.row;
+    all_scale = out.all;
   }
   if (sizeof(T) == 2 || h)
     hipLaunchKernelGGL((k_grad_scales<T>), dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a.g, a.target, a.N, a.V,
-                       static_cast<const T*>(a.h), a.K, s_i, s_i + a.N, s_i + 2 * a.N, h);
+                       static_cast<const T*>(a.h), W, a.lse, a.K, out, h);
   for (int k = 0; k < q.pieces; ++k) {
     const int64_t v0 = k * q.piece, rows = std::min(q.piece, a.V - v0), ldp = up64(rows);
     VocabTile t{};
     t.a = W + v0 * a.K; t.b = a.h;
     t.rows_a = rows; t.rows_b = a.N;
     t.k = t.lda = t.ldb = a.K;
-    t.target = a.target; t.lse = a.lse; t.g = factor;
+    t.target = a.target; t.lse = lse; t.g = factor; t.at_target = at_target;
     t.p = p; t.ldp = ldp;
     t.v0 = v0; t.V = a.V; t.N = a.N;
     launch_nt<T, kGrad>(t, nt_plan(ldp, a.N, steps_of(a.K, sizeof(T)), sizeof(T), 1, false), ldp, a.N, s);
