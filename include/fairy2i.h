@@ -427,8 +427,9 @@ int fairy2i_lora_backward(const void* dy, const void* x, int x_dtype, int64_t N,
  *           loss is 0.
  *   loss, lse  out, fp32 [N], overlapping nothing else.
  * Sums are fp32 with a running maximum.  fp32 operands are multiplied as three bf16 parts each, which
- * hold them exactly; the products left out are under 2^-23 of |h W|.  A NaN or infinity in a row of h
- * stays in that token's loss and lse (fp32: an infinity as NaN).
+ * hold them exactly; the products left out are under 2^-23 of |h W|, of either sign.  A NaN or infinity in
+ * a row of h stays in that token's loss and lse (fp32: an infinity, or a logit past fp32's range, may come
+ * out as NaN).
  * workspace: fairy2i_vocab_loss_workspace_bytes(...) bytes, 16-byte aligned; calls that share one must
  * not overlap. */
 size_t fairy2i_vocab_loss_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype);

@@ -443,3 +443,25 @@ def test_target_entry_shifts_no_row(kind):
     sums = (N + 16) * E24 * (((p.abs().t() @ h.abs())[at]) * h.abs()).sum(1)
     over = (got - 6 * chance.sqrt() - (ep.t()[at] * cross.abs()).sum(1) - sums) / (h ** 2).sum(1) / g.double()
     assert over.max() <= 0, ("dW", over.max().item(), (over > 0).sum().item())
+
+
+@pytest.mark.parametrize("w", [1 + 2.0 ** -7 - 2.0 ** -23, 1 + 2.0 ** -8 - 2.0 ** -23, 1.7, -0.6180339, 1.5 + 2.0 ** -8 + 2.0 ** -16])
+def test_fp32_product_of_two_values(w):
+    """One term and one vocabulary entry, so that lse is the product itself.  Parts rounded to bf16 leave
+    |x2| <= 2^-8 and |x3| <= 2^-17 of x's power of two, so the three products left out are within
+    (2 2^-25 + 2^-34) of |h W|; the five smaller products are under 2^-6 of it, their sums' roundings (2^-23
+    each if the matrix cores cut instead of rounding) under 2^-27 together, and the last sum costs 2^-23."""
+    dev = device()
+    gen = torch.Generator().manual_seed(47)
+    x = torch.cat([torch.tensor([1 + 2.0 ** -7 - 2.0 ** -23, 1 + 2.0 ** -8 + 2.0 ** -23, -1.0, 1 + 2.0 ** -16, 3.0e38, -3.4e38]),
+                   torch.randn(4000, generator=gen), torch.rand(90, generator=gen) * 1e30])
+    h = torch.zeros(len(x), 64)
+    h[:, 5] = x
+    W = torch.zeros(1, 64)
+    W[0, 5] = w
+    big = 2.0 ** -10 if abs(w) > 1 else 1.0                  # the products stay in range
+    W *= big
+    announce("vocab fp32 product", w)
+    _, lse = f2.fairy2i_vocab_loss(h.to(dev), W.to(dev), torch.zeros(len(x), dtype=torch.int64, device=dev))
+    want = x.double() * W[0, 5].double()
+    close(lse, want, (2.0 ** -24 + 2.0 ** -33 + 2.0 ** -27 + 2.0 ** -23) * want.abs(), w)

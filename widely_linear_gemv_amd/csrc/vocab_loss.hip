@@ -354,10 +354,12 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
 }
 
 // The same product for fp32 operands, on the bf16 matrix instructions: every value is cut into three bf16
-// parts of 8 bits each (x = x1 + x2 + x3 exactly: each part is the leading half of what is left), and of
-// the nine products of two values' parts the six largest are summed; the other three are under 2^-23 of
-// |a b| together, within the rounding of the fp32 sums.  Six bf16 products take 96 cycles of a SIMD for
-// 16 x 16 x 32, the fp32 instructions 256.
+// parts of 8 bits each (x = x1 + x2 + x3 exactly: each part is what is left, rounded to nearest, so
+// |x2| <= 2^-8 and |x3| <= 2^-17 of x's power of two), and of the nine products of two values' parts the six
+// largest are summed; the other three are at most (1 + 2^-9) 2^-24 of |a b| together and of either sign,
+// within the rounding of the fp32 sums.  (Parts cut off instead of rounded leave up to 2^-21, always of a b's
+// own sign: every sum shrinks.)  Six bf16 products take 96 cycles of a SIMD for 16 x 16 x 32, the fp32
+// instructions 256.
 //
 // Workgroup and waves as k_nt.  Steps of 32 along the contraction: while step s is multiplied from one of
 // two LDS buffers, each thread cuts its 16-byte pieces of step s + 1 and writes the three parts to the
@@ -399,8 +401,9 @@ struct SplitSide {
   }
 };
 
-// Four fp32 values cut into parts, two bf16 to a word: out[p] holds part p.  (Of an infinity NaN is left,
-// so that its products are NaN.)
+// Four fp32 values cut into parts, two bf16 to a word: out[p] holds part p.  The first part is at most the
+// largest bf16, to which fp32 values past it would not round.  (Of an infinity NaN is left, so that its
+// products are NaN.)
 __device__ __forceinline__ void cut(const v4u& x, v2u (&out)[3]) {
   float f[4];
 #pragma unroll
@@ -409,14 +412,15 @@ __device__ __forceinline__ void cut(const v4u& x, v2u (&out)[3]) {
   for (int p = 0; p < 3; ++p) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t a = __float_as_uint(f[2 * h]), b = __float_as_uint(f[2 * h + 1]);
-      out[p][h] = __builtin_amdgcn_perm(b, a, 0x07060302u);    // the leading halves
-    }
-    if (p < 2) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[e] -= __uint_as_float(__float_as_uint(f[e]) & 0xFFFF0000u);
+      constexpr float kMost = 0x1.FEp127f;
+      float a = f[2 * h], b = f[2 * h + 1];
+      if (p == 0) {
+        a = __builtin_amdgcn_fmed3f(a, -kMost, kMost);
+        b = __builtin_amdgcn_fmed3f(b, -kMost, kMost);
       }
+      out[p][h] = pack_bf16(a, b);
+      f[2 * h] -= bf16_lo(out[p][h]);
+      f[2 * h + 1] -= bf16_hi(out[p][h]);
     }
   }
 }
