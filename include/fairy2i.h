@@ -446,7 +446,7 @@ int fairy2i_vocab_loss(const void* h, const void* W, int x_dtype, int64_t N, int
  * probabilities of 0.2 to 0.7: dh 0.0017 of its norm, the error of its own rounding, and dW 0.0024.)  A
  * token that does not count or has g_i = 0 adds nothing, whatever its row of h holds (padding may hold
  * NaN).
- *   dh [N][K], dW [V][K], x_dtype, overlapping none of h, W and each other; either may be NULL (not
+ *   dh [N][K], dW [V][K], x_dtype, overlapping no input and not each other; either may be NULL (not
  *   computed: a frozen W needs no dW). */
 size_t fairy2i_vocab_loss_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype);
 int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K,

@@ -119,6 +119,17 @@ def test_vocab_loss_backward_errors(L, kw, status):
     assert L.fairy2i_vocab_loss_backward(*grad_args(**kw)) == status
 
 
+def test_vocab_loss_backward_refuses_outputs_over_inputs(L):
+    """target, lse and g are read for every piece of the vocabulary, after the first ones' dW is stored."""
+    far = 1 << 30
+    size = {"target": 4 * 8, "lse": 4 * 4, "g": 4 * 4}
+    for out, nbytes in (("dh", 4 * 64 * 2), ("dW", 100 * 64 * 2)):
+        for name, key in (("target", "t"), ("lse", "lse"), ("g", "g")):
+            for at in (far, far - size[name] + 8, far + nbytes - 8):
+                call = L.fairy2i_vocab_loss_backward(*grad_args(**{out: far, key: at}))
+                assert call == 2 and "overlap" in f2.fairy2i_last_error(), (out, name, at - far)
+
+
 def test_clip_errors(L):
     ptrs = lambda *v: (ctypes.c_void_p * len(v))(*v)
     num = lambda *v: (ctypes.c_int64 * len(v))(*v)

@@ -852,10 +852,14 @@ int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64
   if (!aligned(h, 16) || !aligned(W, 16) || !aligned(dh, 16) || !aligned(dW, 16) || !aligned(target, 8) ||
       !aligned(lse, 4) || !aligned(g, 4))
     return fail(FAIRY2I_ERR_ALIGN, "h, W, dh and dW need 16-byte alignment, target 8, lse and g 4");
+  // a piece's dW is stored before the next piece reads the inputs again
   const uint64_t xe = x_dtype == FAIRY2I_BF16 ? 2 : 4, hb = (uint64_t)N * K * xe, wb = (uint64_t)V * K * xe;
-  if (overlap(dh, hb, h, hb) || overlap(dh, hb, W, wb) || overlap(dW, wb, h, hb) || overlap(dW, wb, W, wb) ||
-      overlap(dh, hb, dW, wb))
-    return fail(FAIRY2I_ERR_SHAPE, "dh and dW must not overlap h, W or each other");
+  const struct { const void* p; uint64_t bytes; } in[] = {
+      {h, hb}, {W, wb}, {target, (uint64_t)N * 8}, {lse, (uint64_t)N * 4}, {g, (uint64_t)N * 4}};
+  for (const auto& r : in)
+    if (overlap(dh, hb, r.p, r.bytes) || overlap(dW, wb, r.p, r.bytes))
+      return fail(FAIRY2I_ERR_SHAPE, "dh and dW must not overlap h, W, target, lse or g");
+  if (overlap(dh, hb, dW, wb)) return fail(FAIRY2I_ERR_SHAPE, "dh and dW must not overlap each other");
   if (int s = check_workspace(workspace, workspace_bytes, fairy2i_vocab_loss_backward_workspace_bytes(N, V, K, x_dtype)))
     return s;
   f2i::VocabArgs a{};
