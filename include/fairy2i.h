@@ -368,7 +368,8 @@ int fairy2i_gemm_noalloc(const uint8_t* packed, const float* scales, int64_t n, 
  *                segment per request; neighbouring rows of one adapter may share a segment.
  *                1 <= S <= 2^20.
  *   seg_adapter  int32 [S] on the device; the same adapter may serve several segments.
- *   base, y      [N][2n], y_dtype FAIRY2I_F32 or FAIRY2I_BF16; y is base or does not overlap it.
+ *   base, y      [N][2n], y_dtype FAIRY2I_F32 or FAIRY2I_BF16; y is base or does not overlap it, and
+ *                overlaps no other argument.
  *                Rows in no segment, and rows of a segment whose adapter is outside [0, L) (-1, say),
  *                are not written.
  * fp32 sums; y is rounded once.  Rows do not affect each other: a NaN or infinity in one request's
@@ -394,8 +395,8 @@ typedef struct {
 
 /* fairy2i_lora for `count` projections that read the same x (q, k and v; gate and up) and share N,
  * m, L, r, the segments and the dtypes, eight to a launch.  items is a HOST array, read during the
- * call only; no item's y overlaps x or another item's y or base (two sets of adapters on one output are
- * two calls).  workspace: fairy2i_lora_workspace_bytes with the same count. */
+ * call only; no item's y overlaps any item's A, B or alpha, another item's y or base, or a shared argument
+ * (two sets of adapters on one output are two calls).  workspace: fairy2i_lora_workspace_bytes with the same count. */
 int fairy2i_lora_grouped(const fairy2i_lora_item* items, int count, const void* x, int x_dtype, int64_t N, int64_t m,
                          int64_t L, int r, const int32_t* seg_start, const int32_t* seg_adapter, int64_t S, int y_dtype,
                          void* workspace, size_t workspace_bytes, hipStream_t stream);

@@ -70,6 +70,24 @@ def test_lora_grouped_errors(L):
     assert call(items, 2) == 2                                                  # item 1's y is item 0's base
 
 
+def test_lora_refuses_y_over_the_adapters(L):
+    """Workgroups that store y run beside others that still read A, B, alpha and the segments."""
+    far, y_bytes = 1 << 30, 4 * 64 * 4
+    size = {"A": 2 * 8 * 128 * 2, "B": 2 * 64 * 8 * 2, "alpha": 2 * 4, "ss": 3 * 4, "sa": 2 * 4}
+    for name, nbytes in size.items():
+        for at in (far, far - (nbytes - 1) // 16 * 16, far + y_bytes - 16):
+            assert L.fairy2i_lora(*lora_args(y=far, **{name: at})) == 2, (name, at - far)
+            assert "overlaps" in f2.fairy2i_last_error()
+    # an item's y over another item's adapters
+    for name in ("A", "B", "alpha"):
+        items = (f2.LoraItem * 2)(f2.LoraItem(FAKE, FAKE, FAKE, Y, Y, 32), f2.LoraItem(FAKE, FAKE, FAKE, Z, Z, 32))
+        setattr(items[1], name, Y)
+        assert L.fairy2i_lora_grouped(items, 2, FAKE, 1, 4, 64, 2, 8, FAKE, FAKE, 2, 0, FAKE, 1 << 30, S) == 2, name
+        items = (f2.LoraItem * 2)(f2.LoraItem(FAKE, FAKE, FAKE, Y, Y, 32), f2.LoraItem(FAKE, FAKE, FAKE, Z, Z, 32))
+        setattr(items[0], name, Z)
+        assert L.fairy2i_lora_grouped(items, 2, FAKE, 1, 4, 64, 2, 8, FAKE, FAKE, 2, 0, FAKE, 1 << 30, S) == 2, name
+
+
 def back_args(**kw):
     a = dict(dy=FAKE, x=FAKE, x_dtype=1, N=4, m=64, A=FAKE, B=FAKE, alpha=FAKE, L=2, r=8, n=32, ss=FAKE, sa=FAKE, S=2,
              dxb=Y, dx=Y, dx_dtype=0, dA=Q, dB=Z, ws=FAKE, wsb=1 << 40, st=S)

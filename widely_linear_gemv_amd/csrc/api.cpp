@@ -723,16 +723,22 @@ int fairy2i_lora_grouped(const fairy2i_lora_item* items, int count, const void* 
     if (!aligned(items[k].A, 16) || !aligned(items[k].B, 16) || !aligned(items[k].base, 16) || !aligned(items[k].y, 16) ||
         !aligned(items[k].alpha, 4))
       return fail(FAIRY2I_ERR_ALIGN, "item %d: A, B, base and y need 16-byte alignment, alpha 4", k);
-  // every item's y is written while the others' inputs are read
+  // every item's y is written while the others' inputs, and all adapters and segments, are read
   const uint64_t ye = y_dtype == FAIRY2I_BF16 ? 2 : 4, xe = x_dtype == FAIRY2I_BF16 ? 2 : 4;
   for (int k = 0; k < count; ++k) {
+    const void* y = items[k].y;
     const uint64_t yb = (uint64_t)N * 2 * items[k].n * ye;
-    if (overlap(items[k].y, yb, x, (uint64_t)N * 2 * m * xe) || (items[k].y != items[k].base && overlap(items[k].y, yb, items[k].base, yb)))
+    if (overlap(y, yb, x, (uint64_t)N * 2 * m * xe) || (y != items[k].base && overlap(y, yb, items[k].base, yb)))
       return fail(FAIRY2I_ERR_SHAPE, "item %d: y overlaps x, or base without being base", k);
+    if (overlap(y, yb, seg_start, (uint64_t)(S + 1) * 4) || overlap(y, yb, seg_adapter, (uint64_t)S * 4))
+      return fail(FAIRY2I_ERR_SHAPE, "item %d: y overlaps seg_start or seg_adapter", k);
     for (int j = 0; j < count; ++j) {
       const uint64_t ob = (uint64_t)N * 2 * items[j].n * ye;
-      if (j != k && (overlap(items[k].y, yb, items[j].y, ob) || overlap(items[k].y, yb, items[j].base, ob)))
+      if (j != k && (overlap(y, yb, items[j].y, ob) || overlap(y, yb, items[j].base, ob)))
         return fail(FAIRY2I_ERR_SHAPE, "y of item %d overlaps y or base of item %d", k, j);
+      if (overlap(y, yb, items[j].A, (uint64_t)L * r * 2 * m * xe) ||
+          overlap(y, yb, items[j].B, (uint64_t)L * 2 * items[j].n * r * xe) || overlap(y, yb, items[j].alpha, (uint64_t)L * 4))
+        return fail(FAIRY2I_ERR_SHAPE, "y of item %d overlaps A, B or alpha of item %d", k, j);
     }
   }
   if (int s = check_workspace(workspace, workspace_bytes, f2i::lora_workspace_bytes(count, N, m, r, S))) return s;
