@@ -406,7 +406,7 @@ int fairy2i_lora_grouped(const fairy2i_lora_item* items, int count, const void* 
  *     dA_a = sum_i dh_i x_i^T        dB_a = sum_i alpha_a dy_i (A_a x_i)^T     (rows i of adapter a)
  *   dy           [N][2n], x's dtype.
  *   dx_base, dx  [N][2m], dx_dtype FAIRY2I_F32 or FAIRY2I_BF16: dx_base is the gradient through
- *                the shared projection and dx may be dx_base (but overlaps neither x nor dy); both
+ *                the shared projection and dx may be dx_base (but overlaps no other argument); both
  *                NULL: dx is not computed.  Rows without an adapter are not written.
  *   dA, dB       out, fp32 [L][r][2m] and [L][2n][r]; zero for an adapter that no row uses.  An
  *                adapter of several segments gets the sum over all of them.  They overlap no other

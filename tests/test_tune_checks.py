@@ -106,6 +106,18 @@ def test_lora_backward_errors(L, kw, status):
     assert L.fairy2i_lora_backward(*back_args(**kw)) == status
 
 
+def test_lora_backward_refuses_outputs_over_inputs(L):
+    """dx is written while A, B, alpha and the segments may still be read, dA and dB while the segments are."""
+    far, out_bytes = 1 << 30, {"dx": 4 * 128 * 4, "dA": 2 * 8 * 128 * 4, "dB": 2 * 64 * 8 * 4}
+    size = {"A": 2 * 8 * 128 * 2, "B": 2 * 64 * 8 * 2, "alpha": 2 * 4, "ss": 3 * 4, "sa": 2 * 4}
+    for out, nbytes in out_bytes.items():
+        for name, have in size.items():
+            for at in (far, far - (have - 1) // 16 * 16, far + nbytes - 16):
+                kw = {out: far, name: at, **({"dxb": far} if out == "dx" else {})}
+                assert L.fairy2i_lora_backward(*back_args(**kw)) == 2, (out, name, at - far)
+                assert "overlaps" in f2.fairy2i_last_error()
+
+
 def loss_args(**kw):
     a = dict(h=FAKE, W=FAKE, dt=1, N=4, V=100, K=64, t=FAKE, loss=Y, lse=Z, ws=FAKE, wsb=1 << 30, st=S)
     a.update(kw)

@@ -788,18 +788,18 @@ int fairy2i_lora_backward(const void* dy, const void* x, int x_dtype, int64_t N,
     return fail(FAIRY2I_ERR_ALIGN, "dy, x, A, B, dx_base, dx, dA and dB need 16-byte alignment, alpha and the segments 4");
   const uint64_t xe = x_dtype == FAIRY2I_BF16 ? 2 : 4, de = dx_dtype == FAIRY2I_BF16 ? 2 : 4;
   const uint64_t dx_bytes = (uint64_t)N * 2 * m * de;
-  if (overlap(dx, dx_bytes, x, (uint64_t)N * 2 * m * xe) || overlap(dx, dx_bytes, dy, (uint64_t)N * 2 * n * xe) ||
-      (dx != dx_base && overlap(dx, dx_bytes, dx_base, dx_bytes)))
-    return fail(FAIRY2I_ERR_SHAPE, "dx overlaps x, dy, or dx_base without being dx_base");
-  // dA and dB are written while the other gradients' inputs are read
-  const struct { const void* p; uint64_t bytes; } all[] = {
-      {dA, (uint64_t)L * r * 2 * m * 4}, {dB, (uint64_t)L * 2 * n * r * 4}, {dx, dx_bytes}, {dx_base, dx_bytes},
-      {A, (uint64_t)L * r * 2 * m * xe}, {B, (uint64_t)L * 2 * n * r * xe}, {x, (uint64_t)N * 2 * m * xe},
-      {dy, (uint64_t)N * 2 * n * xe}};
-  for (int k = 0; k < 2; ++k)
-    for (int j = k + 1; j < 8; ++j)
+  if (dx != dx_base && overlap(dx, dx_bytes, dx_base, dx_bytes))
+    return fail(FAIRY2I_ERR_SHAPE, "dx overlaps dx_base without being dx_base");
+  // dA, dB and dx are written while the other gradients' inputs are read (dx and dx_base: above)
+  const struct { const void* p; uint64_t bytes; const char* name; } all[] = {
+      {dA, (uint64_t)L * r * 2 * m * 4, "dA"}, {dB, (uint64_t)L * 2 * n * r * 4, "dB"}, {dx, dx_bytes, "dx"},
+      {A, (uint64_t)L * r * 2 * m * xe, "A"}, {B, (uint64_t)L * 2 * n * r * xe, "B"}, {alpha, (uint64_t)L * 4, "alpha"},
+      {seg_start, (uint64_t)(S + 1) * 4, "seg_start"}, {seg_adapter, (uint64_t)S * 4, "seg_adapter"},
+      {x, (uint64_t)N * 2 * m * xe, "x"}, {dy, (uint64_t)N * 2 * n * xe, "dy"}, {dx_base, dx_bytes, "dx_base"}};
+  for (int k = 0; k < 3; ++k)
+    for (int j = k + 1; j < (k == 2 ? 10 : 11); ++j)
       if (overlap(all[k].p, all[k].bytes, all[j].p, all[j].bytes))
-        return fail(FAIRY2I_ERR_SHAPE, "%s overlaps an input or another gradient", k ? "dB" : "dA");
+        return fail(FAIRY2I_ERR_SHAPE, "%s overlaps %s", all[k].name, all[j].name);
   if (int s = check_workspace(workspace, workspace_bytes,
                               f2i::lora_backward_workspace_bytes(N, m, n, r, (int)L, S, x_dtype == FAIRY2I_BF16)))
     return s;
