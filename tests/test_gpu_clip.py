@@ -128,3 +128,21 @@ def test_stream_and_graph():
         torch.cuda.synchronize()
         assert torch.equal(norm, want_norm) and all(torch.equal(a, b) for a, b in zip(out, want)), k
         f2.fairy2i_clip_grads(grads, 1.0, out=[torch.empty_like(x) for x in grads])
+
+
+def test_norm_inside_a_gradient_is_refused():
+    """norm is stored before the gradients are scaled: in one of them, or in an output, the call is refused
+    and changes nothing."""
+    dev = device()
+    flat = torch.randn(40, generator=torch.Generator().manual_seed(6)).to(dev)
+    other, before = torch.zeros(40, device=dev), flat.clone()
+    for norm, out in ((flat[3:4], None), (flat[0:1], None), (flat[29:30], [other[:30]]), (other[7:8], [other[:30]])):
+        announce("clip norm inside", norm.data_ptr() - flat.data_ptr(), out is None)
+        with pytest.raises(f2.Fairy2iError, match="norm overlaps") as e:
+            f2.fairy2i_clip_grads([flat[:30]], 1.0, out=out, norm=norm)
+        assert e.value.status == 2
+    torch.cuda.synchronize()
+    assert torch.equal(flat, before) and not other.any()
+    f2.fairy2i_clip_grads([flat[:30]], 1.0, norm=flat[30:31])                    # next to them: taken
+    want = before[:30].double().norm().item()
+    assert abs(flat[30].item() - want) <= 2.0 ** -23 * want and torch.equal(flat[31:], before[31:])

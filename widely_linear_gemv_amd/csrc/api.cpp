@@ -917,6 +917,14 @@ int fairy2i_clip_grads(int count, const void* const* grads, void* const* out, co
     }
     if (written_twice(spans.get(), n))
       return fail(FAIRY2I_ERR_SHAPE, "a tensor is listed twice, or an output overlaps another output or a gradient");
+    // the norm is stored before the gradients are read for the second time
+    const uint64_t at = reinterpret_cast<uintptr_t>(norm);
+    for (int64_t k = 0; k < n; ++k) {
+      if (at >= spans[k].hi || at + 4 <= spans[k].lo) continue;
+      int dev = 0;                                   // without a device every call returns FAIRY2I_ERR_HIP
+      if (const hipError_t e = hipGetDevice(&dev); e != hipSuccess) return hip_status(e, "hipGetDevice");
+      return fail(FAIRY2I_ERR_SHAPE, "norm overlaps a gradient or an output");
+    }
   }
   // workspace: coefficient, table (8-byte entries), partial sums
   float* coef = static_cast<float*>(workspace);
