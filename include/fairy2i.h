@@ -462,8 +462,10 @@ int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64
  *           overlap any gradient; no two outputs overlap, so no tensor is listed twice in place.  A
  *           tensor of 0 elements is skipped (its pointers may be NULL).
  *   max_norm  >= 0; INFINITY computes the norm alone and leaves in-place gradients as they are.
- *   norm    out, fp32 [1], overlapping no gradient or output.  Not finite if a gradient is not finite: c is then 0 or NaN.
- * Squares and sums are fp64 in a fixed order; c is applied in fp32 and each output rounded once.
+ *   norm    out, fp32 [1], overlapping no gradient or output.  Not finite if a gradient is not finite: c
+ *           is then 0 or NaN.  (A norm past fp32's range is stored as infinity; c is right there too.)
+ * Squares, sums and c are fp64, sums in a fixed order; c is applied in fp32, as two factors where fp32's
+ * normal range does not hold it, and each output rounded once.
  *   workspace  fairy2i_clip_grads_workspace_bytes(count, numel) bytes, 16-byte aligned. */
 size_t fairy2i_clip_grads_workspace_bytes(int count, const int64_t* numel);
 int fairy2i_clip_grads(int count, const void* const* grads, void* const* out, const int64_t* numel, const int* dtypes,

@@ -146,3 +146,22 @@ def test_norm_inside_a_gradient_is_refused():
     f2.fairy2i_clip_grads([flat[:30]], 1.0, norm=flat[30:31])                    # next to them: taken
     want = before[:30].double().norm().item()
     assert abs(flat[30].item() - want) <= 2.0 ** -23 * want and torch.equal(flat[31:], before[31:])
+
+
+@pytest.mark.parametrize("size,max_norm", [(1e30, 1e-9), (3e38, 1e-20), (3e38, 1e-37), (1e38, 1.0), (1e-30, 1e-38)])
+def test_coefficients_under_the_normal_range(size, max_norm):
+    """c = max_norm / norm from 1e-40 to 1e-78 beside outputs that fp32 holds: as exact as any other."""
+    dev = device()
+    gen = torch.Generator().manual_seed(8)
+    grads = [((torch.rand(n, generator=gen) + 0.1) * size / 1.1).to(dt).to(dev)
+             for n, dt in ((9000, torch.float32), (77, torch.bfloat16), (5, torch.float32))]
+    before = [g.clone() for g in grads]
+    announce("clip small coefficient", size, max_norm)
+    norm = f2.fairy2i_clip_grads(grads, max_norm)
+    want = math.sqrt(sum(float((b.double() ** 2).sum()) for b in before))
+    assert abs(norm.item() - want) <= 2.0 ** -23 * want or (norm.item() == math.inf and want > 3.4e38)
+    c = min(1.0, torch.tensor(max_norm).double().item() / (want + 1e-6))        # max_norm enters as fp32
+    for g, b in zip(grads, before):
+        w = b.double() * c
+        tiny = 2.0 ** -126 * (w < 2.0 ** -125).double()                          # outputs under the normal range
+        assert ((g.double() - w).abs() <= w.abs() * (2.0 ** -22 + torch.finfo(g.dtype).eps / 2) + tiny).all()

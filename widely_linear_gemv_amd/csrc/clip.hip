@@ -119,7 +119,9 @@ __global__ __launch_bounds__(256) void k_square(const ClipItem* __restrict__ tab
   if (threadIdx.x == 0) part[piece0 + blockIdx.x] = t;
 }
 
-// coef[0] = c (fp32).
+// c = coef[0] coef[1]: 1 and c, or, where c is near or under fp32's smallest normal value, a power of two
+// and a factor that are both well inside the range (huge gradients clipped to a tiny norm: c as one fp32
+// value would keep a few of its 24 bits, or none).
 __global__ __launch_bounds__(1024) void k_norm(const double* __restrict__ part, int64_t pieces, float max_norm,
                                                float* __restrict__ norm, float* __restrict__ coef) {
   __shared__ double s_wave[16];
@@ -129,13 +131,16 @@ __global__ __launch_bounds__(1024) void k_norm(const double* __restrict__ part, 
   if (threadIdx.x == 0) {
     const double nrm = sqrt(t);
     const double c = (double)max_norm / (nrm + 1e-6);
+    const double used = max_norm == INFINITY || c > 1.0 ? 1.0 : c;           // NaN stays, but for the norm alone
+    const double scale = used > 0.0 && used < 0x1p-100 ? ldexp(1.0, ilogb(used) / 2) : 1.0;
     *norm = (float)nrm;
-    *coef = max_norm == INFINITY || c > 1.0 ? 1.f : (float)c;      // NaN stays, but for the norm alone
+    coef[0] = (float)scale;
+    coef[1] = (float)(used / scale);
   }
 }
 
 template <typename T>
-__device__ __forceinline__ void scaled(const T* p, T* o, int n, bool vec, float c) {
+__device__ __forceinline__ void scaled(const T* p, T* o, int n, bool vec, float scale, float c) {
   Chunk<T> q;
   q.load(p, n, vec);
 #pragma unroll
@@ -145,22 +150,22 @@ __device__ __forceinline__ void scaled(const T* p, T* o, int n, bool vec, float 
     uint32_t e[4] = {q.w[j].x, q.w[j].y, q.w[j].z, q.w[j].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 4) e[i] = __float_as_uint(c * __uint_as_float(e[i]));
-      else e[i] = pack_bf16(c * bf16_lo(e[i]), c * bf16_hi(e[i]));
+      if constexpr (sizeof(T) == 4) e[i] = __float_as_uint(c * (scale * __uint_as_float(e[i])));
+      else e[i] = pack_bf16(c * (scale * bf16_lo(e[i])), c * (scale * bf16_hi(e[i])));
     }
     reinterpret_cast<uint4*>(o)[at] = make_uint4(e[0], e[1], e[2], e[3]);
   }
 #pragma unroll 4
-  for (int i = q.whole + threadIdx.x; i < n; i += 256) store_out(o, i, c * value(p[i]));
+  for (int i = q.whole + threadIdx.x; i < n; i += 256) store_out(o, i, c * (scale * value(p[i])));
 }
 
 __global__ __launch_bounds__(256) void k_scale(const ClipItem* __restrict__ table, int count, int64_t pieces,
                                                int64_t piece0, const float* __restrict__ coef) {
-  const float c = *coef;
+  const float scale = coef[0], c = coef[1];
   const Piece q = find_piece(table, count, pieces, piece0 + blockIdx.x);
-  if (c == 1.f && q.out == q.g) return;
-  if (q.bf16) scaled(static_cast<const uint16_t*>(q.g) + q.i0, static_cast<uint16_t*>(q.out) + q.i0, q.n, q.vec, c);
-  else scaled(static_cast<const float*>(q.g) + q.i0, static_cast<float*>(q.out) + q.i0, q.n, q.vec, c);
+  if (scale == 1.f && c == 1.f && q.out == q.g) return;
+  if (q.bf16) scaled(static_cast<const uint16_t*>(q.g) + q.i0, static_cast<uint16_t*>(q.out) + q.i0, q.n, q.vec, scale, c);
+  else scaled(static_cast<const float*>(q.g) + q.i0, static_cast<float*>(q.out) + q.i0, q.n, q.vec, scale, c);
 }
 
 int64_t clip_pieces(int64_t numel) { return (numel + kPiece - 1) / kPiece; }
