@@ -354,7 +354,8 @@ int fairy2i_gemm_noalloc(const uint8_t* packed, const float* scales, int64_t n, 
 /* ---- beside the packed layers: low-rank adapters, the vocabulary loss, gradient clipping ----
  * Serving one frozen packed layer for many tenants, and tuning on top of it (the card's "Method"
  * keeps full-precision weights for training; here the packed layer stays fixed and small matrices
- * beside it learn).  Plain real-valued operators in the x~ / y~ layout above. */
+ * beside it learn).  Plain real-valued operators in the x~ / y~ layout above.  A call's workspace overlaps
+ * none of its other arguments. */
 
 /* Low-rank adapters of many requests at once: for every row i of segment s, with a = seg_adapter[s],
  *     y_i = base_i + alpha_a B_a (A_a x_i)

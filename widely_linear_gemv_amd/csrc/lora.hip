@@ -472,8 +472,9 @@ __global__ __launch_bounds__(256) void k_reduce_join(LoraReduceGroup grp, const 
 // 8 (i / 4) + 4 (f % 2) + i % 4 for bf16 (one instruction then covers 64 contiguous bytes of each row).  With long segments workgroups are ordered with the outputs innermost, so those that
 // run together read and write whole rows (beside gate/up, 2048 rows: 46 us, rows innermost 55).
 //
-// Bound by HBM: base is read and y written once.  Beside gate/up, 2048 x 11008 bf16 twice: 180 MB in 46 us,
-// 3.9 TB/s, where a copy of 1 GiB reaches 5.2.  (Stores and loads past the caches: 48.5 and 55 us.)  One
+// Bound by HBM: base is read and y written once.  Beside gate/up, 2048 x 11008 bf16 twice: 46 us for 137 MB
+// fetched and 89 written, 4.9 TB/s, where a copy of 1 GiB reaches 5.2; 102 MB of the fetch are needed, the
+// rest is adapters that several L2s fetch.  (Stores and loads past the caches: 48.5 and 55 us.)  One
 // row and one adapter, 4096 outputs, is latency: 7 us, three dependent loads deep.
 template <typename T, typename YT, int TF, bool READY, int RANKS>
 __global__ __launch_bounds__(256) void k_expand(LoraExpandGroup grp, const int32_t* __restrict__ seg_start,
@@ -666,7 +667,7 @@ __global__ __launch_bounds__(256) void k_transpose(LoraTranspose ta, LoraTranspo
 // the contraction).  Rows of other segments are neither copied (zeros stand for them) nor counted (their
 // factors are masked), so a NaN in another request's row cannot reach the sum.  Splits are joined in
 // order by k_outer_join (splits > 1), so the result never depends on scheduling.  2048 x 4096 bf16 twice at
-// rank 16: 12.5 us for 33.6 MB (2.7 TB/s; register operands, read two bytes at a time, took 20.2), and 4 us
+// rank 16: 12 us for 33.6 MB (2.8 TB/s; register operands, read two bytes at a time, took 20.2), and 4 us
 // for the join of 8 splits.
 template <typename T, int RT>
 __global__ __launch_bounds__(256) void k_outer(LoraOuterGroup grp, const int32_t* __restrict__ seg_start,

@@ -47,8 +47,10 @@ __device__ __forceinline__ void mma(v4f& acc, const v4u& a, const v4u& b) {
 }
 __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
-// exp(x) for x <= 0: off by |x| 2^-24 of itself, which in sum_v exp(l_v - top) comes to at most
-// log(V) 2^-24 of the sum (the mean distance from the maximum under the softmax is at most log V).
+// exp(x) for x <= 0: off by 1.25 |x| 2^-24 of itself (the product's rounding, and the constant's, a quarter
+// of that) and by the exp2 instruction's own error, about a unit in the last place (2^-23).  In
+// sum_v exp(l_v - top) that comes to at most 1.25 log(V) 2^-24 + 2^-23 of the sum (the mean distance from the
+// maximum under the softmax is at most log V).
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
 // exp(l - top), 1 where both are the same infinity.
@@ -226,9 +228,9 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
 // into its buffer and have NB - 1.5 steps to land.  Rows
 // past the end of a matrix read as 0; past the last step the copies repeat it, which nothing reads.
 //
-// Bound by the matrix cores under the power limit for many tokens: 2048 x 32000 x 4096 takes 400-480 us as
-// logits (1342-1119 TFLOP/s; the card's best library product reaches 1399 at 8192^3; on zeros the same
-// launch takes 365), 431-451 as p, 460-488 as dh and 464-498 as dW.  For 24 tokens by W from HBM:
+// Bound by the matrix cores under the power limit for many tokens: 2048 x 32000 x 4096 takes 400-500 us as
+// logits (1342-1074 TFLOP/s; the card's best library product reaches 1399 at 8192^3; on zeros the same
+// launch takes 365), 431-451 as p, 460-491 as dh and 464-507 as dW.  For 24 tokens by W from HBM:
 // 262 MB in 59 us, 4.4 TB/s (two buffers 64 us).
 template <int BM, int BN, int WA, int WB, int EPI, int NB = 2>
 __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
@@ -368,10 +370,11 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
 // 2048 x 32000 x 4096 3390 us against 3150.  Operands of the next step read between the products, or each
 // piece's load issued right after its cut, changed nothing: 2228-2350 us either way.)
 //
-// Bound by the matrix cores under the power limit: 2048 x 32000 x 4096 takes 2.23-2.39 ms as logits, six
-// bf16 products at 1445-1345 TFLOP/s (on zeros 2.02); p 2.3-2.5 ms, dh 2.3-2.5, dW 2.5-2.7.  263 x 5003 x
-// 1088: 30-33 us each, 200 tiles of 128 x 64 on 256 CUs; a step takes 0.66 us, of which the products alone
-// would be 0.32 and loads without anything else 0.32 (without cuts 0.47, without loads 0.51).
+// Bound by the matrix cores under the power limit: 2048 x 32000 x 4096 takes 2.33-2.42 ms as logits, six
+// bf16 products at 1383-1335 TFLOP/s (on zeros 2.08); p 2.38-2.46 ms, dh 2.42-2.48, dW 2.7.  263 x 5003 x
+// 1088: 31-38 us each, 200 tiles of 128 x 64 on 256 CUs; a step takes 0.69 us, of which the products alone
+// would be 0.32 and loads without anything else 0.32.  (With the parts cut off, two instructions fewer a pair:
+// 0.66 us a step, without cuts 0.47, without loads 0.51.)
 //   Plain operand: a part's row R is 64 bytes, its 16-byte segment sg in place sg ^ (R / 2 % 4).
 //   Transposed: rows of the contraction as in Side<bf16, ROWS, true>.
 template <int ROWS, bool TRANS, int THREADS>
@@ -581,8 +584,8 @@ __global__ __launch_bounds__(256) void k_hidden_join(const float* __restrict__ a
 // (with a longer run of padding in front G is 1: equal g then cost dW the rounding that different ones do).  A
 // g that is not finite is its own s_i, so that it reaches its outputs.
 // Rows of `scaled` are 0 for tokens that do not count or have g = 0: padding may hold anything, and p = 0
-// times a NaN would be one in every row of dW.  fp32 needs the copy for this alone.  13 us for 2048 x 4096
-// bf16 (8 without the target's logits), of a step's 1890; fp32 13 us of 9310.
+// times a NaN would be one in every row of dW.  fp32 needs the copy for this alone.  12-13 us for 2048 x 4096
+// bf16 (8 without the target's logits), of a step's 1840-1890; fp32 13 us of 9870-10070.
 constexpr int kScanned = 4096;
 constexpr float kLeastRest = 0x1p-16f;       // f_i under which it stays in p
 struct GradScales {                          // [N] each, but for all [1]
