@@ -465,3 +465,30 @@ def test_fp32_product_of_two_values(w):
     _, lse = f2.fairy2i_vocab_loss(h.to(dev), W.to(dev), torch.zeros(len(x), dtype=torch.int64, device=dev))
     want = x.double() * W[0, 5].double()
     close(lse, want, (2.0 ** -24 + 2.0 ** -33 + 2.0 ** -27 + 2.0 ** -23) * want.abs(), w)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_confident_targets(dt):
+    """Targets whose probability leaves from 0.1 down to under 2^-20 of it to the rest (bf16: on both sides of
+    where 1 - p_target stays in p), and tokens as sure of another entry: the formula's gradients."""
+    dev = device()
+    N, V, K = 96, 800, 512
+    gen = torch.Generator().manual_seed(53)
+    W = torch.randn(V, K, generator=gen) * K ** -0.5
+    sure = torch.randperm(V, generator=gen)[:N]
+    rest = 10.0 ** torch.linspace(-1, -8, N)
+    h = W[sure] / (W[sure] ** 2).sum(1, keepdim=True) * (V / rest).log()[:, None]
+    t = torch.where(torch.arange(N) % 3 == 2, (sure + 1) % V, sure)
+    c = {"h": h.to(dt), "W": W.to(dt), "t": t, "g": torch.rand(N, generator=gen) + 0.5}
+    d = {k: v.to(dev) for k, v in c.items()}
+    announce("vocab confident targets", dt)
+    loss, lse = f2.fairy2i_vocab_loss(d["h"], d["W"], d["t"])
+    z, _, wl, bl, wo, bo, _, at = reference(c)
+    f = 1 - (z[torch.arange(N), at] - wl).exp()
+    assert (f < 2.0 ** -18).any() and (f > 0.9).any() and ((f > 2.0 ** -15) & (f < 2.0 ** -8)).any()
+    close(lse, wl, bl, "lse")
+    close(loss, wo, bo, "loss")
+    dh, dW = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], d["t"], lse, d["g"])
+    wh, bh, wW, bW = grad_reference(c)
+    close(dh, wh, bh, "dh")
+    close(dW, wW, bW, "dW")
