@@ -443,9 +443,10 @@ int fairy2i_vocab_loss(const void* h, const void* W, int x_dtype, int64_t N, int
  *     dh_i = sum_v p_iv W_v        dW_v = sum_i p_iv h_i
  * in pieces of the vocabulary, whose logits are computed again; p is held in x_dtype between the two
  * products, sums are fp32 and each output is rounded once.  (bf16: p is in units of g_i (1 - p_target),
- * so the target's entry is not rounded; these are applied to the fp32 sums of dh and cost dW one rounding of
- * h, which is small where all g are equal and targets are unlikely.  Against 64 bits, with target
- * probabilities of 0.2 to 0.7: dh 0.0017 of its norm, the error of its own rounding, and dW 0.0024.)  A
+ * so the target's entry is not rounded unless 1 - p_target < 2^-16; these are applied to the fp32 sums of dh
+ * and cost dW one rounding of h, which is small where all g are equal and targets are unlikely.  Against 64
+ * bits, with target probabilities of 0.2 to 0.7: dh 0.0017 of its norm, the error of its own rounding, and dW
+ * 0.0024.  fp32: tokens with |g_i| under 2^-110 keep fewer bits, as p's parts leave bf16's normal range.)  A
  * token that does not count or has g_i = 0 adds nothing, whatever its row of h holds (padding may hold
  * NaN).
  *   dh [N][K], dW [V][K], x_dtype, overlapping no input and not each other; either may be NULL (not
