@@ -102,7 +102,7 @@ def prepare(case, seed):
         st["xs"] = _normal((case["B"], cols), 1.0, gen, dt)
         if own:
             import widely_linear_gemv_amd as f2
-            st["layer"] = f2.fairy2i_w4_pack(st["codes"], st["scale"], G, st["zero"])
+            st["layer"] = f2.fairy2i_pack_w4(st["codes"], st["scale"], G, st["zero"])
     elif case["op"] in ("distill", "distill_grad"):
         N, K, V, top = case["N"], case["K"], case["V"], min(case["top"], case["V"])
         st["h"] = _normal((N, K), 1.0, gen, dt)
@@ -219,7 +219,7 @@ def run(st):
     if own:
         import widely_linear_gemv_amd as f2
         if op == "w4":
-            return f2.fairy2i_w4_gemv(st["layer"], st["xs"], y_dtype=_DT[st["y"]])
+            return f2.fairy2i_gemv_w4(st["layer"], st["xs"], y_dtype=_DT[st["y"]])
         if op == "distill":
             loss, lse = f2.fairy2i_distill(st["h"], st["W"], st["top_index"], st["top_logit"], st["temperature"])
             return {"loss": loss, "lse": lse}
