@@ -351,6 +351,36 @@ int fairy2i_gemm_noalloc(const uint8_t* packed, const float* scales, int64_t n, 
                          const void* x, int x_dtype, float* x_scale, int64_t N,
                          void* y, int y_dtype, hipStream_t stream);
 
+/* ---- a packed layer beside the model it came from ----
+ * Layers that two bits hurt too much are kept at four. */
+
+/* A real layer W [rows][cols] held as four-bit codes with a scale and a zero point for every row and
+ * group of `group` neighbouring columns (the last group may be short), from any quantizer of that form:
+ *     W_ij = s_{i, j / group} (c_ij - z_{i, j / group})
+ * fairy2i_pack_w4 lays it out once for fairy2i_gemv_w4.
+ *   codes    uint8 [rows][cols], one code 0..15 a byte (higher bits are ignored).
+ *   scales   [rows][ceil(cols / group)], scales_dtype FAIRY2I_F32 or FAIRY2I_BF16, kept as they are.
+ *   zeros    uint8 [rows][ceil(cols / group)], any byte, or NULL: 8 everywhere.
+ *   packed   out, fairy2i_packed_bytes_w4(...) bytes, 16-byte aligned, overlapping no input: per tile of 16 rows
+ *            (the last padded) and 128 columns 1 KB of codes, tiles one after another; then per tile and
+ *            group 16 scales and 16 zero points.
+ * group 32, 64 or 128; 1 <= rows <= 2^24, 1 <= cols <= 2^20 and ceil(rows / 16) ceil(cols / 128) <= 2^23.
+ * Projections that read the same x (q, k and v) are one layer, their rows one after another. */
+size_t fairy2i_packed_bytes_w4(int64_t rows, int64_t cols, int group, int scales_dtype);
+int fairy2i_pack_w4(const uint8_t* codes, const void* scales, int scales_dtype, const uint8_t* zeros, int64_t rows,
+                    int64_t cols, int group, uint8_t* packed, hipStream_t stream);
+
+/* y_b = W x_b for 1 <= b <= B <= 16.
+ *   packed   from fairy2i_pack_w4 with the same rows, cols, group and scales_dtype.
+ *   x        [B][cols], x_dtype FAIRY2I_F32 or FAIRY2I_BF16; 16-byte aligned as a whole, rows of any length.
+ *   y        out, [B][rows], y_dtype FAIRY2I_F32 or FAIRY2I_BF16 (rounded once), 16-byte aligned, overlapping
+ *            neither packed nor x.
+ * Exact products of bf16 x (fp32 x: as three bf16 parts that hold it) in fp32 sums of sum_j (16 + c) x and
+ * sum_j x for each group, in an order that does not depend on B or the launch.  A NaN in a batch entry stays
+ * in that entry; an infinity gives NaN or infinity in its outputs.  Uses no workspace. */
+int fairy2i_gemv_w4(const uint8_t* packed, int64_t rows, int64_t cols, int group, int scales_dtype, const void* x,
+                    int x_dtype, int64_t B, void* y, int y_dtype, hipStream_t stream);
+
 /* ---- beside the packed layers: low-rank adapters, the vocabulary loss, gradient clipping ----
  * Serving one frozen packed layer for many tenants, and tuning on top of it (the card's "Method"
  * keeps full-precision weights for training; here the packed layer stays fixed and small matrices

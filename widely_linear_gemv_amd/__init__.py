@@ -98,6 +98,10 @@ SIGNATURES["fairy2i_clip_grads_workspace_bytes"] = (_SZ, [_INT, ctypes.POINTER(_
 SIGNATURES["fairy2i_clip_grads"] = (_INT, [_INT, ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.POINTER(_I64),
                                            ctypes.POINTER(_INT), _F32, _P, _P, _SZ, _P])
 
+SIGNATURES["fairy2i_packed_bytes_w4"] = (_SZ, [_I64, _I64, _INT, _INT])
+SIGNATURES["fairy2i_pack_w4"] = (_INT, [_P, _P, _INT, _P, _I64, _I64, _INT, _P, _P])
+SIGNATURES["fairy2i_gemv_w4"] = (_INT, [_P, _I64, _I64, _INT, _INT, _P, _INT, _I64, _P, _INT, _P])
+
 _lib = None
 
 
@@ -1036,3 +1040,88 @@ def _refuse_clip(grads, outs, max_norm, norm):
         _check_plain(norm, "norm", (torch.float32,), (1,))
     _gpu(*[(g, f"grads[{k}]") for k, g in enumerate(grads)], *[(o, f"out[{k}]") for k, o in enumerate(outs)], (norm, "norm"))
     raise ValueError("fairy2i_clip_grads: the arguments do not fit together")
+
+
+# ---- a packed layer beside the model it came from: layers kept at four bits ----
+
+class W4Layer:
+    """A layer kept at four bits, as fairy2i_pack_w4 lays it out: the uint8 buffer, its rows, columns and
+    group, and the dtype its scales are held in."""
+
+    def __init__(self, buf: torch.Tensor, rows: int, cols: int, group: int, scales_dtype=torch.bfloat16):
+        _tensor(buf, "buf")
+        _dtype(buf, "buf", torch.uint8)
+        if scales_dtype not in _FLOATS:
+            raise ValueError(f"scales_dtype: {scales_dtype}, need torch.float32 or torch.bfloat16")
+        nbytes = fairy2i_packed_bytes_w4(rows, cols, group, scales_dtype)
+        if nbytes == 0:
+            raise ValueError(f"rows = {rows}, cols = {cols}, group = {group}: sizes out of range")
+        _min_bytes(buf, "buf", nbytes)
+        _on_gpu(buf, "buf")
+        self.buf, self.rows, self.cols, self.group, self.scales_dtype = buf, rows, cols, group, scales_dtype
+
+    @property
+    def device(self):
+        return self.buf.device
+
+
+def fairy2i_packed_bytes_w4(rows: int, cols: int, group: int, scales_dtype=torch.bfloat16) -> int:
+    return int(lib().fairy2i_packed_bytes_w4(rows, cols, group, _DTYPE[scales_dtype]))
+
+
+@_on_stream
+def fairy2i_pack_w4(codes: torch.Tensor, scales: torch.Tensor, group: int, zeros=None, *, packed=None) -> W4Layer:
+    """codes uint8 [rows][cols] (0..15, one a byte), scales [rows][ceil(cols / group)] (fp32 or bf16) and zero
+    points uint8 of the same shape (None: 8) -> the layer W = scale (code - zero), laid out for
+    fairy2i_gemv_w4.  packed: a uint8 buffer to fill (allocated when None)."""
+    _tensor(codes, "codes")
+    _dtype(codes, "codes", torch.uint8)
+    if codes.dim() != 2:
+        raise ValueError(f"codes: shape {tuple(codes.shape)}, need [rows][cols]")
+    if group not in (32, 64, 128):
+        raise ValueError(f"group: {group}, need 32, 64 or 128")
+    rows, cols = codes.shape
+    _on_gpu(codes, "codes")
+    _check_plain(scales, "scales", (torch.float32, torch.bfloat16), (rows, -(-cols // group)))
+    if zeros is not None:
+        _check_plain(zeros, "zeros", (torch.uint8,), (rows, -(-cols // group)))
+    if packed is None:
+        packed = torch.empty((fairy2i_packed_bytes_w4(rows, cols, group, scales.dtype),), dtype=torch.uint8, device=codes.device)
+    layer = W4Layer(packed, rows, cols, group, scales.dtype)
+    _gpu((codes, "codes"), (scales, "scales"), (zeros, "zeros"), (packed, "packed"))
+    _check(lib().fairy2i_pack_w4(codes.data_ptr(), scales.data_ptr(), _DTYPE[scales.dtype], _ptr(zeros), rows, cols, group,
+                                 packed.data_ptr(), _stream()))
+    return layer
+
+
+def fairy2i_gemv_w4(layer: W4Layer, x: torch.Tensor, *, y_dtype=torch.float32, y=None, stream=None) -> torch.Tensor:
+    """y = x W^T of a layer kept at four bits: x [B][cols] fp32 or bf16, B <= 16 -> y [B][rows]."""
+    if not isinstance(layer, W4Layer):
+        raise TypeError(f"layer: expected a W4Layer, got {type(layer).__name__}")
+    with _scope(x, stream):
+        dev = layer.buf.get_device()
+        if not (isinstance(x, torch.Tensor) and x.dtype in _FLOATS and x.dim() == 2 and x.shape[1] == layer.cols
+                and x.is_contiguous() and x.get_device() == dev >= 0
+                and (y is None or isinstance(y, torch.Tensor) and y.dtype in _FLOATS
+                     and _fits(y, y.dtype, (x.shape[0], layer.rows), dev))):
+            _refuse_gemv_w4(layer, x, y)
+        if y is None:
+            if y_dtype not in _FLOATS:
+                raise ValueError(f"y_dtype: {y_dtype}, need torch.float32 or torch.bfloat16")
+            y = torch.empty((x.shape[0], layer.rows), dtype=y_dtype, device=x.device)
+        _check(lib().fairy2i_gemv_w4(layer.buf.data_ptr(), layer.rows, layer.cols, layer.group, _DTYPE[layer.scales_dtype],
+                                     x.data_ptr(), _DTYPE[x.dtype], x.shape[0], y.data_ptr(), _DTYPE[y.dtype], _stream()))
+    return y
+
+
+def _refuse_gemv_w4(layer, x, y):
+    """Raises for the first argument of fairy2i_gemv_w4 that does not fit."""
+    _tensor(x, "x")
+    _dtype(x, "x", torch.float32, torch.bfloat16)
+    if x.dim() != 2 or x.shape[1] != layer.cols:
+        raise ValueError(f"x: shape {tuple(x.shape)}, need [B][{layer.cols}]")
+    _on_gpu(x, "x")
+    if y is not None:
+        _check_y(y, (x.shape[0], layer.rows), x.device)
+    _gpu((layer.buf, "layer"), (x, "x"), (y, "y"))
+    raise ValueError("fairy2i_gemv_w4: the arguments do not fit together")

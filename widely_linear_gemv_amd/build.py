@@ -53,6 +53,7 @@ SOURCES = {
     "gemv_f8x.hip": [],
     "prefill.hip": ["-ffp-contract=off"],
     "dequant.hip": ["-ffp-contract=off"],
+    "w4.hip": [],
     "lora.hip": [],
     "vocab_loss.hip": [],
     "clip.hip": [],

@@ -874,6 +874,58 @@ int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64
   return hip_status(f2i::launch_vocab_loss_backward(a, stream), "vocabulary loss backward launch");
 }
 
+// Layers kept at four bits: tiles x blocks of 128 columns bounds the threads of one packing launch.
+static bool w4_sizes_ok(int64_t rows, int64_t cols, int group) {
+  return (group == 32 || group == 64 || group == 128) && rows >= 1 && rows <= (int64_t(1) << 24) && cols >= 1 &&
+         cols <= (int64_t(1) << 20) && (rows + 15) / 16 * ((cols + 127) / 128) <= (int64_t(1) << 23);
+}
+
+static int check_w4_sizes(int64_t rows, int64_t cols, int group) {
+  if (w4_sizes_ok(rows, cols, group)) return FAIRY2I_OK;
+  return fail(FAIRY2I_ERR_SHAPE, "rows = %lld, cols = %lld, group = %d: need 1 <= rows <= 2^24, 1 <= cols <= 2^20, "
+              "ceil(rows / 16) ceil(cols / 128) <= 2^23 and groups of 32, 64 or 128", (long long)rows, (long long)cols, group);
+}
+
+size_t fairy2i_packed_bytes_w4(int64_t rows, int64_t cols, int group, int scales_dtype) {
+  if (!w4_sizes_ok(rows, cols, group) || (scales_dtype != FAIRY2I_F32 && scales_dtype != FAIRY2I_BF16)) return 0;
+  return f2i::w4_bytes(rows, cols, group, scales_dtype == FAIRY2I_BF16);
+}
+
+int fairy2i_pack_w4(const uint8_t* codes, const void* scales, int scales_dtype, const uint8_t* zeros, int64_t rows,
+                    int64_t cols, int group, uint8_t* packed, hipStream_t stream) {
+  if (!codes || !scales || !packed) return fail(FAIRY2I_ERR_NULL, "codes, scales and packed are required");
+  if (int s = check_float_dtype(scales_dtype, "scales_dtype")) return s;
+  if (int s = check_w4_sizes(rows, cols, group)) return s;
+  const uint64_t se = scales_dtype == FAIRY2I_BF16 ? 2 : 4, groups = (uint64_t)(cols + group - 1) / group;
+  if (!aligned(packed, 16) || !aligned(scales, se))
+    return fail(FAIRY2I_ERR_ALIGN, "packed needs 16-byte alignment, scales their element's");
+  const uint64_t pb = f2i::w4_bytes(rows, cols, group, scales_dtype == FAIRY2I_BF16);
+  if (overlap(packed, pb, codes, (uint64_t)rows * cols) || overlap(packed, pb, scales, rows * groups * se) ||
+      overlap(packed, pb, zeros, rows * groups))
+    return fail(FAIRY2I_ERR_SHAPE, "packed must not overlap codes, scales or zeros");
+  return hip_status(f2i::launch_w4_pack(codes, scales, scales_dtype == FAIRY2I_BF16, zeros, rows, cols, group, packed, stream),
+                    "four-bit pack launch");
+}
+
+int fairy2i_gemv_w4(const uint8_t* packed, int64_t rows, int64_t cols, int group, int scales_dtype, const void* x,
+                    int x_dtype, int64_t B, void* y, int y_dtype, hipStream_t stream) {
+  if (!packed || !x || !y) return fail(FAIRY2I_ERR_NULL, "packed, x and y are required");
+  if (int s = check_float_dtype(scales_dtype, "scales_dtype")) return s;
+  if (int s = check_float_dtype(x_dtype, "x_dtype")) return s;
+  if (int s = check_float_dtype(y_dtype, "y_dtype")) return s;
+  if (int s = check_w4_sizes(rows, cols, group)) return s;
+  if (B < 1 || B > 16) return fail(FAIRY2I_ERR_SHAPE, "B = %lld: need 1 <= B <= 16", (long long)B);
+  if (!aligned(packed, 16) || !aligned(x, 16) || !aligned(y, 16))
+    return fail(FAIRY2I_ERR_ALIGN, "packed, x and y need 16-byte alignment");
+  const uint64_t yb = (uint64_t)B * rows * (y_dtype == FAIRY2I_BF16 ? 2 : 4);
+  if (overlap(y, yb, packed, f2i::w4_bytes(rows, cols, group, scales_dtype == FAIRY2I_BF16)) ||
+      overlap(y, yb, x, (uint64_t)B * cols * (x_dtype == FAIRY2I_BF16 ? 2 : 4)))
+    return fail(FAIRY2I_ERR_SHAPE, "y must not overlap packed or x");
+  const f2i::W4Args a{packed, x, y, rows, cols, group, scales_dtype == FAIRY2I_BF16, x_dtype == FAIRY2I_BF16,
+                      y_dtype == FAIRY2I_BF16, (int)B};
+  return hip_status(f2i::launch_w4_gemv(a, stream), "four-bit gemv launch");
+}
+
 static int64_t clip_total_pieces(int count, const int64_t* numel) {
   int64_t pieces = 0;
   for (int k = 0; k < count; ++k)

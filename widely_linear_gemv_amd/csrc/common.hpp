@@ -217,6 +217,19 @@ hipError_t launch_gemm(const uint8_t* packed, const float* scales, int n, int m,
                        const int8_t* q, const float* delta, int N, void* y, int y_mode,
                        hipStream_t s);
 
+// ---- layers kept at four bits (w4.hip) ----
+struct W4Args {
+  const uint8_t* packed;
+  const void* x;        // [B][cols]
+  void* y;              // [B][rows]
+  int64_t rows, cols;
+  int group, scales_bf16, x_bf16, y_bf16, B;
+};
+size_t w4_bytes(int64_t rows, int64_t cols, int group, int scales_bf16);
+hipError_t launch_w4_pack(const uint8_t* codes, const void* scales, int scales_bf16, const uint8_t* zeros, int64_t rows,
+                          int64_t cols, int group, uint8_t* packed, hipStream_t s);
+hipError_t launch_w4_gemv(const W4Args& a, hipStream_t s);
+
 // ---- low-rank adapters (lora.hip) ----
 constexpr int kMaxLoraItems = 8;      // projections per launch; the tables travel in the kernel arguments
 constexpr int kMaxLoraRank = 128;

@@ -15,6 +15,9 @@ digits_given=True the digit forms are made once when the step is built and the s
 GEMVs alone (for inputs that arrive in digit form, from a producer that writes it).  This module only sequences
 calls of the C ABI (through the binding); all arithmetic runs in the library's kernels.
 
+A projection may be kept at four bits (a W4Layer in place of its packed form and scales): it is a
+launch of its own behind its group's, and takes the x itself whatever form the group's is in.
+
 With adapters, each group's launch is followed by one grouped low-rank adapter call (two launches)
 that adds every request's own adapter to the group's outputs in place.
 """
@@ -23,8 +26,8 @@ from __future__ import annotations
 import torch
 
 from . import (GEMV_AUTO, GEMV_MFMA_F4, GEMV_MFMA_I8, X_DIGITS, X_DIGITS_F6, XDigits,
-               fairy2i_gemv_grouped, fairy2i_lora_grouped, fairy2i_lora_workspace_bytes, fairy2i_x_digits, fairy2i_x_digits_bytes, fairy2i_x_digits_f6,
-               fairy2i_x_digits_f6_bytes)
+               W4Layer, fairy2i_gemv_grouped, fairy2i_lora_grouped, fairy2i_lora_workspace_bytes, fairy2i_x_digits, fairy2i_x_digits_bytes, fairy2i_x_digits_f6,
+               fairy2i_x_digits_f6_bytes, fairy2i_gemv_w4)
 
 # the digit form each digit-form kernel takes: (size in bytes, converter, dtype code)
 _DIGIT_FORMS = {GEMV_MFMA_F4: (fairy2i_x_digits_f6_bytes, fairy2i_x_digits_f6, X_DIGITS_F6),
@@ -37,7 +40,7 @@ GROUPS = 4
 
 
 class DecodeStep:
-    """layers[L][p] = (packed, scales) for projection p of layer L (shapes as PROJECTIONS);
+    """layers[L][p] = (packed, scales) for projection p of layer L (shapes as PROJECTIONS), or its W4Layer;
     xs[L][g] = bf16 input [B][2m] of group g of layer L.  Outputs: self.ys[L][p] fp32 [B][2n].
     digits_given (digit-form algos only): make each x's digit form once, here, instead of in
     every run().
@@ -48,6 +51,10 @@ class DecodeStep:
     def __init__(self, layers, xs, *, algo: int | None = None, digits_given: bool = False, adapters=None,
                  segments=None):
         self.layers, self.xs = layers, xs
+        for L, projs in enumerate(layers):
+            for p, (name, rows, cols, _) in zip(projs, PROJECTIONS):
+                if isinstance(p, W4Layer) and (p.rows, p.cols) != (rows, cols):
+                    raise ValueError(f"layer {L}, {name}: {p.rows} x {p.cols} at four bits, need {rows} x {cols}")
         if (adapters is None) != (segments is None):
             raise ValueError("adapters and segments go together")
         self.adapters, self.segments = adapters, segments
@@ -86,13 +93,18 @@ class DecodeStep:
         for L, projs in enumerate(self.layers):
             for g in range(GROUPS):
                 x = self.xs[L][g]
-                if self.digits_given:
-                    x = self.digits[L][g]
-                elif self.digits is not None:
-                    x = self._convert(x, out=self.digits[L][g], stream=stream)
-                items = [(projs[p][0], projs[p][1], x, self.ys[L][p])
-                         for p, (_, _, _, grp) in enumerate(PROJECTIONS) if grp == g]
-                fairy2i_gemv_grouped(items, algo=self.algo, stream=stream)
+                mine = [p for p, (_, _, _, grp) in enumerate(PROJECTIONS) if grp == g]
+                two_bit = [p for p in mine if not isinstance(projs[p], W4Layer)]
+                if two_bit:
+                    if self.digits_given:
+                        x = self.digits[L][g]
+                    elif self.digits is not None:
+                        x = self._convert(x, out=self.digits[L][g], stream=stream)
+                    fairy2i_gemv_grouped([(projs[p][0], projs[p][1], x, self.ys[L][p]) for p in two_bit], algo=self.algo,
+                                         stream=stream)
+                for p in mine:
+                    if p not in two_bit:
+                        fairy2i_gemv_w4(projs[p], self.xs[L][g], y=self.ys[L][p], stream=stream)
                 if self.adapters is not None:
                     beside = [(*self.adapters[L][p], self.ys[L][p], None) for p, (_, _, _, grp) in enumerate(PROJECTIONS)
                               if grp == g and self.adapters[L][p] is not None]
