@@ -381,6 +381,40 @@ int fairy2i_pack_w4(const uint8_t* codes, const void* scales, int scales_dtype, 
 int fairy2i_gemv_w4(const uint8_t* packed, int64_t rows, int64_t cols, int group, int scales_dtype, const void* x,
                     int x_dtype, int64_t B, void* y, int y_dtype, hipStream_t stream);
 
+/* Distillation from a teacher's top logits, the original model's say, without storing the student's
+ * logits: with the student's l_iv = <h_i, W_v> / temperature, and t_ik the softmax of token i's listed
+ * teacher logits over the temperature, over the slots k whose index lies in [0, V),
+ *     lse_i = log sum_v exp l_iv     loss_i = sum_k t_ik (log t_ik - l_{i, index_ik} + lse_i)
+ * (a slot with t = 0 adds nothing).
+ *   h, W       as fairy2i_vocab_loss.
+ *   top_index  int64 [N][top], 1 <= top <= 128, in any order; a slot whose index is outside [0, V) (-1,
+ *              say) is unused, so lists may be of any length.  An index listed twice counts with both of
+ *              its probabilities.
+ *   top_logit  [N][top], top_dtype FAIRY2I_F32 or FAIRY2I_BF16: finite, or minus infinity for probability 0.
+ *              (NaN or plus infinity gives NaN in that token's loss and gradient.)  Unused slots may hold
+ *              anything.
+ *   temperature  from 2^-20 to 2^20.  (The customary factor temperature^2 belongs into g, below.)
+ *   loss, lse  out, fp32 [N], overlapping nothing else.  A token whose list leaves no probability (no used
+ *              slot, or minus infinity in all) does not count: its loss is 0.
+ * Sums, operands and workspaces as fairy2i_vocab_loss. */
+size_t fairy2i_distill_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype, int top);
+int fairy2i_distill(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K, const int64_t* top_index,
+                    const void* top_logit, int top_dtype, int top, float temperature, float* loss, float* lse,
+                    void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Its gradient: with g_i the gradient of loss_i and lse from the forward call,
+ *     p_iv = g_i / temperature (exp(l_iv - lse_i) - sum of t_ik over the slots with index_ik = v)
+ *     dh_i = sum_v p_iv W_v        dW_v = sum_i p_iv h_i
+ * as fairy2i_vocab_loss_backward in everything else: pieces of the vocabulary, p held in x_dtype between the
+ * products (bf16: in units of a power of two near |g_i|, the rest of g_i applied to the fp32 sums of dh and,
+ * rounded, to h for dW, where all g equal cost nothing), fp32 sums, each output rounded once, either output
+ * NULL.  A token that does not count or has g_i = 0 adds nothing, whatever its row of h holds. */
+size_t fairy2i_distill_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype, int top);
+int fairy2i_distill_backward(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K,
+                             const int64_t* top_index, const void* top_logit, int top_dtype, int top, float temperature,
+                             const float* lse, const float* g, void* dh, void* dW, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
 /* ---- beside the packed layers: low-rank adapters, the vocabulary loss, gradient clipping ----
  * Serving one frozen packed layer for many tenants, and tuning on top of it (the card's "Method"
  * keeps full-precision weights for training; here the packed layer stays fixed and small matrices

@@ -101,6 +101,11 @@ SIGNATURES["fairy2i_clip_grads"] = (_INT, [_INT, ctypes.POINTER(_P), ctypes.POIN
 SIGNATURES["fairy2i_packed_bytes_w4"] = (_SZ, [_I64, _I64, _INT, _INT])
 SIGNATURES["fairy2i_pack_w4"] = (_INT, [_P, _P, _INT, _P, _I64, _I64, _INT, _P, _P])
 SIGNATURES["fairy2i_gemv_w4"] = (_INT, [_P, _I64, _I64, _INT, _INT, _P, _INT, _I64, _P, _INT, _P])
+SIGNATURES["fairy2i_distill_workspace_bytes"] = (_SZ, [_I64, _I64, _I64, _INT, _INT])
+SIGNATURES["fairy2i_distill"] = (_INT, [_P, _P, _INT, _I64, _I64, _I64, _P, _P, _INT, _INT, _F32, _P, _P, _P, _SZ, _P])
+SIGNATURES["fairy2i_distill_backward_workspace_bytes"] = (_SZ, [_I64, _I64, _I64, _INT, _INT])
+SIGNATURES["fairy2i_distill_backward"] = (_INT, [_P, _P, _INT, _I64, _I64, _I64, _P, _P, _INT, _INT, _F32, _P, _P, _P, _P,
+                                                 _P, _SZ, _P])
 
 _lib = None
 
@@ -1125,3 +1130,86 @@ def _refuse_gemv_w4(layer, x, y):
         _check_y(y, (x.shape[0], layer.rows), x.device)
     _gpu((layer.buf, "layer"), (x, "x"), (y, "y"))
     raise ValueError("fairy2i_gemv_w4: the arguments do not fit together")
+
+
+# ---- distillation from a teacher's top logits ----
+
+def _check_lists(h, W, top_index, top_logit):
+    """h [N][K], W [V][K] of one dtype and lists [N][top]; returns (N, V, K, top)."""
+    _tensor(h, "h")
+    _tensor(W, "W")
+    _dtype(h, "h", torch.float32, torch.bfloat16)
+    _dtype(W, "W", h.dtype)
+    if h.dim() != 2:
+        raise ValueError(f"h: shape {tuple(h.shape)}, need [N][K]")
+    if W.dim() != 2 or W.shape[1] != h.shape[1]:
+        raise ValueError(f"W: shape {tuple(W.shape)}, need [V][{h.shape[1]}]")
+    _on_gpu(h, "h")
+    _on_gpu(W, "W")
+    _tensor(top_index, "top_index")
+    _dtype(top_index, "top_index", torch.int64)
+    if top_index.dim() != 2 or top_index.shape[0] != h.shape[0]:
+        raise ValueError(f"top_index: shape {tuple(top_index.shape)}, need [{h.shape[0]}][top]")
+    _on_gpu(top_index, "top_index")
+    _check_plain(top_logit, "top_logit", (torch.float32, torch.bfloat16), tuple(top_index.shape))
+    return h.shape[0], W.shape[0], h.shape[1], top_index.shape[1]
+
+
+def fairy2i_distill_workspace_bytes(N: int, V: int, K: int, x_dtype: int, top: int) -> int:
+    return int(lib().fairy2i_distill_workspace_bytes(N, V, K, x_dtype, top))
+
+
+@_on_stream
+def fairy2i_distill(h: torch.Tensor, W: torch.Tensor, top_index: torch.Tensor, top_logit: torch.Tensor,
+                    temperature: float = 1.0, *, loss=None, lse=None, workspace=None):
+    """Per-token divergence of the student's softmax(h W^T / temperature), h [N][K], W [V][K], from the
+    teacher's, known by its top logits: top_index int64 [N][top] (outside [0, V): unused slot), top_logit fp32
+    or bf16.  Returns (loss, lse) fp32 [N]; tokens with an empty list get loss 0."""
+    N, V, K, top = _check_lists(h, W, top_index, top_logit)
+    f32 = torch.float32
+    if loss is not None:
+        _check_plain(loss, "loss", (f32,), (N,))
+    if lse is not None:
+        _check_plain(lse, "lse", (f32,), (N,))
+    _gpu((h, "h"), (W, "W"), (top_index, "top_index"), (top_logit, "top_logit"), (loss, "loss"), (lse, "lse"))
+    loss = torch.empty((N,), dtype=f32, device=h.device) if loss is None else loss
+    lse = torch.empty((N,), dtype=f32, device=h.device) if lse is None else lse
+    code = _DTYPE[h.dtype]
+    ws, nbytes, keep = _room(workspace, fairy2i_distill_workspace_bytes(N, V, K, code, top), h.device)
+    _check(lib().fairy2i_distill(h.data_ptr(), W.data_ptr(), code, N, V, K, top_index.data_ptr(), top_logit.data_ptr(),
+                                 _DTYPE[top_logit.dtype], top, temperature, loss.data_ptr(), lse.data_ptr(), ws, nbytes,
+                                 _stream()))
+    return loss, lse
+
+
+def fairy2i_distill_backward_workspace_bytes(N: int, V: int, K: int, x_dtype: int, top: int) -> int:
+    return int(lib().fairy2i_distill_backward_workspace_bytes(N, V, K, x_dtype, top))
+
+
+@_on_stream
+def fairy2i_distill_backward(h: torch.Tensor, W: torch.Tensor, top_index: torch.Tensor, top_logit: torch.Tensor,
+                             lse: torch.Tensor, g: torch.Tensor, temperature: float = 1.0, *, want_dh: bool = True,
+                             want_dW: bool = True, dh=None, dW=None, workspace=None):
+    """Gradient of fairy2i_distill: lse from the forward call, g fp32 [N] the gradient of each token's loss.
+    Returns (dh [N][K] or None, dW [V][K] or None), h's dtype; want_dh / want_dW False skip one of them."""
+    N, V, K, top = _check_lists(h, W, top_index, top_logit)
+    _check_plain(lse, "lse", (torch.float32,), (N,))
+    _check_plain(g, "g", (torch.float32,), (N,))
+    if not want_dh and not want_dW:
+        raise ValueError("fairy2i_distill_backward: nothing to compute")
+    if (dh is not None and not want_dh) or (dW is not None and not want_dW):
+        raise ValueError("an output was given for a gradient that is not wanted")
+    if dh is not None:
+        _check_plain(dh, "dh", (h.dtype,), (N, K))
+    if dW is not None:
+        _check_plain(dW, "dW", (h.dtype,), (V, K))
+    _gpu((h, "h"), (W, "W"), (top_index, "top_index"), (top_logit, "top_logit"), (lse, "lse"), (g, "g"), (dh, "dh"),
+         (dW, "dW"))
+    dh = torch.empty_like(h) if want_dh and dh is None else dh
+    dW = torch.empty_like(W) if want_dW and dW is None else dW
+    code = _DTYPE[h.dtype]
+    ws, nbytes, keep = _room(workspace, fairy2i_distill_backward_workspace_bytes(N, V, K, code, top), h.device)
+    _check(lib().fairy2i_distill_backward(h.data_ptr(), W.data_ptr(), code, N, V, K, top_index.data_ptr(),
+                                          top_logit.data_ptr(), _DTYPE[top_logit.dtype], top, temperature, lse.data_ptr(),
+                                          g.data_ptr(), _ptr(dh), _ptr(dW), ws, nbytes, _stream()))
+    return dh, dW

@@ -822,7 +822,7 @@ static int check_vocab_sizes(int64_t N, int64_t V, int64_t K) {
 }
 
 size_t fairy2i_vocab_loss_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype) {
-  return vocab_sizes_ok(N, V, K) ? f2i::vocab_loss_workspace_bytes(N, V, K, x_dtype == FAIRY2I_BF16) : 0;
+  return vocab_sizes_ok(N, V, K) ? f2i::vocab_loss_workspace_bytes(N, V, K, x_dtype == FAIRY2I_BF16, 0) : 0;
 }
 
 int fairy2i_vocab_loss(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K, const int64_t* target,
@@ -845,7 +845,7 @@ int fairy2i_vocab_loss(const void* h, const void* W, int x_dtype, int64_t N, int
 }
 
 size_t fairy2i_vocab_loss_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype) {
-  return vocab_sizes_ok(N, V, K) ? f2i::vocab_loss_backward_workspace_bytes(N, V, K, x_dtype == FAIRY2I_BF16) : 0;
+  return vocab_sizes_ok(N, V, K) ? f2i::vocab_loss_backward_workspace_bytes(N, V, K, x_dtype == FAIRY2I_BF16, 0) : 0;
 }
 
 int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K,
@@ -872,6 +872,87 @@ int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64
   a.h = h; a.W = W; a.target = target; a.N = N; a.V = V; a.K = K; a.bf16 = x_dtype == FAIRY2I_BF16;
   a.lse = lse; a.g = g; a.dh = dh; a.dW = dW; a.ws = workspace;
   return hip_status(f2i::launch_vocab_loss_backward(a, stream), "vocabulary loss backward launch");
+}
+
+// ---- distillation from a teacher's top logits: the vocabulary's products with lists in place of targets ----
+
+static constexpr int kMaxTop = 128;
+static bool distill_sizes_ok(int64_t N, int64_t V, int64_t K, int64_t top) {
+  return vocab_sizes_ok(N, V, K) && top >= 1 && top <= kMaxTop;
+}
+
+static int check_distill(int64_t N, int64_t V, int64_t K, int64_t top, float temperature) {
+  if (int s = check_vocab_sizes(N, V, K)) return s;
+  if (top < 1 || top > kMaxTop) return fail(FAIRY2I_ERR_SHAPE, "top = %lld: need 1 <= top <= %d", (long long)top, kMaxTop);
+  if (!(temperature >= 0x1p-20f && temperature <= 0x1p20f))
+    return fail(FAIRY2I_ERR_SHAPE, "temperature = %g: need 2^-20 to 2^20", (double)temperature);
+  return FAIRY2I_OK;
+}
+
+size_t fairy2i_distill_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype, int top) {
+  return distill_sizes_ok(N, V, K, top) ? f2i::vocab_loss_workspace_bytes(N, V, K, x_dtype == FAIRY2I_BF16, top) : 0;
+}
+
+int fairy2i_distill(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K, const int64_t* top_index,
+                    const void* top_logit, int top_dtype, int top, float temperature, float* loss, float* lse,
+                    void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!h || !W || !top_index || !top_logit || !loss || !lse)
+    return fail(FAIRY2I_ERR_NULL, "h, W, top_index, top_logit, loss and lse are required");
+  if (int s = check_float_dtype(x_dtype, "x_dtype")) return s;
+  if (int s = check_float_dtype(top_dtype, "top_dtype")) return s;
+  if (int s = check_distill(N, V, K, top, temperature)) return s;
+  const uint64_t xe = x_dtype == FAIRY2I_BF16 ? 2 : 4, te = top_dtype == FAIRY2I_BF16 ? 2 : 4, ob = (uint64_t)N * 4;
+  if (!aligned(h, 16) || !aligned(W, 16) || !aligned(top_index, 8) || !aligned(top_logit, te) || !aligned(loss, 4) ||
+      !aligned(lse, 4))
+    return fail(FAIRY2I_ERR_ALIGN, "h and W need 16-byte alignment, top_index 8, top_logit its element's, loss and lse 4");
+  const struct { const void* p; uint64_t bytes; } in[] = {
+      {h, (uint64_t)N * K * xe}, {W, (uint64_t)V * K * xe}, {top_index, (uint64_t)N * top * 8}, {top_logit, (uint64_t)N * top * te}};
+  for (const auto& r : in)
+    if (overlap(loss, ob, r.p, r.bytes) || overlap(lse, ob, r.p, r.bytes))
+      return fail(FAIRY2I_ERR_SHAPE, "loss and lse must not overlap h, W, top_index or top_logit");
+  if (overlap(loss, ob, lse, ob)) return fail(FAIRY2I_ERR_SHAPE, "loss and lse must not overlap each other");
+  if (int s = check_workspace(workspace, workspace_bytes, fairy2i_distill_workspace_bytes(N, V, K, x_dtype, top))) return s;
+  f2i::VocabArgs a{};
+  a.h = h; a.W = W; a.N = N; a.V = V; a.K = K; a.bf16 = x_dtype == FAIRY2I_BF16;
+  a.loss = loss; a.lse_out = lse; a.ws = workspace;
+  a.top_index = top_index; a.top_logit = top_logit; a.top = top; a.top_bf16 = top_dtype == FAIRY2I_BF16;
+  a.temperature = temperature;
+  return hip_status(f2i::launch_vocab_loss(a, stream), "distillation launch");
+}
+
+size_t fairy2i_distill_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype, int top) {
+  return distill_sizes_ok(N, V, K, top) ? f2i::vocab_loss_backward_workspace_bytes(N, V, K, x_dtype == FAIRY2I_BF16, top) : 0;
+}
+
+int fairy2i_distill_backward(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K,
+                             const int64_t* top_index, const void* top_logit, int top_dtype, int top, float temperature,
+                             const float* lse, const float* g, void* dh, void* dW, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+  if (!h || !W || !top_index || !top_logit || !lse || !g)
+    return fail(FAIRY2I_ERR_NULL, "h, W, top_index, top_logit, lse and g are required");
+  if (!dh && !dW) return fail(FAIRY2I_ERR_NULL, "one of dh and dW is required");
+  if (int s = check_float_dtype(x_dtype, "x_dtype")) return s;
+  if (int s = check_float_dtype(top_dtype, "top_dtype")) return s;
+  if (int s = check_distill(N, V, K, top, temperature)) return s;
+  const uint64_t xe = x_dtype == FAIRY2I_BF16 ? 2 : 4, te = top_dtype == FAIRY2I_BF16 ? 2 : 4;
+  if (!aligned(h, 16) || !aligned(W, 16) || !aligned(dh, 16) || !aligned(dW, 16) || !aligned(top_index, 8) ||
+      !aligned(top_logit, te) || !aligned(lse, 4) || !aligned(g, 4))
+    return fail(FAIRY2I_ERR_ALIGN, "h, W, dh and dW need 16-byte alignment, top_index 8, top_logit its element's, lse and g 4");
+  const uint64_t hb = (uint64_t)N * K * xe, wb = (uint64_t)V * K * xe;
+  const struct { const void* p; uint64_t bytes; } in[] = {
+      {h, hb}, {W, wb}, {top_index, (uint64_t)N * top * 8}, {top_logit, (uint64_t)N * top * te}, {lse, (uint64_t)N * 4}, {g, (uint64_t)N * 4}};
+  for (const auto& r : in)
+    if (overlap(dh, hb, r.p, r.bytes) || overlap(dW, wb, r.p, r.bytes))
+      return fail(FAIRY2I_ERR_SHAPE, "dh and dW must not overlap h, W, top_index, top_logit, lse or g");
+  if (overlap(dh, hb, dW, wb)) return fail(FAIRY2I_ERR_SHAPE, "dh and dW must not overlap each other");
+  if (int s = check_workspace(workspace, workspace_bytes, fairy2i_distill_backward_workspace_bytes(N, V, K, x_dtype, top)))
+    return s;
+  f2i::VocabArgs a{};
+  a.h = h; a.W = W; a.N = N; a.V = V; a.K = K; a.bf16 = x_dtype == FAIRY2I_BF16;
+  a.lse = lse; a.g = g; a.dh = dh; a.dW = dW; a.ws = workspace;
+  a.top_index = top_index; a.top_logit = top_logit; a.top = top; a.top_bf16 = top_dtype == FAIRY2I_BF16;
+  a.temperature = temperature;
+  return hip_status(f2i::launch_vocab_loss_backward(a, stream), "distillation backward launch");
 }
 
 // Layers kept at four bits: tiles x blocks of 128 columns bounds the threads of one packing launch.

@@ -326,9 +326,14 @@ struct VocabArgs {
   void* dh;               // [N][K] or null
   void* dW;               // [V][K] or null
   void* ws;
+  // distillation from a teacher's top logits in place of targets (top > 0)
+  const int64_t* top_index;   // [N][top]
+  const void* top_logit;      // [N][top]
+  int top, top_bf16;
+  float temperature;
 };
-size_t vocab_loss_workspace_bytes(int64_t N, int64_t V, int64_t K, int bf16);
-size_t vocab_loss_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int bf16);
+size_t vocab_loss_workspace_bytes(int64_t N, int64_t V, int64_t K, int bf16, int top);
+size_t vocab_loss_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int bf16, int top);
 hipError_t launch_vocab_loss(const VocabArgs& a, hipStream_t s);
 hipError_t launch_vocab_loss_backward(const VocabArgs& a, hipStream_t s);
 

@@ -24,6 +24,14 @@
 // -s_i (1 - softmax_t).)
 // No part leaves fp32's range: p and the sums keep g's own size to within a factor of 4, but for |g_i| f_i
 // under 2^-60, where s_i stays at 2^-60 (or p would lose its small values) and m_i takes the rest.
+// Distillation from a teacher's top logits runs on the same products: with t_ik the softmax of token i's
+// listed logits over the temperature, l_iv = <h_i, W_v> / temperature,
+//     loss_i = sum_k t_ik (log t_ik - l_{i, index_ik} + lse_i)
+//     p_iv = g_i / temperature (exp(l_iv - lse_i) - sum_{k: index_ik = v} t_ik)
+// k_teacher makes the lists' t_ik once; a finished tile looks up which of its entries are listed in a map
+// that its workgroup fills in LDS, stores their logits (loss) or subtracts their t_ik (p).  A token's gradient
+// has no one entry that dominates it for certain, so f_i is 1 here and g alone is taken apart: the roundings
+// of p's entries then differ from entry to entry.
 // Transposed operands are read from the matrix as it lies in memory: rows of the contraction are
 // copied into LDS and transposed on the way into registers, so no transposed copy is made.
 // Sums are fp32; a C tile has the A rows in its accumulator rows, so a lane holds four consecutive
@@ -36,7 +44,10 @@ namespace f2i {
 
 namespace {
 
-enum { kLoss = 0, kGrad = 1, kHidden = 2, kWeight = 3 };
+enum { kLoss = 0, kGrad = 1, kHidden = 2, kWeight = 3, kDistill = 4, kDistillGrad = 5 };
+constexpr bool loss_like(int epi) { return epi == kLoss || epi == kDistill; }
+constexpr bool grad_like(int epi) { return epi == kGrad || epi == kDistillGrad; }
+constexpr bool listed(int epi) { return epi == kDistill || epi == kDistillGrad; }
 
 // acc += a b on the matrix cores, one 16-byte operand per lane.  The accumulator is tied to its own
 // accumulation registers: left to itself the compiler moves the 256 of a 128 x 128 wave tile about,
@@ -78,9 +89,38 @@ struct VocabTile {
   void* out;                    // [rows_b][rows_a] (kHidden on the last piece, kWeight)
   int64_t v0, V;                // first vocabulary entry of A, vocabulary size
   int64_t N, ldp;
+  const int32_t* list_index;    // [N][top] vocabulary entries, -1 for none (kDistill, kDistillGrad)
+  const float* list_prob;       // [N][top] t_ik (kDistillGrad)
+  float* list_logit;            // [N][top] (kDistill)
+  int top;
+  float inv_temp;               // 1 / temperature (kDistill, kDistillGrad)
   int first, last;              // piece
   int tiles_a, tiles_b;
   int splits;                   // of the contraction (kHidden; 1 otherwise)
+};
+
+// Where a tile's entries are listed: of token n of the tile and row r, byte n * pitch + r is the slot + 1, or
+// 0.  The map takes over the operand buffers; its rows are 16 bytes longer than the tile's, so that the lanes
+// of a read (16 tokens, 4 words each) lie in distinct banks.
+template <int BM, int BN>
+struct ListMap {
+  static constexpr int kPitch = BM + 16;
+  static_assert(kPitch * BN <= (BM + BN) * 256, "fits in two operand buffers");
+  template <int THREADS>
+  __device__ static __forceinline__ void fill(const VocabTile& t, uint8_t* map, int64_t first, int64_t b0) {
+    __syncthreads();                                       // every wave's copies have landed and been read
+    for (int u = threadIdx.x; u < kPitch * BN / 16; u += THREADS) reinterpret_cast<uint4*>(map)[u] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    const int tokens = (int)min((int64_t)BN, t.N - b0);
+    const int32_t* __restrict__ index = t.list_index + b0 * t.top;
+    for (int u = threadIdx.x; u < tokens * t.top; u += THREADS) {
+      const int64_t r = index[u] - first;
+      if (r < 0 || r >= BM) continue;
+      const int n = u / t.top;
+      map[n * kPitch + (int)r] = (uint8_t)(u - n * t.top + 1);
+    }
+    __syncthreads();
+  }
 };
 
 // What happens to a finished tile (above).
@@ -93,7 +133,25 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
   const int wa = wave / WB, wb = wave % WB;
   const int64_t va = a0 + wa * FA * 16 + 4 * g;            // this lane's first A row
   const int64_t nb = b0 + wb * FB * 16 + c;                // its first B row
-  if constexpr (EPI == kLoss) {
+  if constexpr (EPI == kDistill) {
+    using Map = ListMap<BM, BN>;
+    Map::template fill<64 * WA * WB>(t, s_buf, a0, b0);
+#pragma unroll
+    for (int j = 0; j < FB; ++j) {
+      const int64_t tok = nb + 16 * j;
+#pragma unroll
+      for (int i = 0; i < FA; ++i) {
+        acc[i][j] *= t.inv_temp;
+        const uint32_t hit =
+            *reinterpret_cast<const uint32_t*>(s_buf + ((wb * FB + j) * 16 + c) * Map::kPitch + (wa * FA + i) * 16 + 4 * g);
+        if (hit)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (const int slot = (hit >> (8 * e)) & 255) t.list_logit[tok * t.top + slot - 1] = acc[i][j][e];
+      }
+    }
+  }
+  if constexpr (loss_like(EPI)) {
     // The pairs of the tile's waves take over the operand buffers.  (They are not an array of their own:
     // with two arrays in LDS the compiler no longer knows that an operand read cannot meet a copy in
     // flight and waits for every copy before every read, which doubled the time.)
@@ -104,7 +162,7 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
       const int64_t tok = nb + 16 * j;
-      const int64_t tgt = tok < t.N ? t.target[tok] : -1;
+      const int64_t tgt = EPI == kLoss && tok < t.N ? t.target[tok] : -1;
       // this lane has the target's logit if it lies 16 i + e past the lane's first row
       const int d = tgt >= va && tgt < va + FA * 16 && tgt < t.V ? (int)(tgt - va) : 4;
       float top = -INFINITY, mine = 0.f;
@@ -115,7 +173,7 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
           if (!whole && va + 16 * i + e >= t.V) acc[i][j][e] = -INFINITY;
           top = fmaxf(top, acc[i][j][e]);
         }
-      if (__ballot((d & 12) == 0)) {
+      if (EPI == kLoss && __ballot((d & 12) == 0)) {
 #pragma unroll
         for (int i = 0; i < FA; ++i)
 #pragma unroll
@@ -151,6 +209,38 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
 #pragma unroll
       for (int w = 0; w < WA; ++w) sum += s_red[w][k].y * exp_off(s_red[w][k].x, top);
       t.part[(int64_t)ta * t.N + b0 + k] = make_float2(top, sum);
+    }
+  } else if constexpr (EPI == kDistillGrad) {
+    using Map = ListMap<BM, BN>;
+    Map::template fill<64 * WA * WB>(t, s_buf, t.v0 + a0, b0);
+    T* __restrict__ p = static_cast<T*>(t.p);
+#pragma unroll
+    for (int j = 0; j < FB; ++j) {
+      const int64_t tok = nb + 16 * j;
+      if (tok >= t.N) continue;
+      const float gi = t.g[tok];                           // 0 for tokens that do not count
+      const bool live = gi != 0.f;                         // other tokens give 0 whatever their logits are
+      const float lse = live ? t.lse[tok] : 0.f;
+#pragma unroll
+      for (int i = 0; i < FA; ++i) {
+        const int64_t r = va + 16 * i;                     // row within the piece
+        if (r >= t.ldp) continue;
+        const uint32_t hit =
+            *reinterpret_cast<const uint32_t*>(s_buf + ((wb * FB + j) * 16 + c) * Map::kPitch + (wa * FA + i) * 16 + 4 * g);
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float off = fmaf(acc[i][j][e], t.inv_temp, -lse);
+          float v = sizeof(T) == 2 ? fast_exp(off) : expf(off);
+          if (const int slot = (hit >> (8 * e)) & 255) v -= t.list_prob[tok * t.top + slot - 1];
+          x[e] = live && r + e < t.rows_a ? gi * v : 0.f;
+        }
+        if constexpr (sizeof(T) == 2)
+          *reinterpret_cast<uint2*>(p + tok * t.ldp + r) =
+              make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        else
+          *reinterpret_cast<v4f*>(p + tok * t.ldp + r) = v4f{x[0], x[1], x[2], x[3]};
+      }
     }
   } else if constexpr (EPI == kGrad) {
     T* __restrict__ p = static_cast<T*>(t.p);
@@ -537,6 +627,15 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt_split(VocabTile t) {
   finish<float, BM, BN, WA, WB, FA, FB, EPI>(t, acc, s_buf, a0, b0, ta, split);
 }
 
+// A call's lists as k_teacher leaves them: [N][top] each, but for entropy and live [N].
+constexpr int kMaxTop = 128;
+struct TeacherLists {
+  int32_t* index;
+  float* prob;
+  float* entropy;        // sum_k t_ik log t_ik
+  int32_t* live;         // whether the token counts
+};
+
 // Joins the tiles' pairs in order (one wave per token) into lse, and the loss from the target's logit:
 // launch-bound (4.6 us for 24 tokens, 5.2 for 2048).
 __global__ __launch_bounds__(256) void k_loss_join(const float2* __restrict__ part, const float* __restrict__ tlogit,
@@ -560,6 +659,110 @@ __global__ __launch_bounds__(256) void k_loss_join(const float2* __restrict__ pa
     lse[i] = l;
     const int64_t t = target[i];
     loss[i] = t >= 0 && t < V ? l - tlogit[i] : 0.f;
+  }
+}
+
+// A teacher's lists, one wave per token: t_ik = softmax over the slots whose index lies in [0, V) of
+// logit / temperature (0 for a slot at minus infinity), and what the loss needs of it, sum_k t_ik log t_ik.
+// An entry listed more than once keeps its first slot, with the sum of its probabilities; its other slots,
+// and slots without probability, get index -1.  A token without any probability does not count.
+template <typename LT>
+__global__ __launch_bounds__(256) void k_teacher(const int64_t* __restrict__ index, const LT* __restrict__ logit,
+                                                 int64_t N, int64_t V, int top, float inv_temp, TeacherLists out) {
+  __shared__ int32_t s_index[4][kMaxTop];
+  __shared__ float s_prob[4][kMaxTop];
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+  const int64_t i = (int64_t)blockIdx.x * 4 + w;
+  if (i >= N) return;                                      // whole waves: no barrier below
+  constexpr int kEach = kMaxTop / kWave;
+  float z[kEach];
+  int32_t at[kEach];
+  float best = -INFINITY, sum = 0.f, bad = 0.f;
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    const int k = q * kWave + lane;
+    z[q] = -INFINITY;
+    at[q] = -1;
+    if (k >= top) continue;
+    const int64_t v = index[i * top + k];
+    if (v < 0 || v >= V) continue;
+    at[q] = (int32_t)v;
+    float l;
+    if constexpr (sizeof(LT) == 2) l = __uint_as_float((uint32_t)logit[i * top + k] << 16);
+    else l = logit[i * top + k];
+    z[q] = l * inv_temp;
+    best = fmaxf(best, z[q]);
+    if (!(z[q] < INFINITY)) bad = NAN;                     // NaN or plus infinity: the token's loss is NaN
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) best = fmaxf(best, __shfl_xor(best, off));
+  bad = wave_sum(bad);
+  const bool live = best > -INFINITY || bad != bad;
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) sum += z[q] > -INFINITY ? expf(z[q] - best) : 0.f;
+  sum = wave_sum(sum) + bad;
+  const float log_sum = logf(sum);
+  float entropy = 0.f;
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    const int k = q * kWave + lane;
+    float p = z[q] > -INFINITY ? expf(z[q] - best) / sum : 0.f;
+    if (bad != bad && at[q] >= 0) p = bad;
+    if (p > 0.f) entropy += p * (z[q] - best - log_sum);
+    s_index[w][k] = p == 0.f ? -1 : at[q];
+    s_prob[w][k] = p;
+  }
+  entropy = wave_sum(entropy) + bad;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    const int k = q * kWave + lane;
+    if (k >= top) continue;
+    int32_t v = s_index[w][k];
+    float p = 0.f;
+    if (v >= 0)
+      for (int j = 0; j < top; ++j)
+        if (s_index[w][j] == v) {
+          if (j < k) {
+            v = -1;
+            p = 0.f;
+            break;
+          }
+          p += s_prob[w][j];
+        }
+    out.index[i * top + k] = v;
+    out.prob[i * top + k] = p;
+  }
+  if (lane == 0) {
+    out.entropy[i] = entropy;
+    out.live[i] = live;
+  }
+}
+
+// lse as k_loss_join, and the distillation loss from the listed logits.
+__global__ __launch_bounds__(256) void k_distill_join(const float2* __restrict__ part, TeacherLists list,
+                                                      const float* __restrict__ list_logit, int64_t N, int top, int tiles,
+                                                      float* __restrict__ loss, float* __restrict__ lse) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
+  if (i >= N) return;
+  float best = -INFINITY;
+  for (int s = lane; s < tiles; s += kWave) best = fmaxf(best, part[(int64_t)s * N + i].x);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) best = fmaxf(best, __shfl_xor(best, off));
+  float sum = 0.f, cross = 0.f;
+  for (int s = lane; s < tiles; s += kWave) {
+    const float2 v = part[(int64_t)s * N + i];
+    sum += v.y * exp_off(v.x, best);
+  }
+  for (int k = lane; k < top; k += kWave)
+    if (list.index[i * top + k] >= 0) cross += list.prob[i * top + k] * list_logit[i * top + k];
+  sum = wave_sum(sum);
+  cross = wave_sum(cross);
+  if (lane == 0) {
+    const float l = best + logf(sum);
+    lse[i] = l;
+    loss[i] = list.live[i] ? list.entropy[i] + (l - cross) : 0.f;
   }
 }
 
@@ -673,6 +876,68 @@ __global__ __launch_bounds__(256) void k_grad_scales(const float* __restrict__ g
   }
 }
 
+// Distillation: g alone, over the temperature: s_i, G m_i / temperature, G / temperature, m_i h_i; fp32: s_i is
+// g_i / temperature itself.
+template <typename T>
+__global__ __launch_bounds__(256) void k_distill_scales(const float* __restrict__ g, const int32_t* __restrict__ counts,
+                                                        int64_t N, const T* __restrict__ h, int64_t K, float inv_temp,
+                                                        GradScales out, T* __restrict__ scaled) {
+  constexpr int kEach = 16 / sizeof(T);
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
+  if (i >= N) return;
+  const float gi = g[i];
+  const bool live = counts[i] && gi != 0.f;
+  float m = 1.f;
+  if constexpr (sizeof(T) == 2) {
+    float G = 1.f;
+    for (int64_t t0 = 0; t0 < min(N, (int64_t)kScanned); t0 += kWave) {
+      const int64_t t = min(t0 + lane, N - 1);
+      const float v = fabsf(g[t]);
+      const uint64_t good = __ballot(counts[t] && v > 0.f && v < INFINITY);
+      if (good) {
+        G = __uint_as_float((__float_as_uint(__shfl(v, __builtin_ctzll(good))) & 0x007FFFFFu) | 0x3F800000u);
+        break;
+      }
+    }
+    float si = 0.f;
+    if (live) {
+      si = gi;
+      if (const float ratio = fabsf(gi) / G; ratio < INFINITY) {
+        float top = fmaxf(__uint_as_float(__float_as_uint(ratio) & 0x7F800000u), 0x1p-60f);   // 2^floor(log2(ratio))
+        m = ratio / top;
+        if (m > 1.f && top < 0x1p127f) {
+          m *= 0.5f;
+          top *= 2.f;
+        }
+        si = copysignf(top, gi);
+      }
+    }
+    if (lane == 0) {
+      out.s[i] = si;
+      out.row[i] = G * m * inv_temp;
+      if (i == 0) *out.all = G * inv_temp;
+    }
+  } else if (lane == 0) {
+    out.s[i] = live ? gi * inv_temp : 0.f;
+  }
+  if (!scaled) return;
+  const T* __restrict__ from = h + i * K;
+  T* __restrict__ to = scaled + i * K;
+  for (int64_t k = lane * kEach; k < K; k += kWave * kEach) {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (live) {
+      w = *reinterpret_cast<const uint4*>(from + k);
+      if constexpr (sizeof(T) == 2) {
+        uint32_t* e = &w.x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[j] = pack_bf16(m * bf16_lo(e[j]), m * bf16_hi(e[j]));
+      }
+    }
+    *reinterpret_cast<uint4*>(to + k) = w;
+  }
+}
+
 namespace {
 
 constexpr int kCUs = 256;
@@ -730,8 +995,8 @@ void launch_nt(VocabTile& t, const NtPlan& plan, int64_t cover_a, int64_t cover_
       case 1: hipLaunchKernelGGL((k_nt<256, 128, 4, 2, EPI>), grid, dim3(512), 0, s, t); break;
       case 2: hipLaunchKernelGGL((k_nt<128, 128, 2, 2, EPI>), grid, dim3(256), 0, s, t); break;
       default:
-        if ((EPI == kLoss || EPI == kGrad) && t.tiles_a * t.tiles_b <= kCUs)
-          hipLaunchKernelGGL((k_nt<128, 64, 2, 2, EPI, EPI == kLoss || EPI == kGrad ? 4 : 2>), grid, dim3(256), 0, s, t);
+        if ((loss_like(EPI) || grad_like(EPI)) && t.tiles_a * t.tiles_b <= kCUs)
+          hipLaunchKernelGGL((k_nt<128, 64, 2, 2, EPI, loss_like(EPI) || grad_like(EPI) ? 4 : 2>), grid, dim3(256), 0, s, t);
         else
           hipLaunchKernelGGL((k_nt<128, 64, 2, 2, EPI>), grid, dim3(256), 0, s, t);
         break;
@@ -747,16 +1012,47 @@ void launch_nt(VocabTile& t, const NtPlan& plan, int64_t cover_a, int64_t cover_
 
 int64_t steps_of(int64_t k, int elem) { return (k * elem + 127) / 128; }
 
+// The lists' place in a workspace from `at` on, which moves behind them.
+struct ListPlan {
+  size_t index, prob, entropy, live;
+};
+ListPlan list_plan(int64_t N, int top, size_t& at) {
+  ListPlan l{};
+  if (top == 0) return l;
+  auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
+  l.index = take((size_t)N * top * 4);
+  l.prob = take((size_t)N * top * 4);
+  l.entropy = take((size_t)N * 4);
+  l.live = take((size_t)N * 4);
+  return l;
+}
+TeacherLists lists_at(uint8_t* ws, const ListPlan& l) {
+  return TeacherLists{reinterpret_cast<int32_t*>(ws + l.index), reinterpret_cast<float*>(ws + l.prob),
+                      reinterpret_cast<float*>(ws + l.entropy), reinterpret_cast<int32_t*>(ws + l.live)};
+}
+void launch_teacher(const VocabArgs& a, const TeacherLists& lists, hipStream_t s) {
+  const dim3 grid((unsigned)((a.N + 3) / 4));
+  const float inv = 1.f / a.temperature;
+  if (a.top_bf16)
+    hipLaunchKernelGGL((k_teacher<uint16_t>), grid, dim3(256), 0, s, a.top_index, static_cast<const uint16_t*>(a.top_logit),
+                       a.N, a.V, a.top, inv, lists);
+  else
+    hipLaunchKernelGGL((k_teacher<float>), grid, dim3(256), 0, s, a.top_index, static_cast<const float*>(a.top_logit), a.N,
+                       a.V, a.top, inv, lists);
+}
+
 struct LossPlan {
   NtPlan nt;
-  size_t part, tlogit, total;
+  size_t part, tlogit, total;     // tlogit: [N], or the listed logits [N][top]
+  ListPlan list;
 };
-LossPlan loss_plan(int64_t N, int64_t V, int64_t K, int elem) {
+LossPlan loss_plan(int64_t N, int64_t V, int64_t K, int elem, int top) {
   LossPlan p;
   p.nt = nt_plan(V, N, steps_of(K, elem), elem, 1, false);
   p.part = 0;
   p.tlogit = up256((size_t)tiles(V, kTiles[p.nt.shape].a) * N * sizeof(float2));
-  p.total = p.tlogit + up256((size_t)N * 4);
+  p.total = p.tlogit + up256((size_t)N * std::max(top, 1) * 4);
+  p.list = list_plan(N, top, p.total);
   return p;
 }
 
@@ -765,8 +1061,9 @@ struct GradPlan {
   int pieces;
   NtPlan hidden;
   size_t p, acc, scales, scaled, total;
+  ListPlan list;
 };
-GradPlan grad_plan(int64_t N, int64_t V, int64_t K, int elem) {
+GradPlan grad_plan(int64_t N, int64_t V, int64_t K, int elem, int top) {
   GradPlan g;
   const int64_t fit = std::min((int64_t(1) << 27) / N, (int64_t(1) << 30) / (K * elem)) / 256 * 256;
   const int64_t most = std::max<int64_t>(256, std::min<int64_t>(kPieceRows, fit));
@@ -778,15 +1075,16 @@ GradPlan grad_plan(int64_t N, int64_t V, int64_t K, int elem) {
   auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
   g.p = take((size_t)N * g.piece * elem);
   g.acc = take(g.pieces > 1 || g.hidden.splits > 1 ? (size_t)g.hidden.splits * N * K * 4 : 0);
-  g.scales = take(elem == 2 ? ((size_t)4 * N + 1) * 4 : 0);
+  g.scales = take(elem == 2 || top > 0 ? ((size_t)4 * N + 1) * 4 : 0);
   g.scaled = take((size_t)N * K * elem);
+  g.list = list_plan(N, top, at);
   g.total = at;
   return g;
 }
 
 template <typename T>
 hipError_t loss_t(const VocabArgs& a, hipStream_t s) {
-  const LossPlan p = loss_plan(a.N, a.V, a.K, sizeof(T));
+  const LossPlan p = loss_plan(a.N, a.V, a.K, sizeof(T), a.top);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   VocabTile t{};
   t.a = a.W; t.b = a.h;
@@ -796,6 +1094,15 @@ hipError_t loss_t(const VocabArgs& a, hipStream_t s) {
   t.part = reinterpret_cast<float2*>(ws + p.part);
   t.tlogit = reinterpret_cast<float*>(ws + p.tlogit);
   t.V = a.V; t.N = a.N;
+  if (a.top > 0) {
+    const TeacherLists lists = lists_at(ws, p.list);
+    launch_teacher(a, lists, s);
+    t.list_index = lists.index; t.list_logit = t.tlogit; t.top = a.top; t.inv_temp = 1.f / a.temperature;
+    launch_nt<T, kDistill>(t, p.nt, a.V, a.N, s);
+    hipLaunchKernelGGL(k_distill_join, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, t.part, lists, t.list_logit, a.N,
+                       a.top, t.tiles_a, a.loss, a.lse_out);
+    return hipGetLastError();
+  }
   launch_nt<T, kLoss>(t, p.nt, a.V, a.N, s);
   hipLaunchKernelGGL(k_loss_join, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, t.part, t.tlogit, a.target, a.N, a.V,
                      t.tiles_a, a.loss, a.lse_out);
@@ -804,7 +1111,7 @@ hipError_t loss_t(const VocabArgs& a, hipStream_t s) {
 
 template <typename T>
 hipError_t grad_t(const VocabArgs& a, hipStream_t s) {
-  const GradPlan q = grad_plan(a.N, a.V, a.K, sizeof(T));
+  const GradPlan q = grad_plan(a.N, a.V, a.K, sizeof(T), a.top);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   T* p = reinterpret_cast<T*>(ws + q.p);
   float* acc = reinterpret_cast<float*>(ws + q.acc);
@@ -815,12 +1122,21 @@ hipError_t grad_t(const VocabArgs& a, hipStream_t s) {
   T* h = a.dW ? reinterpret_cast<T*>(ws + q.scaled) : nullptr;
   if (sizeof(T) == 2) {
     factor = out.s;
-    lse = out.lse;
-    at_target = out.at_target;
     row_scale = out.row;
     all_scale = out.all;
   }
-  if (sizeof(T) == 2 || h)
+  if (sizeof(T) == 2 && a.top == 0) {
+    lse = out.lse;
+    at_target = out.at_target;
+  }
+  TeacherLists lists{};
+  if (a.top > 0) {
+    lists = lists_at(ws, q.list);
+    factor = out.s;
+    launch_teacher(a, lists, s);
+    hipLaunchKernelGGL((k_distill_scales<T>), dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a.g, lists.live, a.N,
+                       static_cast<const T*>(a.h), a.K, 1.f / a.temperature, out, h);
+  } else if (sizeof(T) == 2 || h)
     hipLaunchKernelGGL((k_grad_scales<T>), dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a.g, a.target, a.N, a.V,
                        static_cast<const T*>(a.h), W, a.lse, a.K, out, h);
   for (int k = 0; k < q.pieces; ++k) {
@@ -832,7 +1148,13 @@ hipError_t grad_t(const VocabArgs& a, hipStream_t s) {
     t.target = a.target; t.lse = lse; t.g = factor; t.at_target = at_target;
     t.p = p; t.ldp = ldp;
     t.v0 = v0; t.V = a.V; t.N = a.N;
-    launch_nt<T, kGrad>(t, nt_plan(ldp, a.N, steps_of(a.K, sizeof(T)), sizeof(T), 1, false), ldp, a.N, s);
+    const NtPlan plan = nt_plan(ldp, a.N, steps_of(a.K, sizeof(T)), sizeof(T), 1, false);
+    if (a.top > 0) {
+      t.list_index = lists.index; t.list_prob = lists.prob; t.top = a.top; t.inv_temp = 1.f / a.temperature;
+      launch_nt<T, kDistillGrad>(t, plan, ldp, a.N, s);
+    } else {
+      launch_nt<T, kGrad>(t, plan, ldp, a.N, s);
+    }
     if (a.dh) {
       VocabTile d{};
       d.a = W + v0 * a.K; d.b = p;
@@ -862,11 +1184,11 @@ hipError_t grad_t(const VocabArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t vocab_loss_workspace_bytes(int64_t N, int64_t V, int64_t K, int bf16) {
-  return loss_plan(N, V, K, bf16 ? 2 : 4).total;
+size_t vocab_loss_workspace_bytes(int64_t N, int64_t V, int64_t K, int bf16, int top) {
+  return loss_plan(N, V, K, bf16 ? 2 : 4, top).total;
 }
-size_t vocab_loss_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int bf16) {
-  return grad_plan(N, V, K, bf16 ? 2 : 4).total;
+size_t vocab_loss_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int bf16, int top) {
+  return grad_plan(N, V, K, bf16 ? 2 : 4, top).total;
 }
 hipError_t launch_vocab_loss(const VocabArgs& a, hipStream_t s) { return a.bf16 ? loss_t<uint16_t>(a, s) : loss_t<float>(a, s); }
 hipError_t launch_vocab_loss_backward(const VocabArgs& a, hipStream_t s) {
