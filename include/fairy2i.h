@@ -415,6 +415,32 @@ int fairy2i_distill_backward(const void* h, const void* W, int x_dtype, int64_t 
                              const float* lse, const float* g, void* dh, void* dW, void* workspace, size_t workspace_bytes,
                              hipStream_t stream);
 
+/* Verification of tokens that a draft model (the packed one) proposed to a target model (its original), so
+ * that what is kept is distributed as the target's own tokens.  With the sequence's target probabilities p_j
+ * at its D + 1 positions and the draft's q_j at its first D:
+ *   - draft x_j is kept while u_j q_j(x_j) < p_j(x_j); a is the first position where it is not, or the
+ *     number of drafts.  (A draft outside [0, V) is not kept.)
+ *   - the next token is drawn from w = max(p_a - q_a, 0), or from p_a where no draft was refused or that
+ *     is nowhere positive: the lowest v with sum_{v' <= v} w_v' > r sum_v' w_v' (where rounding leaves none,
+ *     the last v with w_v > 0).
+ *   p          [S][D + 1][V], p_dtype FAIRY2I_F32 or FAIRY2I_BF16; need not be normalised.
+ *   q          [S][D][V], p's dtype, or NULL: the draft was greedy, q_j is 1 at x_j and 0 elsewhere.
+ *   draft      int64 [S][D].
+ *   draft_len  int32 [S], how many of a sequence's drafts there are (limited to 0..D), or NULL: D.  Nothing of
+ *              the others is used.
+ *   u, r       fp32 [S][D] and [S], independent uniform numbers of [0, 1).
+ *   tokens     out, int64 [S][D + 1]: the kept drafts, the next token, then -1.
+ *   accepted   out, int32 [S]: a.
+ * Comparisons, differences and sums are fp64, sums in a fixed order.  Entries of w that are not finite or not
+ * positive count as 0; a row without any weight gives the token -1.
+ * 1 <= S <= 2^20, 1 <= D <= 63, 1 <= V <= 2^24, S ceil(V / 4096) <= 2^23; p and q need their element's
+ * alignment only.  workspace: fairy2i_verify_draft_workspace_bytes(...) bytes, 16-byte aligned.  Outputs overlap
+ * nothing else, and calls that share a workspace must not overlap. */
+size_t fairy2i_verify_draft_workspace_bytes(int64_t S, int64_t D, int64_t V);
+int fairy2i_verify_draft(const void* p, const void* q, int p_dtype, int64_t S, int64_t D, int64_t V, const int64_t* draft,
+                         const int32_t* draft_len, const float* u, const float* r, int64_t* tokens, int32_t* accepted,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* ---- beside the packed layers: low-rank adapters, the vocabulary loss, gradient clipping ----
  * Serving one frozen packed layer for many tenants, and tuning on top of it (the card's "Method"
  * keeps full-precision weights for training; here the packed layer stays fixed and small matrices

@@ -106,6 +106,8 @@ SIGNATURES["fairy2i_distill"] = (_INT, [_P, _P, _INT, _I64, _I64, _I64, _P, _P, 
 SIGNATURES["fairy2i_distill_backward_workspace_bytes"] = (_SZ, [_I64, _I64, _I64, _INT, _INT])
 SIGNATURES["fairy2i_distill_backward"] = (_INT, [_P, _P, _INT, _I64, _I64, _I64, _P, _P, _INT, _INT, _F32, _P, _P, _P, _P,
                                                  _P, _SZ, _P])
+SIGNATURES["fairy2i_verify_draft_workspace_bytes"] = (_SZ, [_I64, _I64, _I64])
+SIGNATURES["fairy2i_verify_draft"] = (_INT, [_P, _P, _INT, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _SZ, _P])
 
 _lib = None
 
@@ -1213,3 +1215,61 @@ def fairy2i_distill_backward(h: torch.Tensor, W: torch.Tensor, top_index: torch.
                                           top_logit.data_ptr(), _DTYPE[top_logit.dtype], top, temperature, lse.data_ptr(),
                                           g.data_ptr(), _ptr(dh), _ptr(dW), ws, nbytes, _stream()))
     return dh, dW
+
+
+# ---- verification of drafted tokens ----
+
+def fairy2i_verify_draft_workspace_bytes(S: int, D: int, V: int) -> int:
+    return int(lib().fairy2i_verify_draft_workspace_bytes(S, D, V))
+
+
+@_on_stream
+def fairy2i_verify_draft(p: torch.Tensor, q, draft: torch.Tensor, u: torch.Tensor, r: torch.Tensor, *, draft_len=None,
+                         tokens=None, accepted=None, workspace=None):
+    """Drafted tokens against the target's probabilities: p [S][D + 1][V] of the target, q [S][D][V] of the
+    draft (None: it was greedy), fp32 or bf16, draft int64 [S][D] and, if they differ, draft_len int32 [S], u
+    fp32 [S][D] and r fp32 [S] uniform in [0, 1).  Returns (tokens int64 [S][D + 1]: the kept drafts, the
+    next token, then -1; accepted int32 [S])."""
+    i64, i32, f32 = torch.int64, torch.int32, torch.float32
+    try:
+        dt, dev = p.dtype, p.get_device()
+        S, D1, V = p.shape
+        D = D1 - 1
+        good = (dt in _FLOATS and dev >= 0 and p.is_contiguous() and (q is None or _fits(q, dt, (S, D, V), dev))
+                and _fits(draft, i64, (S, D), dev) and _fits(u, f32, (S, D), dev) and _fits(r, f32, (S,), dev)
+                and (draft_len is None or _fits(draft_len, i32, (S,), dev))
+                and (tokens is None or _fits(tokens, i64, (S, D1), dev))
+                and (accepted is None or _fits(accepted, i32, (S,), dev)))
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _refuse_verify(p, q, draft, u, r, draft_len, tokens, accepted)
+    tokens = torch.empty((S, D1), dtype=i64, device=p.device) if tokens is None else tokens
+    accepted = torch.empty((S,), dtype=i32, device=p.device) if accepted is None else accepted
+    ws, nbytes, keep = _room(workspace, fairy2i_verify_draft_workspace_bytes(S, D, V), p.device)
+    _check(lib().fairy2i_verify_draft(p.data_ptr(), None if q is None else q.data_ptr(), _DTYPE[dt], S, D, V, draft.data_ptr(),
+                                      None if draft_len is None else draft_len.data_ptr(), u.data_ptr(), r.data_ptr(),
+                                      tokens.data_ptr(), accepted.data_ptr(), ws, nbytes, _stream()))
+    return tokens, accepted
+
+
+def _refuse_verify(p, q, draft, u, r, draft_len, tokens, accepted):
+    """Raises for the first argument of fairy2i_verify_draft that does not fit."""
+    _tensor(p, "p")
+    _dtype(p, "p", torch.float32, torch.bfloat16)
+    if p.dim() != 3 or p.shape[1] < 2:
+        raise ValueError(f"p: shape {tuple(p.shape)}, need [S][D + 1][V]")
+    _on_gpu(p, "p")
+    S, D, V = p.shape[0], p.shape[1] - 1, p.shape[2]
+    if q is not None:
+        _check_plain(q, "q", (p.dtype,), (S, D, V))
+    _check_plain(draft, "draft", (torch.int64,), (S, D))
+    _check_plain(u, "u", (torch.float32,), (S, D))
+    _check_plain(r, "r", (torch.float32,), (S,))
+    for t, name, dt, shape in ((draft_len, "draft_len", torch.int32, (S,)), (tokens, "tokens", torch.int64, (S, D + 1)),
+                               (accepted, "accepted", torch.int32, (S,))):
+        if t is not None:
+            _check_plain(t, name, (dt,), shape)
+    _gpu((p, "p"), (q, "q"), (draft, "draft"), (u, "u"), (r, "r"), (draft_len, "draft_len"), (tokens, "tokens"),
+         (accepted, "accepted"))
+    raise ValueError("fairy2i_verify_draft: the arguments do not fit together")

@@ -54,6 +54,7 @@ SOURCES = {
     "prefill.hip": ["-ffp-contract=off"],
     "dequant.hip": ["-ffp-contract=off"],
     "w4.hip": [],
+    "verify.hip": [],
     "lora.hip": [],
     "vocab_loss.hip": [],
     "clip.hip": [],

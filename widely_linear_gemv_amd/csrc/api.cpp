@@ -874,6 +874,44 @@ int fairy2i_vocab_loss_backward(const void* h, const void* W, int x_dtype, int64
   return hip_status(f2i::launch_vocab_loss_backward(a, stream), "vocabulary loss backward launch");
 }
 
+// ---- verification of drafted tokens ----
+
+// S pieces bounds the workgroups of one launch; a wave looks at a sequence's drafts, one a lane.
+static bool verify_sizes_ok(int64_t S, int64_t D, int64_t V) {
+  return S >= 1 && S <= kMaxTokens && D >= 1 && D <= 63 && V >= 1 && V <= (int64_t(1) << 24) &&
+         S * ((V + 4095) / 4096) <= (int64_t(1) << 23);
+}
+
+size_t fairy2i_verify_draft_workspace_bytes(int64_t S, int64_t D, int64_t V) {
+  return verify_sizes_ok(S, D, V) ? f2i::verify_workspace_bytes(S, V) : 0;
+}
+
+int fairy2i_verify_draft(const void* p, const void* q, int p_dtype, int64_t S, int64_t D, int64_t V, const int64_t* draft,
+                         const int32_t* draft_len, const float* u, const float* r, int64_t* tokens, int32_t* accepted,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!p || !draft || !u || !r || !tokens || !accepted)
+    return fail(FAIRY2I_ERR_NULL, "p, draft, u, r, tokens and accepted are required");
+  if (int s = check_float_dtype(p_dtype, "p_dtype")) return s;
+  if (!verify_sizes_ok(S, D, V))
+    return fail(FAIRY2I_ERR_SHAPE, "S = %lld, D = %lld, V = %lld: need 1 <= S <= 2^20, 1 <= D <= 63, 1 <= V <= 2^24 and "
+                "S ceil(V / 4096) <= 2^23", (long long)S, (long long)D, (long long)V);
+  const uint64_t e = p_dtype == FAIRY2I_BF16 ? 2 : 4;
+  if (!aligned(p, e) || !aligned(q, e) || !aligned(draft, 8) || !aligned(draft_len, 4) || !aligned(u, 4) || !aligned(r, 4) ||
+      !aligned(tokens, 8) || !aligned(accepted, 4))
+    return fail(FAIRY2I_ERR_ALIGN, "p, q, draft, draft_len, u, r, tokens and accepted need their element's alignment");
+  const uint64_t tb = (uint64_t)S * (D + 1) * 8, ab = (uint64_t)S * 4;
+  const struct { const void* at; uint64_t bytes; } in[] = {
+      {p, (uint64_t)S * (D + 1) * V * e}, {q, (uint64_t)S * D * V * e}, {draft, (uint64_t)S * D * 8},
+      {draft_len, (uint64_t)S * 4}, {u, (uint64_t)S * D * 4}, {r, (uint64_t)S * 4}};
+  for (const auto& k : in)
+    if (overlap(tokens, tb, k.at, k.bytes) || overlap(accepted, ab, k.at, k.bytes))
+      return fail(FAIRY2I_ERR_SHAPE, "tokens and accepted must not overlap an input");
+  if (overlap(tokens, tb, accepted, ab)) return fail(FAIRY2I_ERR_SHAPE, "tokens and accepted must not overlap each other");
+  if (int s = check_workspace(workspace, workspace_bytes, f2i::verify_workspace_bytes(S, V))) return s;
+  const f2i::VerifyArgs a{p, q, draft, draft_len, u, r, tokens, accepted, S, V, (int)D};
+  return hip_status(f2i::launch_verify(a, p_dtype == FAIRY2I_BF16, workspace, stream), "draft verification launch");
+}
+
 // ---- distillation from a teacher's top logits: the vocabulary's products with lists in place of targets ----
 
 static constexpr int kMaxTop = 128;

@@ -230,6 +230,22 @@ hipError_t launch_w4_pack(const uint8_t* codes, const void* scales, int scales_b
                           int64_t cols, int group, uint8_t* packed, hipStream_t s);
 hipError_t launch_w4_gemv(const W4Args& a, hipStream_t s);
 
+// ---- verification of drafted tokens (verify.hip) ----
+struct VerifyArgs {
+  const void* p;            // [S][D + 1][V]
+  const void* q;            // [S][D][V] or null
+  const int64_t* draft;     // [S][D]
+  const int32_t* draft_len; // [S] or null
+  const float* u;           // [S][D]
+  const float* r;           // [S]
+  int64_t* tokens;          // [S][D + 1]
+  int32_t* accepted;        // [S]
+  int64_t S, V;
+  int D;
+};
+size_t verify_workspace_bytes(int64_t S, int64_t V);
+hipError_t launch_verify(const VerifyArgs& a, int bf16, void* ws, hipStream_t s);
+
 // ---- low-rank adapters (lora.hip) ----
 constexpr int kMaxLoraItems = 8;      // projections per launch; the tables travel in the kernel arguments
 constexpr int kMaxLoraRank = 128;
