@@ -361,9 +361,9 @@ int fairy2i_gemm_noalloc(const uint8_t* packed, const float* scales, int64_t n, 
  *   codes    uint8 [rows][cols], one code 0..15 a byte (higher bits are ignored).
  *   scales   [rows][ceil(cols / group)], scales_dtype FAIRY2I_F32 or FAIRY2I_BF16, kept as they are.
  *   zeros    uint8 [rows][ceil(cols / group)], any byte, or NULL: 8 everywhere.
- *   packed   out, fairy2i_packed_bytes_w4(...) bytes, 16-byte aligned, overlapping no input: per tile of 16 rows
- *            (the last padded) and 128 columns 1 KB of codes, tiles one after another; then per tile and
- *            group 16 scales and 16 zero points.
+ *   packed   out, fairy2i_packed_bytes_w4(...) bytes, 16-byte aligned, overlapping no input: tiles of 16 rows
+ *            (the last padded), one after another, each in blocks of 128 columns (the last padded): 1 KB of
+ *            codes, then 16 scales and 16 zero points for each of the block's groups.
  * group 32, 64 or 128; 1 <= rows <= 2^24, 1 <= cols <= 2^20 and ceil(rows / 16) ceil(cols / 128) <= 2^23.
  * Projections that read the same x (q, k and v) are one layer, their rows one after another. */
 size_t fairy2i_packed_bytes_w4(int64_t rows, int64_t cols, int group, int scales_dtype);

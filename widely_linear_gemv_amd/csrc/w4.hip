@@ -9,10 +9,12 @@
 // with exact products, fp32 sums, and sum_j x_j made once per workgroup.  (The value 128 + c takes the same
 // instructions but leaves five bits less of the sums.)  fp32 x enters as three bf16 parts that hold it.
 //
-// Packed form: tiles of 16 rows, one after another; a tile's codes are 1 KB blocks of 128 columns, and in a
-// block lane l = 16 g + r of a wave owns the 16 bytes of row r: word s holds columns 32 s + 8 g + e, e < 8, of
-// the block, e even in nibble e / 2 and e odd in nibble 4 + e / 2, as the matrix instruction's operand takes
-// them.  Behind all codes, for each tile and group: the 16 rows' scales, then their 16 zero points (a byte each).
+// Packed form: tiles of 16 rows, one after another, each in blocks of 128 columns.  A block is 1 KB of codes,
+// then its scales, then its zero points.  In the codes lane l = 16 g + r of a wave owns the 16 bytes of row r:
+// word s holds columns 32 s + 8 g + e, e < 8, of the block, e even in nibble e / 2 and e odd in nibble
+// 4 + e / 2, the whole word rotated left by 3 bits: nibbles n and n + 4 are then two neighbouring values of the
+// matrix instruction's operand after a rotation by 4 n.  Scales and zero points (a byte each) are ordered
+// [row][group of the block].
 #include <algorithm>
 
 #include "tiles.hpp"
@@ -21,17 +23,18 @@ namespace f2i {
 
 namespace {
 
-constexpr int kChunk = 128;              // columns of a block of codes
-constexpr int kWaves = 8;
-constexpr int kLdsX = 56 * 1024;         // bytes of x that a workgroup holds at once
+constexpr int kChunk = 128;              // columns of a block
 
 __host__ __device__ __forceinline__ int64_t w4_tiles(int64_t rows) { return (rows + 15) / 16; }
 __host__ __device__ __forceinline__ int64_t w4_chunks(int64_t cols) { return (cols + kChunk - 1) / kChunk; }
-__host__ __device__ __forceinline__ int w4_group_bytes(int scale_bytes) { return 16 * scale_bytes + 16; }
+__host__ __device__ __forceinline__ constexpr int w4_block_bytes(int group, int scale_bytes) {
+  return 1024 + kChunk / group * 16 * (scale_bytes + 1);
+}
 
 // One word of codes a thread.
 __global__ __launch_bounds__(256) void k_w4_codes(const uint8_t* __restrict__ codes, int64_t rows, int64_t cols,
-                                                  int64_t chunks, int64_t words, uint32_t* __restrict__ out) {
+                                                  int64_t chunks, int64_t words, int block_bytes,
+                                                  uint8_t* __restrict__ out) {
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= words) return;
   const int s = at & 3, lane = (at >> 2) & 63;
@@ -44,197 +47,311 @@ __global__ __launch_bounds__(256) void k_w4_codes(const uint8_t* __restrict__ co
     for (int e = 0; e < 8; ++e)
       if (j + e < cols) w |= (uint32_t)(p[e] & 15) << (4 * ((e >> 1) + 4 * (e & 1)));
   }
-  out[at] = w;
+  *reinterpret_cast<uint32_t*>(out + block * block_bytes + (at & 255) * 4) = w << 3 | w >> 29;
 }
 
-// One row of one tile and group a thread.
+// One row of one block and group a thread.
 template <typename ST>
 __global__ __launch_bounds__(256) void k_w4_scales(const ST* __restrict__ scales, const uint8_t* __restrict__ zeros,
-                                                   int64_t rows, int64_t groups, int64_t count,
-                                                   uint8_t* __restrict__ out) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+                                                   int64_t rows, int64_t groups, int64_t chunks, int each, int64_t count,
+                                                   int block_bytes, uint8_t* __restrict__ out) {
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;      // [block][row][group of the block]
   if (at >= count) return;
-  const int r = at & 15;
-  const int64_t block = at >> 4, tile = block / groups, group = block - tile * groups;
-  const int64_t i = tile * 16 + r;
-  uint8_t* __restrict__ to = out + block * w4_group_bytes(sizeof(ST));
-  reinterpret_cast<ST*>(to)[r] = i < rows ? scales[i * groups + group] : ST(0);
-  to[16 * sizeof(ST) + r] = i < rows && zeros ? zeros[i * groups + group] : 8;
+  const int64_t block = at / (16 * each), tile = block / chunks, chunk = block - tile * chunks;
+  const int in = (int)(at - block * 16 * each);
+  const int64_t i = tile * 16 + in / each, group = chunk * each + in % each;
+  const bool have = i < rows && group < groups;
+  uint8_t* __restrict__ to = out + block * block_bytes + 1024;
+  reinterpret_cast<ST*>(to)[in] = have ? scales[i * groups + group] : ST(0);
+  to[16 * each * sizeof(ST) + in] = have && zeros ? zeros[i * groups + group] : 8;
 }
 
-// Four rows' scales times 16, and 1 + z / 16.
-template <typename ST>
-struct RowScales {
-  v4f s, z;
-  __device__ __forceinline__ void load(const uint8_t* group, int g) {
-    if constexpr (sizeof(ST) == 2) {
-      const uint2 w = *reinterpret_cast<const uint2*>(group + 8 * g);
-      s = v4f{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
-    } else {
-      s = *reinterpret_cast<const v4f*>(group + 16 * g);
-    }
-    const uint32_t b = *reinterpret_cast<const uint32_t*>(group + 16 * sizeof(ST) + 4 * g);
+// Eight codes as an operand.  (The masks are kept in registers: as literals they cost an instruction more.)
+struct CodeMask {
+  uint32_t bits = 0x00780078u, one = 0x3F803F80u;
+  __device__ __forceinline__ CodeMask() { asm volatile("" : "+s"(bits), "+v"(one)); }
+};
+__device__ __forceinline__ v4u codes_bf16(uint32_t w, const CodeMask& m) {
+  return v4u{(w & m.bits) | m.one, ((w >> 4) & m.bits) | m.one, ((w >> 8) & m.bits) | m.one,
+             (__builtin_amdgcn_alignbit(w, w, 12) & m.bits) | m.one};
+}
+
+// A load of 16 bytes at any element's alignment.
+struct __attribute__((packed, aligned(2))) Any16 {
+  v4u v;
+};
+
+// One wave's block of x: 128 columns of ROWS batch entries, read in whole cache lines (a wave instruction
+// reads 256 bytes of four rows of bf16, 512 of two of fp32) and turned in LDS into the matrix instruction's operand.
+// A row there is 16 bytes longer than its data, so that the sixteen rows of an operand read lie in distinct
+// banks.  fp32 is cut into three bf16 parts that hold it on the way, the largest first.
+template <typename XT, int ROWS>
+struct XBlock {
+  static constexpr int kParts = sizeof(XT) == 2 ? 1 : 3;
+  static constexpr int kPitch = 2 * kChunk + 16, kPlane = ROWS * kPitch;
+  static constexpr int kLanes = kChunk * sizeof(XT) / 16;            // of a row
+  static constexpr int kLoads = ROWS * kLanes / kWave;
+  static constexpr int kEach = 16 / sizeof(XT);                      // values of a lane's load
+  v4u raw[kLoads];
+  // offset in elements of a lane's piece in load i
+  __device__ static __forceinline__ uint32_t offset(int i, int lane, int B, int64_t cols) {
+    return (uint32_t)(min(i * (kWave / kLanes) + lane / kLanes, B - 1) * cols) + lane % kLanes * kEach;
+  }
+  __device__ __forceinline__ void load(const XT* x, const uint32_t (&off)[kLoads]) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      s[e] *= 16.f;
-      z[e] = fmaf((float)((b >> (8 * e)) & 255), 0.0625f, 1.f);
+    for (int i = 0; i < kLoads; ++i) raw[i] = reinterpret_cast<const Any16*>(x + off[i])->v;
+  }
+  __device__ __forceinline__ void load_end(const XT* x, const uint32_t (&off)[kLoads], int have) {   // the first `have` columns
+    const int mine = have - (int)(threadIdx.x & (kLanes - 1)) * kEach;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(XT) == 4) {
+          raw[i][e] = e < mine ? __float_as_uint(x[off[i] + e]) : 0;
+        } else {
+          const uint32_t lo = 2 * e < mine ? x[off[i] + 2 * e] : 0, hi = 2 * e + 1 < mine ? x[off[i] + 2 * e + 1] : 0;
+          raw[i][e] = lo | hi << 16;
+        }
+      }
+  }
+  __device__ __forceinline__ void store(uint8_t* lds, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      uint8_t* to = lds + (i * (kWave / kLanes) + lane / kLanes) * kPitch + lane % kLanes * kEach * 2;
+      if constexpr (sizeof(XT) == 2) {
+        *reinterpret_cast<v4u*>(to) = raw[i];
+      } else {
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(raw[i][e]);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          constexpr float kMost = 0x1.FEp127f;                       // a value past the largest bf16
+          v2u w;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float a = f[2 * h], b = f[2 * h + 1];
+            w[h] = p == 0 ? pack_bf16(__builtin_amdgcn_fmed3f(a, -kMost, kMost), __builtin_amdgcn_fmed3f(b, -kMost, kMost))
+                          : pack_bf16(a, b);
+            f[2 * h] -= bf16_lo(w[h]);
+            f[2 * h + 1] -= bf16_hi(w[h]);
+          }
+          *reinterpret_cast<v2u*>(to + p * kPlane) = w;
+        }
+      }
     }
   }
 };
 
-// Eight codes as an operand.
-__device__ __forceinline__ v4u codes_bf16(uint32_t w) {
-  constexpr uint32_t kMask = 0x00780078u, kOne = 0x3F803F80u;
-  return v4u{((w << 3) & kMask) | kOne, ((w >> 1) & kMask) | kOne, ((w >> 5) & kMask) | kOne, ((w >> 9) & kMask) | kOne};
-}
-
-__device__ __forceinline__ float wide(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-__device__ __forceinline__ float wide(float v) { return v; }
+// Scales and zero points of a row in a block: N groups.
+template <int N, typename ST>
+struct RowScales {
+  struct __attribute__((packed, aligned(N * sizeof(ST)))) S { ST v[N]; } s;
+  struct __attribute__((packed, aligned(N))) Z { uint8_t v[N]; } z;
+  __device__ __forceinline__ void load(const uint8_t* block, int row) {
+    s = *reinterpret_cast<const S*>(block + 1024 + row * N * sizeof(ST));
+    z = *reinterpret_cast<const Z*>(block + 1024 + 16 * N * sizeof(ST) + row * N);
+  }
+  __device__ __forceinline__ float scale(int q) const {
+    if constexpr (sizeof(ST) == 4) return s.v[q];
+    else return __uint_as_float((uint32_t)s.v[q] << 16);
+  }
+  __device__ __forceinline__ float zero(int q) const { return (float)z.v[q]; }
+};
 
 struct W4Kernel {
   const uint8_t* packed;
   const void* x;
   void* y;
-  int64_t rows, cols, chunks, groups;
-  int B, seg;            // seg: columns of x held at once, a multiple of 128
+  int64_t rows, cols, chunks, tiles;
+  int B, y_bf16;
 };
 
-// A workgroup per tile; its waves take the blocks of codes in turn, and their sums meet in LDS in wave
-// order.  x lies in LDS, `seg` columns at a time, each batch entry's row 16 bytes longer than its data (the
-// sixteen entries of an operand read then cover the banks evenly).
-template <int G, typename XT, typename ST, typename YT>
-__global__ __launch_bounds__(64 * kWaves) void k_w4(W4Kernel t) {
-  constexpr int kParts = sizeof(XT) == 2 ? 1 : 3;
-  extern __shared__ __align__(16) uint8_t s_mem[];
+// Bound by HBM for few entries (32000 x 4096, 68 MB: 15.1 us, 4.5 TB/s; all loads without products or x at 65536
+// columns 5.5 TB/s), by the launch for small layers (4096 x 4096, 8.7 MB: 4.2 us of which 2.6 are left without
+// any data to speak of), and for sixteen entries by x, which every workgroup reads from the L2 (4096 x 11008:
+// 90 MB of x beside 24 MB of codes in 11.5 us).
+// A workgroup of NW waves for RT tiles of 16 rows and all of the batch: the waves take the blocks of columns in
+// turn and their sums meet in LDS in wave order.  Batch entries are the rows of the product, so that a lane
+// holds one weight row's sums for four entries and needs that row's scales alone.
+template <int G, typename XT, typename ST, int NW, int RT, int ROWS, int NB>
+__global__ __launch_bounds__(64 * NW) void k_w4(W4Kernel t) {
+  constexpr int kBlock = w4_block_bytes(G, sizeof(ST)), kGroups = kChunk / G;
+  using X = XBlock<XT, ROWS>;
+  constexpr int kMine = X::kParts * X::kPlane;                       // a wave's bytes of LDS
+  constexpr int kSums = RT * ROWS * 64;                              // and of its sums, which take over
+  __shared__ __align__(16) uint8_t s_mem[NW * (kMine > kSums ? kMine : kSums)];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane & 15, g = lane >> 4;
-  const int64_t tile = blockIdx.x;
-  const int pitch = t.seg * 2 + 16;                                    // bytes
-  const int plane = pitch * t.B;
-  float* s_sum = reinterpret_cast<float*>(s_mem + kParts * plane);     // [B][seg / G]
-  const int sums = t.seg / G;
-  const uint8_t* scales = t.packed + w4_tiles(t.rows) * t.chunks * 1024 + tile * t.groups * w4_group_bytes(sizeof(ST));
-  const v4u* codes = reinterpret_cast<const v4u*>(t.packed + tile * t.chunks * 1024) + lane;
-  const int entry = min(c, t.B - 1);                                   // columns past the batch are not stored
-  v4f y = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int64_t k0 = 0; k0 < t.cols; k0 += t.seg) {
-    if (k0 > 0) __syncthreads();
-    // x and its group sums
-    for (int u = tid; u < t.B * t.seg / 8; u += 64 * kWaves) {
-      const int b = u / (t.seg / 8), k = (u - b * (t.seg / 8)) * 8;
-      const XT* __restrict__ from = static_cast<const XT*>(t.x) + b * t.cols + k0 + k;
-      float f[8];
+  const int64_t tile0 = (int64_t)blockIdx.x * RT;
+  const XT* __restrict__ x = static_cast<const XT*>(t.x);
+  uint32_t off[X::kLoads];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = k0 + k + e < t.cols ? wide(from[e]) : 0.f;
-      float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+  for (int i = 0; i < X::kLoads; ++i) off[i] = X::offset(i, lane, t.B, t.cols);
+  uint8_t* mine_x = s_mem + wave * kMine;
+  const uint8_t* operand = mine_x + min(c, t.B - 1) * X::kPitch + 16 * g;      // entries past the batch are not stored
+  const uint8_t* base[RT];
 #pragma unroll
-      for (int p = 0; p < kParts; ++p) {
-        v4u w;
+  for (int r = 0; r < RT; ++r) base[r] = t.packed + min(tile0 + r, t.tiles - 1) * t.chunks * kBlock;
+  struct Block {
+    v4u w[RT];
+    RowScales<kGroups, ST> s[RT];
+    X x;
+  };
+  auto load_codes = [&](Block& b, int ch) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          float a = f[2 * h], d = f[2 * h + 1];
-          if (kParts > 1 && p == 0) {                                   // a value past the largest bf16
-            constexpr float kMost = 0x1.FEp127f;
-            a = __builtin_amdgcn_fmed3f(a, -kMost, kMost);
-            d = __builtin_amdgcn_fmed3f(d, -kMost, kMost);
-          }
-          w[h] = pack_bf16(a, d);
-          f[2 * h] -= bf16_lo(w[h]);
-          f[2 * h + 1] -= bf16_hi(w[h]);
-        }
-        *reinterpret_cast<v4u*>(s_mem + p * plane + b * pitch + k * 2) = w;
-      }
-      sum = group_sum<G / 8>(sum);
-      if (k % G == 0) s_sum[b * sums + k / G] = sum;
+    for (int r = 0; r < RT; ++r) {
+      const uint8_t* at = base[r] + (int64_t)ch * kBlock;
+      b.w[r] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(at + lane * 16));
+      b.s[r].load(at, c);
     }
-    __syncthreads();
-    const int64_t c0 = k0 / kChunk, c1 = min(c0 + t.seg / kChunk, t.chunks);
-    for (int64_t ch = c0 + ((wave - c0) & (kWaves - 1)); ch < c1; ch += kWaves) {   // wave ch % 8, whatever seg is
-      const v4u w = codes[ch * 64];
-      const uint8_t* xs = s_mem + entry * pitch + (int)(ch - c0) * kChunk * 2 + 16 * g;
-      const float* sum = s_sum + entry * sums + (int)(ch - c0) * (kChunk / G);
+  };
+  float y[RT][NB];
 #pragma unroll
-      for (int q = 0; q < kChunk / G; ++q) {
-        RowScales<ST> rs;
-        rs.load(scales + min(ch * (kChunk / G) + q, t.groups - 1) * w4_group_bytes(sizeof(ST)), g);
-        v4f acc = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int s = q * (G / 32); s < (q + 1) * (G / 32); ++s) {
-          const v4u a = codes_bf16(w[s]);
+    for (int e = 0; e < NB; ++e) y[r][e] = 0.f;
+  const CodeMask mask;
+  auto multiply = [&](const Block& b) {
+    const v4u one = v4u{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    asm volatile("" ::: "memory");                       // a wave's reads and writes of LDS stay in their order
+    b.x.store(mine_x, lane);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-          for (int p = kParts - 1; p >= 0; --p)
-            acc = Mma<uint16_t>::run(a, *reinterpret_cast<const v4u*>(xs + p * plane + s * 64), acc);
+    for (int q = 0; q < kGroups; ++q) {
+      v4f acc[RT], sum = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = q * (G / 32); s < (q + 1) * (G / 32); ++s) {
+#pragma unroll
+        for (int p = X::kParts - 1; p >= 0; --p) {
+          const v4u xp = *reinterpret_cast<const v4u*>(operand + p * X::kPlane + 64 * s);
+          sum = Mma<uint16_t>::run(xp, one, sum);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) acc[r] = Mma<uint16_t>::run(xp, codes_bf16(b.w[r][s], mask), acc[r]);
         }
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = fmaf(rs.s[e], fmaf(-rs.z[e], sum[q], acc[e]), y[e]);
+      for (int r = 0; r < RT; ++r) {
+        const float z = fmaf(b.s[r].zero(q), -0.0625f, -1.f), scale = 16.f * b.s[r].scale(q);
+#pragma unroll
+        for (int e = 0; e < NB; ++e) y[r][e] = fmaf(scale, fmaf(z, sum[e], acc[r][e]), y[r][e]);
       }
     }
+  };
+  const int whole = (int)(t.cols / kChunk);
+  Block b;
+  for (int ch = wave; ch < whole; ch += NW) {
+    load_codes(b, ch);
+    b.x.load(x + ch * kChunk, off);
+    multiply(b);
+  }
+  if (whole < t.chunks && whole % NW == wave) {                          // the last block, of fewer columns
+    load_codes(b, whole);
+    b.x.load_end(x + whole * kChunk, off, (int)t.cols - whole * kChunk);
+    multiply(b);
   }
   __syncthreads();
-  // [wave][entry][row]
-  float* s_y = reinterpret_cast<float*>(s_mem);
-  if (c < t.B) *reinterpret_cast<v4f*>(s_y + (wave * t.B + c) * 16 + 4 * g) = y;
-  __syncthreads();
-  if (tid < t.B * 16) {
-    float v = s_y[tid];
+  float* s_y = reinterpret_cast<float*>(s_mem);                      // [wave][tile][entry][row]
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) v += s_y[w * t.B * 16 + tid];
-    const int64_t i = tile * 16 + (tid & 15);
-    if (i < t.rows) store_out(static_cast<YT*>(t.y), (tid >> 4) * t.rows + i, v);
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int e = 0; e < NB; ++e)
+      if (4 * g + e < t.B) s_y[((wave * RT + r) * ROWS + 4 * g + e) * 16 + c] = y[r][e];
+  __syncthreads();
+  for (int k = tid; k < RT * t.B * 16; k += NW * kWave) {
+    const int r = k / (t.B * 16), at = k - r * t.B * 16;
+    float v = s_y[r * ROWS * 16 + at];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) v += s_y[(w * RT + r) * ROWS * 16 + at];
+    const int64_t i = (tile0 + r) * 16 + (at & 15), to = (at >> 4) * t.rows + i;
+    if (i >= t.rows) continue;
+    if (t.y_bf16) store_out(static_cast<uint16_t*>(t.y), to, v);
+    else store_out(static_cast<float*>(t.y), to, v);
   }
 }
 
-template <int G, typename XT, typename ST, typename YT>
-hipError_t w4_gemv_t(const W4Args& a, hipStream_t s) {
-  constexpr int kParts = sizeof(XT) == 2 ? 1 : 3;
-  W4Kernel t{a.packed, a.x, a.y, a.rows, a.cols, w4_chunks(a.cols), (a.cols + G - 1) / G, a.B, 0};
-  const int64_t fit = kLdsX / a.B / (2 * kParts) / kChunk * kChunk;
-  t.seg = (int)std::min<int64_t>(fit, t.chunks * kChunk);
-  const size_t lds = std::max<size_t>((size_t)a.B * ((t.seg * 2 + 16) * kParts + t.seg / G * 4), (size_t)kWaves * a.B * 64);
-  hipLaunchKernelGGL((k_w4<G, XT, ST, YT>), dim3((unsigned)w4_tiles(a.rows)), dim3(64 * kWaves), lds, s, t);
-  return hipGetLastError();
+template <int G, typename XT, typename ST, int NW, int RT, int ROWS, int NB>
+void w4_run(const W4Kernel& t, hipStream_t s) {
+  hipLaunchKernelGGL((k_w4<G, XT, ST, NW, RT, ROWS, NB>), dim3((unsigned)((t.tiles + RT - 1) / RT)), dim3(64 * NW), 0, s, t);
 }
 
+// Waves to a tile (NW) and tiles to a workgroup (RT).  One block of codes in flight a wave, and as many waves
+// on a CU as its registers hold, beat fewer waves with two to eight blocks in flight by 5-30 % (32000 x 4096,
+// one entry: 14.2-15.1 us, with two blocks 17.6, four 19.7).  Up to a tile a CU sixteen waves share a tile (4096 x 4096, one entry: 16 waves
+// 4.3 us, 8 waves 5.2; 4096 x 11008, 16 entries 11.6 and 11.8), beyond that eight (6144 x 4096: 8 waves 5.8, 16
+// waves 6.7; 32000 x 4096: 16.7 and 21.9).  fp32's three parts of x leave LDS for eight.  More tiles a
+// workgroup share what a block of x costs: two from four tiles a CU on (32000 x 4096, one entry: 14.2 us
+// against 16.7; 11008 x 4096: 7.4 against 7.1), with fp32 x from one on (6144 x 4096: 7.9 against 8.8); with more
+// than four entries, whose x is four times as long, two from one on (8192 x 4096, eight entries: 6.9 against
+// 7.4, four tiles 8.5) and four from two and a half on (11008 x 4096, 16 entries: 9.3, two tiles 11.2; 32000 x
+// 4096: 18.6 and 20.8).  The waves alone decide the order of a sum, so it is the same for every batch.
+constexpr int kCUs = 256;
 template <int G, typename XT, typename ST>
-hipError_t w4_gemv_y(const W4Args& a, hipStream_t s) {
-  return a.y_bf16 ? w4_gemv_t<G, XT, ST, uint16_t>(a, s) : w4_gemv_t<G, XT, ST, float>(a, s);
+void w4_shape(const W4Kernel& t, hipStream_t s) {
+  const bool many = t.B > 4, one = t.B == 1;
+  if constexpr (sizeof(XT) == 2) {
+    if (t.tiles <= kCUs) {
+      if (many) w4_run<G, XT, ST, 16, 1, 16, 4>(t, s);
+      else if (one) w4_run<G, XT, ST, 16, 1, 4, 1>(t, s);
+      else w4_run<G, XT, ST, 16, 1, 4, 4>(t, s);
+      return;
+    }
+    if (!many && t.tiles <= 4 * kCUs) {
+      if (one) w4_run<G, XT, ST, 8, 1, 4, 1>(t, s);
+      else w4_run<G, XT, ST, 8, 1, 4, 4>(t, s);
+      return;
+    }
+  } else if (t.tiles <= kCUs) {
+    if (many) w4_run<G, XT, ST, 8, 1, 16, 4>(t, s);
+    else w4_run<G, XT, ST, 8, 1, 4, 4>(t, s);
+    return;
+  }
+  if constexpr (sizeof(XT) == 2)
+    if (one) return w4_run<G, XT, ST, 8, 2, 4, 1>(t, s);
+  if (many && t.tiles > 5 * kCUs / 2) w4_run<G, XT, ST, 8, 4, 16, 4>(t, s);
+  else if (many) w4_run<G, XT, ST, 8, 2, 16, 4>(t, s);
+  else w4_run<G, XT, ST, 8, 2, 4, 4>(t, s);
 }
-template <int G>
-hipError_t w4_gemv_g(const W4Args& a, hipStream_t s) {
-  if (a.x_bf16) return a.scales_bf16 ? w4_gemv_y<G, uint16_t, uint16_t>(a, s) : w4_gemv_y<G, uint16_t, float>(a, s);
-  return a.scales_bf16 ? w4_gemv_y<G, float, uint16_t>(a, s) : w4_gemv_y<G, float, float>(a, s);
-}
-
 }  // namespace
 
 size_t w4_bytes(int64_t rows, int64_t cols, int group, int scales_bf16) {
-  return (size_t)w4_tiles(rows) *
-         (w4_chunks(cols) * 1024 + (cols + group - 1) / group * w4_group_bytes(scales_bf16 ? 2 : 4));
+  return (size_t)w4_tiles(rows) * w4_chunks(cols) * w4_block_bytes(group, scales_bf16 ? 2 : 4);
 }
 
 hipError_t launch_w4_pack(const uint8_t* codes, const void* scales, int scales_bf16, const uint8_t* zeros, int64_t rows,
                           int64_t cols, int group, uint8_t* packed, hipStream_t s) {
   const int64_t chunks = w4_chunks(cols), words = w4_tiles(rows) * chunks * 256;
-  const int64_t groups = (cols + group - 1) / group, count = w4_tiles(rows) * groups * 16;
+  const int64_t groups = (cols + group - 1) / group, count = w4_tiles(rows) * chunks * (kChunk / group) * 16;
+  const int bytes = w4_block_bytes(group, scales_bf16 ? 2 : 4);
   hipLaunchKernelGGL(k_w4_codes, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, s, codes, rows, cols, chunks, words,
-                     reinterpret_cast<uint32_t*>(packed));
+                     bytes, packed);
   const dim3 grid((unsigned)((count + 255) / 256));
   if (scales_bf16)
     hipLaunchKernelGGL((k_w4_scales<uint16_t>), grid, dim3(256), 0, s, static_cast<const uint16_t*>(scales), zeros, rows,
-                       groups, count, packed + words * 4);
+                       groups, chunks, kChunk / group, count, bytes, packed);
   else
     hipLaunchKernelGGL((k_w4_scales<float>), grid, dim3(256), 0, s, static_cast<const float*>(scales), zeros, rows, groups,
-                       count, packed + words * 4);
+                       chunks, kChunk / group, count, bytes, packed);
   return hipGetLastError();
 }
 
 hipError_t launch_w4_gemv(const W4Args& a, hipStream_t s) {
+  const W4Kernel t{a.packed, a.x, a.y, a.rows, a.cols, w4_chunks(a.cols), w4_tiles(a.rows), a.B, a.y_bf16};
+  const auto run = [&](auto run_g) {
+    if (a.x_bf16) return a.scales_bf16 ? run_g(uint16_t(), uint16_t()) : run_g(uint16_t(), float());
+    return a.scales_bf16 ? run_g(float(), uint16_t()) : run_g(float(), float());
+  };
   switch (a.group) {
-    case 32: return w4_gemv_g<32>(a, s);
-    case 64: return w4_gemv_g<64>(a, s);
-    default: return w4_gemv_g<128>(a, s);
+    case 32: run([&](auto x, auto sc) { w4_shape<32, decltype(x), decltype(sc)>(t, s); }); break;
+    case 64: run([&](auto x, auto sc) { w4_shape<64, decltype(x), decltype(sc)>(t, s); }); break;
+    default: run([&](auto x, auto sc) { w4_shape<128, decltype(x), decltype(sc)>(t, s); }); break;
   }
+  return hipGetLastError();
 }
 
 }  // namespace f2i
