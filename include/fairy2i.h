@@ -434,7 +434,7 @@ int fairy2i_distill_backward(const void* h, const void* W, int x_dtype, int64_t 
  * Comparisons, differences and sums are fp64, sums in a fixed order.  Entries of w that are not finite or not
  * positive count as 0; a row without any weight gives the token -1.
  * 1 <= S <= 2^20, 1 <= D <= 63, 1 <= V <= 2^24, S ceil(V / 4096) <= 2^23; p and q need their element's
- * alignment only.  workspace: fairy2i_verify_draft_workspace_bytes(...) bytes, 16-byte aligned.  Outputs overlap
+ * alignment only.  workspace: fairy2i_verify_draft_workspace_bytes(...) bytes, 16-byte aligned (NULL allowed if 0).  Outputs overlap
  * nothing else, and calls that share a workspace must not overlap. */
 size_t fairy2i_verify_draft_workspace_bytes(int64_t S, int64_t D, int64_t V);
 int fairy2i_verify_draft(const void* p, const void* q, int p_dtype, int64_t S, int64_t D, int64_t V, const int64_t* draft,

@@ -79,7 +79,7 @@ def check(c, dev, label):
 
 
 SIZES = [(1, 1, 1), (1, 1, 2), (2, 63, 3), (5, 4, 63), (3, 2, 4095), (4, 3, 4096), (7, 5, 4097), (33, 8, 5003), (2, 3, 32000),
-         (1, 4, 131072), (40, 1, 8193)]
+         (1, 4, 131072), (40, 1, 8193), (3, 2, 40960), (2, 4, 40961), (600, 1, 700), (3, 2, 262147)]
 
 
 @pytest.mark.parametrize("dt", [F32, BF])
@@ -112,11 +112,12 @@ def test_same_distributions_keep_every_draft():
     assert (kept == 5).all()
 
 
-def test_rows_without_weight():
+@pytest.mark.parametrize("V", [5000, 50000])
+def test_rows_without_weight(V):
     """p nowhere above q though the draft is refused (p itself is drawn from); a row of zeros; NaN, infinity and
     negative values among the entries; a draft outside the vocabulary; lengths outside 0..D; u and r NaN."""
     dev = device()
-    S, D, V = 12, 2, 5000
+    S, D = 12, 2
     c = make(S, D, V, F32, False, 11)
     c["draft_len"][:] = D
     c["u"][:, 0] = 0.9999
@@ -151,14 +152,14 @@ def test_unused_drafts_hold_anything():
     assert torch.equal(accepted.cpu(), kept) and torch.equal(tokens.cpu(), want)
 
 
+@pytest.mark.parametrize("V", [9000, 60000])
 @pytest.mark.parametrize("dt", [F32, BF])
-def test_borders(dt):
+def test_borders(dt, V):
     """Weights that are powers of two, r at the borders themselves: a border belongs to the entry behind it, and
     entries without weight are never drawn."""
     dev = device()
-    V = 9000
     w = torch.zeros(V)
-    at = torch.tensor([0, 1, 15, 16, 255, 256, 4095, 4096, 4097, 8191, 8192, 8999])
+    at = torch.tensor([0, 1, 15, 16, 255, 256, 4095, 4096, 4097, 8191, 8192, V - 1])
     w[at] = 0.0625
     rs = torch.arange(0, 12).float() / 12
     rs = torch.cat([torch.arange(0, 13).float() * 0.0625 / 0.75, torch.tensor([0.0, 1.0, 1.0 - 2.0 ** -24, 0.5])])
@@ -198,8 +199,8 @@ def test_tokens_are_distributed_as_the_target():
 def test_any_alignment_and_borders_of_outputs():
     """p and q at odd offsets; the elements before and behind the outputs stay as they were."""
     dev = device()
-    for dt in (F32, BF):
-        c = make(5, 3, 4999, dt, False, 14)
+    for dt, V in ((F32, 4999), (BF, 4999), (F32, 49999), (BF, 49999)):
+        c = make(5, 3, V, dt, False, 14)
         want, kept = reference(c)
         flat = lambda t, off: torch.cat([torch.zeros(off, dtype=t.dtype), t.flatten()]).to(dev)[off:].view(t.shape)
         tokens = torch.full((5 * 4 + 4,), 99, device=dev)
@@ -213,7 +214,7 @@ def test_any_alignment_and_borders_of_outputs():
 
 def test_streams_graphs_and_shared_workspace():
     dev = device()
-    cs = [make(9, 4, 9001, F32, False, 20), make(9, 4, 9001, F32, False, 21)]
+    cs = [make(9, 4, 50001, F32, False, 20), make(9, 4, 50001, F32, False, 21)]
     want = [reference(c) for c in cs]
     d = {k: v.to(dev) for k, v in cs[0].items()}
     run = lambda **kw: f2.fairy2i_verify_draft(d["p"], d["q"], d["draft"], d["u"], d["r"], draft_len=d["draft_len"], **kw)
@@ -223,7 +224,7 @@ def test_streams_graphs_and_shared_workspace():
     tokens, accepted = run(stream=side)
     side.synchronize()
     assert torch.equal(tokens.cpu(), want[0][0]) and torch.equal(accepted.cpu(), want[0][1])
-    ws = torch.empty(f2.fairy2i_verify_draft_workspace_bytes(9, 4, 9001), dtype=torch.uint8, device=dev)
+    ws = torch.empty(f2.fairy2i_verify_draft_workspace_bytes(9, 4, 50001), dtype=torch.uint8, device=dev)
     announce("verify graphs")
     graphs = []
     for _ in range(2):                                  # two graphs over one workspace

@@ -34,7 +34,7 @@ def args(**kw):
     (dict(V=0), 2), (dict(V=(1 << 24) + 1, S=1), 2), (dict(S=2049, V=1 << 24), 2),
     (dict(p=FAKE + 2), 5), (dict(q=FAKE + 1, dt=1), 5), (dict(draft=FAKE + 4), 5), (dict(len=FAKE + 2), 5), (dict(u=FAKE + 2), 5),
     (dict(r=FAKE + 1), 5), (dict(tokens=Y + 4), 5), (dict(accepted=Z + 2), 5), (dict(ws=FAKE + 8), 5),
-    (dict(ws=None), 6), (dict(wsb=16), 6),
+    (dict(ws=None, V=131072), 6), (dict(wsb=16, V=131072), 6),
     (dict(p=Y), 2), (dict(q=Z), 2), (dict(draft=Y + 8), 2), (dict(len=Z + 4), 2), (dict(u=Y), 2), (dict(r=Z), 2),
     (dict(accepted=Y + 3 * 5 * 8 - 4), 2), (dict(p=Y - 3 * 5 * 100 * 4 + 4), 2)])
 def test_errors(L, kw, status):
@@ -43,7 +43,9 @@ def test_errors(L, kw, status):
 
 
 def test_workspace(L):
-    assert f2.fairy2i_verify_draft_workspace_bytes(3, 4, 4097) == 3 * 2 * 16
+    """None where a sequence has a workgroup to itself."""
+    assert f2.fairy2i_verify_draft_workspace_bytes(3, 4, 4097) == 0
+    assert f2.fairy2i_verify_draft_workspace_bytes(3, 4, 131072) == 3 * (64 + 1) * 16
     assert f2.fairy2i_verify_draft_workspace_bytes(3, 64, 4097) == 0
 
 

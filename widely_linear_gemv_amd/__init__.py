@@ -692,6 +692,11 @@ def _on_stream(fn):
     return call
 
 
+# The current stream of GPU number dev, as the C calls take it (torch.cuda.current_stream makes an object first:
+# 2.7 us of a call's host time against 0.1).
+_here = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _fits(t, dtype, shape, dev):
     """Whether t is what a call needs: a contiguous tensor of this dtype and shape on GPU number dev.
     The calls test all their arguments with it at once; only if one fails does the matching _refuse_
@@ -1117,7 +1122,7 @@ def fairy2i_gemv_w4(layer: W4Layer, x: torch.Tensor, *, y_dtype=torch.float32, y
                 raise ValueError(f"y_dtype: {y_dtype}, need torch.float32 or torch.bfloat16")
             y = torch.empty((x.shape[0], layer.rows), dtype=y_dtype, device=x.device)
         _check(lib().fairy2i_gemv_w4(layer.buf.data_ptr(), layer.rows, layer.cols, layer.group, _DTYPE[layer.scales_dtype],
-                                     x.data_ptr(), _DTYPE[x.dtype], x.shape[0], y.data_ptr(), _DTYPE[y.dtype], _stream()))
+                                     x.data_ptr(), _DTYPE[x.dtype], x.shape[0], y.data_ptr(), _DTYPE[y.dtype], _here(dev)))
     return y
 
 
@@ -1180,7 +1185,7 @@ def fairy2i_distill(h: torch.Tensor, W: torch.Tensor, top_index: torch.Tensor, t
     ws, nbytes, keep = _room(workspace, fairy2i_distill_workspace_bytes(N, V, K, code, top), h.device)
     _check(lib().fairy2i_distill(h.data_ptr(), W.data_ptr(), code, N, V, K, top_index.data_ptr(), top_logit.data_ptr(),
                                  _DTYPE[top_logit.dtype], top, temperature, loss.data_ptr(), lse.data_ptr(), ws, nbytes,
-                                 _stream()))
+                                 _here(h.get_device())))
     return loss, lse
 
 
@@ -1246,10 +1251,13 @@ def fairy2i_verify_draft(p: torch.Tensor, q, draft: torch.Tensor, u: torch.Tenso
         _refuse_verify(p, q, draft, u, r, draft_len, tokens, accepted)
     tokens = torch.empty((S, D1), dtype=i64, device=p.device) if tokens is None else tokens
     accepted = torch.empty((S,), dtype=i32, device=p.device) if accepted is None else accepted
-    ws, nbytes, keep = _room(workspace, fairy2i_verify_draft_workspace_bytes(S, D, V), p.device)
+    nbytes = lib().fairy2i_verify_draft_workspace_bytes(S, D, V)
+    ws = None
+    if nbytes or workspace is not None:
+        ws, nbytes, keep = _room(workspace, nbytes, p.device)
     _check(lib().fairy2i_verify_draft(p.data_ptr(), None if q is None else q.data_ptr(), _DTYPE[dt], S, D, V, draft.data_ptr(),
                                       None if draft_len is None else draft_len.data_ptr(), u.data_ptr(), r.data_ptr(),
-                                      tokens.data_ptr(), accepted.data_ptr(), ws, nbytes, _stream()))
+                                      tokens.data_ptr(), accepted.data_ptr(), ws, nbytes, _here(dev)))
     return tokens, accepted
 
 

@@ -5,64 +5,134 @@
 //
 // Products and differences of fp32 or bf16 values are exact in fp64 (up to the last bits of a difference),
 // and the sums are fp64, so that a token depends on their order only where r falls within 1e-15 of a border.
-// Two launches: every workgroup finds its sequence's position again and sums one piece of its rows of p and
-// q; then one workgroup a sequence finds the piece in which r falls and reads it a second time.
-#include "common.hpp"
+// A wave sums a contiguous piece of the rows of p and q; the piece in which r falls is then read a second time
+// by one wave.  Where a sequence has a workgroup to itself that is one launch; where there are few sequences and
+// a large vocabulary a first launch spreads the sums over the device.
+#include "tiles.hpp"
 
 namespace f2i {
 
 namespace {
 
-constexpr int kPiece = 4096;             // entries of a row per workgroup
-constexpr int kThreads = 256;
-constexpr int kEach = kPiece / kThreads;
+constexpr int kWaves = 16;               // of a sequence's workgroup (one launch)
+constexpr int kPiece = 2048;             // entries of a wave's piece (two launches)
+constexpr int kPieceWaves = 4;
 
 __device__ __forceinline__ float entry(const float* p, int64_t at) { return p[at]; }
 __device__ __forceinline__ float entry(const uint16_t* p, int64_t at) { return __uint_as_float((uint32_t)p[at] << 16); }
 
-// Where a sequence's drafts end: the number kept, and whether one was refused there.
+// 16 bytes of a row, at any element's alignment.
+template <typename T>
+struct Entries {
+  static constexpr int kCount = 16 / sizeof(T);
+  struct __attribute__((packed, aligned(sizeof(T)))) Raw { v4u v; } raw;
+  __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const Raw*>(p); }
+  __device__ __forceinline__ double operator[](int e) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(raw.v[e]);
+    else return e & 1 ? bf16_hi(raw.v[e / 2]) : bf16_lo(raw.v[e / 2]);
+  }
+};
+
+// Where a sequence's drafts end: the number kept, and whether one was refused there (then the draft's token).
 struct Stop {
   int kept;
   bool refused;
+  int64_t x;
 };
 
 // Each wave by itself, one draft a lane.
 template <typename T>
 __device__ __forceinline__ Stop find_stop(const VerifyArgs& a, int64_t s) {
   const int lane = threadIdx.x & (kWave - 1);
+  // all loads that depend on nothing first
   const int len = a.draft_len ? min(max(a.draft_len[s], 0), a.D) : a.D;
+  const int64_t x = lane < a.D ? a.draft[s * a.D + lane] : -1;
+  const float u = lane < a.D ? a.u[s * a.D + lane] : 0.f;
   bool keep = false;
-  if (lane < len) {
-    const int64_t x = a.draft[s * a.D + lane];
-    if (x >= 0 && x < a.V) {
-      const double p = entry(static_cast<const T*>(a.p), (s * (a.D + 1) + lane) * a.V + x);
-      const double q = a.q ? (double)entry(static_cast<const T*>(a.q), (s * a.D + lane) * a.V + x) : 1.0;
-      keep = (double)a.u[s * a.D + lane] * q < p;
-    }
+  if (lane < len && x >= 0 && x < a.V) {
+    const double p = entry(static_cast<const T*>(a.p), (s * (a.D + 1) + lane) * a.V + x);
+    const double q = a.q ? (double)entry(static_cast<const T*>(a.q), (s * a.D + lane) * a.V + x) : 1.0;
+    keep = (double)u * q < p;
   }
-  const uint64_t out = ~__ballot(keep);
-  const int kept = out ? __builtin_ctzll(out) : kWave;
-  return Stop{__builtin_amdgcn_readfirstlane(kept), kept < len};
+  const int kept = __builtin_ctzll(~__ballot(keep));          // lane 63 has no draft
+  return Stop{__builtin_amdgcn_readfirstlane(kept), kept < len, kept < len ? __shfl(x, kept) : -1};
 }
 
 // The weights of a row's entries: (difference, p itself), 0 for values that are not positive or not finite.
-template <typename T>
+// PAIR: the row has a q.  (A load that depends on a condition would make the compiler wait for each one.)
+template <typename T, bool PAIR>
 struct Row {
+  using E = Entries<T>;
+  static constexpr int kStep = E::kCount * kWave;      // entries of a wave's load
+  static constexpr int kBatch = 2048 / kStep;          // loads of a row in flight
   const T* p;
-  const T* q;          // null: a greedy draft, whose whole probability lies at x
-  int64_t x;
+  const T* q;
+  int64_t x, V;        // x: the token that holds all of a greedy draft's probability, or -1
   bool refused;
-  __device__ Row(const VerifyArgs& a, int64_t s, const Stop& stop)
-      : p(static_cast<const T*>(a.p) + (s * (a.D + 1) + stop.kept) * a.V),
-        q(a.q && stop.refused ? static_cast<const T*>(a.q) + (s * a.D + stop.kept) * a.V : nullptr),
-        x(stop.refused ? a.draft[s * a.D + stop.kept] : -1), refused(stop.refused) {}
   __device__ __forceinline__ static double positive(double w) { return w > 0.0 && w < INFINITY ? w : 0.0; }
-  __device__ __forceinline__ double2 weights(int64_t v) const {
-    const double pv = entry(p, v);
-    const double rest = q ? pv - (double)entry(q, v) : v == x ? 0.0 : pv;
-    return make_double2(refused ? positive(rest) : 0.0, positive(pv));
+  __device__ __forceinline__ double2 weigh(double pv, double qv, int64_t v) const {
+    const double rest = PAIR ? pv - qv : v == x ? 0.0 : pv;
+    return make_double2(PAIR || refused ? positive(rest) : 0.0, positive(pv));
   }
+  // f(e, weights) of a lane's entries in the step at v0, which lies inside the row
+  struct Raw {
+    E p, q;
+  };
+  __device__ __forceinline__ Raw load(int64_t v0) const {
+    const int64_t v = v0 + (threadIdx.x & (kWave - 1)) * E::kCount;
+    Raw r;
+    r.p.load(p + v);
+    if constexpr (PAIR) r.q.load(q + v);
+    return r;
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(const Raw& r, int64_t v0, F f) const {
+    const int64_t v = v0 + (threadIdx.x & (kWave - 1)) * E::kCount;
+#pragma unroll
+    for (int e = 0; e < E::kCount; ++e) f(e, weigh(r.p[e], PAIR ? r.q[e] : 0.0, v + e));
+  }
+  // the same in a step that the row may end in
+  template <typename F>
+  __device__ __forceinline__ void each_end(int64_t v0, F f) const {
+    const int64_t v = v0 + (threadIdx.x & (kWave - 1)) * E::kCount;
+#pragma unroll
+    for (int e = 0; e < E::kCount; ++e)
+      f(e, v + e < V ? weigh(entry(p, v + e), PAIR ? entry(q, v + e) : 0.0, v + e) : make_double2(0.0, 0.0));
+  }
+  // sums of the entries from v0 on, up to v1 or the row's end, in every lane
+  __device__ __forceinline__ double2 sums(int64_t v0, int64_t v1) const {
+    double2 sum = make_double2(0.0, 0.0);
+    v1 = min(v1, V);
+    const auto add = [&](int, const double2& w) {
+      sum.x += w.x;
+      sum.y += w.y;
+    };
+    int64_t v = v0;
+    for (; v + kBatch * kStep <= v1; v += kBatch * kStep) {
+      Raw r[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) r[k] = load(v + k * kStep);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) each(r[k], v + k * kStep, add);
+    }
+    for (; v + kStep <= v1; v += kStep) each(load(v), v, add);
+    if (v < v1) each_end(v, add);
+    return make_double2(wave_sum(sum.x), wave_sum(sum.y));
+  }
+  // the first entry with weight, from v0 on, at which `before` and the weights up to it pass `goal`, or the last
+  // with weight; -1 if none has any
+  __device__ __forceinline__ int64_t find(int64_t v0, int64_t v1, bool rest, double before, double goal) const;
 };
+
+// f(row) for the row that a sequence's next token is drawn from.
+template <typename T, typename F>
+__device__ __forceinline__ void with_row(const VerifyArgs& a, int64_t s, const Stop& stop, F f) {
+  const T* p = static_cast<const T*>(a.p) + (s * (a.D + 1) + stop.kept) * a.V;
+  if (a.q && stop.refused)
+    f(Row<T, true>{p, static_cast<const T*>(a.q) + (s * a.D + stop.kept) * a.V, -1, a.V, true});
+  else
+    f(Row<T, false>{p, nullptr, stop.x, a.V, stop.refused});
+}
 
 __device__ __forceinline__ double wave_scan(double v) {      // inclusive
   const int lane = threadIdx.x & (kWave - 1);
@@ -74,137 +144,177 @@ __device__ __forceinline__ double wave_scan(double v) {      // inclusive
   return v;
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_verify_sums(VerifyArgs a, int pieces, double2* __restrict__ sums) {
-  __shared__ double2 s_sum[kThreads / kWave];
-  const int64_t s = blockIdx.x / pieces;
-  const int piece = blockIdx.x - (int)(s * pieces);
-  const Row<T> row(a, s, find_stop<T>(a, s));
-  double2 sum = make_double2(0.0, 0.0);
-#pragma unroll
-  for (int k = 0; k < kEach; ++k) {
-    const int64_t v = (int64_t)piece * kPiece + k * kThreads + threadIdx.x;
-    if (v >= a.V) continue;
-    const double2 w = row.weights(v);
-    sum.x += w.x;
-    sum.y += w.y;
-  }
-  sum.x = wave_sum(sum.x);
-  sum.y = wave_sum(sum.y);
-  if ((threadIdx.x & (kWave - 1)) == 0) s_sum[threadIdx.x / kWave] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int w = 1; w < kThreads / kWave; ++w) {
-      sum.x += s_sum[w].x;
-      sum.y += s_sum[w].y;
+template <typename T, bool PAIR>
+__device__ __forceinline__ int64_t Row<T, PAIR>::find(int64_t v0, int64_t v1, bool rest, double before, double goal) const {
+  v1 = min(v1, V);
+  // the step in which it lies
+  int64_t last = -1;
+  double before_last = before;
+  bool found = false;
+  const auto look = [&](int64_t at, double sum) {
+    if (!found && sum > 0.0) {
+      last = at;
+      before_last = before;
+      found = before + sum > goal;
     }
-    sums[blockIdx.x] = sum;
+    before += sum;
+  };
+  int64_t v = v0;
+  for (; v + kBatch * kStep <= v1 && !found; v += kBatch * kStep) {
+    Raw r[kBatch];
+    double sum[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) r[k] = load(v + k * kStep);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      sum[k] = 0.0;
+      each(r[k], v + k * kStep, [&](int, const double2& both) { sum[k] += rest ? both.x : both.y; });
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) sum[k] = wave_sum(sum[k]);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) look(v + k * kStep, sum[k]);
   }
+  for (; v < v1 && !found; v += kStep) {
+    double sum = 0.0;
+    each_end(v, [&](int, const double2& both) { sum += rest ? both.x : both.y; });
+    look(v, wave_sum(sum));
+  }
+  if (last < 0) return -1;
+  // the entry: with weight, the first past the goal or the step's last
+  double w[E::kCount], sum = 0.0;
+  each_end(last, [&](int e, const double2& both) {
+    w[e] = rest ? both.x : both.y;
+    sum += w[e];
+  });
+  double run = before_last + (wave_scan(sum) - sum);
+  int over = -1, end = -1;
+#pragma unroll
+  for (int e = 0; e < E::kCount; ++e) {
+    run += w[e];
+    if (w[e] > 0.0) {
+      end = e;
+      if (over < 0 && run > goal) over = e;
+    }
+  }
+  const uint64_t past = __ballot(over >= 0), some = __ballot(end >= 0);
+  const int l = past ? __builtin_ctzll(past) : kWave - 1 - __builtin_clzll(some);
+  return last + l * E::kCount + __shfl(past ? over : end, l);
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_verify_pick(VerifyArgs a, int pieces, const double2* __restrict__ sums) {
-  __shared__ double s_wave[kThreads / kWave];
-  __shared__ int s_found[kThreads / kWave], s_last[kThreads / kWave];
-  const int64_t s = blockIdx.x;
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const Stop stop = find_stop<T>(a, s);
-  const Row<T> row(a, s, stop);
-  const double2* __restrict__ mine = sums + s * pieces;
-  // every wave finds the piece for itself: the total first, then the first piece past r of it
+// Where the next token lies, from the sums of a row's pieces in order: in every lane of a wave.
+struct Spot {
+  int piece;            // -1: no weight at all
+  bool rest;
+  double before, goal;  // weights before the piece, r times all
+};
+__device__ __forceinline__ Spot find_spot(const double2* sums, int pieces, double r) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const auto load = [&](int k) { return k + lane < pieces ? sums[k + lane] : make_double2(0.0, 0.0); };
   double2 total = make_double2(0.0, 0.0);
   for (int k = 0; k < pieces; k += kWave) {
-    const double2 w = k + lane < pieces ? mine[k + lane] : make_double2(0.0, 0.0);
-    total.x += __shfl(wave_scan(w.x), kWave - 1);
-    total.y += __shfl(wave_scan(w.y), kWave - 1);
+    const double2 w = load(k);
+    total.x += wave_sum(w.x);
+    total.y += wave_sum(w.y);
   }
   const bool rest = total.x > 0.0;
-  const double all = rest ? total.x : total.y;
-  const double goal = (double)a.r[s] * all;
-  int piece = -1, last = -1;                                  // last: the last piece with any weight
-  double before = 0.0, before_last = 0.0, carry = 0.0;
-  for (int k = 0; k < pieces && piece < 0; k += kWave) {
-    const double2 w = k + lane < pieces ? mine[k + lane] : make_double2(0.0, 0.0);
+  const double goal = r * (rest ? total.x : total.y);
+  Spot last{-1, rest, 0.0, goal};                             // the last piece with any weight
+  double carry = 0.0;
+  for (int k = 0; k < pieces; k += kWave) {
+    const double2 w = load(k);
     const double v = rest ? w.x : w.y, upto = carry + wave_scan(v);
-    if (const uint64_t over = __ballot(v > 0.0 && upto > goal)) {
-      const int at = __builtin_ctzll(over);
-      piece = k + at;
-      before = __shfl(upto - v, at);
-    }
-    if (const uint64_t some = __ballot(v > 0.0)) {
-      const int at = kWave - 1 - __builtin_clzll(some);
-      last = k + at;
-      before_last = __shfl(upto - v, at);
+    const uint64_t over = __ballot(v > 0.0 && upto > goal), some = __ballot(v > 0.0);
+    if (some) {
+      const int at = over ? __builtin_ctzll(over) : kWave - 1 - __builtin_clzll(some);
+      last.piece = k + at;
+      last.before = __shfl(upto - v, at);
+      if (over) break;
     }
     carry = __shfl(upto, kWave - 1);
   }
-  if (piece < 0) {
-    piece = last;
-    before = before_last;
-  }
-  int token = -1;                                             // no weight at all
-  if (piece >= 0) {
-    double w[kEach], sum = 0.0;
-    const int64_t v0 = (int64_t)piece * kPiece + threadIdx.x * kEach;
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      w[k] = 0.0;
-      if (v0 + k < a.V) {
-        const double2 both = row.weights(v0 + k);
-        w[k] = rest ? both.x : both.y;
-      }
-      sum += w[k];
-    }
-    const double upto = wave_scan(sum);
-    if (lane == kWave - 1) s_wave[wave] = upto;
-    __syncthreads();
-    double run = before + (upto - sum);
-    for (int k = 0; k < wave; ++k) run += s_wave[k];
-    int found = kPiece, end = -1;                             // within the piece; entries with weight only
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      run += w[k];
-      if (w[k] > 0.0) {
-        end = threadIdx.x * kEach + k;
-        if (run > goal) found = min(found, end);
-      }
-    }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      found = min(found, __shfl_xor(found, off));
-      end = max(end, __shfl_xor(end, off));
-    }
-    if (lane == 0) {
-      s_found[wave] = found;
-      s_last[wave] = end;
-    }
-    __syncthreads();
-    for (int k = 0; k < kThreads / kWave; ++k) {
-      found = min(found, s_found[k]);
-      end = max(end, s_last[k]);
-    }
-    token = piece * kPiece + (found < kPiece ? found : end);
-  }
-  if (threadIdx.x <= a.D) {
-    const int j = threadIdx.x;
-    a.tokens[s * (a.D + 1) + j] = j < stop.kept ? a.draft[s * a.D + j] : j == stop.kept ? token : -1;
-  }
-  if (threadIdx.x == 0) a.accepted[s] = stop.kept;
+  return last;
+}
+
+// One wave: the outputs of sequence s.
+template <typename T>
+__device__ __forceinline__ void finish(const VerifyArgs& a, int64_t s, const Stop& stop, const Spot& spot, int64_t each) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int64_t token = -1;
+  if (spot.piece >= 0)
+    with_row<T>(a, s, stop, [&](const auto& row) {
+      token = row.find(spot.piece * each, (spot.piece + 1) * each, spot.rest, spot.before, spot.goal);
+    });
+  if (lane <= a.D)
+    a.tokens[s * (a.D + 1) + lane] = lane < stop.kept ? a.draft[s * a.D + lane] : lane == stop.kept ? token : -1;
+  if (lane == 0) a.accepted[s] = stop.kept;
+}
+
+// One launch: a workgroup a sequence.
+template <typename T>
+__global__ __launch_bounds__(kWaves* kWave) void k_verify(VerifyArgs a, int64_t each) {
+  __shared__ double2 s_sums[kWaves];
+  const int64_t s = blockIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const Stop stop = find_stop<T>(a, s);
+  double2 sum;
+  with_row<T>(a, s, stop, [&](const auto& row) { sum = row.sums(wave * each, (wave + 1) * each); });
+  if ((threadIdx.x & (kWave - 1)) == 0) s_sums[wave] = sum;
+  __syncthreads();
+  if (wave == 0) finish<T>(a, s, stop, find_spot(s_sums, kWaves, a.r[s]), each);
+}
+
+// Two launches: every wave finds its sequence's position again and sums a piece; then a wave a sequence, which
+// finds the position behind the sums.
+template <typename T>
+__global__ __launch_bounds__(kPieceWaves* kWave) void k_verify_sums(VerifyArgs a, int groups, int pieces,
+                                                                     double2* __restrict__ sums) {
+  const int64_t s = blockIdx.x / groups;
+  const int piece = (blockIdx.x - (int)(s * groups)) * kPieceWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  if (piece >= pieces) return;
+  const Stop stop = find_stop<T>(a, s);
+  double2 sum;
+  with_row<T>(a, s, stop, [&](const auto& row) { sum = row.sums((int64_t)piece * kPiece, (int64_t)(piece + 1) * kPiece); });
+  if (threadIdx.x & (kWave - 1)) return;
+  sums[s * (pieces + 1) + piece] = sum;
+  if (piece == 0) sums[s * (pieces + 1) + pieces] = make_double2(stop.kept, stop.refused);
 }
 
 template <typename T>
+__global__ __launch_bounds__(kWave) void k_verify_pick(VerifyArgs a, int pieces, const double2* __restrict__ sums) {
+  const int64_t s = blockIdx.x;
+  sums += s * (pieces + 1);
+  const double2 found = sums[pieces];
+  const int kept = __builtin_amdgcn_readfirstlane((int)found.x);
+  const Stop stop{kept, found.y != 0.0, found.y != 0.0 ? a.draft[s * a.D + kept] : -1};
+  finish<T>(a, s, stop, find_spot(sums, pieces, a.r[s]), kPiece);
+}
+
+int pieces_of(int64_t V) { return (int)((V + kPiece - 1) / kPiece); }
+
+// One workgroup a sequence reads its rows at some 50 GB/s: as fast as two launches at 32000 entries (fp32: one
+// sequence 10.0 us against 10.5, 64 of bf16 12.5 and 14.1, 256 18.1 and 22.5), not at 65536 (14.1 and 10.4) nor
+// where there are more sequences than the device holds at once (600: 45 and 39).
+bool alone(int64_t S, int64_t V) { return V <= 40960 && S <= 512; }
+
+template <typename T>
 hipError_t verify_t(const VerifyArgs& a, void* ws, hipStream_t s) {
-  const int pieces = (int)((a.V + kPiece - 1) / kPiece);
+  if (alone(a.S, a.V)) {
+    const int64_t step = Row<T, true>::kStep, each = (a.V + kWaves * step - 1) / (kWaves * step) * step;
+    hipLaunchKernelGGL((k_verify<T>), dim3((unsigned)a.S), dim3(kWaves * kWave), 0, s, a, each);
+    return hipGetLastError();
+  }
+  const int pieces = pieces_of(a.V), groups = (pieces + kPieceWaves - 1) / kPieceWaves;
   double2* sums = static_cast<double2*>(ws);
-  hipLaunchKernelGGL((k_verify_sums<T>), dim3((unsigned)(a.S * pieces)), dim3(kThreads), 0, s, a, pieces, sums);
-  hipLaunchKernelGGL((k_verify_pick<T>), dim3((unsigned)a.S), dim3(kThreads), 0, s, a, pieces, sums);
+  hipLaunchKernelGGL((k_verify_sums<T>), dim3((unsigned)(a.S * groups)), dim3(kPieceWaves * kWave), 0, s, a, groups, pieces,
+                     sums);
+  hipLaunchKernelGGL((k_verify_pick<T>), dim3((unsigned)a.S), dim3(kWave), 0, s, a, pieces, sums);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t verify_workspace_bytes(int64_t S, int64_t V) { return (size_t)S * ((V + kPiece - 1) / kPiece) * sizeof(double2); }
+size_t verify_workspace_bytes(int64_t S, int64_t V) { return alone(S, V) ? 0 : (size_t)S * (pieces_of(V) + 1) * sizeof(double2); }
 
 hipError_t launch_verify(const VerifyArgs& a, int bf16, void* ws, hipStream_t s) {
   return bf16 ? verify_t<uint16_t>(a, ws, s) : verify_t<float>(a, ws, s);
