@@ -89,21 +89,53 @@ struct VocabTile {
   void* out;                    // [rows_b][rows_a] (kHidden on the last piece, kWeight)
   int64_t v0, V;                // first vocabulary entry of A, vocabulary size
   int64_t N, ldp;
-  const int32_t* list_index;    // [N][top] vocabulary entries, -1 for none (kDistill, kDistillGrad)
-  const float* list_prob;       // [N][top] t_ik (kDistillGrad)
-  float* list_logit;            // [N][top] (kDistill)
-  int top;
+  const int32_t* list_index;    // [N][list_pitch] vocabulary entries, -1 for none (kDistill, kDistillGrad)
+  const float* list_prob;       // [N][list_pitch] t_ik (kDistillGrad)
+  float* list_logit;            // [N][list_pitch] (kDistill)
+  int list_pitch;               // a multiple of 4
   float inv_temp;               // 1 / temperature (kDistill, kDistillGrad)
   int first, last;              // piece
   int tiles_a, tiles_b;
   int splits;                   // of the contraction (kHidden; 1 otherwise)
 };
 
-// Where a tile's entries are listed: of token n of the tile and row r, byte n * pitch + r is the slot + 1, or
-// 0.  The map takes over the operand buffers; its rows are 16 bytes longer than the tile's, so that the lanes
-// of a read (16 tokens, 4 words each) lie in distinct banks.
+// Calls f(token of the tile, row of the tile, slot, probability) for the listed entries that lie in a tile's rows
+// first .. first + BM - 1.  The lists' rows are whole groups of four slots; a thread's groups are loaded four at
+// a time (one by one, 16 loads of a tile took 10 us).
+template <int BM, int BN, int THREADS, bool PROB, typename F>
+__device__ __forceinline__ void each_listed(const VocabTile& t, int64_t first, int64_t b0, F f) {
+  constexpr int kBatch = 4;
+  const int width = t.list_pitch / 4, groups = (int)min((int64_t)BN, t.N - b0) * width;
+  const v4u* __restrict__ index = reinterpret_cast<const v4u*>(t.list_index + b0 * t.list_pitch);
+  const v4f* __restrict__ prob = reinterpret_cast<const v4f*>(t.list_prob + b0 * t.list_pitch);
+  for (int u0 = threadIdx.x; u0 < groups; u0 += kBatch * THREADS) {
+    v4u at[kBatch];
+    v4f p[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int u = min(u0 + k * THREADS, groups - 1);
+      at[k] = index[u];
+      if constexpr (PROB) p[k] = prob[u];
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int u = u0 + k * THREADS;
+      if (u >= groups) break;
+      const int n = u / width, slot = (u - n * width) * 4;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t r = (int32_t)at[k][e] - first;
+        if (r >= 0 && r < BM) f(n, (int)r, slot + e, PROB ? p[k][e] : 0.f);
+      }
+    }
+  }
+}
+
+// Which of a tile's entries are listed: of token n and row r, byte n * pitch + r is the slot + 1, or 0.  The map
+// takes over the operand buffers; its rows are 16 bytes longer than the tile's, so that the lanes of a read (16
+// tokens, 4 words each) lie in distinct banks.
 template <int BM, int BN>
-struct ListMap {
+struct SlotMap {
   static constexpr int kPitch = BM + 16;
   static_assert(kPitch * BN <= (BM + BN) * 256, "fits in two operand buffers");
   template <int THREADS>
@@ -111,20 +143,33 @@ struct ListMap {
     __syncthreads();                                       // every wave's copies have landed and been read
     for (int u = threadIdx.x; u < kPitch * BN / 16; u += THREADS) reinterpret_cast<uint4*>(map)[u] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    const int tokens = (int)min((int64_t)BN, t.N - b0);
-    const int32_t* __restrict__ index = t.list_index + b0 * t.top;
-    for (int u = threadIdx.x; u < tokens * t.top; u += THREADS) {
-      const int64_t r = index[u] - first;
-      if (r < 0 || r >= BM) continue;
-      const int n = u / t.top;
-      map[n * kPitch + (int)r] = (uint8_t)(u - n * t.top + 1);
-    }
+    each_listed<BM, BN, THREADS, false>(t, first, b0, [&](int n, int r, int slot, float) { map[n * kPitch + r] = (uint8_t)(slot + 1); });
+    __syncthreads();
+  }
+};
+
+// The listed probabilities of ROWS rows of a tile, 0 elsewhere: of token n and rows 4 s .. 4 s + 3, 16 bytes at
+// (n ROWS / 4 + (s ^ n % 16)) 16 (the sixteen tokens of a read lie in distinct banks).
+template <int ROWS, int BN>
+struct ProbMap {
+  static constexpr int kBytes = ROWS * BN * 4;
+  __device__ static __forceinline__ uint8_t* at(uint8_t* map, int n, int s) {
+    return map + (n * (ROWS / 4) + (s ^ (n & 15))) * 16;
+  }
+  template <int THREADS>
+  __device__ static __forceinline__ void fill(const VocabTile& t, uint8_t* map, int64_t first, int64_t b0) {
+    __syncthreads();                                       // what was here has been read
+    for (int u = threadIdx.x; u < kBytes / 16; u += THREADS) reinterpret_cast<uint4*>(map)[u] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    each_listed<ROWS, BN, THREADS, true>(t, first, b0, [&](int n, int r, int, float p) {
+      *reinterpret_cast<float*>(at(map, n, r >> 2) + (r & 3) * 4) = p;
+    });
     __syncthreads();
   }
 };
 
 // What happens to a finished tile (above).
-template <typename T, int BM, int BN, int WA, int WB, int FA, int FB, int EPI>
+template <typename T, int BM, int BN, int WA, int WB, int FA, int FB, int EPI, int LDS>
 __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], uint8_t* s_buf, int64_t a0, int64_t b0,
                                        int ta, int split) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -134,7 +179,7 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
   const int64_t va = a0 + wa * FA * 16 + 4 * g;            // this lane's first A row
   const int64_t nb = b0 + wb * FB * 16 + c;                // its first B row
   if constexpr (EPI == kDistill) {
-    using Map = ListMap<BM, BN>;
+    using Map = SlotMap<BM, BN>;
     Map::template fill<64 * WA * WB>(t, s_buf, a0, b0);
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
@@ -147,7 +192,7 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
         if (hit)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (const int slot = (hit >> (8 * e)) & 255) t.list_logit[tok * t.top + slot - 1] = acc[i][j][e];
+            if (const int slot = (hit >> (8 * e)) & 255) t.list_logit[tok * t.list_pitch + slot - 1] = acc[i][j][e];
       }
     }
   }
@@ -211,35 +256,49 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
       t.part[(int64_t)ta * t.N + b0 + k] = make_float2(top, sum);
     }
   } else if constexpr (EPI == kDistillGrad) {
-    using Map = ListMap<BM, BN>;
-    Map::template fill<64 * WA * WB>(t, s_buf, t.v0 + a0, b0);
+    // The map of the whole tile, or of one half of its rows after the other where it would not fit.
+    constexpr int kPasses = BM * BN * 4 <= LDS ? 1 : 2;
+    using Map = ProbMap<BM / kPasses, BN>;
+    static_assert(Map::kBytes <= LDS && WA % kPasses == 0, "a pass fits, and a wave has one");
     T* __restrict__ p = static_cast<T*>(t.p);
+    float gs[FB];
 #pragma unroll
-    for (int j = 0; j < FB; ++j) {
-      const int64_t tok = nb + 16 * j;
-      if (tok >= t.N) continue;
-      const float gi = t.g[tok];                           // 0 for tokens that do not count
-      const bool live = gi != 0.f;                         // other tokens give 0 whatever their logits are
-      const float lse = live ? t.lse[tok] : 0.f;
+    for (int j = 0; j < FB; ++j) {                         // softmax first: all waves have that to do at once
+      const int64_t tok = min(nb + 16 * j, t.N - 1);
+      gs[j] = t.g[tok];                                    // 0 for tokens that do not count
+      const float lse = t.lse[tok];
 #pragma unroll
-      for (int i = 0; i < FA; ++i) {
-        const int64_t r = va + 16 * i;                     // row within the piece
-        if (r >= t.ldp) continue;
-        const uint32_t hit =
-            *reinterpret_cast<const uint32_t*>(s_buf + ((wb * FB + j) * 16 + c) * Map::kPitch + (wa * FA + i) * 16 + 4 * g);
-        float x[4];
+      for (int i = 0; i < FA; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float off = fmaf(acc[i][j][e], t.inv_temp, -lse);
-          float v = sizeof(T) == 2 ? fast_exp(off) : expf(off);
-          if (const int slot = (hit >> (8 * e)) & 255) v -= t.list_prob[tok * t.top + slot - 1];
-          x[e] = live && r + e < t.rows_a ? gi * v : 0.f;
+          acc[i][j][e] = sizeof(T) == 2 ? fast_exp(off) : expf(off);
         }
-        if constexpr (sizeof(T) == 2)
-          *reinterpret_cast<uint2*>(p + tok * t.ldp + r) =
-              make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-        else
-          *reinterpret_cast<v4f*>(p + tok * t.ldp + r) = v4f{x[0], x[1], x[2], x[3]};
+    }
+#pragma unroll 1
+    for (int pass = 0; pass < kPasses; ++pass) {
+      Map::template fill<64 * WA * WB>(t, s_buf, t.v0 + a0 + pass * (BM / kPasses), b0);
+      if (wa / (WA / kPasses) != pass) continue;
+      const int s0 = (wa % (WA / kPasses)) * FA * 4 + g;   // the lane's first group of four rows in the map
+#pragma unroll
+      for (int j = 0; j < FB; ++j) {
+        const int64_t tok = nb + 16 * j;
+        if (tok >= t.N) continue;
+        const bool live = gs[j] != 0.f;                    // other tokens give 0 whatever their logits are
+#pragma unroll
+        for (int i = 0; i < FA; ++i) {
+          const int64_t r = va + 16 * i;                   // row within the piece
+          if (r >= t.ldp) continue;
+          const v4f listed = *reinterpret_cast<const v4f*>(Map::at(s_buf, (wb * FB + j) * 16 + c, s0 + 4 * i));
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = live && r + e < t.rows_a ? gs[j] * (acc[i][j][e] - listed[e]) : 0.f;
+          if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint2*>(p + tok * t.ldp + r) =
+                make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+          else
+            *reinterpret_cast<v4f*>(p + tok * t.ldp + r) = v4f{x[0], x[1], x[2], x[3]};
+        }
       }
     }
   } else if constexpr (EPI == kGrad) {
@@ -442,7 +501,7 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
       for (int j = 0; j < FB; ++j) asm volatile("" : "+a"(acc[i][j]));   // read only after settle()
   }
 
-  finish<T, BM, BN, WA, WB, FA, FB, EPI>(t, acc, s_buf, a0, b0, ta, split);
+  finish<T, BM, BN, WA, WB, FA, FB, EPI, NB * kStep>(t, acc, s_buf, a0, b0, ta, split);
 }
 
 // The same product for fp32 operands, on the bf16 matrix instructions: every value is cut into three bf16
@@ -624,11 +683,12 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt_split(VocabTile t) {
 #pragma unroll
       for (int j = 0; j < FB; ++j) asm volatile("" : "+a"(acc[i][j]));   // read only after settle()
   }
-  finish<float, BM, BN, WA, WB, FA, FB, EPI>(t, acc, s_buf, a0, b0, ta, split);
+  finish<float, BM, BN, WA, WB, FA, FB, EPI, 2 * kStep>(t, acc, s_buf, a0, b0, ta, split);
 }
 
-// A call's lists as k_teacher leaves them: [N][top] each, but for entropy and live [N].
+// A call's lists as k_teacher leaves them: [N][list_pitch(top)] each, but for entropy and live [N].
 constexpr int kMaxTop = 128;
+__host__ __device__ constexpr int list_pitch(int top) { return (top + 3) / 4 * 4; }
 struct TeacherLists {
   int32_t* index;
   float* prob;
@@ -717,8 +777,8 @@ __global__ __launch_bounds__(256) void k_teacher(const int64_t* __restrict__ ind
 #pragma unroll
   for (int q = 0; q < kEach; ++q) {
     const int k = q * kWave + lane;
-    if (k >= top) continue;
-    int32_t v = s_index[w][k];
+    if (k >= list_pitch(top)) continue;
+    int32_t v = s_index[w][k];                             // -1 behind the list
     float p = 0.f;
     if (v >= 0)
       for (int j = 0; j < top; ++j)
@@ -730,8 +790,8 @@ __global__ __launch_bounds__(256) void k_teacher(const int64_t* __restrict__ ind
           }
           p += s_prob[w][j];
         }
-    out.index[i * top + k] = v;
-    out.prob[i * top + k] = p;
+    out.index[i * list_pitch(top) + k] = v;
+    out.prob[i * list_pitch(top) + k] = p;
   }
   if (lane == 0) {
     out.entropy[i] = entropy;
@@ -755,8 +815,9 @@ __global__ __launch_bounds__(256) void k_distill_join(const float2* __restrict__
     const float2 v = part[(int64_t)s * N + i];
     sum += v.y * exp_off(v.x, best);
   }
+  const int64_t first = i * list_pitch(top);
   for (int k = lane; k < top; k += kWave)
-    if (list.index[i * top + k] >= 0) cross += list.prob[i * top + k] * list_logit[i * top + k];
+    if (list.index[first + k] >= 0) cross += list.prob[first + k] * list_logit[first + k];
   sum = wave_sum(sum);
   cross = wave_sum(cross);
   if (lane == 0) {
@@ -1020,8 +1081,8 @@ ListPlan list_plan(int64_t N, int top, size_t& at) {
   ListPlan l{};
   if (top == 0) return l;
   auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
-  l.index = take((size_t)N * top * 4);
-  l.prob = take((size_t)N * top * 4);
+  l.index = take((size_t)N * list_pitch(top) * 4);
+  l.prob = take((size_t)N * list_pitch(top) * 4);
   l.entropy = take((size_t)N * 4);
   l.live = take((size_t)N * 4);
   return l;
@@ -1043,7 +1104,7 @@ void launch_teacher(const VocabArgs& a, const TeacherLists& lists, hipStream_t s
 
 struct LossPlan {
   NtPlan nt;
-  size_t part, tlogit, total;     // tlogit: [N], or the listed logits [N][top]
+  size_t part, tlogit, total;     // tlogit: [N], or the listed logits [N][list_pitch]
   ListPlan list;
 };
 LossPlan loss_plan(int64_t N, int64_t V, int64_t K, int elem, int top) {
@@ -1051,7 +1112,7 @@ LossPlan loss_plan(int64_t N, int64_t V, int64_t K, int elem, int top) {
   p.nt = nt_plan(V, N, steps_of(K, elem), elem, 1, false);
   p.part = 0;
   p.tlogit = up256((size_t)tiles(V, kTiles[p.nt.shape].a) * N * sizeof(float2));
-  p.total = p.tlogit + up256((size_t)N * std::max(top, 1) * 4);
+  p.total = p.tlogit + up256((size_t)N * std::max(list_pitch(top), 1) * 4);
   p.list = list_plan(N, top, p.total);
   return p;
 }
@@ -1097,7 +1158,7 @@ hipError_t loss_t(const VocabArgs& a, hipStream_t s) {
   if (a.top > 0) {
     const TeacherLists lists = lists_at(ws, p.list);
     launch_teacher(a, lists, s);
-    t.list_index = lists.index; t.list_logit = t.tlogit; t.top = a.top; t.inv_temp = 1.f / a.temperature;
+    t.list_index = lists.index; t.list_logit = t.tlogit; t.list_pitch = list_pitch(a.top); t.inv_temp = 1.f / a.temperature;
     launch_nt<T, kDistill>(t, p.nt, a.V, a.N, s);
     hipLaunchKernelGGL(k_distill_join, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, t.part, lists, t.list_logit, a.N,
                        a.top, t.tiles_a, a.loss, a.lse_out);
@@ -1150,7 +1211,7 @@ hipError_t grad_t(const VocabArgs& a, hipStream_t s) {
     t.v0 = v0; t.V = a.V; t.N = a.N;
     const NtPlan plan = nt_plan(ldp, a.N, steps_of(a.K, sizeof(T)), sizeof(T), 1, false);
     if (a.top > 0) {
-      t.list_index = lists.index; t.list_prob = lists.prob; t.top = a.top; t.inv_temp = 1.f / a.temperature;
+      t.list_index = lists.index; t.list_prob = lists.prob; t.list_pitch = list_pitch(a.top); t.inv_temp = 1.f / a.temperature;
       launch_nt<T, kDistillGrad>(t, plan, ldp, a.N, s);
     } else {
       launch_nt<T, kGrad>(t, plan, ldp, a.N, s);
