@@ -66,6 +66,47 @@ def test_against_64_bits(size, G):
             check(layer, (codes, scales, zero), G, x, ydt, dev, (size, G, sdt, zeros, B, xdt, ydt))
 
 
+# sizes on both sides of where waves and tiles of a workgroup change (256, 640 and 1024 tiles of 16 rows)
+LARGE = [(4096, 300), (4100, 1405), (10240, 130), (10300, 2000), (16384, 129), (16500, 640)]
+
+
+@pytest.mark.parametrize("xdt", [BF, F32])
+@pytest.mark.parametrize("size", LARGE, ids=lambda s: "%dx%d" % s)
+def test_many_rows(size, xdt):
+    """The 64-bit reference runs on the GPU."""
+    dev = device()
+    rows, cols = size
+    for G, sdt in ((32, F32), (64, BF), (128, BF)):
+        codes, scales, zero, layer = make(rows, cols, G, sdt, True, 21, dev)
+        parts = [t.to(dev) for t in (codes, scales, zero)]
+        x = torch.randn(16, cols, generator=torch.Generator().manual_seed(4)).to(xdt).to(dev)
+        announce("w4 many rows", size, xdt, G)
+        want, bound = reference(*parts, G, x, F32)
+        all16 = f2.fairy2i_gemv_w4(layer, x)
+        assert ((all16.double() - want).abs() <= bound).all(), (size, G)
+        for B in (1, 2, 4, 5):
+            assert torch.equal(f2.fairy2i_gemv_w4(layer, x[:B].contiguous()), all16[:B]), (size, G, B)
+
+
+def test_offsets_past_32_bits():
+    """A layer of 2^33 codes: its last rows' blocks lie past 2^32 bytes.  All weights are 0 but some of theirs."""
+    dev = device()
+    rows, cols = (1 << 17) + 5, (1 << 16) + 100
+    announce("w4 offsets")
+    codes = torch.full((rows, cols), 8, dtype=torch.uint8, device=dev)
+    codes[rows - 1, ::1000], codes[rows - 6, cols - 1], codes[3, 5] = 9, 0, 15
+    scales = torch.ones((rows, -(-cols // 128)), dtype=BF, device=dev)
+    layer = f2.fairy2i_pack_w4(codes, scales, 128)
+    assert layer.buf.numel() > 1 << 32
+    del codes
+    x = torch.ones((2, cols), dtype=BF, device=dev)
+    x[1] = 2.0
+    y = f2.fairy2i_gemv_w4(layer, x)
+    want = torch.zeros(rows, device=dev)
+    want[rows - 1], want[rows - 6], want[3] = -(-cols // 1000), -8.0, 7.0
+    assert torch.equal(y, torch.stack([want, 2 * want]))         # whole numbers under 2^24 are exact
+
+
 def test_every_batch_is_the_same_sum():
     """A batch entry's outputs do not depend on the entries beside it, bit for bit."""
     dev = device()
