@@ -28,8 +28,8 @@
 // listed logits over the temperature, l_iv = <h_i, W_v> / temperature,
 //     loss_i = sum_k t_ik (log t_ik - l_{i, index_ik} + lse_i)
 //     p_iv = g_i / temperature (exp(l_iv - lse_i) - sum_{k: index_ik = v} t_ik)
-// k_teacher makes the lists' t_ik once; a finished tile looks up which of its entries are listed in a map
-// that its workgroup fills in LDS, stores their logits (loss) or subtracts their t_ik (p).  A token's gradient
+// A finished tile looks up which of its entries are listed in a map that its workgroup fills in LDS from the
+// lists, and stores their logits (loss) or subtracts their t_ik (p; k_teacher has made them for all tiles).  A token's gradient
 // has no one entry that dominates it for certain, so f_i is 1 here and g alone is taken apart: the roundings
 // of p's entries then differ from entry to entry.
 // Transposed operands are read from the matrix as it lies in memory: rows of the contraction are
@@ -89,9 +89,11 @@ struct VocabTile {
   void* out;                    // [rows_b][rows_a] (kHidden on the last piece, kWeight)
   int64_t v0, V;                // first vocabulary entry of A, vocabulary size
   int64_t N, ldp;
-  const int32_t* list_index;    // [N][list_pitch] vocabulary entries, -1 for none (kDistill, kDistillGrad)
+  const int64_t* top_index;     // [N][top] (kDistill)
+  float* list_logit;            // [N][top], of each entry's first slot (kDistill)
+  int top;
+  const int32_t* list_index;    // [N][list_pitch] vocabulary entries, -1 for none (kDistillGrad)
   const float* list_prob;       // [N][list_pitch] t_ik (kDistillGrad)
-  float* list_logit;            // [N][list_pitch] (kDistill)
   int list_pitch;               // a multiple of 4
   float inv_temp;               // 1 / temperature (kDistill, kDistillGrad)
   int first, last;              // piece
@@ -99,10 +101,10 @@ struct VocabTile {
   int splits;                   // of the contraction (kHidden; 1 otherwise)
 };
 
-// Calls f(token of the tile, row of the tile, slot, probability) for the listed entries that lie in a tile's rows
+// Calls f(token of the tile, row of the tile, probability) for the listed entries that lie in a tile's rows
 // first .. first + BM - 1.  The lists' rows are whole groups of four slots; a thread's groups are loaded four at
 // a time (one by one, 16 loads of a tile took 10 us).
-template <int BM, int BN, int THREADS, bool PROB, typename F>
+template <int BM, int BN, int THREADS, typename F>
 __device__ __forceinline__ void each_listed(const VocabTile& t, int64_t first, int64_t b0, F f) {
   constexpr int kBatch = 4;
   const int width = t.list_pitch / 4, groups = (int)min((int64_t)BN, t.N - b0) * width;
@@ -115,35 +117,58 @@ __device__ __forceinline__ void each_listed(const VocabTile& t, int64_t first, i
     for (int k = 0; k < kBatch; ++k) {
       const int u = min(u0 + k * THREADS, groups - 1);
       at[k] = index[u];
-      if constexpr (PROB) p[k] = prob[u];
+      p[k] = prob[u];
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int u = u0 + k * THREADS;
       if (u >= groups) break;
-      const int n = u / width, slot = (u - n * width) * 4;
+      const int n = u / width;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int64_t r = (int32_t)at[k][e] - first;
-        if (r >= 0 && r < BM) f(n, (int)r, slot + e, PROB ? p[k][e] : 0.f);
+        if (r >= 0 && r < BM) f(n, (int)r, p[k][e]);
       }
     }
   }
 }
 
-// Which of a tile's entries are listed: of token n and row r, byte n * pitch + r is the slot + 1, or 0.  The map
-// takes over the operand buffers; its rows are 16 bytes longer than the tile's, so that the lanes of a read (16
-// tokens, 4 words each) lie in distinct banks.
+// Which of a tile's entries are listed: of token n and row r, byte n * pitch + r is the first slot that lists it
+// + 1, or 0.  The map takes over the operand buffers; its rows are 16 bytes longer than the tile's, so that the
+// lanes of a read (16 tokens, 4 words each) lie in distinct banks.
 template <int BM, int BN>
 struct SlotMap {
   static constexpr int kPitch = BM + 16;
   static_assert(kPitch * BN <= (BM + BN) * 256, "fits in two operand buffers");
   template <int THREADS>
-  __device__ static __forceinline__ void fill(const VocabTile& t, uint8_t* map, int64_t first, int64_t b0) {
+  __device__ static __forceinline__ void fill(const VocabTile& t, uint8_t* map, int64_t a0, int64_t b0) {
+    constexpr int kBatch = 8;
     __syncthreads();                                       // every wave's copies have landed and been read
     for (int u = threadIdx.x; u < kPitch * BN / 16; u += THREADS) reinterpret_cast<uint4*>(map)[u] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    each_listed<BM, BN, THREADS, false>(t, first, b0, [&](int n, int r, int slot, float) { map[n * kPitch + r] = (uint8_t)(slot + 1); });
+    const int slots = (int)min((int64_t)BN, t.N - b0) * t.top;
+    const int64_t rows = min((int64_t)BM, t.V - a0);
+    const int64_t* __restrict__ index = t.top_index + b0 * t.top;
+    for (int u0 = threadIdx.x; u0 < slots; u0 += kBatch * THREADS) {
+      int64_t r[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) r[k] = index[min(u0 + k * THREADS, slots - 1)];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int u = u0 + k * THREADS;
+        // (both comparisons of the index itself: a difference could overflow)
+        if (u >= slots || r[k] < a0 || r[k] >= a0 + rows) continue;
+        const int n = u / t.top, at = n * kPitch + (int)(r[k] - a0), shift = 8 * (at & 3);
+        const uint32_t mine = (uint32_t)(u - n * t.top + 1) << shift, byte = 255u << shift;
+        uint32_t* word = reinterpret_cast<uint32_t*>(map + (at & ~3));
+        for (uint32_t have = *word;;) {                    // an entry listed twice keeps its first slot
+          if ((have & byte) != 0 && (have & byte) <= mine) break;
+          const uint32_t was = atomicCAS(word, have, (have & ~byte) | mine);
+          if (was == have) break;
+          have = was;
+        }
+      }
+    }
     __syncthreads();
   }
 };
@@ -161,7 +186,7 @@ struct ProbMap {
     __syncthreads();                                       // what was here has been read
     for (int u = threadIdx.x; u < kBytes / 16; u += THREADS) reinterpret_cast<uint4*>(map)[u] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    each_listed<ROWS, BN, THREADS, true>(t, first, b0, [&](int n, int r, int, float p) {
+    each_listed<ROWS, BN, THREADS>(t, first, b0, [&](int n, int r, float p) {
       *reinterpret_cast<float*>(at(map, n, r >> 2) + (r & 3) * 4) = p;
     });
     __syncthreads();
@@ -192,7 +217,7 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
         if (hit)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (const int slot = (hit >> (8 * e)) & 255) t.list_logit[tok * t.list_pitch + slot - 1] = acc[i][j][e];
+            if (const int slot = (hit >> (8 * e)) & 255) t.list_logit[tok * t.top + slot - 1] = acc[i][j][e];
       }
     }
   }
@@ -686,13 +711,12 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt_split(VocabTile t) {
   finish<float, BM, BN, WA, WB, FA, FB, EPI, 2 * kStep>(t, acc, s_buf, a0, b0, ta, split);
 }
 
-// A call's lists as k_teacher leaves them: [N][list_pitch(top)] each, but for entropy and live [N].
+// A call's lists as k_teacher leaves them: [N][list_pitch(top)] each, but for live [N].
 constexpr int kMaxTop = 128;
 __host__ __device__ constexpr int list_pitch(int top) { return (top + 3) / 4 * 4; }
 struct TeacherLists {
   int32_t* index;
   float* prob;
-  float* entropy;        // sum_k t_ik log t_ik
   int32_t* live;         // whether the token counts
 };
 
@@ -722,18 +746,17 @@ __global__ __launch_bounds__(256) void k_loss_join(const float2* __restrict__ pa
   }
 }
 
-// A teacher's lists, one wave per token: t_ik = softmax over the slots whose index lies in [0, V) of
-// logit / temperature (0 for a slot at minus infinity), and what the loss needs of it, sum_k t_ik log t_ik.
-// An entry listed more than once keeps its first slot, with the sum of its probabilities; its other slots,
-// and slots without probability, get index -1.  A token without any probability does not count.
+// A teacher's list, by one wave: t_ik = softmax over the slots whose index lies in [0, V) of logit / temperature,
+// into prob (0 for a slot at minus infinity and for unused ones), the indices (-1 for unused slots) into index.
+// NaN or plus infinity among the used logits makes all of the token's probabilities NaN.
+struct Teacher {
+  float entropy;         // sum_k t_ik log t_ik
+  bool live;             // whether any probability is left: otherwise the token does not count
+};
 template <typename LT>
-__global__ __launch_bounds__(256) void k_teacher(const int64_t* __restrict__ index, const LT* __restrict__ logit,
-                                                 int64_t N, int64_t V, int top, float inv_temp, TeacherLists out) {
-  __shared__ int32_t s_index[4][kMaxTop];
-  __shared__ float s_prob[4][kMaxTop];
-  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
-  const int64_t i = (int64_t)blockIdx.x * 4 + w;
-  if (i >= N) return;                                      // whole waves: no barrier below
+__device__ __forceinline__ Teacher teacher_list(const int64_t* __restrict__ index, const LT* __restrict__ logit, int64_t V,
+                                                int top, float inv_temp, int32_t* s_index, float* s_prob) {
+  const int lane = threadIdx.x & (kWave - 1);
   constexpr int kEach = kMaxTop / kWave;
   float z[kEach];
   int32_t at[kEach];
@@ -744,20 +767,19 @@ __global__ __launch_bounds__(256) void k_teacher(const int64_t* __restrict__ ind
     z[q] = -INFINITY;
     at[q] = -1;
     if (k >= top) continue;
-    const int64_t v = index[i * top + k];
+    const int64_t v = index[k];
     if (v < 0 || v >= V) continue;
     at[q] = (int32_t)v;
     float l;
-    if constexpr (sizeof(LT) == 2) l = __uint_as_float((uint32_t)logit[i * top + k] << 16);
-    else l = logit[i * top + k];
+    if constexpr (sizeof(LT) == 2) l = __uint_as_float((uint32_t)logit[k] << 16);
+    else l = logit[k];
     z[q] = l * inv_temp;
     best = fmaxf(best, z[q]);
-    if (!(z[q] < INFINITY)) bad = NAN;                     // NaN or plus infinity: the token's loss is NaN
+    if (!(z[q] < INFINITY)) bad = NAN;
   }
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) best = fmaxf(best, __shfl_xor(best, off));
   bad = wave_sum(bad);
-  const bool live = best > -INFINITY || bad != bad;
 #pragma unroll
   for (int q = 0; q < kEach; ++q) sum += z[q] > -INFINITY ? expf(z[q] - best) : 0.f;
   sum = wave_sum(sum) + bad;
@@ -769,43 +791,54 @@ __global__ __launch_bounds__(256) void k_teacher(const int64_t* __restrict__ ind
     float p = z[q] > -INFINITY ? expf(z[q] - best) / sum : 0.f;
     if (bad != bad && at[q] >= 0) p = bad;
     if (p > 0.f) entropy += p * (z[q] - best - log_sum);
-    s_index[w][k] = p == 0.f ? -1 : at[q];
-    s_prob[w][k] = p;
+    s_index[k] = at[q];
+    s_prob[k] = p;
   }
-  entropy = wave_sum(entropy) + bad;
   __builtin_amdgcn_wave_barrier();
-#pragma unroll
-  for (int q = 0; q < kEach; ++q) {
-    const int k = q * kWave + lane;
-    if (k >= list_pitch(top)) continue;
+  return Teacher{wave_sum(entropy) + bad, best > -INFINITY || bad != bad};
+}
+
+// The lists for the gradient, one wave per token.  An entry listed more than once keeps its first slot, with the
+// sum of its probabilities; its other slots, and entries without probability, get index -1.
+template <typename LT>
+__global__ __launch_bounds__(256) void k_teacher(const int64_t* __restrict__ index, const LT* __restrict__ logit,
+                                                 int64_t N, int64_t V, int top, float inv_temp, TeacherLists out) {
+  __shared__ int32_t s_index[4][kMaxTop];
+  __shared__ float s_prob[4][kMaxTop];
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+  const int64_t i = (int64_t)blockIdx.x * 4 + w;
+  if (i >= N) return;                                      // whole waves: no barrier here
+  const Teacher teacher = teacher_list(index + i * top, logit + i * top, V, top, inv_temp, s_index[w], s_prob[w]);
+  for (int k = lane; k < list_pitch(top); k += kWave) {
     int32_t v = s_index[w][k];                             // -1 behind the list
     float p = 0.f;
     if (v >= 0)
       for (int j = 0; j < top; ++j)
         if (s_index[w][j] == v) {
           if (j < k) {
-            v = -1;
             p = 0.f;
             break;
           }
           p += s_prob[w][j];
         }
-    out.index[i * list_pitch(top) + k] = v;
+    out.index[i * list_pitch(top) + k] = p == 0.f ? -1 : v;
     out.prob[i * list_pitch(top) + k] = p;
   }
-  if (lane == 0) {
-    out.entropy[i] = entropy;
-    out.live[i] = live;
-  }
+  if (lane == 0) out.live[i] = teacher.live;
 }
 
-// lse as k_loss_join, and the distillation loss from the listed logits.
-__global__ __launch_bounds__(256) void k_distill_join(const float2* __restrict__ part, TeacherLists list,
-                                                      const float* __restrict__ list_logit, int64_t N, int top, int tiles,
+// lse as k_loss_join, and the distillation loss from the list and its entries' logits (each at the first slot that
+// lists it).
+template <typename LT>
+__global__ __launch_bounds__(256) void k_distill_join(const float2* __restrict__ part, const int64_t* __restrict__ index,
+                                                      const LT* __restrict__ logit, const float* __restrict__ list_logit,
+                                                      int64_t N, int64_t V, int top, float inv_temp, int tiles,
                                                       float* __restrict__ loss, float* __restrict__ lse) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
-  if (i >= N) return;
+  __shared__ int32_t s_index[4][kMaxTop];
+  __shared__ float s_prob[4][kMaxTop];
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+  const int64_t i = (int64_t)blockIdx.x * 4 + w;
+  if (i >= N) return;                                      // whole waves: no barrier here
   float best = -INFINITY;
   for (int s = lane; s < tiles; s += kWave) best = fmaxf(best, part[(int64_t)s * N + i].x);
 #pragma unroll
@@ -815,15 +848,20 @@ __global__ __launch_bounds__(256) void k_distill_join(const float2* __restrict__
     const float2 v = part[(int64_t)s * N + i];
     sum += v.y * exp_off(v.x, best);
   }
-  const int64_t first = i * list_pitch(top);
-  for (int k = lane; k < top; k += kWave)
-    if (list.index[first + k] >= 0) cross += list.prob[first + k] * list_logit[first + k];
+  const Teacher teacher = teacher_list(index + i * top, logit + i * top, V, top, inv_temp, s_index[w], s_prob[w]);
+  for (int k = lane; k < top; k += kWave) {
+    const float p = s_prob[w][k];
+    if (p == 0.f) continue;
+    int j = 0;
+    while (s_index[w][j] != s_index[w][k]) ++j;
+    cross += p * list_logit[i * top + j];
+  }
   sum = wave_sum(sum);
   cross = wave_sum(cross);
   if (lane == 0) {
     const float l = best + logf(sum);
     lse[i] = l;
-    loss[i] = list.live[i] ? list.entropy[i] + (l - cross) : 0.f;
+    loss[i] = teacher.live ? teacher.entropy + (l - cross) : 0.f;
   }
 }
 
@@ -1075,7 +1113,7 @@ int64_t steps_of(int64_t k, int elem) { return (k * elem + 127) / 128; }
 
 // The lists' place in a workspace from `at` on, which moves behind them.
 struct ListPlan {
-  size_t index, prob, entropy, live;
+  size_t index, prob, live;
 };
 ListPlan list_plan(int64_t N, int top, size_t& at) {
   ListPlan l{};
@@ -1083,13 +1121,12 @@ ListPlan list_plan(int64_t N, int top, size_t& at) {
   auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
   l.index = take((size_t)N * list_pitch(top) * 4);
   l.prob = take((size_t)N * list_pitch(top) * 4);
-  l.entropy = take((size_t)N * 4);
   l.live = take((size_t)N * 4);
   return l;
 }
 TeacherLists lists_at(uint8_t* ws, const ListPlan& l) {
   return TeacherLists{reinterpret_cast<int32_t*>(ws + l.index), reinterpret_cast<float*>(ws + l.prob),
-                      reinterpret_cast<float*>(ws + l.entropy), reinterpret_cast<int32_t*>(ws + l.live)};
+                      reinterpret_cast<int32_t*>(ws + l.live)};
 }
 void launch_teacher(const VocabArgs& a, const TeacherLists& lists, hipStream_t s) {
   const dim3 grid((unsigned)((a.N + 3) / 4));
@@ -1104,16 +1141,14 @@ void launch_teacher(const VocabArgs& a, const TeacherLists& lists, hipStream_t s
 
 struct LossPlan {
   NtPlan nt;
-  size_t part, tlogit, total;     // tlogit: [N], or the listed logits [N][list_pitch]
-  ListPlan list;
+  size_t part, tlogit, total;     // tlogit: [N], or the listed logits [N][top]
 };
 LossPlan loss_plan(int64_t N, int64_t V, int64_t K, int elem, int top) {
   LossPlan p;
   p.nt = nt_plan(V, N, steps_of(K, elem), elem, 1, false);
   p.part = 0;
   p.tlogit = up256((size_t)tiles(V, kTiles[p.nt.shape].a) * N * sizeof(float2));
-  p.total = p.tlogit + up256((size_t)N * std::max(list_pitch(top), 1) * 4);
-  p.list = list_plan(N, top, p.total);
+  p.total = p.tlogit + up256((size_t)N * std::max(top, 1) * 4);
   return p;
 }
 
@@ -1156,12 +1191,18 @@ hipError_t loss_t(const VocabArgs& a, hipStream_t s) {
   t.tlogit = reinterpret_cast<float*>(ws + p.tlogit);
   t.V = a.V; t.N = a.N;
   if (a.top > 0) {
-    const TeacherLists lists = lists_at(ws, p.list);
-    launch_teacher(a, lists, s);
-    t.list_index = lists.index; t.list_logit = t.tlogit; t.list_pitch = list_pitch(a.top); t.inv_temp = 1.f / a.temperature;
+    const float inv = 1.f / a.temperature;
+    t.top_index = a.top_index; t.list_logit = t.tlogit; t.top = a.top; t.inv_temp = inv;
     launch_nt<T, kDistill>(t, p.nt, a.V, a.N, s);
-    hipLaunchKernelGGL(k_distill_join, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, t.part, lists, t.list_logit, a.N,
-                       a.top, t.tiles_a, a.loss, a.lse_out);
+    const dim3 grid((unsigned)((a.N + 3) / 4));
+    if (a.top_bf16)
+      hipLaunchKernelGGL((k_distill_join<uint16_t>), grid, dim3(256), 0, s, t.part, a.top_index,
+                         static_cast<const uint16_t*>(a.top_logit), t.list_logit, a.N, a.V, a.top, inv, t.tiles_a, a.loss,
+                         a.lse_out);
+    else
+      hipLaunchKernelGGL((k_distill_join<float>), grid, dim3(256), 0, s, t.part, a.top_index,
+                         static_cast<const float*>(a.top_logit), t.list_logit, a.N, a.V, a.top, inv, t.tiles_a, a.loss,
+                         a.lse_out);
     return hipGetLastError();
   }
   launch_nt<T, kLoss>(t, p.nt, a.V, a.N, s);
