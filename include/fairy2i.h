@@ -431,8 +431,8 @@ int fairy2i_distill_backward(const void* h, const void* W, int x_dtype, int64_t 
  *   u, r       fp32 [S][D] and [S], independent uniform numbers of [0, 1).
  *   tokens     out, int64 [S][D + 1]: the kept drafts, the next token, then -1.
  *   accepted   out, int32 [S]: a.
- * Comparisons, differences and sums are fp64, sums in a fixed order.  Entries of w that are not finite or not
- * positive count as 0; a row without any weight gives the token -1.
+ * Comparisons, differences and sums are fp64, sums in a fixed order.  Entries of w that are not positive or not
+ * in fp32's range count as 0; a row without any weight gives the token -1.
  * 1 <= S <= 2^20, 1 <= D <= 63, 1 <= V <= 2^24, S ceil(V / 4096) <= 2^23; p and q need their element's
  * alignment only.  workspace: fairy2i_verify_draft_workspace_bytes(...) bytes, 16-byte aligned (NULL allowed if 0).  Outputs overlap
  * nothing else, and calls that share a workspace must not overlap. */

@@ -45,7 +45,7 @@ def test_errors(L, kw, status):
 def test_workspace(L):
     """None where a sequence has a workgroup to itself."""
     assert f2.fairy2i_verify_draft_workspace_bytes(3, 4, 4097) == 0
-    assert f2.fairy2i_verify_draft_workspace_bytes(3, 4, 131072) == 3 * (64 + 1) * 16
+    assert f2.fairy2i_verify_draft_workspace_bytes(3, 4, 131072) == 3 * (64 + 2) * 8
     assert f2.fairy2i_verify_draft_workspace_bytes(3, 64, 4097) == 0
 
 

@@ -687,7 +687,10 @@ def _on_stream(fn):
         first, args = (args[0], args[1:]) if args else (kwargs.pop(name), args)
         if not isinstance(first, torch.Tensor) and first is not None:
             first = list(first)
-        with _scope(first[0] if isinstance(first, list) and first else first, stream):
+        scope = _scope(first[0] if isinstance(first, list) and first else first, stream)
+        if scope is _HERE_SCOPE:
+            return fn(first, *args, **kwargs)
+        with scope:
             return fn(first, *args, **kwargs)
     return call
 
@@ -1110,19 +1113,27 @@ def fairy2i_gemv_w4(layer: W4Layer, x: torch.Tensor, *, y_dtype=torch.float32, y
     """y = x W^T of a layer kept at four bits: x [B][cols] fp32 or bf16, B <= 16 -> y [B][rows]."""
     if not isinstance(layer, W4Layer):
         raise TypeError(f"layer: expected a W4Layer, got {type(layer).__name__}")
-    with _scope(x, stream):
-        dev = layer.buf.get_device()
-        if not (isinstance(x, torch.Tensor) and x.dtype in _FLOATS and x.dim() == 2 and x.shape[1] == layer.cols
-                and x.is_contiguous() and x.get_device() == dev >= 0
-                and (y is None or isinstance(y, torch.Tensor) and y.dtype in _FLOATS
-                     and _fits(y, y.dtype, (x.shape[0], layer.rows), dev))):
-            _refuse_gemv_w4(layer, x, y)
-        if y is None:
-            if y_dtype not in _FLOATS:
-                raise ValueError(f"y_dtype: {y_dtype}, need torch.float32 or torch.bfloat16")
-            y = torch.empty((x.shape[0], layer.rows), dtype=y_dtype, device=x.device)
-        _check(lib().fairy2i_gemv_w4(layer.buf.data_ptr(), layer.rows, layer.cols, layer.group, _DTYPE[layer.scales_dtype],
-                                     x.data_ptr(), _DTYPE[x.dtype], x.shape[0], y.data_ptr(), _DTYPE[y.dtype], _here(dev)))
+    scope = _scope(x, stream)
+    if scope is _HERE_SCOPE:
+        return _gemv_w4(layer, x, y_dtype, y)
+    with scope:
+        return _gemv_w4(layer, x, y_dtype, y)
+
+
+def _gemv_w4(layer, x, y_dtype, y):
+    dev = layer.buf.get_device()
+    if not (isinstance(x, torch.Tensor) and x.dtype in _FLOATS and x.dim() == 2 and x.shape[1] == layer.cols
+            and x.is_contiguous() and x.get_device() == dev >= 0
+            and (y is None or isinstance(y, torch.Tensor) and y.dtype in _FLOATS
+                 and _fits(y, y.dtype, (x.shape[0], layer.rows), dev))):
+        _refuse_gemv_w4(layer, x, y)
+    B = x.shape[0]
+    if y is None:
+        if y_dtype not in _FLOATS:
+            raise ValueError(f"y_dtype: {y_dtype}, need torch.float32 or torch.bfloat16")
+        y = x.new_empty((B, layer.rows), dtype=y_dtype)
+    _check(lib().fairy2i_gemv_w4(layer.buf.data_ptr(), layer.rows, layer.cols, layer.group, _DTYPE[layer.scales_dtype],
+                                 x.data_ptr(), _DTYPE[x.dtype], B, y.data_ptr(), _DTYPE[y.dtype], _here(dev)))
     return y
 
 
@@ -1249,8 +1260,8 @@ def fairy2i_verify_draft(p: torch.Tensor, q, draft: torch.Tensor, u: torch.Tenso
         good = False
     if not good:
         _refuse_verify(p, q, draft, u, r, draft_len, tokens, accepted)
-    tokens = torch.empty((S, D1), dtype=i64, device=p.device) if tokens is None else tokens
-    accepted = torch.empty((S,), dtype=i32, device=p.device) if accepted is None else accepted
+    tokens = p.new_empty((S, D1), dtype=i64) if tokens is None else tokens
+    accepted = p.new_empty((S,), dtype=i32) if accepted is None else accepted
     nbytes = lib().fairy2i_verify_draft_workspace_bytes(S, D, V)
     ws = None
     if nbytes or workspace is not None:

@@ -7,7 +7,8 @@
 // and the sums are fp64, so that a token depends on their order only where r falls within 1e-15 of a border.
 // A wave sums a contiguous piece of the rows of p and q; the piece in which r falls is then read a second time
 // by one wave.  Where a sequence has a workgroup to itself that is one launch; where there are few sequences and
-// a large vocabulary a first launch spreads the sums over the device.
+// a large vocabulary a first launch spreads the sums over the device.  Which entries have weight is decided in
+// fp32 (a difference's sign is exact there): 9 instructions an entry instead of 16 count where one CU does all.
 #include "tiles.hpp"
 
 namespace f2i {
@@ -58,8 +59,8 @@ __device__ __forceinline__ Stop find_stop(const VerifyArgs& a, int64_t s) {
   return Stop{__builtin_amdgcn_readfirstlane(kept), kept < len, kept < len ? __shfl(x, kept) : -1};
 }
 
-// The weights of a row's entries: (difference, p itself), 0 for values that are not positive or not finite.
-// PAIR: the row has a q.  (A load that depends on a condition would make the compiler wait for each one.)
+// The weights of a row's entries: p, or p - q (PAIR), where that is positive and in fp32's range, and 0 elsewhere.
+// (A load that depended on a condition would make the compiler wait for each one: hence the types.)
 template <typename T, bool PAIR>
 struct Row {
   using E = Entries<T>;
@@ -67,47 +68,43 @@ struct Row {
   static constexpr int kBatch = 2048 / kStep;          // loads of a row in flight
   const T* p;
   const T* q;
-  int64_t x, V;        // x: the token that holds all of a greedy draft's probability, or -1
-  bool refused;
-  __device__ __forceinline__ static double positive(double w) { return w > 0.0 && w < INFINITY ? w : 0.0; }
-  __device__ __forceinline__ double2 weigh(double pv, double qv, int64_t v) const {
-    const double rest = PAIR ? pv - qv : v == x ? 0.0 : pv;
-    return make_double2(PAIR || refused ? positive(rest) : 0.0, positive(pv));
+  int V, x;            // x: an entry without weight (a greedy draft's token), or -1
+  __device__ __forceinline__ double weigh(float pv, float qv, int v) const {
+    const float d = PAIR ? pv - qv : pv;
+    const bool has = __float_as_uint(d) - 1u < 0x7F7FFFFFu && (PAIR || v != x);      // 0 < d < infinity
+    return has ? (PAIR ? (double)pv - (double)qv : (double)pv) : 0.0;
   }
-  // f(e, weights) of a lane's entries in the step at v0, which lies inside the row
+  // f(e, weight) of a lane's entries in the step at v0, which lies inside the row
   struct Raw {
     E p, q;
   };
-  __device__ __forceinline__ Raw load(int64_t v0) const {
-    const int64_t v = v0 + (threadIdx.x & (kWave - 1)) * E::kCount;
+  __device__ __forceinline__ Raw load(int v0) const {
+    const int v = v0 + (threadIdx.x & (kWave - 1)) * E::kCount;
     Raw r;
     r.p.load(p + v);
     if constexpr (PAIR) r.q.load(q + v);
     return r;
   }
   template <typename F>
-  __device__ __forceinline__ void each(const Raw& r, int64_t v0, F f) const {
-    const int64_t v = v0 + (threadIdx.x & (kWave - 1)) * E::kCount;
+  __device__ __forceinline__ void each(const Raw& r, int v0, F f) const {
+    const int v = v0 + (threadIdx.x & (kWave - 1)) * E::kCount;
 #pragma unroll
-    for (int e = 0; e < E::kCount; ++e) f(e, weigh(r.p[e], PAIR ? r.q[e] : 0.0, v + e));
+    for (int e = 0; e < E::kCount; ++e) f(e, weigh(r.p[e], PAIR ? r.q[e] : 0.f, v + e));
   }
   // the same in a step that the row may end in
   template <typename F>
-  __device__ __forceinline__ void each_end(int64_t v0, F f) const {
-    const int64_t v = v0 + (threadIdx.x & (kWave - 1)) * E::kCount;
+  __device__ __forceinline__ void each_end(int v0, F f) const {
+    const int v = v0 + (threadIdx.x & (kWave - 1)) * E::kCount;
 #pragma unroll
     for (int e = 0; e < E::kCount; ++e)
-      f(e, v + e < V ? weigh(entry(p, v + e), PAIR ? entry(q, v + e) : 0.0, v + e) : make_double2(0.0, 0.0));
+      f(e, v + e < V ? weigh(entry(p, v + e), PAIR ? entry(q, v + e) : 0.f, v + e) : 0.0);
   }
-  // sums of the entries from v0 on, up to v1 or the row's end, in every lane
-  __device__ __forceinline__ double2 sums(int64_t v0, int64_t v1) const {
-    double2 sum = make_double2(0.0, 0.0);
+  // the sum of the entries from v0 on, up to v1 or the row's end, in every lane
+  __device__ __forceinline__ double sum(int v0, int v1) const {
+    double sum = 0.0;
     v1 = min(v1, V);
-    const auto add = [&](int, const double2& w) {
-      sum.x += w.x;
-      sum.y += w.y;
-    };
-    int64_t v = v0;
+    const auto add = [&](int, double w) { sum += w; };
+    int v = v0;
     for (; v + kBatch * kStep <= v1; v += kBatch * kStep) {
       Raw r[kBatch];
 #pragma unroll
@@ -117,21 +114,20 @@ struct Row {
     }
     for (; v + kStep <= v1; v += kStep) each(load(v), v, add);
     if (v < v1) each_end(v, add);
-    return make_double2(wave_sum(sum.x), wave_sum(sum.y));
+    return wave_sum(sum);
   }
   // the first entry with weight, from v0 on, at which `before` and the weights up to it pass `goal`, or the last
   // with weight; -1 if none has any
-  __device__ __forceinline__ int64_t find(int64_t v0, int64_t v1, bool rest, double before, double goal) const;
+  __device__ __forceinline__ int find(int v0, int v1, double before, double goal) const;
 };
 
-// f(row) for the row that a sequence's next token is drawn from.
+// f(row) for the weights that a sequence's next token is drawn from: what the target has above the draft, or (all)
+// the target's own.
 template <typename T, typename F>
-__device__ __forceinline__ void with_row(const VerifyArgs& a, int64_t s, const Stop& stop, F f) {
+__device__ __forceinline__ void with_row(const VerifyArgs& a, int64_t s, const Stop& stop, bool all, F f) {
   const T* p = static_cast<const T*>(a.p) + (s * (a.D + 1) + stop.kept) * a.V;
-  if (a.q && stop.refused)
-    f(Row<T, true>{p, static_cast<const T*>(a.q) + (s * a.D + stop.kept) * a.V, -1, a.V, true});
-  else
-    f(Row<T, false>{p, nullptr, stop.x, a.V, stop.refused});
+  if (a.q && !all) f(Row<T, true>{p, static_cast<const T*>(a.q) + (s * a.D + stop.kept) * a.V, (int)a.V, -1});
+  else f(Row<T, false>{p, nullptr, (int)a.V, all || stop.x < 0 || stop.x >= a.V ? -1 : (int)stop.x});
 }
 
 __device__ __forceinline__ double wave_scan(double v) {      // inclusive
@@ -145,13 +141,13 @@ __device__ __forceinline__ double wave_scan(double v) {      // inclusive
 }
 
 template <typename T, bool PAIR>
-__device__ __forceinline__ int64_t Row<T, PAIR>::find(int64_t v0, int64_t v1, bool rest, double before, double goal) const {
+__device__ __forceinline__ int Row<T, PAIR>::find(int v0, int v1, double before, double goal) const {
   v1 = min(v1, V);
   // the step in which it lies
-  int64_t last = -1;
+  int last = -1;
   double before_last = before;
   bool found = false;
-  const auto look = [&](int64_t at, double sum) {
+  const auto look = [&](int at, double sum) {
     if (!found && sum > 0.0) {
       last = at;
       before_last = before;
@@ -159,7 +155,7 @@ __device__ __forceinline__ int64_t Row<T, PAIR>::find(int64_t v0, int64_t v1, bo
     }
     before += sum;
   };
-  int64_t v = v0;
+  int v = v0;
   for (; v + kBatch * kStep <= v1 && !found; v += kBatch * kStep) {
     Raw r[kBatch];
     double sum[kBatch];
@@ -168,7 +164,7 @@ __device__ __forceinline__ int64_t Row<T, PAIR>::find(int64_t v0, int64_t v1, bo
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       sum[k] = 0.0;
-      each(r[k], v + k * kStep, [&](int, const double2& both) { sum[k] += rest ? both.x : both.y; });
+      each(r[k], v + k * kStep, [&](int, double w) { sum[k] += w; });
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) sum[k] = wave_sum(sum[k]);
@@ -177,15 +173,15 @@ __device__ __forceinline__ int64_t Row<T, PAIR>::find(int64_t v0, int64_t v1, bo
   }
   for (; v < v1 && !found; v += kStep) {
     double sum = 0.0;
-    each_end(v, [&](int, const double2& both) { sum += rest ? both.x : both.y; });
+    each_end(v, [&](int, double w) { sum += w; });
     look(v, wave_sum(sum));
   }
   if (last < 0) return -1;
   // the entry: with weight, the first past the goal or the step's last
   double w[E::kCount], sum = 0.0;
-  each_end(last, [&](int e, const double2& both) {
-    w[e] = rest ? both.x : both.y;
-    sum += w[e];
+  each_end(last, [&](int e, double weight) {
+    w[e] = weight;
+    sum += weight;
   });
   double run = before_last + (wave_scan(sum) - sum);
   int over = -1, end = -1;
@@ -205,26 +201,18 @@ __device__ __forceinline__ int64_t Row<T, PAIR>::find(int64_t v0, int64_t v1, bo
 // Where the next token lies, from the sums of a row's pieces in order: in every lane of a wave.
 struct Spot {
   int piece;            // -1: no weight at all
-  bool rest;
   double before, goal;  // weights before the piece, r times all
 };
-__device__ __forceinline__ Spot find_spot(const double2* sums, int pieces, double r) {
+__device__ __forceinline__ Spot find_spot(const double* sums, int pieces, double r) {
   const int lane = threadIdx.x & (kWave - 1);
-  const auto load = [&](int k) { return k + lane < pieces ? sums[k + lane] : make_double2(0.0, 0.0); };
-  double2 total = make_double2(0.0, 0.0);
-  for (int k = 0; k < pieces; k += kWave) {
-    const double2 w = load(k);
-    total.x += wave_sum(w.x);
-    total.y += wave_sum(w.y);
-  }
-  const bool rest = total.x > 0.0;
-  const double goal = r * (rest ? total.x : total.y);
-  Spot last{-1, rest, 0.0, goal};                             // the last piece with any weight
+  const auto load = [&](int k) { return k + lane < pieces ? sums[k + lane] : 0.0; };
+  double total = 0.0;
+  for (int k = 0; k < pieces; k += kWave) total += wave_sum(load(k));
+  Spot last{-1, 0.0, r * total};                              // the last piece with any weight
   double carry = 0.0;
   for (int k = 0; k < pieces; k += kWave) {
-    const double2 w = load(k);
-    const double v = rest ? w.x : w.y, upto = carry + wave_scan(v);
-    const uint64_t over = __ballot(v > 0.0 && upto > goal), some = __ballot(v > 0.0);
+    const double v = load(k), upto = carry + wave_scan(v);
+    const uint64_t over = __ballot(v > 0.0 && upto > last.goal), some = __ballot(v > 0.0);
     if (some) {
       const int at = over ? __builtin_ctzll(over) : kWave - 1 - __builtin_clzll(some);
       last.piece = k + at;
@@ -237,14 +225,8 @@ __device__ __forceinline__ Spot find_spot(const double2* sums, int pieces, doubl
 }
 
 // One wave: the outputs of sequence s.
-template <typename T>
-__device__ __forceinline__ void finish(const VerifyArgs& a, int64_t s, const Stop& stop, const Spot& spot, int64_t each) {
+__device__ __forceinline__ void store(const VerifyArgs& a, int64_t s, const Stop& stop, int64_t token) {
   const int lane = threadIdx.x & (kWave - 1);
-  int64_t token = -1;
-  if (spot.piece >= 0)
-    with_row<T>(a, s, stop, [&](const auto& row) {
-      token = row.find(spot.piece * each, (spot.piece + 1) * each, spot.rest, spot.before, spot.goal);
-    });
   if (lane <= a.D)
     a.tokens[s * (a.D + 1) + lane] = lane < stop.kept ? a.draft[s * a.D + lane] : lane == stop.kept ? token : -1;
   if (lane == 0) a.accepted[s] = stop.kept;
@@ -252,60 +234,91 @@ __device__ __forceinline__ void finish(const VerifyArgs& a, int64_t s, const Sto
 
 // One launch: a workgroup a sequence.
 template <typename T>
-__global__ __launch_bounds__(kWaves* kWave) void k_verify(VerifyArgs a, int64_t each) {
-  __shared__ double2 s_sums[kWaves];
+__global__ __launch_bounds__(kWaves* kWave) void k_verify(VerifyArgs a, int each) {
+  __shared__ double s_sums[kWaves];
   const int64_t s = blockIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const Stop stop = find_stop<T>(a, s);
-  double2 sum;
-  with_row<T>(a, s, stop, [&](const auto& row) { sum = row.sums(wave * each, (wave + 1) * each); });
-  if ((threadIdx.x & (kWave - 1)) == 0) s_sums[wave] = sum;
-  __syncthreads();
-  if (wave == 0) finish<T>(a, s, stop, find_spot(s_sums, kWaves, a.r[s]), each);
+  const double r = a.r[s];
+  // the rest of the target's probability; if that leaves nothing, all of it
+  for (bool all = !stop.refused;; all = true) {
+    double sum;
+    with_row<T>(a, s, stop, all, [&](const auto& row) { sum = row.sum(wave * each, (wave + 1) * each); });
+    if ((threadIdx.x & (kWave - 1)) == 0) s_sums[wave] = sum;
+    __syncthreads();
+    const Spot spot = find_spot(s_sums, kWaves, r);
+    if (spot.piece < 0 && !all) {
+      __syncthreads();
+      continue;
+    }
+    if (wave != 0) return;
+    int token = -1;
+    if (spot.piece >= 0)
+      with_row<T>(a, s, stop, all, [&](const auto& row) {
+        token = row.find(spot.piece * each, (spot.piece + 1) * each, spot.before, spot.goal);
+      });
+    return store(a, s, stop, token);
+  }
 }
 
 // Two launches: every wave finds its sequence's position again and sums a piece; then a wave a sequence, which
-// finds the position behind the sums.
+// finds the position behind the sums.  (Where the rest of the target's probability leaves nothing, which hardly
+// occurs, that wave sums the whole row by itself.)
 template <typename T>
 __global__ __launch_bounds__(kPieceWaves* kWave) void k_verify_sums(VerifyArgs a, int groups, int pieces,
-                                                                     double2* __restrict__ sums) {
+                                                                     double* __restrict__ sums) {
   const int64_t s = blockIdx.x / groups;
   const int piece = (blockIdx.x - (int)(s * groups)) * kPieceWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   if (piece >= pieces) return;
   const Stop stop = find_stop<T>(a, s);
-  double2 sum;
-  with_row<T>(a, s, stop, [&](const auto& row) { sum = row.sums((int64_t)piece * kPiece, (int64_t)(piece + 1) * kPiece); });
+  double sum;
+  with_row<T>(a, s, stop, !stop.refused, [&](const auto& row) { sum = row.sum(piece * kPiece, (piece + 1) * kPiece); });
   if (threadIdx.x & (kWave - 1)) return;
-  sums[s * (pieces + 1) + piece] = sum;
-  if (piece == 0) sums[s * (pieces + 1) + pieces] = make_double2(stop.kept, stop.refused);
+  sums += s * (pieces + 2);
+  sums[piece] = sum;
+  if (piece == 0) {
+    sums[pieces] = stop.kept;
+    sums[pieces + 1] = stop.refused;
+  }
 }
 
 template <typename T>
-__global__ __launch_bounds__(kWave) void k_verify_pick(VerifyArgs a, int pieces, const double2* __restrict__ sums) {
+__global__ __launch_bounds__(kWave) void k_verify_pick(VerifyArgs a, int pieces, const double* __restrict__ sums) {
   const int64_t s = blockIdx.x;
-  sums += s * (pieces + 1);
-  const double2 found = sums[pieces];
-  const int kept = __builtin_amdgcn_readfirstlane((int)found.x);
-  const Stop stop{kept, found.y != 0.0, found.y != 0.0 ? a.draft[s * a.D + kept] : -1};
-  finish<T>(a, s, stop, find_spot(sums, pieces, a.r[s]), kPiece);
+  sums += s * (pieces + 2);
+  const int kept = __builtin_amdgcn_readfirstlane((int)sums[pieces]);
+  const bool refused = sums[pieces + 1] != 0.0;
+  const Stop stop{kept, refused, refused ? a.draft[s * a.D + kept] : -1};
+  const double r = a.r[s];
+  const Spot spot = find_spot(sums, pieces, r);
+  int token = -1;
+  if (spot.piece >= 0)
+    with_row<T>(a, s, stop, !refused, [&](const auto& row) {
+      token = row.find(spot.piece * kPiece, (spot.piece + 1) * kPiece, spot.before, spot.goal);
+    });
+  else if (refused)
+    with_row<T>(a, s, stop, true, [&](const auto& row) { token = row.find(0, (int)a.V, 0.0, r * row.sum(0, (int)a.V)); });
+  store(a, s, stop, token);
 }
 
 int pieces_of(int64_t V) { return (int)((V + kPiece - 1) / kPiece); }
 
 // One workgroup a sequence reads its rows at some 50 GB/s: as fast as two launches at 32000 entries (fp32: one
 // sequence 10.0 us against 10.5, 64 of bf16 12.5 and 14.1, 256 18.1 and 22.5), not at 65536 (14.1 and 10.4) nor
-// where there are more sequences than the device holds at once (600: 45 and 39).
+// where there are more sequences than the device holds at once (600: 45 and 39).  (Measured while an entry took 16
+// instructions; with 9, one sequence of 32000 takes 8.4 us and of 131072, in two launches, 8.6; 64 of 131072, 67
+// MB, 19 us; 256 of 131072, 268 MB, 49 us, 5.5 TB/s.)
 bool alone(int64_t S, int64_t V) { return V <= 40960 && S <= 512; }
 
 template <typename T>
 hipError_t verify_t(const VerifyArgs& a, void* ws, hipStream_t s) {
   if (alone(a.S, a.V)) {
-    const int64_t step = Row<T, true>::kStep, each = (a.V + kWaves * step - 1) / (kWaves * step) * step;
+    const int step = Row<T, true>::kStep, each = (int)((a.V + kWaves * step - 1) / (kWaves * step)) * step;
     hipLaunchKernelGGL((k_verify<T>), dim3((unsigned)a.S), dim3(kWaves * kWave), 0, s, a, each);
     return hipGetLastError();
   }
   const int pieces = pieces_of(a.V), groups = (pieces + kPieceWaves - 1) / kPieceWaves;
-  double2* sums = static_cast<double2*>(ws);
+  double* sums = static_cast<double*>(ws);
   hipLaunchKernelGGL((k_verify_sums<T>), dim3((unsigned)(a.S * groups)), dim3(kPieceWaves * kWave), 0, s, a, groups, pieces,
                      sums);
   hipLaunchKernelGGL((k_verify_pick<T>), dim3((unsigned)a.S), dim3(kWave), 0, s, a, pieces, sums);
@@ -314,7 +327,7 @@ hipError_t verify_t(const VerifyArgs& a, void* ws, hipStream_t s) {
 
 }  // namespace
 
-size_t verify_workspace_bytes(int64_t S, int64_t V) { return alone(S, V) ? 0 : (size_t)S * (pieces_of(V) + 1) * sizeof(double2); }
+size_t verify_workspace_bytes(int64_t S, int64_t V) { return alone(S, V) ? 0 : (size_t)S * (pieces_of(V) + 2) * sizeof(double); }
 
 hipError_t launch_verify(const VerifyArgs& a, int bf16, void* ws, hipStream_t s) {
   return bf16 ? verify_t<uint16_t>(a, ws, s) : verify_t<float>(a, ws, s);
