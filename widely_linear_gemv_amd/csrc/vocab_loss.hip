@@ -101,6 +101,8 @@ struct VocabTile {
   int splits;                   // of the contraction (kHidden; 1 otherwise)
 };
 
+constexpr int kMaxTop = 128;           // slots of a list
+
 // Calls f(token of the tile, row of the tile, probability) for the listed entries that lie in a tile's rows
 // first .. first + BM - 1.  The lists' rows are whole groups of four slots; a thread's groups are loaded four at
 // a time (one by one, 16 loads of a tile took 10 us).
@@ -119,6 +121,8 @@ __device__ __forceinline__ void each_listed(const VocabTile& t, int64_t first, i
       at[k] = index[u];
       p[k] = prob[u];
     }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) asm volatile("" : "+v"(at[k]), "+v"(p[k]));     // loaded here, not where it is used
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int u = u0 + k * THREADS;
@@ -149,24 +153,31 @@ struct SlotMap {
     const int slots = (int)min((int64_t)BN, t.N - b0) * t.top;
     const int64_t rows = min((int64_t)BM, t.V - a0);
     const int64_t* __restrict__ index = t.top_index + b0 * t.top;
-    for (int u0 = threadIdx.x; u0 < slots; u0 += kBatch * THREADS) {
+    // which of the thread's slots lie in the tile, then those alone: few lanes have one at a time, and most have
+    // none (every slot in its turn: 12 us a tile at 64 slots)
+    static_assert(BN * kMaxTop <= 64 * THREADS, "a thread's slots fit in a mask");
+    uint64_t hits = 0;
+    for (int u0 = threadIdx.x, bit = 0; u0 < slots; u0 += kBatch * THREADS, bit += kBatch) {
       int64_t r[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) r[k] = index[min(u0 + k * THREADS, slots - 1)];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int u = u0 + k * THREADS;
-        // (both comparisons of the index itself: a difference could overflow)
-        if (u >= slots || r[k] < a0 || r[k] >= a0 + rows) continue;
-        const int n = u / t.top, at = n * kPitch + (int)(r[k] - a0), shift = 8 * (at & 3);
-        const uint32_t mine = (uint32_t)(u - n * t.top + 1) << shift, byte = 255u << shift;
-        uint32_t* word = reinterpret_cast<uint32_t*>(map + (at & ~3));
-        for (uint32_t have = *word;;) {                    // an entry listed twice keeps its first slot
-          if ((have & byte) != 0 && (have & byte) <= mine) break;
-          const uint32_t was = atomicCAS(word, have, (have & ~byte) | mine);
-          if (was == have) break;
-          have = was;
-        }
+      for (int k = 0; k < kBatch; ++k) asm volatile("" : "+v"(r[k]));      // loaded here, not where it is used
+      uint32_t in = 0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) in |= (u0 + k * THREADS < slots && r[k] >= a0 && r[k] < a0 + rows ? 1u : 0u) << k;
+      hits |= (uint64_t)in << bit;
+    }
+    for (; hits; hits &= hits - 1) {
+      const int u = threadIdx.x + __builtin_ctzll(hits) * THREADS;
+      const int n = u / t.top, at = n * kPitch + (int)(index[u] - a0), shift = 8 * (at & 3);
+      const uint32_t mine = (uint32_t)(u - n * t.top + 1) << shift, byte = 255u << shift;
+      uint32_t* word = reinterpret_cast<uint32_t*>(map + (at & ~3));
+      for (uint32_t have = *word;;) {                      // an entry listed twice keeps its first slot
+        if ((have & byte) != 0 && (have & byte) <= mine) break;
+        const uint32_t was = atomicCAS(word, have, (have & ~byte) | mine);
+        if (was == have) break;
+        have = was;
       }
     }
     __syncthreads();
@@ -712,7 +723,6 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt_split(VocabTile t) {
 }
 
 // A call's lists as k_teacher leaves them: [N][list_pitch(top)] each, but for live [N].
-constexpr int kMaxTop = 128;
 __host__ __device__ constexpr int list_pitch(int top) { return (top + 3) / 4 * 4; }
 struct TeacherLists {
   int32_t* index;
