@@ -375,9 +375,10 @@ int fairy2i_pack_w4(const uint8_t* codes, const void* scales, int scales_dtype, 
  *   x        [B][cols], x_dtype FAIRY2I_F32 or FAIRY2I_BF16; 16-byte aligned as a whole, rows of any length.
  *   y        out, [B][rows], y_dtype FAIRY2I_F32 or FAIRY2I_BF16 (rounded once), 16-byte aligned, overlapping
  *            neither packed nor x.
- * Exact products of bf16 x (fp32 x: as three bf16 parts that hold it) in fp32 sums of sum_j (16 + c) x and
- * sum_j x for each group, in an order that does not depend on B or the launch.  A NaN in a batch entry stays
- * in that entry; an infinity gives NaN or infinity in its outputs.  Uses no workspace. */
+ * Exact products of bf16 x (fp32 x: as three bf16 parts that hold it) in fp32 sums of sum_j (1 + c / 16) x and
+ * sum_j x for each group, in an order that does not depend on B.  Values under bf16's normal range (x under
+ * 2^-126, low parts of fp32 x under 2^-110) may count as 0.  A NaN in a batch entry stays in that entry; an
+ * infinity, or sums past fp32's range, give NaN or infinity in its outputs.  Uses no workspace. */
 int fairy2i_gemv_w4(const uint8_t* packed, int64_t rows, int64_t cols, int group, int scales_dtype, const void* x,
                     int x_dtype, int64_t B, void* y, int y_dtype, hipStream_t stream);
 
@@ -405,10 +406,10 @@ int fairy2i_distill(const void* h, const void* W, int x_dtype, int64_t N, int64_
 /* Its gradient: with g_i the gradient of loss_i and lse from the forward call,
  *     p_iv = g_i / temperature (exp(l_iv - lse_i) - sum of t_ik over the slots with index_ik = v)
  *     dh_i = sum_v p_iv W_v        dW_v = sum_i p_iv h_i
- * as fairy2i_vocab_loss_backward in everything else: pieces of the vocabulary, p held in x_dtype between the
- * products (bf16: in units of a power of two near |g_i|, the rest of g_i applied to the fp32 sums of dh and,
- * rounded, to h for dW, where all g equal cost nothing), fp32 sums, each output rounded once, either output
- * NULL.  A token that does not count or has g_i = 0 adds nothing, whatever its row of h holds. */
+ * (g_i / temperature within fp32's range) as fairy2i_vocab_loss_backward in everything else: pieces of the
+ * vocabulary, p held in x_dtype between the products (bf16: in units of a power of two near |g_i|, the rest of
+ * g_i applied to the fp32 sums of dh and, rounded, to h for dW, where all g equal cost nothing), fp32 sums, each
+ * output rounded once, either output NULL.  A token that does not count or has g_i = 0 adds nothing, whatever its row of h holds. */
 size_t fairy2i_distill_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype, int top);
 int fairy2i_distill_backward(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K,
                              const int64_t* top_index, const void* top_logit, int top_dtype, int top, float temperature,
@@ -434,8 +435,8 @@ int fairy2i_distill_backward(const void* h, const void* W, int x_dtype, int64_t 
  * Comparisons, differences and sums are fp64, sums in a fixed order.  Entries of w that are not positive or not
  * in fp32's range count as 0; a row without any weight gives the token -1.
  * 1 <= S <= 2^20, 1 <= D <= 63, 1 <= V <= 2^24, S ceil(V / 4096) <= 2^23; p and q need their element's
- * alignment only.  workspace: fairy2i_verify_draft_workspace_bytes(...) bytes, 16-byte aligned (NULL allowed if 0).  Outputs overlap
- * nothing else, and calls that share a workspace must not overlap. */
+ * alignment only.  workspace: fairy2i_verify_draft_workspace_bytes(...) bytes, 16-byte aligned (NULL allowed
+ * if 0).  Outputs overlap nothing else, and calls that share a workspace must not overlap. */
 size_t fairy2i_verify_draft_workspace_bytes(int64_t S, int64_t D, int64_t V);
 int fairy2i_verify_draft(const void* p, const void* q, int p_dtype, int64_t S, int64_t D, int64_t V, const int64_t* draft,
                          const int32_t* draft_len, const float* u, const float* r, int64_t* tokens, int32_t* accepted,

@@ -28,7 +28,7 @@ struct Entries {
   static constexpr int kCount = 16 / sizeof(T);
   struct __attribute__((packed, aligned(sizeof(T)))) Raw { v4u v; } raw;
   __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const Raw*>(p); }
-  __device__ __forceinline__ double operator[](int e) const {
+  __device__ __forceinline__ float operator[](int e) const {
     if constexpr (sizeof(T) == 4) return __uint_as_float(raw.v[e]);
     else return e & 1 ? bf16_hi(raw.v[e / 2]) : bf16_lo(raw.v[e / 2]);
   }

@@ -29,9 +29,9 @@
 //     loss_i = sum_k t_ik (log t_ik - l_{i, index_ik} + lse_i)
 //     p_iv = g_i / temperature (exp(l_iv - lse_i) - sum_{k: index_ik = v} t_ik)
 // A finished tile looks up which of its entries are listed in a map that its workgroup fills in LDS from the
-// lists, and stores their logits (loss) or subtracts their t_ik (p; k_teacher has made them for all tiles).  A token's gradient
-// has no one entry that dominates it for certain, so f_i is 1 here and g alone is taken apart: the roundings
-// of p's entries then differ from entry to entry.
+// lists, and stores their logits (loss) or subtracts their t_ik (p; k_teacher has made them for all tiles).  A
+// token's gradient has no one entry that dominates it for certain, so f_i is 1 here and g alone is taken apart:
+// the roundings of p's entries then differ from entry to entry.
 // Transposed operands are read from the matrix as it lies in memory: rows of the contraction are
 // copied into LDS and transposed on the way into registers, so no transposed copy is made.
 // Sums are fp32; a C tile has the A rows in its accumulator rows, so a lane holds four consecutive
@@ -47,7 +47,6 @@ namespace {
 enum { kLoss = 0, kGrad = 1, kHidden = 2, kWeight = 3, kDistill = 4, kDistillGrad = 5 };
 constexpr bool loss_like(int epi) { return epi == kLoss || epi == kDistill; }
 constexpr bool grad_like(int epi) { return epi == kGrad || epi == kDistillGrad; }
-constexpr bool listed(int epi) { return epi == kDistill || epi == kDistillGrad; }
 
 // acc += a b on the matrix cores, one 16-byte operand per lane.  The accumulator is tied to its own
 // accumulation registers: left to itself the compiler moves the 256 of a 128 x 128 wave tile about,
@@ -415,7 +414,8 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
 //
 // Bound by the matrix cores under the power limit for many tokens: 2048 x 32000 x 4096 takes 400-500 us as
 // logits (1342-1074 TFLOP/s; the card's best library product reaches 1399 at 8192^3; on zeros the same
-// launch takes 365), 431-451 as p, 460-491 as dh and 464-507 as dW.  For 24 tokens by W from HBM:
+// launch takes 365), 431-451 as p, 460-491 as dh and 464-507 as dW.  With lists of 64 slots (distillation)
+// the logits take 434 where they took 405 without, p 470 where it took 444.  For 24 tokens by W from HBM:
 // 262 MB in 59 us, 4.4 TB/s (two buffers 64 us).
 template <int BM, int BN, int WA, int WB, int EPI, int NB = 2>
 __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt(VocabTile t) {
@@ -808,7 +808,7 @@ __device__ __forceinline__ Teacher teacher_list(const int64_t* __restrict__ inde
   return Teacher{wave_sum(entropy) + bad, best > -INFINITY || bad != bad};
 }
 
-// The lists for the gradient, one wave per token.  An entry listed more than once keeps its first slot, with the
+// The lists for the gradient, one wave per token: 8 us for 2048 lists of 32 slots, 12 of 64.  An entry listed more than once keeps its first slot, with the
 // sum of its probabilities; its other slots, and entries without probability, get index -1.
 template <typename LT>
 __global__ __launch_bounds__(256) void k_teacher(const int64_t* __restrict__ index, const LT* __restrict__ logit,
@@ -838,7 +838,7 @@ __global__ __launch_bounds__(256) void k_teacher(const int64_t* __restrict__ ind
 }
 
 // lse as k_loss_join, and the distillation loss from the list and its entries' logits (each at the first slot that
-// lists it).
+// lists it): 9 us for 2048 lists of 32 or 64 slots, 6 for 24 of 8.
 template <typename LT>
 __global__ __launch_bounds__(256) void k_distill_join(const float2* __restrict__ part, const int64_t* __restrict__ index,
                                                       const LT* __restrict__ logit, const float* __restrict__ list_logit,
@@ -985,7 +985,7 @@ __global__ __launch_bounds__(256) void k_grad_scales(const float* __restrict__ g
   }
 }
 
-// Distillation: g alone, over the temperature: s_i, G m_i / temperature, G / temperature, m_i h_i; fp32: s_i is
+// Distillation (8 us for 2048 x 4096 bf16): g alone, over the temperature: s_i, G m_i / temperature, G / temperature, m_i h_i; fp32: s_i is
 // g_i / temperature itself.
 template <typename T>
 __global__ __launch_bounds__(256) void k_distill_scales(const float* __restrict__ g, const int32_t* __restrict__ counts,

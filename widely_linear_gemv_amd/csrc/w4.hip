@@ -289,14 +289,15 @@ void w4_run(const W4Kernel& t, hipStream_t s) {
 
 // Waves to a tile (NW) and tiles to a workgroup (RT).  One block of codes in flight a wave, and as many waves
 // on a CU as its registers hold, beat fewer waves with two to eight blocks in flight by 5-30 % (32000 x 4096,
-// one entry: 14.2-15.1 us, with two blocks 17.6, four 19.7).  Up to a tile a CU sixteen waves share a tile (4096 x 4096, one entry: 16 waves
-// 4.3 us, 8 waves 5.2; 4096 x 11008, 16 entries 11.6 and 11.8), beyond that eight (6144 x 4096: 8 waves 5.8, 16
-// waves 6.7; 32000 x 4096: 16.7 and 21.9).  fp32's three parts of x leave LDS for eight.  More tiles a
-// workgroup share what a block of x costs: two from four tiles a CU on (32000 x 4096, one entry: 14.2 us
-// against 16.7; 11008 x 4096: 7.4 against 7.1), with fp32 x from one on (6144 x 4096: 7.9 against 8.8); with more
-// than four entries, whose x is four times as long, two from one on (8192 x 4096, eight entries: 6.9 against
-// 7.4, four tiles 8.5) and four from two and a half on (11008 x 4096, 16 entries: 9.3, two tiles 11.2; 32000 x
-// 4096: 18.6 and 20.8).  The waves alone decide the order of a sum, so it is the same for every batch.
+// one entry: 14.2-15.1 us, with two blocks 17.6, four 19.7).  Up to a tile a CU sixteen waves share a tile (4096
+// x 4096, one entry: 16 waves 4.3 us, 8 waves 5.2; 4096 x 11008, 16 entries 11.6 and 11.8), beyond that eight
+// (6144 x 4096: 8 waves 5.8, 16 waves 6.7; 32000 x 4096: 16.7 and 21.9).  fp32's three parts of x leave LDS for
+// eight.  More tiles a workgroup share what a block of x costs: two from four tiles a CU on (32000 x 4096, one
+// entry: 14.2 us against 16.7; 11008 x 4096: 7.4 against 7.1), with fp32 x from one on (6144 x 4096: 7.9 against
+// 8.8); with more than four entries, whose x is four times as long, two from one on (8192 x 4096, eight entries:
+// 6.9 against 7.4, four tiles 8.5) and four from two and a half on (11008 x 4096, 16 entries: 9.3, two tiles
+// 11.2; 32000 x 4096: 18.6 and 20.8).  The waves alone decide the order of a sum, so it is the same for every
+// batch.
 constexpr int kCUs = 256;
 template <int G, typename XT, typename ST>
 void w4_shape(const W4Kernel& t, hipStream_t s) {

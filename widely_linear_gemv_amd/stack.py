@@ -25,9 +25,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (GEMV_AUTO, GEMV_MFMA_F4, GEMV_MFMA_I8, X_DIGITS, X_DIGITS_F6, XDigits,
-               W4Layer, fairy2i_gemv_grouped, fairy2i_lora_grouped, fairy2i_lora_workspace_bytes, fairy2i_x_digits, fairy2i_x_digits_bytes, fairy2i_x_digits_f6,
-               fairy2i_x_digits_f6_bytes, fairy2i_gemv_w4)
+from . import (GEMV_AUTO, GEMV_MFMA_F4, GEMV_MFMA_I8, X_DIGITS, X_DIGITS_F6, W4Layer, XDigits, fairy2i_gemv_grouped,
+               fairy2i_gemv_w4, fairy2i_lora_grouped, fairy2i_lora_workspace_bytes, fairy2i_x_digits,
+               fairy2i_x_digits_bytes, fairy2i_x_digits_f6, fairy2i_x_digits_f6_bytes)
 
 # the digit form each digit-form kernel takes: (size in bytes, converter, dtype code)
 _DIGIT_FORMS = {GEMV_MFMA_F4: (fairy2i_x_digits_f6_bytes, fairy2i_x_digits_f6, X_DIGITS_F6),
