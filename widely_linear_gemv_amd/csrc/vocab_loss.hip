@@ -29,7 +29,7 @@
 //     loss_i = sum_k t_ik (log t_ik - l_{i, index_ik} + lse_i)
 //     p_iv = g_i / temperature (exp(l_iv - lse_i) - sum_{k: index_ik = v} t_ik)
 // A finished tile looks up which of its entries are listed in a map that its workgroup fills in LDS from the
-// lists, and stores their logits (loss) or subtracts their t_ik (p; k_teacher has made them for all tiles).  A
+// lists, and stores their logits (loss) or subtracts their t_ik (p; k_distill_scales has made them for all tiles).  A
 // token's gradient has no one entry that dominates it for certain, so f_i is 1 here and g alone is taken apart:
 // the roundings of p's entries then differ from entry to entry.
 // Transposed operands are read from the matrix as it lies in memory: rows of the contraction are
@@ -722,12 +722,11 @@ __global__ __launch_bounds__(64 * WA * WB, 1) void k_nt_split(VocabTile t) {
   finish<float, BM, BN, WA, WB, FA, FB, EPI, 2 * kStep>(t, acc, s_buf, a0, b0, ta, split);
 }
 
-// A call's lists as k_teacher leaves them: [N][list_pitch(top)] each, but for live [N].
+// A call's lists for the gradient's products, [N][list_pitch(top)] each.
 __host__ __device__ constexpr int list_pitch(int top) { return (top + 3) / 4 * 4; }
 struct TeacherLists {
   int32_t* index;
   float* prob;
-  int32_t* live;         // whether the token counts
 };
 
 // Joins the tiles' pairs in order (one wave per token) into lse, and the loss from the target's logit:
@@ -806,35 +805,6 @@ __device__ __forceinline__ Teacher teacher_list(const int64_t* __restrict__ inde
   }
   __builtin_amdgcn_wave_barrier();
   return Teacher{wave_sum(entropy) + bad, best > -INFINITY || bad != bad};
-}
-
-// The lists for the gradient, one wave per token: 8 us for 2048 lists of 32 slots, 12 of 64.  An entry listed more than once keeps its first slot, with the
-// sum of its probabilities; its other slots, and entries without probability, get index -1.
-template <typename LT>
-__global__ __launch_bounds__(256) void k_teacher(const int64_t* __restrict__ index, const LT* __restrict__ logit,
-                                                 int64_t N, int64_t V, int top, float inv_temp, TeacherLists out) {
-  __shared__ int32_t s_index[4][kMaxTop];
-  __shared__ float s_prob[4][kMaxTop];
-  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
-  const int64_t i = (int64_t)blockIdx.x * 4 + w;
-  if (i >= N) return;                                      // whole waves: no barrier here
-  const Teacher teacher = teacher_list(index + i * top, logit + i * top, V, top, inv_temp, s_index[w], s_prob[w]);
-  for (int k = lane; k < list_pitch(top); k += kWave) {
-    int32_t v = s_index[w][k];                             // -1 behind the list
-    float p = 0.f;
-    if (v >= 0)
-      for (int j = 0; j < top; ++j)
-        if (s_index[w][j] == v) {
-          if (j < k) {
-            p = 0.f;
-            break;
-          }
-          p += s_prob[w][j];
-        }
-    out.index[i * list_pitch(top) + k] = p == 0.f ? -1 : v;
-    out.prob[i * list_pitch(top) + k] = p;
-  }
-  if (lane == 0) out.live[i] = teacher.live;
 }
 
 // lse as k_loss_join, and the distillation loss from the list and its entries' logits (each at the first slot that
@@ -985,25 +955,47 @@ __global__ __launch_bounds__(256) void k_grad_scales(const float* __restrict__ g
   }
 }
 
-// Distillation (8 us for 2048 x 4096 bf16): g alone, over the temperature: s_i, G m_i / temperature, G / temperature, m_i h_i; fp32: s_i is
-// g_i / temperature itself.
-template <typename T>
-__global__ __launch_bounds__(256) void k_distill_scales(const float* __restrict__ g, const int32_t* __restrict__ counts,
-                                                        int64_t N, const T* __restrict__ h, int64_t K, float inv_temp,
-                                                        GradScales out, T* __restrict__ scaled) {
+// Distillation: what the gradient's products need, one wave per token.  The token's list: an entry listed more
+// than once keeps its first slot, with the sum of its probabilities; its other slots, and entries without
+// probability, get index -1.  The factors as k_grad_scales with f_i = 1, over the temperature: s_i, G m_i /
+// temperature, G / temperature, m_i h_i (fp32: s_i is g_i / temperature itself); G is taken from the first token
+// whose first slot is used.  14 us for 2048 x 4096 bf16 with lists of 32, 6 for 263 x 1088 fp32 with 17.
+template <typename T, typename LT>
+__global__ __launch_bounds__(256) void k_distill_scales(const int64_t* __restrict__ index, const LT* __restrict__ logit,
+                                                        const float* __restrict__ g, int64_t N, int64_t V, int top,
+                                                        float inv_temp, const T* __restrict__ h, int64_t K,
+                                                        TeacherLists list, GradScales out, T* __restrict__ scaled) {
+  __shared__ int32_t s_index[4][kMaxTop];
+  __shared__ float s_prob[4][kMaxTop];
   constexpr int kEach = 16 / sizeof(T);
-  const int lane = threadIdx.x & (kWave - 1);
-  const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
-  if (i >= N) return;
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+  const int64_t i = (int64_t)blockIdx.x * 4 + w;
+  if (i >= N) return;                                      // whole waves: no barrier here
   const float gi = g[i];
-  const bool live = counts[i] && gi != 0.f;
+  const Teacher teacher = teacher_list(index + i * top, logit + i * top, V, top, inv_temp, s_index[w], s_prob[w]);
+  for (int k = lane; k < list_pitch(top); k += kWave) {
+    int32_t v = s_index[w][k];                             // -1 behind the list
+    float p = 0.f;
+    if (v >= 0)
+      for (int j = 0; j < top; ++j)
+        if (s_index[w][j] == v) {
+          if (j < k) {
+            p = 0.f;
+            break;
+          }
+          p += s_prob[w][j];
+        }
+    list.index[i * list_pitch(top) + k] = p == 0.f ? -1 : v;
+    list.prob[i * list_pitch(top) + k] = p;
+  }
+  const bool live = teacher.live && gi != 0.f;
   float m = 1.f;
   if constexpr (sizeof(T) == 2) {
     float G = 1.f;
     for (int64_t t0 = 0; t0 < min(N, (int64_t)kScanned); t0 += kWave) {
-      const int64_t t = min(t0 + lane, N - 1);
+      const int64_t t = min(t0 + lane, N - 1), first = index[t * top];
       const float v = fabsf(g[t]);
-      const uint64_t good = __ballot(counts[t] && v > 0.f && v < INFINITY);
+      const uint64_t good = __ballot(first >= 0 && first < V && v > 0.f && v < INFINITY);
       if (good) {
         G = __uint_as_float((__float_as_uint(__shfl(v, __builtin_ctzll(good))) & 0x007FFFFFu) | 0x3F800000u);
         break;
@@ -1013,13 +1005,13 @@ __global__ __launch_bounds__(256) void k_distill_scales(const float* __restrict_
     if (live) {
       si = gi;
       if (const float ratio = fabsf(gi) / G; ratio < INFINITY) {
-        float top = fmaxf(__uint_as_float(__float_as_uint(ratio) & 0x7F800000u), 0x1p-60f);   // 2^floor(log2(ratio))
-        m = ratio / top;
-        if (m > 1.f && top < 0x1p127f) {
+        float most = fmaxf(__uint_as_float(__float_as_uint(ratio) & 0x7F800000u), 0x1p-60f);   // 2^floor(log2(ratio))
+        m = ratio / most;
+        if (m > 1.f && most < 0x1p127f) {
           m *= 0.5f;
-          top *= 2.f;
+          most *= 2.f;
         }
-        si = copysignf(top, gi);
+        si = copysignf(most, gi);
       }
     }
     if (lane == 0) {
@@ -1034,16 +1026,16 @@ __global__ __launch_bounds__(256) void k_distill_scales(const float* __restrict_
   const T* __restrict__ from = h + i * K;
   T* __restrict__ to = scaled + i * K;
   for (int64_t k = lane * kEach; k < K; k += kWave * kEach) {
-    uint4 w = make_uint4(0, 0, 0, 0);
+    uint4 x = make_uint4(0, 0, 0, 0);
     if (live) {
-      w = *reinterpret_cast<const uint4*>(from + k);
+      x = *reinterpret_cast<const uint4*>(from + k);
       if constexpr (sizeof(T) == 2) {
-        uint32_t* e = &w.x;
+        uint32_t* e = &x.x;
 #pragma unroll
         for (int j = 0; j < 4; ++j) e[j] = pack_bf16(m * bf16_lo(e[j]), m * bf16_hi(e[j]));
       }
     }
-    *reinterpret_cast<uint4*>(to + k) = w;
+    *reinterpret_cast<uint4*>(to + k) = x;
   }
 }
 
@@ -1123,7 +1115,7 @@ int64_t steps_of(int64_t k, int elem) { return (k * elem + 127) / 128; }
 
 // The lists' place in a workspace from `at` on, which moves behind them.
 struct ListPlan {
-  size_t index, prob, live;
+  size_t index, prob;
 };
 ListPlan list_plan(int64_t N, int top, size_t& at) {
   ListPlan l{};
@@ -1131,24 +1123,11 @@ ListPlan list_plan(int64_t N, int top, size_t& at) {
   auto take = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
   l.index = take((size_t)N * list_pitch(top) * 4);
   l.prob = take((size_t)N * list_pitch(top) * 4);
-  l.live = take((size_t)N * 4);
   return l;
 }
 TeacherLists lists_at(uint8_t* ws, const ListPlan& l) {
-  return TeacherLists{reinterpret_cast<int32_t*>(ws + l.index), reinterpret_cast<float*>(ws + l.prob),
-                      reinterpret_cast<int32_t*>(ws + l.live)};
+  return TeacherLists{reinterpret_cast<int32_t*>(ws + l.index), reinterpret_cast<float*>(ws + l.prob)};
 }
-void launch_teacher(const VocabArgs& a, const TeacherLists& lists, hipStream_t s) {
-  const dim3 grid((unsigned)((a.N + 3) / 4));
-  const float inv = 1.f / a.temperature;
-  if (a.top_bf16)
-    hipLaunchKernelGGL((k_teacher<uint16_t>), grid, dim3(256), 0, s, a.top_index, static_cast<const uint16_t*>(a.top_logit),
-                       a.N, a.V, a.top, inv, lists);
-  else
-    hipLaunchKernelGGL((k_teacher<float>), grid, dim3(256), 0, s, a.top_index, static_cast<const float*>(a.top_logit), a.N,
-                       a.V, a.top, inv, lists);
-}
-
 struct LossPlan {
   NtPlan nt;
   size_t part, tlogit, total;     // tlogit: [N], or the listed logits [N][top]
@@ -1245,9 +1224,15 @@ hipError_t grad_t(const VocabArgs& a, hipStream_t s) {
   if (a.top > 0) {
     lists = lists_at(ws, q.list);
     factor = out.s;
-    launch_teacher(a, lists, s);
-    hipLaunchKernelGGL((k_distill_scales<T>), dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a.g, lists.live, a.N,
-                       static_cast<const T*>(a.h), a.K, 1.f / a.temperature, out, h);
+    const dim3 grid((unsigned)((a.N + 3) / 4));
+    if (a.top_bf16)
+      hipLaunchKernelGGL((k_distill_scales<T, uint16_t>), grid, dim3(256), 0, s, a.top_index,
+                         static_cast<const uint16_t*>(a.top_logit), a.g, a.N, a.V, a.top, 1.f / a.temperature,
+                         static_cast<const T*>(a.h), a.K, lists, out, h);
+    else
+      hipLaunchKernelGGL((k_distill_scales<T, float>), grid, dim3(256), 0, s, a.top_index,
+                         static_cast<const float*>(a.top_logit), a.g, a.N, a.V, a.top, 1.f / a.temperature,
+                         static_cast<const T*>(a.h), a.K, lists, out, h);
   } else if (sizeof(T) == 2 || h)
     hipLaunchKernelGGL((k_grad_scales<T>), dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a.g, a.target, a.N, a.V,
                        static_cast<const T*>(a.h), W, a.lse, a.K, out, h);
