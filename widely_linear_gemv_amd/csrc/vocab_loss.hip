@@ -757,7 +757,9 @@ __global__ __launch_bounds__(256) void k_loss_join(const float2* __restrict__ pa
 
 // A teacher's list, by one wave: t_ik = softmax over the slots whose index lies in [0, V) of logit / temperature,
 // into prob (0 for a slot at minus infinity and for unused ones), the indices (-1 for unused slots) into index.
-// NaN or plus infinity among the used logits makes all of the token's probabilities NaN.
+// The distance from the largest logit is taken before the temperature, which could carry a finite logit (a mask's
+// lowest value) out of fp32's range.  NaN or plus infinity among the used logits makes all of the token's
+// probabilities NaN.
 struct Teacher {
   float entropy;         // sum_k t_ik log t_ik
   bool live;             // whether any probability is left: otherwise the token does not count
@@ -779,10 +781,8 @@ __device__ __forceinline__ Teacher teacher_list(const int64_t* __restrict__ inde
     const int64_t v = index[k];
     if (v < 0 || v >= V) continue;
     at[q] = (int32_t)v;
-    float l;
-    if constexpr (sizeof(LT) == 2) l = __uint_as_float((uint32_t)logit[k] << 16);
-    else l = logit[k];
-    z[q] = l * inv_temp;
+    if constexpr (sizeof(LT) == 2) z[q] = __uint_as_float((uint32_t)logit[k] << 16);
+    else z[q] = logit[k];
     best = fmaxf(best, z[q]);
     if (!(z[q] < INFINITY)) bad = NAN;
   }
@@ -790,16 +790,20 @@ __device__ __forceinline__ Teacher teacher_list(const int64_t* __restrict__ inde
   for (int off = 32; off >= 1; off >>= 1) best = fmaxf(best, __shfl_xor(best, off));
   bad = wave_sum(bad);
 #pragma unroll
-  for (int q = 0; q < kEach; ++q) sum += z[q] > -INFINITY ? expf(z[q] - best) : 0.f;
+  for (int q = 0; q < kEach; ++q) {
+    z[q] = z[q] > -INFINITY ? (z[q] - best) * inv_temp : -INFINITY;
+    sum += expf(z[q]);
+  }
   sum = wave_sum(sum) + bad;
   const float log_sum = logf(sum);
   float entropy = 0.f;
 #pragma unroll
   for (int q = 0; q < kEach; ++q) {
     const int k = q * kWave + lane;
-    float p = z[q] > -INFINITY ? expf(z[q] - best) / sum : 0.f;
+    float p = expf(z[q]) / sum;
+    if (at[q] < 0 || z[q] == -INFINITY) p = 0.f;           // also where no slot has any
     if (bad != bad && at[q] >= 0) p = bad;
-    if (p > 0.f) entropy += p * (z[q] - best - log_sum);
+    if (p > 0.f) entropy += p * (z[q] - log_sum);
     s_index[k] = at[q];
     s_prob[k] = p;
   }
