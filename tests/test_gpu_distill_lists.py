@@ -48,3 +48,54 @@ def test_logits_that_leave_fp32_over_the_temperature(T, tdt):
     wh, bh, wW, bW = grad_reference(shifted, r)
     close(dh, wh, bh, "dh")
     close(dW, wW, bW, "dW")
+
+
+def two_entries(N, V, K, dev, seed):
+    """Lists of two entries (their softmax is the same bit for bit wherever they stand) and equal g."""
+    c, d = make(N, V, K, 2, BF, seed, dev, ignored=0.0)
+    c["index"] = torch.stack([torch.randperm(V, generator=torch.Generator().manual_seed(i))[:2] for i in range(N)])
+    c["logit"] = torch.randn(N, 2, generator=torch.Generator().manual_seed(seed)) * 0.3
+    c["g"] = torch.full((N,), 1 / 261.0)
+    d.update({k: c[k].to(dev) for k in ("index", "logit", "g")})
+    return d
+
+
+@pytest.mark.parametrize("places", [(0, 1), (1, 2), (5, 0), (70, 71), (127, 3), (126, 127), (40, 64)], ids=str)
+def test_unused_slots_anywhere(places):
+    """Where a list's used slots stand changes no bit of the gradient, equal g among all tokens (whose common
+    factor costs h no rounding)."""
+    dev = device()
+    d = two_entries(300, 900, 256, dev, 8)
+    announce("distill unused slots", places)
+    _, lse = forward(d)
+    dh, dW = backward(d, lse)
+    wide = dict(d, index=torch.full((300, 128), -1, device=dev), logit=torch.full((300, 128), math.nan, device=dev))
+    for k, place in enumerate(places):
+        wide["index"][:, place], wide["logit"][:, place] = d["index"][:, k], d["logit"][:, k]
+    _, lse2 = forward(wide)
+    dh2, dW2 = backward(wide, lse2)
+    assert torch.equal(lse2, lse) and torch.equal(dh2, dh) and torch.equal(dW2, dW)
+
+
+@pytest.mark.parametrize("leading", [1, 20, 100])
+@pytest.mark.parametrize("kind", ["minus infinity", "empty", "outside"])
+def test_tokens_that_do_not_count_lend_no_factor(kind, leading):
+    """In front, tokens that do not count, with other g than the rest's common one (some of them 0, infinite or
+    NaN): the same gradient, bit for bit, as with the common g there."""
+    dev = device()
+    if kind == "minus infinity":
+        leading = min(leading, 30)                         # further tokens with used slots are not looked at
+    d = two_entries(300, 900, 256, dev, 9)
+    if kind == "minus infinity":
+        d["logit"][:leading] = -math.inf
+    else:
+        d["index"][:leading] = -1 if kind == "empty" else 900
+    announce("distill tokens that do not count", kind, leading)
+    _, lse = forward(d)
+    dh, dW = backward(d, lse)
+    assert not dh[:leading].any()
+    g = d["g"].clone()
+    g[:leading] = torch.linspace(0.3, 0.5, leading, device=dev)
+    g[leading // 2] = torch.tensor([0.0, math.inf, math.nan])[leading % 3].item()
+    dh2, dW2 = backward(dict(d, g=g), lse)
+    assert torch.equal(dh2, dh) and torch.equal(dW2, dW)

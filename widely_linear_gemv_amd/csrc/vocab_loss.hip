@@ -959,11 +959,46 @@ __global__ __launch_bounds__(256) void k_grad_scales(const float* __restrict__ g
   }
 }
 
+// G of a distillation: the significand of |g| of a token that counts and has a finite g other than 0, the same in
+// every wave.  Among the first 4096 tokens those whose first or last slot is used (lists that are padded at one
+// end) are candidates, and the first 32 of them have their whole list read, by the whole wave (mostly one is); if
+// none counts, of the first token with such a g, and 1 if there is none: all g equal give the same G either way.
+constexpr int kLooked = 32;
+template <typename LT>
+__device__ __forceinline__ float common_factor(const int64_t* __restrict__ index, const LT* __restrict__ logit,
+                                               const float* __restrict__ g, int64_t N, int64_t V, int top) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const auto used = [&](int64_t at) { return index[at] >= 0 && index[at] < V; };
+  const auto significand = [](float v) { return __uint_as_float((__float_as_uint(v) & 0x007FFFFFu) | 0x3F800000u); };
+  float any = 0.f;
+  int looked = 0;
+  for (int64_t t0 = 0; t0 < min(N, (int64_t)kScanned); t0 += kWave) {
+    const int64_t t = min(t0 + lane, N - 1);
+    const float v = fabsf(g[t]);
+    const bool first = used(t * top), last = used(t * top + top - 1), has = v > 0.f && v < INFINITY;
+    if (const uint64_t some = __ballot(has); some && any == 0.f) any = __shfl(v, __builtin_ctzll(some));
+    for (uint64_t good = __ballot(has && (first || last)); good && looked < kLooked; good &= good - 1, ++looked) {
+      const int l = __builtin_ctzll(good);
+      const int64_t from = min(t0 + l, N - 1) * top;
+      bool counts = false;
+      for (int k = lane; k < top; k += kWave) {
+        float z;
+        if constexpr (sizeof(LT) == 2) z = __uint_as_float((uint32_t)logit[from + k] << 16);
+        else z = logit[from + k];
+        counts |= used(from + k) && z != -INFINITY;
+      }
+      if (__ballot(counts)) return significand(__shfl(v, l));
+    }
+    if (looked >= kLooked) break;
+  }
+  return any > 0.f ? significand(any) : 1.f;
+}
+
 // Distillation: what the gradient's products need, one wave per token.  The token's list: an entry listed more
 // than once keeps its first slot, with the sum of its probabilities; its other slots, and entries without
 // probability, get index -1.  The factors as k_grad_scales with f_i = 1, over the temperature: s_i, G m_i /
-// temperature, G / temperature, m_i h_i (fp32: s_i is g_i / temperature itself); G is taken from the first token
-// whose first slot is used.  14 us for 2048 x 4096 bf16 with lists of 32, 6 for 263 x 1088 fp32 with 17.
+// temperature, G / temperature, m_i h_i (fp32: s_i is g_i / temperature itself).  16 us for 2048 x 4096 bf16
+// with lists of 32, 6 for 263 x 1088 fp32 with 17.
 template <typename T, typename LT>
 __global__ __launch_bounds__(256) void k_distill_scales(const int64_t* __restrict__ index, const LT* __restrict__ logit,
                                                         const float* __restrict__ g, int64_t N, int64_t V, int top,
@@ -995,16 +1030,7 @@ __global__ __launch_bounds__(256) void k_distill_scales(const int64_t* __restric
   const bool live = teacher.live && gi != 0.f;
   float m = 1.f;
   if constexpr (sizeof(T) == 2) {
-    float G = 1.f;
-    for (int64_t t0 = 0; t0 < min(N, (int64_t)kScanned); t0 += kWave) {
-      const int64_t t = min(t0 + lane, N - 1), first = index[t * top];
-      const float v = fabsf(g[t]);
-      const uint64_t good = __ballot(first >= 0 && first < V && v > 0.f && v < INFINITY);
-      if (good) {
-        G = __uint_as_float((__float_as_uint(__shfl(v, __builtin_ctzll(good))) & 0x007FFFFFu) | 0x3F800000u);
-        break;
-      }
-    }
+    const float G = common_factor(index, logit, g, N, V, top);
     float si = 0.f;
     if (live) {
       si = gi;
