@@ -410,8 +410,9 @@ int fairy2i_distill(const void* h, const void* W, int x_dtype, int64_t N, int64_
  * vocabulary, p held in x_dtype between the products (bf16: in units of a power of two near |g_i|, the rest of
  * g_i applied to the fp32 sums of dh and, rounded, to h for dW, where equal g of all tokens that count cost nothing:
  * at most 32 tokens with used slots but no probability, or 4096 others, may lie in front of them with a g of their
- * own), fp32 sums, each output rounded once, either output NULL.  A token that does not count or has g_i = 0 adds
- * nothing, whatever its row of h holds. */
+ * own; where one entry has half of a list's probability, |g_i| times that entry's |softmax - t| in place of |g_i|,
+ * so that its p is exact), fp32 sums, each output rounded once, either output NULL.  A token that does not count or
+ * has g_i = 0 adds nothing, whatever its row of h holds. */
 size_t fairy2i_distill_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype, int top);
 int fairy2i_distill_backward(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K,
                              const int64_t* top_index, const void* top_logit, int top_dtype, int top, float temperature,

@@ -8,6 +8,8 @@ import torch
 from gpu_util import announce, device
 from test_gpu_distill import BF, F32, backward, close, forward, grad_reference, make, reference
 
+import widely_linear_gemv_amd as f2
+
 pytestmark = pytest.mark.gpu
 
 
@@ -99,3 +101,63 @@ def test_tokens_that_do_not_count_lend_no_factor(kind, leading):
     g[leading // 2] = torch.tensor([0.0, math.inf, math.nan])[leading % 3].item()
     dh2, dW2 = backward(dict(d, g=g), lse)
     assert torch.equal(dh2, dh) and torch.equal(dW2, dW)
+
+
+@pytest.mark.parametrize("N", [50, 300])
+def test_a_list_of_one_has_the_cross_entropys_roundings(N):
+    """bf16, one listed entry, temperature 1: the products are those of the vocabulary loss, and so is every bit of
+    the gradient."""
+    dev = device()
+    c, d = make(N, 700, 128, 1, BF, 3, dev, ignored=0.3)
+    target = torch.where((d["index"] >= 0) & (d["index"] < 700), d["index"], torch.full_like(d["index"], -1))[:, 0].contiguous()
+    announce("distill lists of one", N)
+    _, lse = forward(d)
+    dh, dW = backward(d, lse)
+    _, lse2 = f2.fairy2i_vocab_loss(d["h"], d["W"], target)
+    dh2, dW2 = f2.fairy2i_vocab_loss_backward(d["h"], d["W"], target, lse2, d["g"])
+    assert torch.equal(lse, lse2) and torch.equal(dh, dh2) and torch.equal(dW, dW2)
+
+
+@pytest.mark.parametrize("T", [1.0, 2.0])
+@pytest.mark.parametrize("sure", [0.55, 0.9, 0.97, 1.0])
+def test_an_entry_that_dominates_moves_no_whole_row(sure, T):
+    """bf16, a teacher that gives one entry of each list the probability `sure` and more: that entry's p dominates
+    the token's dh and its own row of dW, so that its rounding would move all their values together, by up to
+    2^-8 of themselves.  Along each such row the error is at most what is left: the roundings of the row's own
+    K values, of variance 2^-16 / 3 at most, six standard deviations 6 2^-8 (3 / K)^0.5 / 3^0.5 = 2^-11.4 for
+    normal values; the other entries' roundings, u = 2^-8 of each at most; and 2^-14 for fp32's.  A row of dW has
+    the roundings of m h too, with m in (1/2, 1] the token's own factor: one for each of the 128 significands that
+    a bf16 h has, the largest with up to 1.5 / 128 of the row's square: 2^-8 (1.5 / 128 / 3)^0.5 = 2^-12 of
+    standard deviation, or, with m within 2^-9 of 1, which is one token in 2^8, up to 2^-9 that is alike for all.
+    So no row of dW more than 2^-9, and their root mean square (three of 64 such tokens: (3 2^-18 / 64 + 2^-24)^0.5)
+    at most 2^-11."""
+    dev = device()
+    N, V, K, top = 64, 900, 4096, 6
+    c, d = make(N, V, K, top, BF, 44, dev, T, ignored=0.0, near=False)
+    c["index"] = torch.randperm(V, generator=torch.Generator().manual_seed(1))[:N * top].view(N, top)
+    share = torch.rand(N, top, generator=torch.Generator().manual_seed(2)).double() + 0.1
+    first = sure + (1 - sure) * torch.rand(N, generator=torch.Generator().manual_seed(3)).double()
+    share[:, 0] = 0
+    share = share / share.sum(1, keepdim=True) * (1 - first[:, None])
+    share[:, 0] = first
+    c["logit"] = (share.log() * T).float()
+    c["index"][::3], c["logit"][::3] = c["index"][::3].flip(1), c["logit"][::3].flip(1)
+    c["g"] = torch.rand(N, generator=torch.Generator().manual_seed(4)) + 0.5
+    d.update({k: c[k].to(dev) for k in ("index", "logit", "g")})
+    announce("distill dominating entry", sure, T)
+    _, lse = forward(d)
+    dh, dW = (t.double().cpu() for t in backward(d, lse))
+    r = reference(c)
+    wh, _, wW, _ = grad_reference(c, r)
+    h, W = c["h"].double(), c["W"].double()
+    at = c["index"].gather(1, c["logit"].argmax(1, keepdim=True))[:, 0]
+    rows = torch.arange(N)
+    p = (r["l"] - r["lse"][:, None]).exp().scatter_add_(1, r["at"], -r["t"]) * (c["g"].double() / T)[:, None]
+    p[rows, at] = 0.0                                      # the others
+    own, u = 6 * 2.0 ** -8 / K ** 0.5, 2.0 ** -8
+    for err, want, left, room in ((dh - wh, wh, p.abs() * (wh @ W.t()).abs(), own),
+                                  (dW[at] - wW[at], wW[at], (p.abs() * (h @ wW.t()).abs())[:, at].t(), own + 2.0 ** -9)):
+        size = (want * want).sum(1)
+        along, rest = ((err * want).sum(1) / size).abs(), u * left.sum(1) / size + 2.0 ** -14
+        assert (along <= room + rest).all(), (along.max(), room)
+        assert (along - rest).clamp(min=0).square().mean().sqrt() <= 2.0 ** -11

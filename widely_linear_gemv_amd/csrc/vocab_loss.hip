@@ -29,9 +29,14 @@
 //     loss_i = sum_k t_ik (log t_ik - l_{i, index_ik} + lse_i)
 //     p_iv = g_i / temperature (exp(l_iv - lse_i) - sum_{k: index_ik = v} t_ik)
 // A finished tile looks up which of its entries are listed in a map that its workgroup fills in LDS from the
-// lists, and stores their logits (loss) or subtracts their t_ik (p; k_distill_scales has made them for all tiles).  A
-// token's gradient has no one entry that dominates it for certain, so f_i is 1 here and g alone is taken apart:
-// the roundings of p's entries then differ from entry to entry.
+// lists, and stores their logits (loss) or subtracts their t_ik (p; k_distill_scales has made them for all tiles).
+// bf16: where one entry has at least half of a list's probability, its rounding would move whole rows as the
+// target's would, and f_i = |softmax - t| there makes it a power of two likewise.  64 tokens, 900 x 4096: rows of
+// dh 0.0011 off along themselves (root mean square; at most 0.0029), with f_i 0.00005 (0.0004); of dW 0.0011 and
+// 0.0002, where m_i within 2^-9 of 1 is what is left (h rounded back to itself).  In lists without such an entry
+// the roundings differ from entry to entry: f_i is 1, g alone is taken apart and equal g round h no second time
+// (entries of 0.3: dh would get 0.0010 off before its final rounding instead of 0.0017, but dW 0.0019 instead of
+// 0.0017; at 0.5 dh 0.0007 instead of 0.0017, dW 0.0018 instead of 0.0017).
 // Transposed operands are read from the matrix as it lies in memory: rows of the contraction are
 // copied into LDS and transposed on the way into registers, so no transposed copy is made.
 // Sums are fp32; a C tile has the A rows in its accumulator rows, so a lane holds four consecutive
@@ -76,7 +81,7 @@ struct VocabTile {
   const void* a;
   const void* b;
   const int64_t* target;        // [N]
-  const float* lse;             // [N] (kGrad; bf16: with log f_i added)
+  const float* lse;             // [N] (kGrad, kDistillGrad; bf16: with log f_i added)
   const float* g;               // [N] factor of p (kGrad; bf16: s_i)
   const float* at_target;       // [N] p over that factor at the target (kGrad, bf16)
   const float* row_scale;       // [N] factor of dh's rows, or null (kHidden)
@@ -92,7 +97,7 @@ struct VocabTile {
   float* list_logit;            // [N][top], of each entry's first slot (kDistill)
   int top;
   const int32_t* list_index;    // [N][list_pitch] vocabulary entries, -1 for none (kDistillGrad)
-  const float* list_prob;       // [N][list_pitch] t_ik (kDistillGrad)
+  const float* list_prob;       // [N][list_pitch] t_ik (kDistillGrad; bf16: over f_i, under 0 for an exact entry)
   int list_pitch;               // a multiple of 4
   float inv_temp;               // 1 / temperature (kDistill, kDistillGrad)
   int first, last;              // piece
@@ -101,6 +106,7 @@ struct VocabTile {
 };
 
 constexpr int kMaxTop = 128;           // slots of a list
+constexpr float kExactEntry = 2.f;     // a listed value y under 0 says that p is s_i (y + this): -1 or 1
 
 // Calls f(token of the tile, row of the tile, probability) for the listed entries that lie in a tile's rows
 // first .. first + BM - 1.  The lists' rows are whole groups of four slots; a thread's groups are loaded four at
@@ -327,7 +333,11 @@ __device__ __forceinline__ void finish(const VocabTile& t, v4f (&acc)[FA][FB], u
           const v4f listed = *reinterpret_cast<const v4f*>(Map::at(s_buf, (wb * FB + j) * 16 + c, s0 + 4 * i));
           float x[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = live && r + e < t.rows_a ? gs[j] * (acc[i][j][e] - listed[e]) : 0.f;
+          for (int e = 0; e < 4; ++e) {
+            float v = acc[i][j][e] - listed[e];
+            if (sizeof(T) == 2 && listed[e] < 0.f) v = listed[e] + kExactEntry;
+            x[e] = live && r + e < t.rows_a ? gs[j] * v : 0.f;
+          }
           if constexpr (sizeof(T) == 2)
             *reinterpret_cast<uint2*>(p + tok * t.ldp + r) =
                 make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
@@ -877,6 +887,18 @@ constexpr float kLeastRest = 0x1p-16f;       // f_i under which it stays in p
 struct GradScales {                          // [N] each, but for all [1]
   float *s, *row, *at_target, *lse, *all;
 };
+__device__ __forceinline__ float row_dot(const uint16_t* __restrict__ a, const uint16_t* __restrict__ b, int64_t K) {
+  float sum = 0.f;                                         // <a, b>, by one wave
+  for (int64_t k = (threadIdx.x & (kWave - 1)) * 8; k < K; k += kWave * 8) {
+    const v4u x = *reinterpret_cast<const v4u*>(a + k), y = *reinterpret_cast<const v4u*>(b + k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      sum = fmaf(bf16_lo(x[j]), bf16_lo(y[j]), sum);
+      sum = fmaf(bf16_hi(x[j]), bf16_hi(y[j]), sum);
+    }
+  }
+  return wave_sum(sum);
+}
 template <typename T>
 __global__ __launch_bounds__(256) void k_grad_scales(const float* __restrict__ g, const int64_t* __restrict__ target,
                                                      int64_t N, int64_t V, const T* __restrict__ h,
@@ -903,18 +925,7 @@ __global__ __launch_bounds__(256) void k_grad_scales(const float* __restrict__ g
     }
     float si = 0.f, at_target = 0.f, base = 0.f;
     if (live) {
-      const T* __restrict__ hi = h + i * K;
-      const T* __restrict__ wt = W + tgt * K;
-      float logit = 0.f;
-      for (int64_t k = lane * kEach; k < K; k += kWave * kEach) {
-        const v4u a = *reinterpret_cast<const v4u*>(hi + k), b = *reinterpret_cast<const v4u*>(wt + k);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          logit = fmaf(bf16_lo(a[j]), bf16_lo(b[j]), logit);
-          logit = fmaf(bf16_hi(a[j]), bf16_hi(b[j]), logit);
-        }
-      }
-      logit = wave_sum(logit);
+      const float logit = row_dot(h + i * K, W + tgt * K, K);
       base = lse[i];
       float f = -expm1f(logit - base);
       const bool apart = f >= kLeastRest;                                  // not a NaN either
@@ -996,45 +1007,63 @@ __device__ __forceinline__ float common_factor(const int64_t* __restrict__ index
 
 // Distillation: what the gradient's products need, one wave per token.  The token's list: an entry listed more
 // than once keeps its first slot, with the sum of its probabilities; its other slots, and entries without
-// probability, get index -1.  The factors as k_grad_scales with f_i = 1, over the temperature: s_i, G m_i /
-// temperature, G / temperature, m_i h_i (fp32: s_i is g_i / temperature itself).  16 us for 2048 x 4096 bf16
-// with lists of 32, 6 for 263 x 1088 fp32 with 17.
+// probability, get index -1; bf16: probabilities over f_i.  The factors as k_grad_scales, over the temperature: s_i,
+// G m_i / temperature, G / temperature, lse_i + log f_i, m_i h_i (fp32: s_i is g_i / temperature itself).  18
+// us for 2048 x 4096 bf16 with lists of 32, 6 for 263 x 1088 fp32 with 17.
 template <typename T, typename LT>
 __global__ __launch_bounds__(256) void k_distill_scales(const int64_t* __restrict__ index, const LT* __restrict__ logit,
                                                         const float* __restrict__ g, int64_t N, int64_t V, int top,
-                                                        float inv_temp, const T* __restrict__ h, int64_t K,
-                                                        TeacherLists list, GradScales out, T* __restrict__ scaled) {
+                                                        float inv_temp, const T* __restrict__ h, const T* __restrict__ W,
+                                                        const float* __restrict__ lse, int64_t K, TeacherLists list,
+                                                        GradScales out, T* __restrict__ scaled) {
   __shared__ int32_t s_index[4][kMaxTop];
   __shared__ float s_prob[4][kMaxTop];
-  constexpr int kEach = 16 / sizeof(T);
+  constexpr int kEach = 16 / sizeof(T), kSlots = kMaxTop / kWave;
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
   const int64_t i = (int64_t)blockIdx.x * 4 + w;
   if (i >= N) return;                                      // whole waves: no barrier here
   const float gi = g[i];
   const Teacher teacher = teacher_list(index + i * top, logit + i * top, V, top, inv_temp, s_index[w], s_prob[w]);
-  for (int k = lane; k < list_pitch(top); k += kWave) {
-    int32_t v = s_index[w][k];                             // -1 behind the list
-    float p = 0.f;
-    if (v >= 0)
-      for (int j = 0; j < top; ++j)
-        if (s_index[w][j] == v) {
-          if (j < k) {
-            p = 0.f;
-            break;
-          }
-          p += s_prob[w][j];
+  float p[kSlots];
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    const int k = q * kWave + lane, v = s_index[w][k];     // -1 behind the list
+    p[q] = 0.f;
+    if (v < 0) continue;
+    for (int j = 0; j < top; ++j)
+      if (s_index[w][j] == v) {
+        if (j < k) {
+          p[q] = 0.f;
+          break;
         }
-    list.index[i * list_pitch(top) + k] = p == 0.f ? -1 : v;
-    list.prob[i * list_pitch(top) + k] = p;
+        p[q] += s_prob[w][j];
+      }
   }
   const bool live = teacher.live && gi != 0.f;
-  float m = 1.f;
+  float m = 1.f, over_f = 1.f, exact = 0.f;                // 1 / f_i, what the exact entry's p is over s_i (0: no such)
+  int slot = -1;                                           // and its slot
   if constexpr (sizeof(T) == 2) {
     const float G = common_factor(index, logit, g, N, V, top);
-    float si = 0.f;
+    float si = 0.f, base = 0.f;
     if (live) {
+      base = lse[i];
+      float f = 1.f;
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q)
+        if (const uint64_t half = __ballot(p[q] >= 0.5f); half && slot < 0) slot = q * kWave + __builtin_ctzll(half);
+      if (slot >= 0) {
+        const float logit_s = row_dot(h + i * K, W + (int64_t)s_index[w][slot] * K, K) * inv_temp;
+        const float t = __shfl(slot < kWave ? p[0] : p[kSlots - 1], slot & (kWave - 1));
+        const float off = t - 1.f - expm1f(logit_s - base);                // t - softmax
+        if (fabsf(off) >= kLeastRest) {                                    // not a NaN either
+          exact = off > 0.f ? -1.f : 1.f;
+          f = fabsf(off);
+          over_f = 1.f / f;
+          base += logf(f);
+        }
+      }
       si = gi;
-      if (const float ratio = fabsf(gi) / G; ratio < INFINITY) {
+      if (const float ratio = fabsf(gi) * f / G; ratio < INFINITY) {
         float most = fmaxf(__uint_as_float(__float_as_uint(ratio) & 0x7F800000u), 0x1p-60f);   // 2^floor(log2(ratio))
         m = ratio / most;
         if (m > 1.f && most < 0x1p127f) {
@@ -1047,10 +1076,19 @@ __global__ __launch_bounds__(256) void k_distill_scales(const int64_t* __restric
     if (lane == 0) {
       out.s[i] = si;
       out.row[i] = G * m * inv_temp;
+      out.lse[i] = base;
       if (i == 0) *out.all = G * inv_temp;
     }
   } else if (lane == 0) {
     out.s[i] = live ? gi * inv_temp : 0.f;
+  }
+#pragma unroll
+  for (int q = 0; q < kSlots; ++q) {
+    const int k = q * kWave + lane;
+    if (k >= list_pitch(top)) continue;
+    const float y = exact != 0.f && k == slot ? exact - kExactEntry : p[q] * over_f;
+    list.index[i * list_pitch(top) + k] = p[q] == 0.f ? -1 : s_index[w][k];
+    list.prob[i * list_pitch(top) + k] = y;
   }
   if (!scaled) return;
   const T* __restrict__ from = h + i * K;
@@ -1245,8 +1283,6 @@ hipError_t grad_t(const VocabArgs& a, hipStream_t s) {
     factor = out.s;
     row_scale = out.row;
     all_scale = out.all;
-  }
-  if (sizeof(T) == 2 && a.top == 0) {
     lse = out.lse;
     at_target = out.at_target;
   }
@@ -1258,11 +1294,11 @@ hipError_t grad_t(const VocabArgs& a, hipStream_t s) {
     if (a.top_bf16)
       hipLaunchKernelGGL((k_distill_scales<T, uint16_t>), grid, dim3(256), 0, s, a.top_index,
                          static_cast<const uint16_t*>(a.top_logit), a.g, a.N, a.V, a.top, 1.f / a.temperature,
-                         static_cast<const T*>(a.h), a.K, lists, out, h);
+                         static_cast<const T*>(a.h), W, a.lse, a.K, lists, out, h);
     else
       hipLaunchKernelGGL((k_distill_scales<T, float>), grid, dim3(256), 0, s, a.top_index,
                          static_cast<const float*>(a.top_logit), a.g, a.N, a.V, a.top, 1.f / a.temperature,
-                         static_cast<const T*>(a.h), a.K, lists, out, h);
+                         static_cast<const T*>(a.h), W, a.lse, a.K, lists, out, h);
   } else if (sizeof(T) == 2 || h)
     hipLaunchKernelGGL((k_grad_scales<T>), dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, s, a.g, a.target, a.N, a.V,
                        static_cast<const T*>(a.h), W, a.lse, a.K, out, h);
