@@ -53,3 +53,12 @@ def test_borders_of_what_is_drawn_instead(dt, V):
     c = {"p": p.to(dt), "q": None, "draft": torch.full((3, 1), 3000), "u": torch.full((3, 1), 0.75), "r": torch.rand(3), "draft_len": None}
     want, kept = check(c, dev, ("the refused token", dt, V))
     assert not kept.any() and (want[:, 0] == 3000).all()
+
+
+@pytest.mark.parametrize("size", [(255, 2, 1001), (256, 2, 1001), (257, 2, 1001), (400, 1, 9001), (512, 1, 700), (513, 1, 700)],
+                         ids=lambda s: "S%d-D%d-V%d" % s)
+def test_numbers_of_sequences(size):
+    """Around where a workgroup a sequence becomes many."""
+    dev = device()
+    for dt, greedy in ((F32, False), (BF, True)):
+        check(make(*size, dt, greedy, 33), dev, (size, dt, greedy))

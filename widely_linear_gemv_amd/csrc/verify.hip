@@ -308,12 +308,12 @@ __global__ __launch_bounds__(kWave) void k_verify_pick(VerifyArgs a, int pieces,
 
 int pieces_of(int64_t V) { return (int)((V + kPiece - 1) / kPiece); }
 
-// One workgroup a sequence reads its rows at some 50 GB/s: as fast as two launches at 32000 entries (fp32: one
-// sequence 10.0 us against 10.5, 64 of bf16 12.5 and 14.1, 256 18.1 and 22.5), not at 65536 (14.1 and 10.4) nor
-// where there are more sequences than the device holds at once (600: 45 and 39).  (Measured while an entry took 16
-// instructions; with 9, one sequence of 32000 takes 8.4 us and of 131072, in two launches, 8.6; 64 of 131072, 67
-// MB, 19 us; 256 of 131072, 268 MB, 49 us, 5.5 TB/s.)
-bool alone(int64_t S, int64_t V) { return V <= 40960 && S <= 512; }
+// One workgroup a sequence, or two launches.  fp32 p and q, kernels in a row, one launch and two: one sequence of
+// 5003 entries 5.7 and 8.2 us, 32000 8.0 and 8.4, 40960 8.6 and 8.7, 50257 12.9 and 8.6, 131072 16.9 and 8.6; 64
+// sequences 6.8 and 10.3, 8.6 and 9.3, 10.6 and 10.0, 14.1 and 10.7, 24.0 and 17.1; 256, one a CU, 7.1 and 10.3, 15.4
+// and 18.3, 17.3 and 18.5, 22.7 and 22.0, 45.1 and 40.1; 512, two a CU, 12.6 and 11.4, 28.7 and 27.3, 31.1 and 28.4.
+// (bf16, 256: 7.9 and 11.0, 11.1 and 14.5, 11.6 and 14.1, 17.8 and 18.3; 512: 14.2 and 11.9, 24.1 and 22.6.)
+bool alone(int64_t S, int64_t V) { return V <= 40960 && S <= 256; }
 
 template <typename T>
 hipError_t verify_t(const VerifyArgs& a, void* ws, hipStream_t s) {
