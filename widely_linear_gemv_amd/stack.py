@@ -55,6 +55,13 @@ class DecodeStep:
             for p, (name, rows, cols, _) in zip(projs, PROJECTIONS):
                 if isinstance(p, W4Layer) and (p.rows, p.cols) != (rows, cols):
                     raise ValueError(f"layer {L}, {name}: {p.rows} x {p.cols} at four bits, need {rows} x {cols}")
+        # per layer and group: its projections at two bits, and those at four
+        self._groups = []
+        for projs in layers:
+            four = [isinstance(p, W4Layer) for p in projs]
+            self._groups.append([([p for p, proj in enumerate(PROJECTIONS) if proj[3] == g and not four[p]],
+                                  [p for p, proj in enumerate(PROJECTIONS) if proj[3] == g and four[p]])
+                                 for g in range(GROUPS)])
         if (adapters is None) != (segments is None):
             raise ValueError("adapters and segments go together")
         self.adapters, self.segments = adapters, segments
@@ -82,19 +89,19 @@ class DecodeStep:
         if self.algo in _DIGIT_FORMS:
             nbytes, self._convert, code = _DIGIT_FORMS[self.algo]
             self.digits = [[XDigits(torch.empty((nbytes(x.shape[1] // 2, B),), dtype=torch.uint8, device=dev),
-                                    B, x.shape[1] // 2, code)
-                            for x in layer_xs] for layer_xs in xs]
+                                    B, x.shape[1] // 2, code) if two_bit else None      # nothing would read it
+                            for x, (two_bit, _) in zip(layer_xs, groups)] for layer_xs, groups in zip(xs, self._groups)]
             if digits_given:
                 for layer_xs, layer_digits in zip(xs, self.digits):
                     for x, d in zip(layer_xs, layer_digits):
-                        self._convert(x, out=d)
+                        if d is not None:
+                            self._convert(x, out=d)
 
     def run(self, stream=None):
         for L, projs in enumerate(self.layers):
             for g in range(GROUPS):
                 x = self.xs[L][g]
-                mine = [p for p, (_, _, _, grp) in enumerate(PROJECTIONS) if grp == g]
-                two_bit = [p for p in mine if not isinstance(projs[p], W4Layer)]
+                two_bit, four_bit = self._groups[L][g]
                 if two_bit:
                     if self.digits_given:
                         x = self.digits[L][g]
@@ -102,9 +109,8 @@ class DecodeStep:
                         x = self._convert(x, out=self.digits[L][g], stream=stream)
                     fairy2i_gemv_grouped([(projs[p][0], projs[p][1], x, self.ys[L][p]) for p in two_bit], algo=self.algo,
                                          stream=stream)
-                for p in mine:
-                    if p not in two_bit:
-                        fairy2i_gemv_w4(projs[p], self.xs[L][g], y=self.ys[L][p], stream=stream)
+                for p in four_bit:
+                    fairy2i_gemv_w4(projs[p], self.xs[L][g], y=self.ys[L][p], stream=stream)
                 if self.adapters is not None:
                     beside = [(*self.adapters[L][p], self.ys[L][p], None) for p, (_, _, _, grp) in enumerate(PROJECTIONS)
                               if grp == g and self.adapters[L][p] is not None]
