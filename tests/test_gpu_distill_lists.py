@@ -161,3 +161,38 @@ def test_an_entry_that_dominates_moves_no_whole_row(sure, T):
         along, rest = ((err * want).sum(1) / size).abs(), u * left.sum(1) / size + 2.0 ** -14
         assert (along <= room + rest).all(), (along.max(), room)
         assert (along - rest).clamp(min=0).square().mean().sqrt() <= 2.0 ** -11
+
+
+@pytest.mark.parametrize("kind", ["mean", "two", "random"])
+def test_no_rounding_of_g_reaches_all_values(kind):
+    """bf16, g that lie 2^-8 of themselves from the nearest bf16 value (both of `two` in the same direction): the
+    part of dh's and dW's error along dh and dW themselves.  A g rounded to bf16 makes it 14.3 2^-12 (mean) and
+    12.3 2^-12 (two; 14.3 and 11.2 2^-12 in the halves of dh); `random` g are rounded in all directions.  What may
+    be there: the final roundings, six standard deviations 6 2^-8 (3 / (N K))^0.5 / 3^0.5 < 2^-14; those of p, of
+    which each entry's share is p_iv <W_v, dh_i> / |dh|^2 (six deviations of their sum, computed below); 2^-13 for
+    values of unequal size; and for dW the rounding of m h, one for each of the 128 significands of h, which is the
+    same m for half of the tokens of `two`: six deviations of half of 2^-8 (1.5 / 128 / 3)^0.5, 3 2^-12."""
+    dev = device()
+    N, V, K = 300, 2000, 512
+    c, d = make(N, V, K, 16, BF, 16, dev, ignored=0.1, near=False)
+    one, other = 2.0 ** -8 * (1 + 0.9 * 2.0 ** -8), 1.25 * 2.0 ** -8 * (1 + 0.7 * 2.0 ** -8)
+    g = {"mean": torch.full((N,), one), "two": torch.where(torch.arange(N) % 2 == 0, one, other), "random": c["g"]}[kind]
+    c["g"], d["g"] = g, g.to(dev)
+    announce("distill rounding of g", kind)
+    _, lse = forward(d)
+    dh, dW = (t.double().cpu() for t in backward(d, lse))
+    r = reference(c)
+    wh, _, wW, _ = grad_reference(c, r)
+    h, W = c["h"].double(), c["W"].double()
+    p = (r["l"] - r["lse"][:, None]).exp().scatter_add_(1, r["at"], -r["t"]) * torch.where(r["counts"], g.double(), 0.0)[:, None]
+    along = lambda err, want: abs(((err * want).sum() / (want * want).sum()).item())
+    for got, want, shares, more in ((dh, wh, p * (wh @ W.t()), 0.0), (dW, wW, p * (h @ wW.t()), 3 * 2.0 ** -12)):
+        own = 6 * 2.0 ** -8 / 3 ** 0.5 * shares.square().sum().sqrt().item() / (want * want).sum().item()
+        limit = 2.0 ** -12 + own + more
+        assert limit < 10 * 2.0 ** -12                     # a rounded g is seen
+        assert along(got - want, want) <= limit, (along(got - want, want), limit)
+    if kind == "two":                                       # each half by itself
+        for half in (0, 1):
+            want = wh[half::2]
+            own = 6 * 2.0 ** -8 / 3 ** 0.5 * (p * (wh @ W.t()))[half::2].square().sum().sqrt().item() / (want * want).sum().item()
+            assert along((dh - wh)[half::2], want) <= 2.0 ** -12 + own < 10 * 2.0 ** -12
