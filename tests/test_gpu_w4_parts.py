@@ -1,0 +1,56 @@
+"""Four-bit products: what fp32 sums of exact products have to give to the last bits, beside test_gpu_w4.py, whose
+bounds grow with the columns."""
+import pytest
+import torch
+
+from gpu_util import announce, device
+
+import widely_linear_gemv_amd as f2
+
+pytestmark = pytest.mark.gpu
+E24 = 2.0 ** -24
+BF, F32 = torch.bfloat16, torch.float32
+SIZES = [(33, 1405), (4096, 300), (4100, 700), (10240, 130), (10300, 2000), (16384, 129), (16500, 640)]
+
+
+def layer_of(rows, cols, G, sdt, seed, dev):
+    """Codes 7..15 over zero points 0..3, some over 19 and more, and scales that are powers of two."""
+    g = torch.Generator(device=dev).manual_seed(seed)
+    groups = -(-cols // G)
+    codes = torch.randint(7, 16, (rows, cols), generator=g, device=dev, dtype=torch.uint8)
+    zero = torch.randint(0, 4, (rows, groups), generator=g, device=dev, dtype=torch.uint8)
+    far = torch.rand(rows, groups, generator=g, device=dev) < 0.3
+    zero[far] = torch.randint(19, 256, (int(far.sum()),), generator=g, device=dev, dtype=torch.uint8)
+    scales = torch.exp2(torch.randint(-6, 7, (rows, groups), generator=g, device=dev).float()).to(sdt)
+    return codes, scales, zero, f2.fairy2i_pack_w4(codes, scales, G, zero)
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "%dx%d" % s)
+def test_every_bit_of_fp32_x_counts(size, G):
+    """One value a batch entry: y is s (c - z) x, off by the rounding of (16 + c) x / 16 in a sum (2^-24 of it;
+    twice that allows for a matrix instruction that rounds once more) and that of the result.  x is 24 bits of
+    which the second eight are 0x40..0x6f and the last 0x30..0x3f: cut into bf16 parts, the third is 48 2^-23 of x's
+    power of two or more, and a product without it would be off by |c - z| 48 / (2 (16 + c + |c - z|)) times what is
+    allowed here, 3.5 times at least (c - z >= 4, or <= -4)."""
+    dev = device()
+    rows, cols = size
+    g = torch.Generator(device=dev).manual_seed(5)
+    codes, scales, zero, layer = layer_of(rows, cols, G, BF if G == 64 else F32, 3, dev)
+    every = torch.arange(cols, device=dev) if rows < 100 else torch.unique(torch.cat([
+        torch.randint(0, cols, (40,), generator=g, device=dev), torch.tensor([0, 1, 31, 32, 127, 128, cols - 1], device=dev)]))
+    announce("w4 every bit", size, G)
+    for B in (16, 4, 1):
+        for k in range(0, len(every) if B == 16 or rows < 100 else 3 * B, B):
+            at = every[k:k + B]
+            n = len(at)
+            draw = lambda lo, hi: torch.randint(lo, hi, (n,), generator=g, device=dev)
+            bits = 0x3F800000 | draw(0, 128) << 16 | draw(0x40, 0x70) << 8 | draw(0x30, 0x40)
+            v = bits.to(torch.int32).view(F32) * torch.where(torch.arange(n, device=dev) % 2 == 0, 1.0, -1.0)
+            x = torch.zeros((n, cols), device=dev)
+            x[torch.arange(n, device=dev), at] = v
+            y = f2.fairy2i_gemv_w4(layer, x).double()
+            c, z, s = codes[:, at].t().double(), zero[:, at // G].t().double(), scales[:, at // G].t().double()
+            want = s * (c - z) * v.double()[:, None]
+            room = 2 * E24 * s * v.double().abs()[:, None] * (16 + c + (c - z).abs())
+            assert ((y - want).abs() <= room).all(), (size, G, B, k, ((y - want).abs() / room).max())
