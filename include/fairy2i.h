@@ -375,10 +375,11 @@ int fairy2i_pack_w4(const uint8_t* codes, const void* scales, int scales_dtype, 
  *   x        [B][cols], x_dtype FAIRY2I_F32 or FAIRY2I_BF16; 16-byte aligned as a whole, rows of any length.
  *   y        out, [B][rows], y_dtype FAIRY2I_F32 or FAIRY2I_BF16 (rounded once), 16-byte aligned, overlapping
  *            neither packed nor x.
- * Exact products of bf16 x (fp32 x: as three bf16 parts that hold it) in fp32 sums of sum_j (1 + c / 16) x and
- * sum_j x for each group, in an order that does not depend on B.  Values under bf16's normal range (x under
- * 2^-126, low parts of fp32 x under 2^-110) may count as 0.  A NaN in a batch entry stays in that entry; an
- * infinity, or sums past fp32's range, give NaN or infinity in its outputs.  Uses no workspace. */
+ * Exact products in fp32 sums, in an order that does not depend on B: of bf16 x the sums of (1 + c / 16) x and of x
+ * for each group, of fp32 x (as three bf16 parts that hold it) those of (c - z) x.  Values under bf16's normal
+ * range (x under 2^-126, low parts of fp32 x under 2^-110) may count as 0.  A NaN in a batch entry stays in that
+ * entry; an infinity, or a group's sums past fp32's range before its scale, give NaN or infinity in its outputs.
+ * Uses no workspace. */
 int fairy2i_gemv_w4(const uint8_t* packed, int64_t rows, int64_t cols, int group, int scales_dtype, const void* x,
                     int x_dtype, int64_t B, void* y, int y_dtype, hipStream_t stream);
 

@@ -54,3 +54,46 @@ def test_every_bit_of_fp32_x_counts(size, G):
             want = s * (c - z) * v.double()[:, None]
             room = 2 * E24 * s * v.double().abs()[:, None] * (16 + c + (c - z).abs())
             assert ((y - want).abs() <= room).all(), (size, G, B, k, ((y - want).abs() / room).max())
+
+
+@pytest.mark.parametrize("G", [32, 64, 128])
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "%dx%d" % s)
+def test_weights_that_are_zero_give_zero(size, G):
+    """fp32 x, codes that are their zero points: every product is 0, and so is y, whatever x is."""
+    dev = device()
+    rows, cols = size
+    g = torch.Generator(device=dev).manual_seed(6)
+    zero = torch.randint(0, 16, (rows, -(-cols // G)), generator=g, device=dev, dtype=torch.uint8)
+    codes = zero.repeat_interleave(G, 1)[:, :cols].contiguous()
+    layer = f2.fairy2i_pack_w4(codes, torch.rand(zero.shape, generator=g, device=dev), G, zero)
+    announce("w4 zero weights", size, G)
+    for B in (1, 3, 16):
+        x = torch.randn((B, cols), generator=g, device=dev) * 10 + 3
+        assert not f2.fairy2i_gemv_w4(layer, x).any()
+
+
+@pytest.mark.parametrize("mean", [0.0, 3.0, 100.0])
+@pytest.mark.parametrize("size", [(1003, 1405, 32), (4096, 4096, 128), (512, 11008, 64), (12000, 4096, 128), (6144, 2048, 64)],
+                         ids=lambda s: "%dx%d-G%d" % s)
+def test_no_less_exact_than_a_product_of_the_layer_written_out(size, mean):
+    """fp32 x of any mean: y is no farther from 64 bits (2-norm) than the fp32 product with the matrix itself,
+    whose entries s (c - z) fp32 holds exactly for bf16 scales.  Both have terms of size |s (c - z) x|; a matrix
+    instruction sums 32 of them here where the other product rounds after one or a few."""
+    dev = device()
+    rows, cols, G = size
+    g = torch.Generator(device=dev).manual_seed(7)
+    groups = -(-cols // G)
+    codes = torch.randint(0, 16, (rows, cols), generator=g, device=dev, dtype=torch.uint8)
+    zero = torch.randint(5, 11, (rows, groups), generator=g, device=dev, dtype=torch.uint8)
+    scales = (torch.rand(rows, groups, generator=g, device=dev) + 0.5).to(BF)
+    layer = f2.fairy2i_pack_w4(codes, scales, G, zero)
+    wide = lambda t: t.double().repeat_interleave(G, 1)[:, :cols]
+    W = wide(scales) * (codes.double() - wide(zero))
+    assert torch.equal(W.float().double(), W)
+    announce("w4 exactness", size, mean)
+    for B in (1, 5, 16):
+        x = torch.randn((B, cols), generator=g, device=dev) + mean
+        want = x.double() @ W.t()
+        mine = (f2.fairy2i_gemv_w4(layer, x).double() - want).norm().item()
+        plain = ((x @ W.float().t()).double() - want).norm().item()
+        assert mine <= plain, (size, mean, B, mine / want.norm().item(), plain / want.norm().item())

@@ -3,11 +3,18 @@
 //
 //     W_ij = s_i,j/G (c_ij - z_i,j/G)        y_bi = sum_j W_ij x_bj
 //
-// On the bf16 matrix cores: a code becomes the bf16 value 1 + c / 16 by a shift and one and-or for two of
-// them (its bits are the top of the significand), so within a group
+// On the bf16 matrix cores, with exact products and fp32 sums.  bf16 x: a code becomes the bf16 value 1 + c / 16 by
+// a shift and one and-or for two of them (its bits are the top of the significand), so within a group
 //     sum_j (c_j - z) x_j = 16 (sum_j (1 + c_j / 16) x_j - (1 + z / 16) sum_j x_j)
-// with exact products, fp32 sums, and sum_j x_j made once per workgroup.  (The value 128 + c takes the same
-// instructions but leaves five bits less of the sums.)  fp32 x enters as three bf16 parts that hold it.
+// with sum_j x_j made once for a workgroup's tiles.  (The value 128 + c takes the same instructions but leaves five
+// bits less of the sums.)  The two sums are larger than their difference; outputs are 1.0e-7 to 2.3e-7 of their norm
+// off, for x of mean 3 0.5e-7 to 1.0e-7, less than an fp32 product with the matrix written out (2.2e-7 to 9e-7).
+// fp32 x enters as three bf16 parts that hold it, so that three times as many roundings count: there a code becomes
+// c - z itself, exact in bf16 for every byte z (4.75 instructions for two codes instead of 1.75).  A weight that is
+// 0 then adds 0, and outputs are 1.2e-7 off instead of 3.5e-7 to 1.3e-6, for x of mean 3 1.0e-7 instead of 5e-7 to
+// 1.9e-6 (the matrix written out 3e-7 to 11e-7).  It costs 0.1-1.7 us: 4096 x 4096, one entry 7.1 -> 7.2 us; 11008 x
+// 4096, 16 entries 14.9 -> 16.2, one entry 10.8 -> 12.5.  (With bf16 x the same would cost 32000 x 4096, one entry,
+// 14.4 -> 17.2 us.)
 //
 // Packed form: tiles of 16 rows, one after another, each in blocks of 128 columns.  A block is 1 KB of codes,
 // then its scales, then its zero points.  In the codes lane l = 16 g + r of a wave owns the 16 bytes of row r:
@@ -74,14 +81,28 @@ __global__ __launch_bounds__(256) void k_w4_scales(const ST* __restrict__ scales
 }
 
 // Eight codes as an operand.  (The masks are kept in registers: as literals they cost an instruction more.)
-struct CodeMask {
-  uint32_t bits = 0x00780078u, one = 0x3F803F80u;
-  __device__ __forceinline__ CodeMask() { asm volatile("" : "+s"(bits), "+v"(one)); }
+template <bool EXACT>
+struct Codes {
+  uint32_t bits = 0x00780078u, one = EXACT ? 0x64006400u : 0x3F803F80u;
+  __device__ __forceinline__ Codes() { asm volatile("" : "+s"(bits), "+v"(one)); }
+  __device__ __forceinline__ uint32_t two(uint32_t w, int n) const {           // nibbles n and n + 4
+    return ((n < 3 ? w >> (4 * n) : __builtin_amdgcn_alignbit(w, w, 12)) & bits) | one;
+  }
+  // 1 + c / 16
+  __device__ __forceinline__ v4u plain(uint32_t w) const { return v4u{two(w, 0), two(w, 1), two(w, 2), two(w, 3)}; }
+  // c - z from the fp16 value 1024 + 8 c
+  __device__ __forceinline__ v4u minus(uint32_t w, float z) const {
+    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+    const float off = -128.f - z;
+    v4u out;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const v2h h = __builtin_bit_cast(v2h, two(w, n));
+      out[n] = pack_bf16(fmaf((float)h[0], 0.125f, off), fmaf((float)h[1], 0.125f, off));
+    }
+    return out;
+  }
 };
-__device__ __forceinline__ v4u codes_bf16(uint32_t w, const CodeMask& m) {
-  return v4u{(w & m.bits) | m.one, ((w >> 4) & m.bits) | m.one, ((w >> 8) & m.bits) | m.one,
-             (__builtin_amdgcn_alignbit(w, w, 12) & m.bits) | m.one};
-}
 
 // A load of 16 bytes at any element's alignment.
 struct __attribute__((packed, aligned(2))) Any16 {
@@ -220,7 +241,8 @@ __global__ __launch_bounds__(64 * NW) void k_w4(W4Kernel t) {
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int e = 0; e < NB; ++e) y[r][e] = 0.f;
-  const CodeMask mask;
+  constexpr bool kExact = sizeof(XT) == 4;
+  const Codes<kExact> codes;
   auto multiply = [&](const Block& b) {
     const v4u one = v4u{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
     asm volatile("" ::: "memory");                       // a wave's reads and writes of LDS stay in their order
@@ -234,19 +256,25 @@ __global__ __launch_bounds__(64 * NW) void k_w4(W4Kernel t) {
       for (int r = 0; r < RT; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = q * (G / 32); s < (q + 1) * (G / 32); ++s) {
+        v4u w[RT];
+        if constexpr (kExact)
+#pragma unroll
+          for (int r = 0; r < RT; ++r) w[r] = codes.minus(b.w[r][s], b.s[r].zero(q));
 #pragma unroll
         for (int p = X::kParts - 1; p >= 0; --p) {
           const v4u xp = *reinterpret_cast<const v4u*>(operand + p * X::kPlane + 64 * s);
-          sum = Mma<uint16_t>::run(xp, one, sum);
+          if constexpr (!kExact) sum = Mma<uint16_t>::run(xp, one, sum);
 #pragma unroll
-          for (int r = 0; r < RT; ++r) acc[r] = Mma<uint16_t>::run(xp, codes_bf16(b.w[r][s], mask), acc[r]);
+          for (int r = 0; r < RT; ++r)
+            acc[r] = Mma<uint16_t>::run(xp, kExact ? w[r] : codes.plain(b.w[r][s]), acc[r]);
         }
       }
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const float z = fmaf(b.s[r].zero(q), -0.0625f, -1.f), scale = 16.f * b.s[r].scale(q);
+        const float z = fmaf(b.s[r].zero(q), -0.0625f, -1.f), scale = b.s[r].scale(q);
 #pragma unroll
-        for (int e = 0; e < NB; ++e) y[r][e] = fmaf(scale, fmaf(z, sum[e], acc[r][e]), y[r][e]);
+        for (int e = 0; e < NB; ++e)
+          y[r][e] = kExact ? fmaf(scale, acc[r][e], y[r][e]) : fmaf(16.f * scale, fmaf(z, sum[e], acc[r][e]), y[r][e]);
       }
     }
   };
