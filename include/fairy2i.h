@@ -365,7 +365,7 @@ int fairy2i_gemm_noalloc(const uint8_t* packed, const float* scales, int64_t n, 
  *            (the last padded), one after another, each in blocks of 128 columns (the last padded): 1 KB of
  *            codes, then 16 scales and 16 zero points for each of the block's groups.
  * group 32, 64 or 128; 1 <= rows <= 2^24, 1 <= cols <= 2^20 and ceil(rows / 16) ceil(cols / 128) <= 2^23.
- * Projections that read the same x (q, k and v) are one layer, their rows one after another. */
+ * Projections that read the same x (q, k and v) may be one layer, their rows one after another: one launch. */
 size_t fairy2i_packed_bytes_w4(int64_t rows, int64_t cols, int group, int scales_dtype);
 int fairy2i_pack_w4(const uint8_t* codes, const void* scales, int scales_dtype, const uint8_t* zeros, int64_t rows,
                     int64_t cols, int group, uint8_t* packed, hipStream_t stream);

@@ -196,10 +196,12 @@ struct W4Kernel {
   int B, y_bf16;
 };
 
-// Bound by HBM for few entries (32000 x 4096, 68 MB: 15.1 us, 4.5 TB/s; all loads without products or x at 65536
-// columns 5.5 TB/s), by the launch for small layers (4096 x 4096, 8.7 MB: 4.2 us of which 2.6 are left without
-// any data to speak of), and for sixteen entries by x, which every workgroup reads from the L2 (4096 x 11008:
-// 90 MB of x beside 24 MB of codes in 11.5 us).
+// Bound by HBM for few entries (32000 x 4096, 68 MB: 13.4-15.1 us, 4.5-5.1 TB/s; all loads without products or x at
+// 65536 columns 5.5 TB/s), by the launch for small layers (4096 x 4096, 8.7 MB: 4.2 us of which 2.6 are left
+// without any data to speak of), and for sixteen entries by the chain of a wave's blocks: it waits for one, turns x
+// in LDS, multiplies, and loads the next.  A round of 2048 columns of 4096 rows takes 1.0 us for one entry, 1.6-1.8
+// for sixteen (4096 x 11008: 11.5 us for 26 MB of codes and 90 MB of x, 14-21 bytes a clock and CU, which the L2 has
+// more of); with fp32 x one of 1024 columns 1.2 and 1.75.
 // A workgroup of NW waves for RT tiles of 16 rows and all of the batch: the waves take the blocks of columns in
 // turn and their sums meet in LDS in wave order.  Batch entries are the rows of the product, so that a lane
 // holds one weight row's sums for four entries and needs that row's scales alone.
@@ -316,16 +318,21 @@ void w4_run(const W4Kernel& t, hipStream_t s) {
 }
 
 // Waves to a tile (NW) and tiles to a workgroup (RT).  One block of codes in flight a wave, and as many waves
-// on a CU as its registers hold, beat fewer waves with two to eight blocks in flight by 5-30 % (32000 x 4096,
-// one entry: 14.2-15.1 us, with two blocks 17.6, four 19.7).  Up to a tile a CU sixteen waves share a tile (4096
+// on a CU as its registers hold, beat fewer waves with two to eight blocks in flight by 5-30 % where there are
+// tiles for them (32000 x 4096, one entry: 14.2-15.1 us, with two blocks 17.6, four 19.7; not measured up to a tile a
+// CU, where the grid and not the registers bounds the waves).  Up to a tile a CU sixteen waves share a tile (4096
 // x 4096, one entry: 16 waves 4.3 us, 8 waves 5.2; 4096 x 11008, 16 entries 11.6 and 11.8), beyond that eight
 // (6144 x 4096: 8 waves 5.8, 16 waves 6.7; 32000 x 4096: 16.7 and 21.9).  fp32's three parts of x leave LDS for
-// eight.  More tiles a workgroup share what a block of x costs: two from four tiles a CU on (32000 x 4096, one
-// entry: 14.2 us against 16.7; 11008 x 4096: 7.4 against 7.1), with fp32 x from one on (6144 x 4096: 7.9 against
-// 8.8); with more than four entries, whose x is four times as long, two from one on (8192 x 4096, eight entries:
-// 6.9 against 7.4, four tiles 8.5) and four from two and a half on (11008 x 4096, 16 entries: 9.3, two tiles
-// 11.2; 32000 x 4096: 18.6 and 20.8).  The waves alone decide the order of a sum, so it is the same for every
-// batch.
+// eight at sixteen entries (13 KB a wave), and fewer entries take eight too: the waves alone decide the order of a
+// sum, which is to be the same for every batch.
+// More tiles a workgroup share what a block of x costs.  bf16 x: two from four tiles a CU on (32000 x 4096, one
+// entry: 14.2 us against 16.7; 11008 x 4096: 7.4 against 7.1); with more than four entries, whose x is four times as
+// long, two from one on (8192 x 4096, eight entries: 6.9 against 7.4, four tiles 8.5) and four from two and a half on
+// (11008 x 4096, 16 entries: 9.3, two tiles 11.2; 32000 x 4096: 18.6 and 20.8).  fp32 x: two from one tile a CU on
+// (one entry, groups of 128: 6144 x 4096 8.8 us, one tile 8.9, four 13.0; 11008 x 4096 12.5, 12.0 and 13.4; 16384 x
+// 4096 13.2, 15.3 and 13.8; 32000 x 4096 23.0, 26.6 and 21.8, but groups of 32 25.3, 28.2 and 27.8), with more than
+// four entries as for bf16 (16 entries: 8192 x 4096 two tiles 12.6, four 16.0, one 18.5; 11008 x 4096 22.5, 16.3 and
+// 26.3; 32000 x 4096 44.7, 32.2 and 67.6; groups of 32 45.2, 34.2 and 69.9).
 constexpr int kCUs = 256;
 template <int G, typename XT, typename ST>
 void w4_shape(const W4Kernel& t, hipStream_t s) {
