@@ -1008,7 +1008,7 @@ __device__ __forceinline__ float common_factor(const int64_t* __restrict__ index
 // Distillation: what the gradient's products need, one wave per token.  The token's list: an entry listed more
 // than once keeps its first slot, with the sum of its probabilities; its other slots, and entries without
 // probability, get index -1; bf16: probabilities over f_i.  The factors as k_grad_scales, over the temperature: s_i,
-// G m_i / temperature, G / temperature, lse_i + log f_i, m_i h_i (fp32: s_i is g_i / temperature itself).  18
+// G m_i / temperature, G / temperature, lse_i + log f_i, m_i h_i (fp32: s_i is g_i / temperature itself).  17
 // us for 2048 x 4096 bf16 with lists of 32, 6 for 263 x 1088 fp32 with 17.
 template <typename T, typename LT>
 __global__ __launch_bounds__(256) void k_distill_scales(const int64_t* __restrict__ index, const LT* __restrict__ logit,

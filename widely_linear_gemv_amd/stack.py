@@ -15,8 +15,8 @@ digits_given=True the digit forms are made once when the step is built and the s
 GEMVs alone (for inputs that arrive in digit form, from a producer that writes it).  This module only sequences
 calls of the C ABI (through the binding); all arithmetic runs in the library's kernels.
 
-A projection may be kept at four bits (a W4Layer in place of its packed form and scales): it is a
-launch of its own behind its group's, and takes the x itself whatever form the group's is in.
+A projection may be kept at four bits (a W4Layer of its own in place of its packed form and scales): it
+is a launch of its own behind its group's, and takes the x itself whatever form the group's is in.
 
 With adapters, each group's launch is followed by one grouped low-rank adapter call (two launches)
 that adds every request's own adapter to the group's outputs in place.
