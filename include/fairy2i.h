@@ -409,10 +409,11 @@ int fairy2i_distill(const void* h, const void* W, int x_dtype, int64_t N, int64_
  *     dh_i = sum_v p_iv W_v        dW_v = sum_i p_iv h_i
  * (g_i / temperature within fp32's range) as fairy2i_vocab_loss_backward in everything else: pieces of the
  * vocabulary, p held in x_dtype between the products (bf16: in units of a power of two near |g_i|, the rest of
- * g_i applied to the fp32 sums of dh and, rounded, to h for dW, where equal g of all tokens that count cost nothing:
- * at most 32 tokens with used slots but no probability, or 4096 others, may lie in front of them with a g of their
- * own; where one entry has half of a list's probability, |g_i| times that entry's |softmax - t| in place of |g_i|,
- * so that its p is exact), fp32 sums, each output rounded once, either output NULL.  A token that does not count or
+ * g_i applied to the fp32 sums of dh and, rounded, to h for dW; equal g cost h nothing: of all tokens, or of those
+ * that count, if one of them with its list's first or last slot used is among the first 4096 and at most 31 such
+ * tokens without any probability, whose g may be others, are in front of it; where one entry has half of a list's
+ * probability, |g_i| times that entry's |softmax - t| in place of |g_i|, so that its p is exact and h is rounded),
+ * fp32 sums, each output rounded once, either output NULL.  A token that does not count or
  * has g_i = 0 adds nothing, whatever its row of h holds. */
 size_t fairy2i_distill_backward_workspace_bytes(int64_t N, int64_t V, int64_t K, int x_dtype, int top);
 int fairy2i_distill_backward(const void* h, const void* W, int x_dtype, int64_t N, int64_t V, int64_t K,
