@@ -196,3 +196,32 @@ def test_no_rounding_of_g_reaches_all_values(kind):
             want = wh[half::2]
             own = 6 * 2.0 ** -8 / 3 ** 0.5 * (p * (wh @ W.t()))[half::2].square().sum().sqrt().item() / (want * want).sum().item()
             assert along((dh - wh)[half::2], want) <= 2.0 ** -12 + own < 10 * 2.0 ** -12
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_the_most_tokens(dt):
+    """2^20 tokens with lists of 128: rows from both ends and between, as in test_gpu_distill.py; the gradient of W
+    of tokens that do not count but for those rows."""
+    dev = device()
+    N, V, K, top = 1 << 20, 70, 64, 128
+    g = torch.Generator(device=dev).manual_seed(51)
+    d = {"h": torch.randn(N, K, generator=g, device=dev).to(dt), "W": (torch.randn(V, K, generator=g, device=dev) / 8).to(dt),
+         "index": torch.randint(-20, V + 20, (N, top), generator=g, device=dev),
+         "logit": torch.randn(N, top, generator=g, device=dev), "g": torch.rand(N, generator=g, device=dev), "T": 1.0}
+    rows = torch.cat([torch.arange(500), torch.arange(N // 2 - 250, N // 2 + 250), torch.arange(N - 500, N)]).to(dev)
+    few = {k: v[rows] if k not in ("W", "T") else v for k, v in d.items()}
+    announce("distill most tokens", dt)
+    loss, lse = forward(d)
+    r = reference(few)
+    close(lse[rows], r["lse"], r["dl"], "lse")
+    close(loss[rows], r["loss"], r["dloss"], "loss")
+    dh, _ = backward(d, lse, want_dW=False)
+    wh, bh, wW, bW = grad_reference(few, r)
+    close(dh[rows], wh, bh, "dh")
+    others = torch.ones(N, dtype=torch.bool, device=dev)
+    others[rows] = False
+    d["index"][others] = -1
+    dh2, dW = backward(d, lse)
+    assert not dh2[others].any()
+    close(dh2[rows], wh, bh, "dh alone")
+    close(dW, wW, bW, "dW")

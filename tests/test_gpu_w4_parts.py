@@ -97,3 +97,34 @@ def test_no_less_exact_than_a_product_of_the_layer_written_out(size, mean):
         mine = (f2.fairy2i_gemv_w4(layer, x).double() - want).norm().item()
         plain = ((x @ W.float().t()).double() - want).norm().item()
         assert mine <= plain, (size, mean, B, mine / want.norm().item(), plain / want.norm().item())
+
+
+@pytest.mark.parametrize("xdt", [BF, F32])
+def test_the_most_rows_and_the_most_columns(xdt):
+    """2^24 rows of one column: y = s (c - z) x, each factor a whole number or a power of two.  2^20 columns of five
+    rows: all weights 0 but a few, whole sums."""
+    dev = device()
+    rows = 1 << 24
+    announce("w4 most rows", xdt)
+    codes = (torch.arange(rows, device=dev) % 16).to(torch.uint8).view(rows, 1)
+    scales = torch.exp2((torch.arange(rows, device=dev) % 7 - 3).float()).view(rows, 1).to(BF)
+    layer = f2.fairy2i_pack_w4(codes, scales, 128)
+    x = torch.arange(1, 17, device=dev).view(16, 1).to(xdt)
+    y = f2.fairy2i_gemv_w4(layer, x)
+    want = (scales.float() * (codes.float() - 8))[:, 0]
+    for b in range(16):
+        assert torch.equal(y[b], want * (b + 1)), b
+    del y, want, codes, scales, layer
+    cols = 1 << 20
+    announce("w4 most columns", xdt)
+    codes = torch.full((5, cols), 8, dtype=torch.uint8, device=dev)
+    codes[0, ::1000], codes[3, cols - 1], codes[4, cols // 2:] = 9, 0, 9
+    layer = f2.fairy2i_pack_w4(codes, torch.ones((5, cols // 32), device=dev), 32)
+    x = torch.ones((16, cols), dtype=xdt, device=dev)
+    x[15] = 2.0
+    want = torch.tensor([-(-cols // 1000), 0.0, 0.0, -8.0, cols // 2], device=dev).repeat(16, 1)
+    want[15] *= 2
+    if xdt == F32:
+        assert torch.equal(f2.fairy2i_gemv_w4(layer, x), want)
+    else:                                                 # sums of 1 + c / 16 of either sign, off by 2^-24 of 2^21 in all
+        assert ((f2.fairy2i_gemv_w4(layer, x) - want).abs() <= 2.0 ** -3).all()
